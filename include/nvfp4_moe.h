@@ -224,6 +224,37 @@ int moe_rmsnorm_quantize_act(const void* x, const void* gamma, float eps, int64_
                              int64_t cols, uint8_t* codes, uint8_t* sf, float* ts, float* rrms,
                              void* workspace, size_t ws_bytes, moe_stream_t stream);
 
+/* Residual addition, RMSNorm and MXFP8 output in one pass: what stands before a W4A8 layer in a
+ * transformer block.  Per row: h = bf16(x + residual), r = 1 / sqrt(mean(h^2) + eps),
+ * y = (h * r) * gamma in FP32; then, quantised from the FP32 y, MXFP8 (per 32 elements the E8M0
+ * scale byte and the E4M3 codes of MOE_FLAG_ACT_MXFP8 above), which moe_run_quantized takes, and
+ * optionally y rounded to BF16 (for the router, or as the norm of a layer that is trained).
+ *   x, residual, h, y: [rows, cols] BF16, gamma: [cols] BF16, all 16-byte aligned; cols a multiple
+ *   of 32, at most 16384; codes [rows, cols] (8-byte aligned), sf [rows, cols/32]; rrms: NULL or
+ *   device FP32 [rows] that receives each row's r.
+ *   residual and h are both given or both NULL (then h is x itself).  h may be the buffer of
+ *   residual or of x (in place); no other two buffers may overlap.  codes and sf are both given
+ *   or both NULL; y may be NULL if they are given.
+ * A 32-element block of y that holds an infinity or NaN gets scale byte 255 (NaN) and codes 0x7F
+ * (NaN); the sum of squares is FP32, so rows with elements above 2^63 can overflow it (r = 0).
+ * No workspace, one launch.  rows == 0 is MOE_OK. */
+int moe_add_rmsnorm_quantize_mx(const void* x, const void* residual, const void* gamma, float eps,
+                                int64_t rows, int64_t cols, void* h, uint8_t* codes, uint8_t* sf,
+                                void* y, float* rrms, moe_stream_t stream);
+
+/* Its backward pass; the quantisation is passed straight through (dy is the gradient of y).
+ * With a = gamma * dy: dx = dh + r * a - h * r^3 * mean(a * h) - the gradient of x and of the
+ * residual alike - and dgamma = sum over rows of dy * (h * r).
+ *   dy, h, dx: [rows, cols] BF16; dh: NULL or [rows, cols] BF16, the gradient that reaches h over
+ *   the residual stream; rrms: [rows] FP32 of the forward pass; gamma: [cols] BF16; dgamma:
+ *   [cols] FP32 (overwritten).  16-byte aligned (rrms, dgamma 4).  dx may be the buffer of dy or dh.
+ * dgamma is summed in a fixed order: the same call gives the same bits.  workspace: 16-byte
+ * aligned, of the size below; it carries no status word.  rows == 0 zeroes dgamma. */
+size_t moe_add_rmsnorm_backward_workspace_size(int64_t rows, int64_t cols);
+int moe_add_rmsnorm_backward(const void* dy, const void* dh, const void* h, const float* rrms,
+                             const void* gamma, int64_t rows, int64_t cols, void* dx,
+                             float* dgamma, void* workspace, size_t ws_bytes, moe_stream_t stream);
+
 /* ---------------------------------------------------------------------------------------------
  * Router + plan.  logits [T,E] FP32 -> topk_ids [T,k] (slot 0 the largest), topk_w [T,k],
  * counts [E], offsets [E+1] (exclusive prefix sums, offsets[E] = T*k), perm_src [T*k]
@@ -233,6 +264,56 @@ size_t moe_plan_workspace_size(int32_t T, int32_t E, int32_t k);
 int moe_plan(const float* logits, int32_t T, int32_t E, int32_t k, int32_t* topk_ids,
              float* topk_w, int32_t* counts, int32_t* offsets, int32_t* perm_src, int32_t* inv,
              void* workspace, size_t ws_bytes, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Router losses.  Per-expert counts, the balance loss and the z loss of one batch of routed
+ * tokens, and the gradient of the logits.  A token counts unless mask (uint8 [T], may be NULL) is
+ * 0 there - its logits and ids are then not read - or all its logits are -infinity; n tokens
+ * count.  p are the token's expert probabilities over all E: softmax(logits), or with
+ * MOE_FLAG_ROUTER_SQRTSOFTPLUS in flags s / sum(s), s = sqrt(softplus(logit)); lse = log sum
+ * exp(logits) for either router.
+ *   counts_e (int32 [E]): how often e stands in topk_ids [T,k];  tokens (int32 [1]): n;
+ *   probs_e (FP32 [E]) = (1/n) sum_t p_te;
+ *   losses (FP32 [2]): [0] balance = E * sum_e (counts_e / (n k)) * probs_e,
+ *                      [1] z = (1/n) sum_t lse_t^2.   n = 0: zeros.
+ * An id outside [0, E) is not counted and leaves MOE_ERR_INVALID_ARG in the device status (first
+ * word of the workspace).  NaN or +infinity logits of a token that counts make the losses NaN.
+ * Sums run in a fixed order: the same call gives the same bits.
+ *
+ * Backward: counts and tokens as moe_router_loss wrote them (constants of the gradient);
+ * grad_losses: device FP32 [2], the gradients of the two losses (NULL: zeros); grad_topk_w: FP32
+ * [T,k], the gradient of the top-k weights that the router gave topk_ids (softmax over the k
+ * chosen logits, or s / sum of the k chosen s), NULL: none.  dlogits [T,E] is overwritten; tokens
+ * that do not count get zeros; ids outside [0, E) are left out; an id that stands twice gets both
+ * shares.
+ * 1 <= E <= 1024, 1 <= k <= min(E, 32); FP32 pointers 4-byte aligned.
+ * ------------------------------------------------------------------------------------------- */
+size_t moe_router_loss_workspace_size(int32_t T, int32_t E);
+int moe_router_loss(const float* logits, const int32_t* topk_ids, const uint8_t* mask, int32_t T,
+                    int32_t E, int32_t k, uint32_t flags, float* losses, int32_t* counts,
+                    int32_t* tokens, float* probs, void* workspace, size_t ws_bytes,
+                    moe_stream_t stream);
+int moe_router_loss_backward(const float* logits, const int32_t* topk_ids, const uint8_t* mask,
+                             int32_t T, int32_t E, int32_t k, uint32_t flags,
+                             const int32_t* counts, const int32_t* tokens,
+                             const float* grad_losses, const float* grad_topk_w, float* dlogits,
+                             moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * 4-bit matrix-vector product for decode-sized batches (the dense projections around the layer):
+ * y[t,n] = sum_k x[t,k] * W[n,k] for 0..64 rows x [T,K] BF16, W in the canonical layout:
+ *   NVFP4 (default): codes [N,K/2], sf [N,K/16] E4M3, ts: device FP32 tensor scale, as
+ *     moe_quantize_act (of the BF16 matrix [N,K]) and moe_weights_export write them;
+ *   MXFP4 (MOE_LINEAR_MXFP4): codes [N,K/2], sf [N,K/32] E8M0, ts NULL.
+ * y [T,N] is BF16, or FP32 with MOE_LINEAR_F32_OUT (router logits).  The products are exact, the
+ * sums FP32 in a fixed order that does not depend on the other rows of x.  K a multiple of 32, at
+ * most 2^20; N at most 2^30; x and codes 16-byte aligned, sf 2.  More than 64 rows:
+ * MOE_ERR_UNSUPPORTED_SHAPE.  No workspace, one launch.
+ * ------------------------------------------------------------------------------------------- */
+#define MOE_LINEAR_MXFP4 1u
+#define MOE_LINEAR_F32_OUT 2u
+int moe_linear_w4(const void* x, const uint8_t* codes, const uint8_t* sf, const float* ts,
+                  int32_t T, int64_t N, int64_t K, uint32_t flags, void* y, moe_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------------
  * moe_plan_static: moe_plan without a workspace argument.  It has no counterpart on the pages
@@ -288,7 +369,10 @@ int moe_run(const moe_config* cfg, const void* wbuf, const void* x, const float*
  * MoE directly).  xq [T, H/2] E2M1 codes (16-byte aligned), xsf [T, H/16] E4M3 scales (4-byte
  * aligned) and ts_a (device FP32 scalar, the tensor scale the codes were made with) are read
  * as they are; everything else as for moe_run, with the same workspace size, launch count and
- * output.  A negative, NaN or infinite *ts_a sets MOE_ERR_NONFINITE in the device status. */
+ * output.  A negative, NaN or infinite *ts_a sets MOE_ERR_NONFINITE in the device status.
+ * A W4A8 layer (MOE_FLAG_ACT_MXFP8) takes MXFP8 here: xq [T, H] E4M3 codes, xsf [T, H/32] E8M0
+ * scales (as moe_add_rmsnorm_quantize_mx writes them) and ts_a NULL; a code or scale that is not
+ * finite sets MOE_ERR_NONFINITE.  A W4A16 layer takes BF16 input only (MOE_ERR_INVALID_ARG). */
 int moe_run_quantized(const moe_config* cfg, const void* wbuf, const uint8_t* xq,
                       const uint8_t* xsf, const float* ts_a, const float* logits, int32_t T,
                       int32_t k, void* y, void* workspace, size_t ws_bytes, moe_stream_t stream,

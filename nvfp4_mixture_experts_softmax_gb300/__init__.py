@@ -7,6 +7,7 @@ library must have been built (``__graft_entry__.build()``); there is no fallback
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 
 import torch
@@ -25,7 +26,10 @@ EXPORTED = ["moe_status_string", "moe_config_check", "moe_weights_size", "moe_qu
             "moe_plan_workspace_size", "moe_plan", "moe_workspace_size", "moe_run",
             "moe_last_device_status", "moe_plan_static", "moe_run_kernel_count",
             "moe_set_router_bias", "moe_rmsnorm_workspace_size", "moe_rmsnorm_quantize_act",
-            "moe_run_quantized"]
+            "moe_run_quantized", "moe_add_rmsnorm_quantize_mx",
+            "moe_add_rmsnorm_backward_workspace_size", "moe_add_rmsnorm_backward",
+            "moe_router_loss_workspace_size", "moe_router_loss", "moe_router_loss_backward",
+            "moe_linear_w4"]
 
 
 class MoeConfig(C.Structure):
@@ -65,6 +69,7 @@ def lib():
                                "__graft_entry__ as g; g.build()')")
         L = C.CDLL(LIB_PATH)
         vp, i32, i64, sz = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t
+        u32, f32 = C.c_uint32, C.c_float
         cfgp = C.POINTER(MoeConfig)
         sig = {
             "moe_status_string": (C.c_char_p, [C.c_int]),
@@ -87,6 +92,17 @@ def lib():
             "moe_rmsnorm_workspace_size": (sz, [i64]),
             "moe_rmsnorm_quantize_act": (C.c_int, [vp, vp, C.c_float, i64, i64, vp, vp, vp, vp, vp, sz,
                                                    vp]),
+            "moe_add_rmsnorm_quantize_mx": (C.c_int, [vp, vp, vp, f32, i64, i64, vp, vp, vp, vp,
+                                                      vp, vp]),
+            "moe_add_rmsnorm_backward_workspace_size": (sz, [i64, i64]),
+            "moe_add_rmsnorm_backward": (C.c_int, [vp, vp, vp, vp, vp, i64, i64, vp, vp, vp, sz,
+                                                   vp]),
+            "moe_router_loss_workspace_size": (sz, [i32, i32]),
+            "moe_router_loss": (C.c_int, [vp, vp, vp, i32, i32, i32, u32, vp, vp, vp, vp, vp, sz,
+                                          vp]),
+            "moe_router_loss_backward": (C.c_int, [vp, vp, vp, i32, i32, i32, u32, vp, vp, vp, vp,
+                                                   vp, vp]),
+            "moe_linear_w4": (C.c_int, [vp, vp, vp, vp, i32, i64, i64, u32, vp, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -314,10 +330,11 @@ def run(cfg: MoeConfig, wbuf, x, logits, k=None, y=None, workspace=None, debug=F
         timer: StageTimer = None, quantized=None, inject: int = 0):
     """The layer: y [T, H] BF16 (and, with debug=True, a dict of its intermediates).  x is the BF16
     input [T, H]; or pass x=None and quantized=(xq [T, H/2] u8, xsf [T, H/16] u8, ts_a [1] f32),
-    already-NVFP4 activations (moe_run_quantized)."""
+    already-NVFP4 activations (moe_run_quantized).  A W4A8 layer takes MXFP8 there: (xq [T, H] u8,
+    xsf [T, H/32] u8, None), as add_rmsnorm_quantize_mx gives them."""
     if quantized is not None:
         xq, xsf, ts_a = quantized
-        T, H = xq.shape[0], xq.shape[1] * 2
+        T, H = xq.shape[0], xq.shape[1] * (1 if cfg.flags & FLAG_ACT_MXFP8 else 2)
         dev = xq.device
     else:
         T, H = x.shape
@@ -376,6 +393,233 @@ def run(cfg: MoeConfig, wbuf, x, logits, k=None, y=None, workspace=None, debug=F
         _check(lib().moe_run(C.byref(cfg), _ptr(wbuf), _ptr(x), _ptr(logits), T, k, _ptr(y),
                              _ptr(workspace), workspace.numel(), _stream(stream), dptr), "moe_run")
     return (y, dbg) if debug else y
+
+
+# ---- operators around the layer ----
+
+def _scoped(fn):
+    """Runs fn with its first tensor's device current and, if `stream` is passed, on that stream
+    (what fn allocates then belongs to that stream); otherwise on the device's current stream."""
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kw):
+        dev = first.device
+        if dev.type != "cuda":
+            raise ValueError(f"{fn.__name__} needs CUDA tensors, got one on {dev}")
+        if stream is None and dev.index == torch.cuda.current_device():
+            return fn(first, *args, **kw)
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"{fn.__name__}: the stream is on {stream.device}, the tensors on {dev}")
+        with torch.cuda.device(dev), torch.cuda.stream(stream):
+            return fn(first, *args, **kw)
+    return call
+
+
+def _given(t, name, dtype, shape, dev):
+    """Device address of a tensor argument after its checks (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                         f"{dev}, got {t.dtype} {tuple(t.shape)} stride {t.stride()} on {t.device}")
+    return t.data_ptr()
+
+
+def _need(t, name):
+    if t is None:
+        raise ValueError(f"{name} is required")
+    return t
+
+
+def _bytes_on(n, device):
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+_U8, _BF16, _F32, _I32 = torch.uint8, torch.bfloat16, torch.float32, torch.int32
+
+
+@_scoped
+def add_rmsnorm_quantize_mx(x, residual, gamma, eps: float = 1e-6, want_y: bool = False,
+                            want_rrms: bool = False, quantize: bool = True, out=None):
+    """h = bf16(x + residual), y = RMSNorm(h) * gamma and MXFP8 of y, in one launch.
+
+    x, residual [rows, cols] BF16 (residual None: h is x), gamma [cols] BF16.  Returns a dict of
+    h (absent without a residual), codes [rows, cols] u8 (E4M3) and sf [rows, cols/32] u8 (E8M0)
+    unless quantize is False, y [rows, cols] BF16 (want_y) and rrms [rows] FP32 (want_rrms).
+    out: a dict of preallocated tensors that takes the place of those switches; out["h"] may be
+    residual or x itself (in place).  stream: see run."""
+    if x.dim() != 2 or x.shape[1] % 32:
+        raise ValueError(f"x must be [rows, cols] with cols a multiple of 32, got {tuple(x.shape)}")
+    rows, cols = shape = x.shape
+    dev = x.device
+    if out is None:
+        out = {}
+        if residual is not None:
+            out["h"] = torch.empty_like(x)
+        if quantize:
+            out["codes"] = torch.empty(shape, dtype=_U8, device=dev)
+            out["sf"] = torch.empty(rows, cols // 32, dtype=_U8, device=dev)
+        if want_y:
+            out["y"] = torch.empty_like(x)
+        if want_rrms:
+            out["rrms"] = torch.empty(rows, dtype=_F32, device=dev)
+    get = out.get
+    st = lib().moe_add_rmsnorm_quantize_mx(
+        _given(x, "x", _BF16, shape, dev), _given(residual, "residual", _BF16, shape, dev),
+        _given(_need(gamma, "gamma"), "gamma", _BF16, (cols,), dev), eps, rows, cols,
+        _given(get("h"), "h", _BF16, shape, dev), _given(get("codes"), "codes", _U8, shape, dev),
+        _given(get("sf"), "sf", _U8, (rows, cols // 32), dev),
+        _given(get("y"), "y", _BF16, shape, dev), _given(get("rrms"), "rrms", _F32, (rows,), dev),
+        torch.cuda.current_stream().cuda_stream)
+    if st:
+        _check(st, "moe_add_rmsnorm_quantize_mx")
+    return out
+
+
+def add_rmsnorm_backward_workspace(rows: int, cols: int, device="cuda"):
+    return _bytes_on(lib().moe_add_rmsnorm_backward_workspace_size(rows, cols), device)
+
+
+@_scoped
+def add_rmsnorm_backward(dy, h, rrms, gamma, dh=None, out=None, workspace=None):
+    """Backward pass of add_rmsnorm_quantize_mx's norm, the quantisation passed straight through.
+
+    dy, h [rows, cols] BF16, rrms [rows] FP32, gamma [cols] BF16 as in the forward pass; dh: the
+    gradient that reaches h over the residual stream (BF16, or None).  Returns a dict of dx
+    [rows, cols] BF16 (the gradient of x and of the residual alike; out["dx"] may be dy or dh) and
+    dgamma [cols] FP32.  stream: see run."""
+    if dy.dim() != 2 or dy.shape[1] % 32:
+        raise ValueError(f"dy must be [rows, cols] with cols a multiple of 32, got {tuple(dy.shape)}")
+    rows, cols = shape = dy.shape
+    dev = dy.device
+    if out is None:
+        out = {"dx": torch.empty_like(dy), "dgamma": torch.empty(cols, dtype=_F32, device=dev)}
+    if workspace is None:
+        workspace = add_rmsnorm_backward_workspace(rows, cols, dev)
+    st = lib().moe_add_rmsnorm_backward(
+        _given(dy, "dy", _BF16, shape, dev), _given(dh, "dh", _BF16, shape, dev),
+        _given(_need(h, "h"), "h", _BF16, shape, dev),
+        _given(_need(rrms, "rrms"), "rrms", _F32, (rows,), dev),
+        _given(_need(gamma, "gamma"), "gamma", _BF16, (cols,), dev), rows, cols,
+        _given(out["dx"], "dx", _BF16, shape, dev),
+        _given(out["dgamma"], "dgamma", _F32, (cols,), dev),
+        _given(workspace, "workspace", _U8, workspace.shape, dev), workspace.numel(),
+        torch.cuda.current_stream().cuda_stream)
+    if st:
+        _check(st, "moe_add_rmsnorm_backward")
+    return out
+
+
+_ROUTER_FLAGS = {"softmax": 0, "sqrtsoftplus": FLAG_ROUTER_SQRTSOFTPLUS}
+
+
+def _router_flag(router):
+    if router not in _ROUTER_FLAGS:
+        raise ValueError(f"unknown router {router!r}")
+    return _ROUTER_FLAGS[router]
+
+
+def _mask_ptr(mask, T, dev):
+    if mask is None:
+        return None
+    return _given(mask, "mask", torch.bool if mask.dtype is torch.bool else _U8, (T,), dev)
+
+
+def _routing_shape(logits, topk_ids):
+    if logits.dim() != 2 or _need(topk_ids, "topk_ids").dim() != 2:
+        raise ValueError("logits must be [T, E] and topk_ids [T, k]")
+    return logits.shape[0], logits.shape[1], topk_ids.shape[1]
+
+
+def router_loss_workspace(T: int, E: int, device="cuda"):
+    return _bytes_on(lib().moe_router_loss_workspace_size(T, E), device)
+
+
+@_scoped
+def router_loss(logits, topk_ids, mask=None, router: str = "softmax", out=None, workspace=None):
+    """Per-expert counts and the router's losses for logits [T, E] FP32 and topk_ids [T, k] int32
+    (as plan gives them); mask [T] (bool or uint8) is 0 for padded tokens.
+
+    Returns a dict of losses [2] FP32 (balance, z), counts [E] int32, tokens [1] int32 and probs
+    [E] FP32 (mean expert probabilities); pass it to router_loss_backward.  An id outside [0, E)
+    is reported in the workspace's device status (last_device_status).  stream: see run."""
+    T, E, k = _routing_shape(logits, topk_ids)
+    dev = logits.device
+    if out is None:
+        out = dict(losses=torch.empty(2, dtype=_F32, device=dev),
+                   counts=torch.empty(E, dtype=_I32, device=dev),
+                   tokens=torch.empty(1, dtype=_I32, device=dev),
+                   probs=torch.empty(E, dtype=_F32, device=dev))
+    if workspace is None:
+        workspace = router_loss_workspace(T, E, dev)
+    st = lib().moe_router_loss(
+        _given(logits, "logits", _F32, (T, E), dev), _given(topk_ids, "topk_ids", _I32, (T, k), dev),
+        _mask_ptr(mask, T, dev), T, E, k, _router_flag(router),
+        _given(out["losses"], "losses", _F32, (2,), dev),
+        _given(out["counts"], "counts", _I32, (E,), dev),
+        _given(out["tokens"], "tokens", _I32, (1,), dev),
+        _given(out["probs"], "probs", _F32, (E,), dev),
+        _given(workspace, "workspace", _U8, workspace.shape, dev), workspace.numel(),
+        torch.cuda.current_stream().cuda_stream)
+    if st:
+        _check(st, "moe_router_loss")
+    return out
+
+
+@_scoped
+def router_loss_backward(logits, topk_ids, stats, grad_losses=None, grad_topk_w=None, mask=None,
+                         router: str = "softmax", dlogits=None):
+    """Gradient [T, E] FP32 of the logits from grad_losses [2] FP32 (on the device; the gradients
+    of the balance and z losses) and grad_topk_w [T, k] FP32 (of the top-k weights); either may be
+    None.  stats: what router_loss returned for the same logits, ids, mask and router."""
+    T, E, k = _routing_shape(logits, topk_ids)
+    dev = logits.device
+    if dlogits is None:
+        dlogits = torch.empty(T, E, dtype=_F32, device=dev)
+    st = lib().moe_router_loss_backward(
+        _given(logits, "logits", _F32, (T, E), dev), _given(topk_ids, "topk_ids", _I32, (T, k), dev),
+        _mask_ptr(mask, T, dev), T, E, k, _router_flag(router),
+        _given(stats["counts"], "counts", _I32, (E,), dev),
+        _given(stats["tokens"], "tokens", _I32, (1,), dev),
+        _given(grad_losses, "grad_losses", _F32, (2,), dev),
+        _given(grad_topk_w, "grad_topk_w", _F32, (T, k), dev),
+        _given(dlogits, "dlogits", _F32, (T, E), dev), torch.cuda.current_stream().cuda_stream)
+    if st:
+        _check(st, "moe_router_loss_backward")
+    return dlogits
+
+
+LINEAR_MXFP4 = 1
+LINEAR_F32_OUT = 2
+LINEAR_MAX_TOKENS = 64
+
+
+@_scoped
+def linear_w4(x, codes, sf, ts=None, out_dtype=torch.bfloat16, y=None):
+    """x [T, K] BF16 (T <= 64) times a 4-bit matrix: y [T, N] in out_dtype (bfloat16 or float32).
+
+    codes [N, K/2] u8 with sf [N, K/16] u8 (E4M3) and ts [1] FP32: NVFP4, as quantize_act(W) gives
+    them; with sf [N, K/32] u8 (E8M0) and no ts: MXFP4.  stream: see run."""
+    if x.dim() != 2 or codes.dim() != 2 or sf.dim() != 2:
+        raise ValueError("x must be [T, K], codes [N, K/2] and sf [N, K/16] or [N, K/32]")
+    (T, K), N, dev = x.shape, codes.shape[0], x.device
+    flags, block = (LINEAR_MXFP4, 32) if ts is None else (0, 16)
+    if K % 32:
+        raise ValueError(f"K must be a multiple of 32, got {K}")
+    if y is None:
+        y = torch.empty(T, N, dtype=out_dtype, device=dev)
+    if y.dtype is _F32:
+        flags |= LINEAR_F32_OUT
+    elif y.dtype is not _BF16:
+        raise ValueError(f"the output is bfloat16 or float32, not {y.dtype}")
+    if ts is not None and ts.dim() == 0:
+        ts = ts.reshape(1)
+    st = lib().moe_linear_w4(
+        _given(x, "x", _BF16, (T, K), dev), _given(codes, "codes", _U8, (N, K // 2), dev),
+        _given(sf, "sf", _U8, (N, K // block), dev), _given(ts, "ts", _F32, (1,), dev), T, N, K,
+        flags, _given(y, "y", y.dtype, (T, N), dev), torch.cuda.current_stream().cuda_stream)
+    if st:
+        _check(st, "moe_linear_w4")
+    return y
 
 
 def last_device_status(workspace) -> int:

@@ -6,6 +6,7 @@
 #include <tuple>
 
 #include "internal.h"
+#include "ops.h"
 
 using namespace nvfp4moe;
 
@@ -256,7 +257,8 @@ int moe_run_kernel_count(const moe_config* cfg, int32_t T) {
 namespace {
 
 // The layer for BF16 input x (qx == nullptr) or for already quantised input (qx: codes
-// [T, H/2], qsf: scales [T, H/16], qts: device tensor scale; x unused), at widths that are
+// [T, H/2], qsf: scales [T, H/16], qts: device tensor scale; a W4A8 layer takes MXFP8: codes
+// [T, H], scales [T, H/32], no tensor scale; x unused), at widths that are
 // multiples of 256.  Hl, Il: the caller's widths (equal to cfg's unless run_layer padded them),
 // used for the debug copies.
 int run_core(const moe_config* cfg, int Hl, int Il, const void* wbuf, const void* x,
@@ -274,11 +276,12 @@ int run_core(const moe_config* cfg, int Hl, int Il, const void* wbuf, const void
   if (!aligned(workspace, kAlign)) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   const bool quantised = qx != nullptr || qsf != nullptr || qts != nullptr;
-  if (quantised && L.w16) return MOE_ERR_INVALID_ARG;   // a W4A16 layer takes BF16 input
+  const bool mx_input = (cfg->flags & MOE_FLAG_ACT_MXFP8) != 0u;   // MXFP8: no tensor scale
+  if (quantised && L.w16 && !L.mx) return MOE_ERR_INVALID_ARG;   // W4A16 takes BF16 input
   if (!wbuf || !logits || !y) return MOE_ERR_INVALID_ARG;
   if (!aligned(wbuf, kAlign) || !aligned(y, 8)) return MOE_ERR_INVALID_ARG;
   if (quantised) {
-    if (!qx || !qsf || !qts) return MOE_ERR_INVALID_ARG;
+    if (!qx || !qsf || (qts == nullptr) != mx_input) return MOE_ERR_INVALID_ARG;
     if (!aligned(qx, 16) || !aligned(qsf, 4) || !aligned(qts, 4)) return MOE_ERR_INVALID_ARG;
   } else if (!x || !aligned(x, 16)) {
     return MOE_ERR_INVALID_ARG;
@@ -342,9 +345,11 @@ int run_core(const moe_config* cfg, int Hl, int Il, const void* wbuf, const void
     if (e == cudaSuccess) e = launch_plan(pa, s);
     if (e == cudaSuccess) e = mark(2);
     if (e == cudaSuccess)
-      e = L.mx ? launch_act_mx_encode_perm(x, T, H, k, shared, L.Rt, i32(L.inv), ws + L.xq8,
-                                           ws + L.xq8 + (size_t)T * H, ws + L.xb_perm,
-                                           &hdr->status, s)
+      e = quantised ? launch_mx_decode_perm(qx, qsf, T, H, k, shared, L.Rt, i32(L.inv),
+                                            ws + L.xb_perm, &hdr->status, s)
+          : L.mx ? launch_act_mx_encode_perm(x, T, H, k, shared, L.Rt, i32(L.inv), ws + L.xq8,
+                                             ws + L.xq8 + (size_t)T * H, ws + L.xb_perm,
+                                             &hdr->status, s)
                : launch_permute_rows_bf16(x, T, H, L.Rt, i32(L.perm_src), ws + L.xb_perm,
                                           &hdr->status, s);
     if (e != cudaSuccess) return MOE_ERR_CUDA;
@@ -403,10 +408,12 @@ int run_core(const moe_config* cfg, int Hl, int Il, const void* wbuf, const void
           e = cudaMemcpyAsync(dst, ws + off, bytes, cudaMemcpyDeviceToDevice, s);
       };
       // rows of the caller's width out of rows of the layer's width
-      auto cp2 = [&](void* dst, size_t off, size_t rows, size_t width, size_t pitch) {
+      auto cp2p = [&](void* dst, const void* src, size_t rows, size_t width, size_t pitch) {
         if (dst && e == cudaSuccess && rows > 0)
-          e = cudaMemcpy2DAsync(dst, width, ws + off, pitch, width, rows,
-                                cudaMemcpyDeviceToDevice, s);
+          e = cudaMemcpy2DAsync(dst, width, src, pitch, width, rows, cudaMemcpyDeviceToDevice, s);
+      };
+      auto cp2 = [&](void* dst, size_t off, size_t rows, size_t width, size_t pitch) {
+        cp2p(dst, ws + off, rows, width, pitch);
       };
       const size_t R = (size_t)L.R, Rt = (size_t)L.Rt;
       cp(debug->topk_ids, L.ids, 4 * R);
@@ -416,8 +423,8 @@ int run_core(const moe_config* cfg, int Hl, int Il, const void* wbuf, const void
       cp(debug->inv, L.inv, 4 * R);
       cp2(debug->hb, L.hb, Rt, (size_t)Il * 2, (size_t)I * 2);
       if (L.mx) {   // MXFP8 codes and E8M0 scales of x and h
-        cp2(debug->xq, L.xq8, T, Hl, H);
-        cp2(debug->xsf, L.xq8 + (size_t)T * H, T, Hl / 32, H / 32);
+        cp2p(debug->xq, quantised ? qx : ws + L.xq8, T, Hl, H);
+        cp2p(debug->xsf, quantised ? qsf : ws + L.xq8 + (size_t)T * H, T, Hl / 32, H / 32);
         cp2(debug->hq, L.hq8, Rt, Il, I);
         cp2(debug->hsf, L.hq8 + Rt * I, Rt, Il / 32, I / 32);
       }
@@ -694,9 +701,10 @@ int run_layer(const moe_config* cfg, const void* wbuf, const void* x, const uint
   if (!aligned(workspace, kAlign)) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   const bool quantised = qx != nullptr || qsf != nullptr || qts != nullptr;
+  const bool mx_input = (cfg->flags & MOE_FLAG_ACT_MXFP8) != 0u;   // MXFP8: no tensor scale
   if (!y || !aligned(y, 8)) return MOE_ERR_INVALID_ARG;
   if (quantised) {
-    if (!qx || !qsf || !qts) return MOE_ERR_INVALID_ARG;
+    if (!qx || !qsf || (qts == nullptr) != mx_input) return MOE_ERR_INVALID_ARG;
     if (!aligned(qx, 16) || !aligned(qsf, 4) || !aligned(qts, 4)) return MOE_ERR_INVALID_ARG;
   } else if (!x || !aligned(x, 16)) {
     return MOE_ERR_INVALID_ARG;
@@ -705,13 +713,15 @@ int run_layer(const moe_config* cfg, const void* wbuf, const void* x, const uint
   const size_t H = (size_t)cfg->hidden, Hp = (size_t)pc.hidden, rows = (size_t)T;
   uint8_t* xp = static_cast<uint8_t*>(workspace) + core;
   uint8_t* yp = xp + align_up(rows * Hp * 2);
-  uint8_t* sfp = xp + align_up(rows * Hp / 2);   // quantised input: the scales after the codes
+  // quantised input: bytes of the caller's and of the padded rows, the scales after the codes
+  const size_t cb = mx_input ? H : H / 2, sb = mx_input ? H / 32 : H / 16;
+  const size_t cbp = mx_input ? Hp : Hp / 2, sbp = mx_input ? Hp / 32 : Hp / 16;
+  uint8_t* sfp = xp + align_up(rows * cbp);
   auto ok = [](cudaError_t e) { return e == cudaSuccess; };
   if (quantised) {
-    if (!ok(cudaMemsetAsync(xp, 0, align_up(rows * Hp / 2) + rows * Hp / 16, s)) ||
-        !ok(cudaMemcpy2DAsync(xp, Hp / 2, qx, H / 2, H / 2, rows, cudaMemcpyDeviceToDevice, s)) ||
-        !ok(cudaMemcpy2DAsync(sfp, Hp / 16, qsf, H / 16, H / 16, rows, cudaMemcpyDeviceToDevice,
-                              s)))
+    if (!ok(cudaMemsetAsync(xp, 0, align_up(rows * cbp) + rows * sbp, s)) ||
+        !ok(cudaMemcpy2DAsync(xp, cbp, qx, cb, cb, rows, cudaMemcpyDeviceToDevice, s)) ||
+        !ok(cudaMemcpy2DAsync(sfp, sbp, qsf, sb, sb, rows, cudaMemcpyDeviceToDevice, s)))
       return MOE_ERR_CUDA;
     st = run_core(&pc, cfg->hidden, Il, wbuf, nullptr, xp, sfp, qts, logits, T, k, yp,
                   workspace, core, stream, debug);
@@ -743,7 +753,9 @@ int moe_run_quantized(const moe_config* cfg, const void* wbuf, const uint8_t* xq
                       const uint8_t* xsf, const float* ts_a, const float* logits, int32_t T,
                       int32_t k, void* y, void* workspace, size_t ws_bytes, moe_stream_t stream,
                       const moe_debug* debug) {
-  if (T > 0 && (!xq || !xsf || !ts_a)) return MOE_ERR_INVALID_ARG;
+  // (MXFP8 input of a W4A8 layer has no tensor scale)
+  if (T > 0 && (!xq || !xsf || (!ts_a && !(cfg && (cfg->flags & MOE_FLAG_ACT_MXFP8)))))
+    return MOE_ERR_INVALID_ARG;
   return run_layer(cfg, wbuf, nullptr, xq, xsf, ts_a, logits, T, k, y, workspace, ws_bytes,
                    stream, debug);
 }

@@ -10,6 +10,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "ops.h"
 
 namespace nvfp4moe {
 
@@ -670,6 +671,58 @@ __global__ void __launch_bounds__(kThreads) act_mx_encode_perm_kernel(
   }
 }
 
+// The W4A8 layer's already quantised activations: one thread per 32-element block decodes its E4M3
+// codes and E8M0 scale to BF16 and writes them into each of the token's expert-ordered rows, as
+// act_mx_encode_perm_kernel does with the codes it makes.
+__global__ void __launch_bounds__(kThreads) mx_decode_perm_kernel(
+    const uint4* __restrict__ codes, const uint8_t* __restrict__ sf, int T, int H, int k,
+    int shared, int Rt, const int32_t* __restrict__ inv, uint4* __restrict__ xb_perm,
+    int32_t* status) {
+  griddep_wait();
+  griddep_launch();
+  const int nkb = H / 32;
+  const int64_t nblk = (int64_t)T * nkb;
+  const int64_t stride = (int64_t)gridDim.x * blockDim.x;
+  for (int64_t u = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; u < nblk; u += stride) {
+    const int t = (int)(u / nkb), b = (int)(u - (int64_t)t * nkb);
+    const uint4 c0 = __ldg(codes + 2 * u), c1 = __ldg(codes + 2 * u + 1);
+    const uint32_t cw[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+    const uint32_t sb = __ldg(sf + u);
+    const float X = e8m0_to_f32(sb);
+    uint4 out[4];
+    bool finite = sb != 255u;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t ow[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 v = e4m3x2_to_f32x2((cw[2 * q + i / 2] >> (16 * (i & 1))) & 0xFFFFu);
+        const __nv_bfloat162 bb = __floats2bfloat162_rn(v.x * X, v.y * X);
+        ow[i] = *reinterpret_cast<const uint32_t*>(&bb);
+        finite = finite && (ow[i] & 0x7F80u) != 0x7F80u && (ow[i] & 0x7F800000u) != 0x7F800000u;
+      }
+      out[q] = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+    }
+    if (!finite) set_status(status, MOE_ERR_NONFINITE);
+    for (int j = 0; j <= k; ++j) {
+      int p;
+      if (j < k) {
+        p = __ldg(inv + (int64_t)t * k + j);
+      } else {
+        if (!shared) break;
+        p = T * k + t;
+      }
+      if (p < 0 || p >= Rt) {
+        set_status(status, MOE_ERR_INVALID_ARG);
+        continue;
+      }
+      uint4* dst = xb_perm + ((size_t)p * H + (size_t)b * 32) / 8;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) dst[q] = out[q];
+    }
+  }
+}
+
 int grid_for(int64_t work, int per_block, int cap) {
   int64_t g = (work + per_block - 1) / per_block;
   if (g < 1) g = 1;
@@ -862,6 +915,15 @@ cudaError_t launch_act_mx_encode_perm(const void* x, int T, int H, int k, int sh
   return launch_pdl(act_mx_encode_perm_kernel, dim3(grid_for(nblk, kThreads, num_sms() * 16)),
                     dim3(kThreads), 0, s, reinterpret_cast<const uint4*>(x), T, H, k, shared, Rt,
                     inv, codes, sf, reinterpret_cast<uint4*>(xb_perm), status);
+}
+
+cudaError_t launch_mx_decode_perm(const uint8_t* codes, const uint8_t* sf, int T, int H, int k,
+                                  int shared, int Rt, const int32_t* inv, void* xb_perm,
+                                  int32_t* status, cudaStream_t s) {
+  const int64_t nblk = (int64_t)T * H / 32;
+  return launch_pdl(mx_decode_perm_kernel, dim3(grid_for(nblk, kThreads, num_sms() * 16)),
+                    dim3(kThreads), 0, s, reinterpret_cast<const uint4*>(codes), sf, T, H, k,
+                    shared, Rt, inv, reinterpret_cast<uint4*>(xb_perm), status);
 }
 
 cudaError_t launch_finalize(const float* yacc, void* y, int64_t n, cudaStream_t s) {

@@ -1,0 +1,185 @@
+"""The 4-bit matrix-vector product against decoded weights in 64 bits.
+
+Two kinds of check.  With whole-number x (|x| <= 4) and power-of-two block scales every product
+is a multiple of 1/2 of a bounded size and every partial sum is exact in FP32, so the result is
+exact whatever the order: equality, which no wrong index survives.  With normal data: the products
+are exact, and the sum of K terms runs through at most K / 128 + 8 FP32 accumulations of
+tensor-core dot products, each within 2^-21 of the sum of magnitudes: (K / 128 + 16) * 2^-21 of
+sum |x w|, plus half a BF16 step for BF16 output."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+E2M1 = [0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0]
+
+
+@pytest.fixture(scope="module")
+def moe():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import nvfp4_mixture_experts_softmax_gb300 as m
+    m.lib()
+    return m
+
+
+def decode(codes, sf, ts):
+    t = torch.tensor(E2M1 + [-v for v in E2M1], dtype=torch.float64, device="cuda")
+    v = t[torch.stack([codes & 15, codes >> 4], -1).reshape(codes.shape[0], -1).long()]
+    s = sf.view(torch.float8_e4m3fn).double() * ts.double() if ts is not None else torch.exp2(sf.double() - 127)
+    return v * s.repeat_interleave(v.shape[1] // sf.shape[1], 1)
+
+
+def random_weights(N, K, fmt, exact, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    codes = torch.randint(0, 256, (N, K // 2), device="cuda", generator=g, dtype=torch.uint8)
+    if fmt == "nvfp4":
+        if exact:    # 1, 2 or 4
+            sf = torch.exp2(torch.randint(0, 3, (N, K // 16), device="cuda", generator=g).float()).to(torch.float8_e4m3fn).view(torch.uint8)
+            ts = torch.tensor([0.5], device="cuda")
+        else:        # any positive finite scale, subnormal ones too
+            sf = torch.randint(0, 0x7F, (N, K // 16), device="cuda", generator=g, dtype=torch.uint8)
+            ts = torch.tensor([3.7e-5], device="cuda")
+        return codes, sf, ts
+    lo, hi = (126, 129) if exact else (100, 140)
+    return codes, torch.randint(lo, hi, (N, K // 32), device="cuda", generator=g).to(torch.uint8), None
+
+
+SHAPES = [(1, 1, 32), (1, 16, 128), (3, 17, 96), (8, 2048, 2048), (9, 40, 4064), (16, 129, 1024), (17, 33, 160), (32, 100, 2080),
+          (33, 15, 224), (64, 257, 7168), (64, 16, 32), (1, 511, 16384), (2, 1000, 992), (7, 4097, 512), (63, 31, 1056), (5, 3, 65536)]
+
+
+@pytest.mark.parametrize("T,N,K", SHAPES)
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_exact(moe, T, N, K, fmt, dtype):
+    codes, sf, ts = random_weights(N, K, fmt, True, T + N + K)
+    g = torch.Generator(device="cuda").manual_seed(K)
+    x = torch.randint(-4, 5, (T, K), device="cuda", generator=g).bfloat16()
+    buf = torch.full((T + 2, N), 7.0, dtype=dtype, device="cuda")
+    y = moe.linear_w4(x, codes, sf, ts, y=buf[1:T + 1])
+    want = (x.double() @ decode(codes, sf, ts).t()).float().to(dtype)
+    assert torch.equal(y, want)
+    assert bool((buf[0] == 7).all()) and bool((buf[T + 1] == 7).all())
+    assert torch.equal(moe.linear_w4(x, codes, sf, ts, out_dtype=dtype), want)
+
+
+@pytest.mark.parametrize("T,N,K", SHAPES)
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_normal_data(moe, T, N, K, fmt):
+    codes, sf, ts = random_weights(N, K, fmt, False, T + N + K)
+    g = torch.Generator(device="cuda").manual_seed(K)
+    x = torch.randn(T, K, device="cuda", generator=g).bfloat16()
+    w = decode(codes, sf, ts)
+    want, size = x.double() @ w.t(), x.double().abs() @ w.abs().t()
+    tol = (K / 128 + 16) * 2.0 ** -21 * size
+    y = moe.linear_w4(x, codes, sf, ts, out_dtype=torch.float32)
+    assert bool(((y.double() - want).abs() <= tol).all())
+    b = moe.linear_w4(x, codes, sf, ts)
+    assert torch.equal(b, y.bfloat16())
+    # a token's result does not depend on the other tokens of the same launch size class
+    one = moe.linear_w4(x[:1].contiguous(), codes, sf, ts, out_dtype=torch.float32)
+    assert bool(((one.double() - want[:1]).abs() <= tol[:1]).all())
+
+
+def test_quantised_matrix_and_every_code(moe):
+    """quantize_act of a BF16 matrix is the weight format; then every code with every scale."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    W = (torch.randn(96, 512, device="cuda", generator=g) * 0.02).bfloat16()
+    codes, sf, ts = moe.quantize_act(W)
+    x = torch.randn(4, 512, device="cuda", generator=g).bfloat16()
+    y = moe.linear_w4(x, codes, sf, ts, out_dtype=torch.float32)
+    want = x.double() @ decode(codes, sf, ts).t()
+    assert float((y.double() - want).norm() / want.norm()) <= 2.0 ** -20
+    assert float((y.double() - x.double() @ W.double().t()).norm() / want.norm()) < 0.2
+    # one-hot x reads single weights: bit-exact in FP32 for every finite scale byte of both signs
+    sfb = torch.tensor([b for b in range(256) if (b & 0x7F) != 0x7F], device="cuda", dtype=torch.uint8)
+    N = sfb.numel()
+    codes = (torch.arange(8, device="cuda") * 2 + (torch.arange(8, device="cuda") * 2 + 1) * 16).to(torch.uint8).repeat(N, 2)
+    sf = sfb[:, None].repeat(1, 2).contiguous()
+    one = torch.tensor([1.0], device="cuda")
+    y = moe.linear_w4(torch.eye(32, device="cuda").bfloat16(), codes, sf, one, out_dtype=torch.float32)
+    assert torch.equal(y.t().double(), decode(codes, sf, one))
+    # every E8M0 scale: the products are exact down to BF16's smallest subnormal
+    b = torch.arange(0, 253, device="cuda", dtype=torch.uint8)
+    codes = codes[:1].repeat(253, 1)
+    y = moe.linear_w4(torch.eye(32, device="cuda").bfloat16(), codes, b[:, None].contiguous(), out_dtype=torch.float32)
+    assert torch.equal(y.t().double(), decode(codes, b[:, None], None))
+
+
+@pytest.mark.parametrize("T", [1, 12, 40])
+def test_nonfinite(moe, T):
+    codes, sf, ts = random_weights(40, 256, "nvfp4", False, 7)
+    x = torch.randn(T, 256, device="cuda").bfloat16()
+    clean = moe.linear_w4(x, codes, sf, ts)
+    sf2 = sf.clone()
+    sf2[5, 3] = 0x7F                      # NaN scale: its row alone
+    y = moe.linear_w4(x, codes, sf2, ts)
+    rest = [n for n in range(40) if n != 5]
+    assert bool(y[:, 5].isnan().all()) and torch.equal(y[:, rest], clean[:, rest])
+    mx = random_weights(40, 256, "mxfp4", False, 8)
+    s2 = mx[1].clone()
+    s2[9, 1] = 255
+    y = moe.linear_w4(x, mx[0], s2)
+    assert bool(y[:, 9].isnan().all()) and bool(y[:, rest[:8]].isfinite().all())
+    x2 = x.clone()
+    x2[T - 1, 17] = float("nan")          # NaN in one token: that token alone
+    y = moe.linear_w4(x2, codes, sf, ts)
+    assert bool(y[T - 1].isnan().all()) and torch.equal(y[:T - 1], clean[:T - 1])
+
+
+def test_large_offsets(moe):
+    """More than 2^32 bytes of codes: the last rows."""
+    N, K = 70000, 131072
+    if torch.cuda.mem_get_info()[0] < (12 << 30):
+        pytest.skip("not enough memory")
+    codes = torch.zeros(N, K // 2, dtype=torch.uint8, device="cuda")
+    sf = torch.full((N, K // 32), 127, dtype=torch.uint8, device="cuda")
+    codes[-3:] = 0x22                     # ones
+    x = torch.ones(2, K, dtype=torch.bfloat16, device="cuda")
+    y = moe.linear_w4(x, codes, sf, out_dtype=torch.float32)
+    assert bool((y[:, -3:] == K).all()) and not y[:, :-3].any()
+
+
+def test_empty_stream_and_graph(moe):
+    codes, sf, ts = random_weights(48, 512, "nvfp4", False, 9)
+    x = torch.randn(3, 512, device="cuda").bfloat16()
+    assert moe.linear_w4(x[:0], codes, sf, ts).shape == (0, 48)
+    assert moe.linear_w4(x, codes[:0], sf[:0], ts).shape == (3, 0)
+    want = moe.linear_w4(x, codes, sf, ts)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = moe.linear_w4(x, codes, sf, ts, stream=s)
+    s.synchronize()
+    assert torch.equal(got, want)
+    y = torch.empty_like(want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.linear_w4(x, codes, sf, ts, y=y)
+    x.copy_(torch.randn(3, 512, device="cuda"))
+    graph.replay()
+    want = moe.linear_w4(x, codes, sf, ts)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
+
+
+def test_refusals(moe):
+    codes, sf, ts = random_weights(48, 512, "nvfp4", False, 9)
+    x = torch.randn(3, 512, device="cuda").bfloat16()
+    with pytest.raises(ValueError, match="x must"):
+        moe.linear_w4(x.float(), codes, sf, ts)
+    with pytest.raises(ValueError, match="codes"):
+        moe.linear_w4(x, codes[:, :128].contiguous(), sf, ts)
+    with pytest.raises(ValueError, match="sf"):
+        moe.linear_w4(x, codes, sf)                 # NVFP4 scales without a tensor scale
+    with pytest.raises(ValueError, match="x must"):
+        moe.linear_w4(x[:, ::2], codes[:, ::2], sf[:, ::2], ts)
+    with pytest.raises(ValueError, match="output"):
+        moe.linear_w4(x, codes, sf, ts, out_dtype=torch.float16)
+    with pytest.raises(ValueError, match="multiple of 32"):
+        moe.linear_w4(x[:, :40].contiguous(), codes, sf, ts)
+    with pytest.raises(RuntimeError, match="UNSUPPORTED_SHAPE"):
+        moe.linear_w4(x[:1].repeat(65, 1), codes, sf, ts)
+    flat = torch.zeros(3 * 512 + 1, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(RuntimeError, match="INVALID_ARG"):
+        moe.linear_w4(flat[1:].reshape(3, 512), codes, sf, ts)
