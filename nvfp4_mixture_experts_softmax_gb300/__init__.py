@@ -398,30 +398,32 @@ def run(cfg: MoeConfig, wbuf, x, logits, k=None, y=None, workspace=None, debug=F
 # ---- operators around the layer ----
 
 def _scoped(fn):
-    """Runs fn with its first tensor's device current and, if `stream` is passed, on that stream
-    (what fn allocates then belongs to that stream); otherwise on the device's current stream."""
+    """Calls fn(stream handle, ...) with its first tensor's device current, on `stream` if that is
+    passed (what fn allocates then belongs to that stream) or on the device's current stream."""
     @functools.wraps(fn)
     def call(first, *args, stream=None, **kw):
-        dev = first.device
-        if dev.type != "cuda":
-            raise ValueError(f"{fn.__name__} needs CUDA tensors, got one on {dev}")
-        if stream is None and dev.index == torch.cuda.current_device():
-            return fn(first, *args, **kw)
-        if stream is not None and stream.device != dev:
-            raise ValueError(f"{fn.__name__}: the stream is on {stream.device}, the tensors on {dev}")
+        if not first.is_cuda:
+            raise ValueError(f"{fn.__name__} needs CUDA tensors, got one on {first.device}")
+        dev = first.get_device()
+        if stream is None and dev == torch.cuda.current_device():
+            return fn(torch.cuda.current_stream(dev).cuda_stream, first, *args, **kw)
+        if stream is not None and stream.device != first.device:
+            raise ValueError(f"{fn.__name__}: the stream is on {stream.device}, the tensors on "
+                             f"{first.device}")
         with torch.cuda.device(dev), torch.cuda.stream(stream):
-            return fn(first, *args, **kw)
+            return fn(torch.cuda.current_stream(dev).cuda_stream, first, *args, **kw)
     return call
 
 
 def _given(t, name, dtype, shape, dev):
-    """Device address of a tensor argument after its checks (None stays None)."""
+    """Device address of a tensor argument after its checks (None stays None); dev: the index of
+    the device that it has to be on."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
-                         f"{dev}, got {t.dtype} {tuple(t.shape)} stride {t.stride()} on {t.device}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                     f"cuda:{dev}, got {t.dtype} {tuple(t.shape)} stride {t.stride()} on {t.device}")
 
 
 def _need(t, name):
@@ -438,7 +440,7 @@ _U8, _BF16, _F32, _I32 = torch.uint8, torch.bfloat16, torch.float32, torch.int32
 
 
 @_scoped
-def add_rmsnorm_quantize_mx(x, residual, gamma, eps: float = 1e-6, want_y: bool = False,
+def add_rmsnorm_quantize_mx(handle, x, residual, gamma, eps: float = 1e-6, want_y: bool = False,
                             want_rrms: bool = False, quantize: bool = True, out=None):
     """h = bf16(x + residual), y = RMSNorm(h) * gamma and MXFP8 of y, in one launch.
 
@@ -450,7 +452,7 @@ def add_rmsnorm_quantize_mx(x, residual, gamma, eps: float = 1e-6, want_y: bool 
     if x.dim() != 2 or x.shape[1] % 32:
         raise ValueError(f"x must be [rows, cols] with cols a multiple of 32, got {tuple(x.shape)}")
     rows, cols = shape = x.shape
-    dev = x.device
+    dev = x.get_device()
     if out is None:
         out = {}
         if residual is not None:
@@ -469,7 +471,7 @@ def add_rmsnorm_quantize_mx(x, residual, gamma, eps: float = 1e-6, want_y: bool 
         _given(get("h"), "h", _BF16, shape, dev), _given(get("codes"), "codes", _U8, shape, dev),
         _given(get("sf"), "sf", _U8, (rows, cols // 32), dev),
         _given(get("y"), "y", _BF16, shape, dev), _given(get("rrms"), "rrms", _F32, (rows,), dev),
-        torch.cuda.current_stream().cuda_stream)
+        handle)
     if st:
         _check(st, "moe_add_rmsnorm_quantize_mx")
     return out
@@ -480,7 +482,7 @@ def add_rmsnorm_backward_workspace(rows: int, cols: int, device="cuda"):
 
 
 @_scoped
-def add_rmsnorm_backward(dy, h, rrms, gamma, dh=None, out=None, workspace=None):
+def add_rmsnorm_backward(handle, dy, h, rrms, gamma, dh=None, out=None, workspace=None):
     """Backward pass of add_rmsnorm_quantize_mx's norm, the quantisation passed straight through.
 
     dy, h [rows, cols] BF16, rrms [rows] FP32, gamma [cols] BF16 as in the forward pass; dh: the
@@ -490,7 +492,7 @@ def add_rmsnorm_backward(dy, h, rrms, gamma, dh=None, out=None, workspace=None):
     if dy.dim() != 2 or dy.shape[1] % 32:
         raise ValueError(f"dy must be [rows, cols] with cols a multiple of 32, got {tuple(dy.shape)}")
     rows, cols = shape = dy.shape
-    dev = dy.device
+    dev = dy.get_device()
     if out is None:
         out = {"dx": torch.empty_like(dy), "dgamma": torch.empty(cols, dtype=_F32, device=dev)}
     if workspace is None:
@@ -503,7 +505,7 @@ def add_rmsnorm_backward(dy, h, rrms, gamma, dh=None, out=None, workspace=None):
         _given(out["dx"], "dx", _BF16, shape, dev),
         _given(out["dgamma"], "dgamma", _F32, (cols,), dev),
         _given(workspace, "workspace", _U8, workspace.shape, dev), workspace.numel(),
-        torch.cuda.current_stream().cuda_stream)
+        handle)
     if st:
         _check(st, "moe_add_rmsnorm_backward")
     return out
@@ -535,7 +537,7 @@ def router_loss_workspace(T: int, E: int, device="cuda"):
 
 
 @_scoped
-def router_loss(logits, topk_ids, mask=None, router: str = "softmax", out=None, workspace=None):
+def router_loss(handle, logits, topk_ids, mask=None, router: str = "softmax", out=None, workspace=None):
     """Per-expert counts and the router's losses for logits [T, E] FP32 and topk_ids [T, k] int32
     (as plan gives them); mask [T] (bool or uint8) is 0 for padded tokens.
 
@@ -543,7 +545,7 @@ def router_loss(logits, topk_ids, mask=None, router: str = "softmax", out=None, 
     [E] FP32 (mean expert probabilities); pass it to router_loss_backward.  An id outside [0, E)
     is reported in the workspace's device status (last_device_status).  stream: see run."""
     T, E, k = _routing_shape(logits, topk_ids)
-    dev = logits.device
+    dev = logits.get_device()
     if out is None:
         out = dict(losses=torch.empty(2, dtype=_F32, device=dev),
                    counts=torch.empty(E, dtype=_I32, device=dev),
@@ -559,20 +561,20 @@ def router_loss(logits, topk_ids, mask=None, router: str = "softmax", out=None, 
         _given(out["tokens"], "tokens", _I32, (1,), dev),
         _given(out["probs"], "probs", _F32, (E,), dev),
         _given(workspace, "workspace", _U8, workspace.shape, dev), workspace.numel(),
-        torch.cuda.current_stream().cuda_stream)
+        handle)
     if st:
         _check(st, "moe_router_loss")
     return out
 
 
 @_scoped
-def router_loss_backward(logits, topk_ids, stats, grad_losses=None, grad_topk_w=None, mask=None,
+def router_loss_backward(handle, logits, topk_ids, stats, grad_losses=None, grad_topk_w=None, mask=None,
                          router: str = "softmax", dlogits=None):
     """Gradient [T, E] FP32 of the logits from grad_losses [2] FP32 (on the device; the gradients
     of the balance and z losses) and grad_topk_w [T, k] FP32 (of the top-k weights); either may be
     None.  stats: what router_loss returned for the same logits, ids, mask and router."""
     T, E, k = _routing_shape(logits, topk_ids)
-    dev = logits.device
+    dev = logits.get_device()
     if dlogits is None:
         dlogits = torch.empty(T, E, dtype=_F32, device=dev)
     st = lib().moe_router_loss_backward(
@@ -582,7 +584,7 @@ def router_loss_backward(logits, topk_ids, stats, grad_losses=None, grad_topk_w=
         _given(stats["tokens"], "tokens", _I32, (1,), dev),
         _given(grad_losses, "grad_losses", _F32, (2,), dev),
         _given(grad_topk_w, "grad_topk_w", _F32, (T, k), dev),
-        _given(dlogits, "dlogits", _F32, (T, E), dev), torch.cuda.current_stream().cuda_stream)
+        _given(dlogits, "dlogits", _F32, (T, E), dev), handle)
     if st:
         _check(st, "moe_router_loss_backward")
     return dlogits
@@ -594,14 +596,14 @@ LINEAR_MAX_TOKENS = 64
 
 
 @_scoped
-def linear_w4(x, codes, sf, ts=None, out_dtype=torch.bfloat16, y=None):
+def linear_w4(handle, x, codes, sf, ts=None, out_dtype=torch.bfloat16, y=None):
     """x [T, K] BF16 (T <= 64) times a 4-bit matrix: y [T, N] in out_dtype (bfloat16 or float32).
 
     codes [N, K/2] u8 with sf [N, K/16] u8 (E4M3) and ts [1] FP32: NVFP4, as quantize_act(W) gives
     them; with sf [N, K/32] u8 (E8M0) and no ts: MXFP4.  stream: see run."""
     if x.dim() != 2 or codes.dim() != 2 or sf.dim() != 2:
         raise ValueError("x must be [T, K], codes [N, K/2] and sf [N, K/16] or [N, K/32]")
-    (T, K), N, dev = x.shape, codes.shape[0], x.device
+    (T, K), N, dev = x.shape, codes.shape[0], x.get_device()
     flags, block = (LINEAR_MXFP4, 32) if ts is None else (0, 16)
     if K % 32:
         raise ValueError(f"K must be a multiple of 32, got {K}")
@@ -616,7 +618,7 @@ def linear_w4(x, codes, sf, ts=None, out_dtype=torch.bfloat16, y=None):
     st = lib().moe_linear_w4(
         _given(x, "x", _BF16, (T, K), dev), _given(codes, "codes", _U8, (N, K // 2), dev),
         _given(sf, "sf", _U8, (N, K // block), dev), _given(ts, "ts", _F32, (1,), dev), T, N, K,
-        flags, _given(y, "y", y.dtype, (T, N), dev), torch.cuda.current_stream().cuda_stream)
+        flags, _given(y, "y", y.dtype, (T, N), dev), handle)
     if st:
         _check(st, "moe_linear_w4")
     return y

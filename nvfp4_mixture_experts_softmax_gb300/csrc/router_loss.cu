@@ -11,12 +11,15 @@
 //        | gb (E/n) (f_e - sum_j f_j p_j) / sum(s) * ds_e/dl_e                  (sqrt-softplus)
 //        + gz (2/n) lse softmax(l)_e
 //        + [e = e_j] ( w_j (g_j - sum_i g_i w_i) | (g_j - sum_i g_i w_i) / sum_k(s) * ds/dl ).
-// A token that does not count has a zero gradient row.
+// A token that does not count has a zero gradient row.  Everything is FP32: sums of positive terms
+// in short chains and trees (FP64 runs at a few instructions a clock here: one double division per
+// thread of a block costs it about 5 us).
 //
 // G lanes of a warp hold one token's row in registers (VPL logits each), so a warp takes 32 / G
-// tokens at a time and the row is read once.
+// tokens at a time and each row is read once; the next row's loads are issued before the current
+// one is reduced.
 #include <algorithm>
-#include <cfloat>
+#include <type_traits>
 
 #include "common.cuh"
 #include "ops.h"
@@ -25,27 +28,48 @@ namespace nvfp4moe {
 
 namespace {
 
-constexpr int kLossThreads = 256;
-constexpr int kLossWarps = kLossThreads / 32;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kJoinCtas = 8;
+constexpr int kJoinThreads = 512;
 
-// Logits of one row held by a lane: VEC consecutive ones, then the next VEC 32-lane stripe.
+// Expert of logit i of lane `sub` of a G-lane group: VEC consecutive ones per stripe of G * VEC.
 template <int G, int VPL, int VEC>
 __device__ __forceinline__ int expert_of(int sub, int i) {
   return (i / VEC) * G * VEC + sub * VEC + i % VEC;
 }
 
+// What a lane holds of one token: its logits, whether the mask keeps the token, its first slot's
+// id.
+template <int VPL>
+struct TokenRow {
+  float v[VPL];
+  bool kept;
+  int32_t id;
+};
+
+// Loads of one token's row (t < T, otherwise nothing is kept); row: logits + t * E.  Experts behind
+// E are -infinity.
 template <int G, int VPL, int VEC>
-__device__ __forceinline__ void load_row(const float* __restrict__ row, int E, int sub, bool live,
-                                         float (&v)[VPL]) {
+__device__ __forceinline__ void load_row(const float* __restrict__ row,
+                                         const int32_t* __restrict__ ids,
+                                         const uint8_t* __restrict__ mask, int64_t t, int64_t T,
+                                         int E, int k, int sub, TokenRow<VPL>& r) {
+  const bool in = t < T;
+  r.kept = in && (!mask || __ldg(mask + t));
+  r.id = in && ids && sub < k ? __ldg(ids + t * k + sub) : -1;
+  const int left = in ? E - sub * VEC : 0;   // experts from this lane's first on
+  const float* p = row + sub * VEC;
 #pragma unroll
   for (int i = 0; i < VPL; i += VEC) {
-    const int e = expert_of<G, VPL, VEC>(sub, i);
+    constexpr int kStripe = G * VEC;
+    const int o = i / VEC * kStripe;
     if constexpr (VEC == 4) {
-      const float4 q = live && e < E ? __ldg(reinterpret_cast<const float4*>(row + e))
-                                     : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      v[i] = q.x; v[i + 1] = q.y; v[i + 2] = q.z; v[i + 3] = q.w;
+      const float4 q = o < left ? __ldg(reinterpret_cast<const float4*>(p + o))
+                                : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      r.v[i] = q.x; r.v[i + 1] = q.y; r.v[i + 2] = q.z; r.v[i + 3] = q.w;
     } else {
-      v[i] = live && e < E ? __ldg(row + e) : -INFINITY;
+      r.v[i] = o < left ? __ldg(p + o) : -INFINITY;
     }
   }
 }
@@ -69,16 +93,52 @@ __device__ __forceinline__ float group_max(float v) {
   return v;
 }
 
-// s = sqrt(softplus(l)) with softplus(l) = l above 20.  Below -15, softplus(l) = e^l (1 - e^l/2
-// + ...) is e^l to 2^-22, so s = e^(l/2), which does not underflow before l = -174.
-__device__ __forceinline__ float sqrtsp_score(float l) {
-  if (l < -15.0f) return expf(0.5f * l);
-  return sqrtf(l > 20.0f ? l : log1pf(expf(l)));
+__device__ __forceinline__ float ex2(float x) {
+  float d;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(x));
+  return d;
 }
-// ds/dl = sigmoid(l) / (2 s); s / 2 far below zero.
-__device__ __forceinline__ float sqrtsp_slope(float l, float s) {
-  if (l < -15.0f) return 0.5f * s;
-  return 0.5f / ((1.0f + expf(-l)) * s);
+__device__ __forceinline__ float rsqrt_approx(float x) {
+  float d;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(x));
+  return d;
+}
+__device__ __forceinline__ float lg2_approx(float x) {
+  float d;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(x));
+  return d;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float d;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(x));
+  return d;
+}
+
+// Score s = sqrt(softplus(l)) of the sqrt-softplus router and its slope ds/dl = sigmoid(l)/(2 s),
+// from h = e^(-|l|/2) and w = h^2 without a branch or a cancellation:
+//   softplus(l) = max(l, 0) + log1p(w),  log1p(w) = w P(w) with P a polynomial on [0, 1];
+//   l <= 0: s = h sqrt(P(w)),          slope = h / (2 (1 + w) sqrt(P(w)));
+//   l > 0:  s = sqrt(l + w P(w)),      slope = 1 / (2 (1 + w) s).
+// P interpolates log1p(w)/w at Chebyshev points of [0, 1] with P(0) = 1: within 2.3 * 2^-24
+// relative in FP32.  The library's log1pf(expf(l)) costs about three times the instructions, and
+// underflows below l = -103; this score does not before -174.
+__device__ __forceinline__ float sqrtsp_score(float l, float& slope) {
+  const float h = ex2(fabsf(l) * (-0.5f * kLog2e));
+  const float w = h * h;
+  float p = -0.004579766187816858f;
+  p = fmaf(p, w, 0.025682786479592323f);
+  p = fmaf(p, w, -0.06751181185245514f);
+  p = fmaf(p, w, 0.11626528203487396f);
+  p = fmaf(p, w, -0.15878385305404663f);
+  p = fmaf(p, w, 0.19862109422683716f);
+  p = fmaf(p, w, -0.2498755156993866f);
+  p = fmaf(p, w, 0.3333289325237274f);
+  p = fmaf(p, w, -0.4999999701976776f);
+  p = fmaf(p, w, 1.0f);
+  const float q = l > 0.0f ? fmaf(w, p, l) : p;
+  const float root = rsqrt_approx(q) * (l > 0.0f ? 1.0f : h);
+  slope = 0.5f * root * rcp_approx(1.0f + w);
+  return q * root;
 }
 
 struct LossArgs {
@@ -93,74 +153,100 @@ struct LossArgs {
   float* part_z;
   int32_t* part_n;
   int32_t* part_bad;
+  // outputs
+  float* losses;
+  int32_t* counts;
+  int32_t* tokens;
+  float* probs;
+  int32_t* status;
 };
 
+// One block per SM whose registers hold a row of VPL logits a lane, its successor and the sums: 640
+// threads of 96 registers for up to 16 logits a lane, 512 of 128 for 32.  (131072 x 256: 512, 640,
+// 768 and 1024 threads take 33.6, 30.6, 29.8 and 31.8 us with softmax, 48.2, 43.1, 44.5 and 49.1
+// us with the sqrt-softplus router; 8192 x 256: 7.7, 8.1, 8.5 and 9.5 us.)
+template <int VPL>
+constexpr int loss_threads() { return VPL <= 16 ? 640 : 512; }
+
+// One block takes every gridDim-th group of rows; its sums go to partials, or, if it is the only
+// block, straight to the outputs.
 template <int G, int VPL, int VEC, bool SQRTSP>
-__global__ void __launch_bounds__(kLossThreads) router_loss_kernel(LossArgs a) {
+__global__ void __launch_bounds__(loss_threads<VPL>(), 1) router_loss_kernel(LossArgs a) {
+  constexpr int kThreads = loss_threads<VPL>(), kWarps = kThreads / 32;
+  constexpr int R = 32 / G;   // rows of a warp at a time
   extern __shared__ float dyn[];
-  float* s_p = dyn;                                            // [E]
-  int32_t* s_c = reinterpret_cast<int32_t*>(dyn + a.E);         // [E]
-  __shared__ float s_z[kLossWarps];
-  __shared__ int32_t s_n[kLossWarps], s_bad[kLossWarps];
-  griddep_wait();
-  griddep_launch();
+  float* s_p = dyn;                                                     // [warps][E]
+  int32_t* s_c = reinterpret_cast<int32_t*>(dyn + kWarps * a.E);         // [E]
+  __shared__ float s_z[kWarps];
+  __shared__ int32_t s_n[kWarps], s_bad[kWarps];
+  __shared__ float s_dot[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane % G;
-  for (int e = threadIdx.x; e < a.E; e += kLossThreads) {
-    s_p[e] = 0.0f;
-    s_c[e] = 0;
-  }
+  for (int e = threadIdx.x; e < a.E; e += kThreads) s_c[e] = 0;
   __syncthreads();
-  constexpr int R = 32 / G;   // rows of a warp at a time
+  griddep_wait();
+  griddep_launch();
   float acc[VPL];
 #pragma unroll
   for (int i = 0; i < VPL; ++i) acc[i] = 0.0f;
   float z = 0.0f;
   int32_t n = 0, bad = 0;
-  const int64_t step = (int64_t)gridDim.x * kLossWarps * R;
-  for (int64_t t0 = ((int64_t)blockIdx.x * kLossWarps + warp) * R; t0 < a.T; t0 += step) {
-    const int64_t t = t0 + lane / G;
-    bool live = t < a.T && (!a.mask || a.mask[t]);
-    float v[VPL];
-    load_row<G, VPL, VEC>(a.logits + t * a.E, a.E, sub, live, v);
-    float top = v[0];
+  const int64_t step = (int64_t)gridDim.x * kWarps * R;
+  int64_t t = ((int64_t)blockIdx.x * kWarps + warp) * R + lane / G;
+  const float* row = a.logits + t * a.E;
+
+  auto take = [&](TokenRow<VPL>& r) {
+    float top = r.v[0];
 #pragma unroll
-    for (int i = 1; i < VPL; ++i) top = nan_max(top, v[i]);
+    for (int i = 1; i < VPL; ++i) top = nan_max(top, r.v[i]);
     top = group_max<G>(top);
-    live = live && top != -INFINITY;
-    float sum = 0.0f, sc = 0.0f, ex[VPL];
+    float sum = 0.0f, sc = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      ex[i] = expf(v[i] - top);
-      sum += ex[i];
+      const float ex = ex2((r.v[i] - top) * kLog2e);
+      sum += ex;
+      if constexpr (SQRTSP) {
+        float slope;
+        r.v[i] = sqrtsp_score(r.v[i], slope);
+        sc += r.v[i];
+      } else {
+        r.v[i] = ex;
+      }
     }
     sum = group_sum<G>(sum);
-    if constexpr (SQRTSP) {
+    if constexpr (SQRTSP) sc = group_sum<G>(sc);
+    else sc = sum;
+    if (r.kept && top != -INFINITY) {
+      const float lse = fmaf(lg2_approx(sum), kLn2, top);
+      z = fmaf(lse, lse, z);   // (the same on the G lanes; one of them is added up)
+      ++n;
+      const float inv = sc == 0.0f ? 0.0f : rcp_approx(sc);   // scores that all underflowed: 0
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        ex[i] = sqrtsp_score(v[i]);
-        sc += ex[i];
+      for (int i = 0; i < VPL; ++i) acc[i] = fmaf(r.v[i], inv, acc[i]);
+      if (sub < a.k) {
+        if ((uint32_t)r.id < (uint32_t)a.E) atomicAdd(s_c + r.id, 1);
+        else bad = 1;
       }
-      sc = group_sum<G>(sc);
-    } else {
-      sc = sum;
-    }
-    if (live) {
-      const float lse = top + logf(sum);
-      if (sub == 0) {
-        z = fmaf(lse, lse, z);
-        ++n;
-      }
-      const float inv = sc == 0.0f ? 0.0f : 1.0f / sc;   // scores that all underflowed: no share
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) acc[i] = fmaf(ex[i], inv, acc[i]);
-      for (int j = sub; j < a.k; j += G) {
+      for (int j = sub + G; j < a.k; j += G) {
         const int id = __ldg(a.ids + t * a.k + j);
         if ((uint32_t)id < (uint32_t)a.E) atomicAdd(s_c + id, 1);
         else bad = 1;
       }
     }
+    t += step;
+    row += step * a.E;
+  };
+  TokenRow<VPL> r0, r1;
+  load_row<G, VPL, VEC>(row, a.ids, a.mask, t, a.T, a.E, a.k, sub, r0);
+  while (true) {   // the warp's first row decides: t - lane / G
+    if (t - lane / G >= a.T) break;
+    load_row<G, VPL, VEC>(row + step * a.E, a.ids, a.mask, t + step, a.T, a.E, a.k, sub, r1);
+    take(r0);
+    if (t - lane / G >= a.T) break;
+    load_row<G, VPL, VEC>(row + step * a.E, a.ids, a.mask, t + step, a.T, a.E, a.k, sub, r0);
+    take(r1);
   }
+  if (sub != 0) z = 0.0f, n = 0;
   // rows of one warp, then the warps in order: every sum in a fixed order
 #pragma unroll
   for (int i = 0; i < VPL; ++i)
@@ -177,47 +263,106 @@ __global__ void __launch_bounds__(kLossThreads) router_loss_kernel(LossArgs a) {
     s_n[warp] = n;
     s_bad[warp] = bad;
   }
-  for (int w = 0; w < kLossWarps; ++w) {
-    if (warp == w && lane < G) {
+  if (lane < G) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        const int e = expert_of<G, VPL, VEC>(sub, i);
-        if (e < a.E) s_p[e] += acc[i];
-      }
+    for (int i = 0; i < VPL; ++i) {
+      const int e = expert_of<G, VPL, VEC>(sub, i);
+      if (e < a.E) s_p[warp * a.E + e] = acc[i];
     }
-    __syncthreads();
   }
-  for (int e = threadIdx.x; e < a.E; e += kLossThreads) {
-    a.part_p[(int64_t)blockIdx.x * a.E + e] = s_p[e];
-    a.part_c[(int64_t)blockIdx.x * a.E + e] = s_c[e];
+  __syncthreads();
+  z = 0.0f;
+  n = bad = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    z += s_z[w];
+    n += s_n[w];
+    bad |= s_bad[w];
   }
+  const bool only = gridDim.x == 1;
+  const float inv_n = n > 0 ? 1.0f / (float)n : 0.0f;
+  float dot = 0.0f;
+  for (int e = threadIdx.x; e < a.E; e += kThreads) {
+    float p = 0.0f;
+#pragma unroll 8
+    for (int w = 0; w < kWarps; ++w) p += s_p[w * a.E + e];
+    const int32_t c = s_c[e];
+    if (only) {
+      p *= inv_n;
+      a.counts[e] = c;
+      a.probs[e] = p;
+      dot = fmaf((float)c, p, dot);
+    } else {
+      a.part_p[(int64_t)blockIdx.x * a.E + e] = p;
+      a.part_c[(int64_t)blockIdx.x * a.E + e] = c;
+    }
+  }
+  if (!only) {
+    if (threadIdx.x == 0) {
+      a.part_z[blockIdx.x] = z;
+      a.part_n[blockIdx.x] = n;
+      a.part_bad[blockIdx.x] = bad;
+    }
+    return;
+  }
+  for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+  if (lane == 0) s_dot[warp] = dot;
+  __syncthreads();
   if (threadIdx.x == 0) {
-    for (int w = 1; w < kLossWarps; ++w) {
-      s_z[0] += s_z[w];
-      s_n[0] += s_n[w];
-      s_bad[0] |= s_bad[w];
-    }
-    a.part_z[blockIdx.x] = s_z[0];
-    a.part_n[blockIdx.x] = s_n[0];
-    a.part_bad[blockIdx.x] = s_bad[0];
+    for (int w = 1; w < kWarps; ++w) dot += s_dot[w];
+    a.losses[0] = dot * inv_n * ((float)a.E / (float)a.k);
+    a.losses[1] = z * inv_n;
+    *a.tokens = n;
+    *a.status = bad ? MOE_ERR_INVALID_ARG : MOE_OK;
   }
 }
 
-// One block joins the blocks' partials in their order.
-__global__ void __launch_bounds__(1024) router_loss_join_kernel(
-    LossArgs a, int nb, float* __restrict__ losses, int32_t* __restrict__ counts,
-    int32_t* __restrict__ tokens, float* __restrict__ probs, int32_t* status) {
-  __shared__ double s_sum[32];
-  __shared__ double s_z;
+// Joins the blocks' partials in a fixed order: a cluster of kJoinCtas blocks, each with its share
+// of the experts, whose warps take 32 experts x every slices-th partial; block 0 then adds the
+// blocks' parts of sum_e counts_e P_e through distributed shared memory.
+__global__ void __launch_bounds__(kJoinThreads) router_loss_join_kernel(LossArgs a, int nb) {
+  constexpr int kWarps = kJoinThreads / 32;
+  __shared__ float s_p[kWarps][32];
+  __shared__ int32_t s_c[kWarps][32];
+  __shared__ float s_dot[4];
+  __shared__ float s_part;
+  __shared__ float s_z;
   __shared__ int32_t s_n, s_bad;
   griddep_wait();
   griddep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (warp == 0) {
-    double z = 0.0;
+  const int rank = (int)cluster_ctarank();
+  const int per = (a.E + kJoinCtas - 1) / kJoinCtas;       // experts of a block, at most 128
+  const int chunks = (per + 31) / 32, slices = kWarps / chunks;
+  const int chunk = warp % chunks, slice = warp / chunks;
+  const int e = rank * per + chunk * 32 + lane;
+  const bool mine = chunk * 32 + lane < per && e < a.E;
+  float p = 0.0f;
+  int32_t c = 0;
+  if (mine && slice < slices) {
+    for (int b0 = slice; b0 < nb; b0 += 10 * slices) {   // ten partials in flight
+      float pv[10];
+      int32_t cv[10];
+#pragma unroll
+      for (int u = 0; u < 10; ++u) {
+        const int b = b0 + u * slices;
+        pv[u] = b < nb ? __ldcg(a.part_p + (int64_t)b * a.E + e) : 0.0f;
+        cv[u] = b < nb ? __ldcg(a.part_c + (int64_t)b * a.E + e) : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < 10; ++u) {
+        p += pv[u];
+        c += cv[u];
+      }
+    }
+  }
+  s_p[warp][lane] = p;
+  s_c[warp][lane] = c;
+  if (warp == kWarps - 1) {
+    float z = 0.0f;
     int32_t n = 0, bad = 0;
     for (int b = lane; b < nb; b += 32) {
-      z += (double)__ldcg(a.part_z + b);
+      z += __ldcg(a.part_z + b);
       n += __ldcg(a.part_n + b);
       bad |= __ldcg(a.part_bad + b);
     }
@@ -233,30 +378,38 @@ __global__ void __launch_bounds__(1024) router_loss_join_kernel(
     }
   }
   __syncthreads();
-  const double inv_n = s_n > 0 ? 1.0 / (double)s_n : 0.0;
-  double dot = 0.0;
-  for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
-    double p = 0.0;
-    int32_t c = 0;
-    for (int b = 0; b < nb; ++b) {
-      p += (double)__ldcg(a.part_p + (int64_t)b * a.E + e);
-      c += __ldcg(a.part_c + (int64_t)b * a.E + e);
+  const float inv_n = s_n > 0 ? 1.0f / (float)s_n : 0.0f;
+  if (warp < chunks) {   // slice 0: warp == chunk
+    for (int q = 1; q < slices; ++q) {
+      p += s_p[q * chunks + chunk][lane];
+      c += s_c[q * chunks + chunk][lane];
     }
-    p *= inv_n;
-    counts[e] = c;
-    probs[e] = (float)p;
-    dot += (double)c * p;
+    float dot = 0.0f;
+    if (mine) {
+      p *= inv_n;
+      a.counts[e] = c;
+      a.probs[e] = p;
+      dot = (float)c * p;
+    }
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if (lane == 0) s_dot[warp] = dot;
   }
-  for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-  if (lane == 0) s_sum[warp] = dot;
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int w = 1; w < (int)(blockDim.x >> 5); ++w) dot += s_sum[w];
-    losses[0] = (float)(dot * inv_n / a.k * a.E);
-    losses[1] = (float)(s_z * inv_n);
-    *tokens = s_n;
-    *status = s_bad ? MOE_ERR_INVALID_ARG : MOE_OK;
+    float d = 0.0f;
+    for (int w = 0; w < chunks; ++w) d += s_dot[w];
+    s_part = d;
   }
+  cluster_sync();
+  if (rank == 0 && threadIdx.x == 0) {
+    float dot = 0.0f;
+    for (int r = 0; r < kJoinCtas; ++r) dot += __uint_as_float(ld_dsmem_u32(&s_part, r));
+    a.losses[0] = dot * inv_n * ((float)a.E / (float)a.k);
+    a.losses[1] = s_z * inv_n;
+    *a.tokens = s_n;
+    *a.status = s_bad ? MOE_ERR_INVALID_ARG : MOE_OK;
+  }
+  cluster_sync();   // block 0 has read the others' shared memory
 }
 
 struct LossBwdArgs {
@@ -272,132 +425,211 @@ struct LossBwdArgs {
   float* dlogits;
 };
 
+constexpr int kBwdThreads = 256;
+constexpr int kBwdWarps = kBwdThreads / 32;
+constexpr int kBwdBlocks = 2;   // per SM: 128 registers a thread
+
 template <int G, int VPL, int VEC, bool SQRTSP>
-__global__ void __launch_bounds__(kLossThreads) router_loss_backward_kernel(LossBwdArgs a) {
+__global__ void __launch_bounds__(kBwdThreads, kBwdBlocks)
+router_loss_backward_kernel(LossBwdArgs a) {
   extern __shared__ float dyn[];
   constexpr int R = 32 / G;
-  float* s_f = dyn;                                       // [E] f_e * gb * E / n
+  constexpr int kWidth = G * VPL;                           // E rounded up to the lanes' layout
+  float* s_f = dyn;                                         // [kWidth] gb (E / n) f_e
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane % G;
-  float* s_row = dyn + a.E + (warp * R + lane / G) * a.E;   // this token's gradient row
+  float* s_row = dyn + kWidth * (1 + warp * R + lane / G);  // this token's gradient row
   griddep_wait();
   griddep_launch();
+  const int64_t step = (int64_t)gridDim.x * kBwdWarps * R;
+  int64_t t = ((int64_t)blockIdx.x * kBwdWarps + warp) * R + lane / G;
+  const float* row = a.logits + t * a.E;
+  float* out = a.dlogits + t * a.E + sub * VEC;
+  const int32_t* ids = a.grad_w ? a.ids : nullptr;
+  constexpr bool kAhead = VPL <= 16;   // two rows of 32 logits a lane would spill
+  TokenRow<VPL> next;
+  if constexpr (kAhead)
+    load_row<G, VPL, VEC>(row, ids, a.mask, t, a.T, a.E, a.k, sub, next);
   const int32_t n = __ldg(a.tokens);
   const float inv_n = n > 0 ? 1.0f / (float)n : 0.0f;
   const float gb = a.grad_losses ? __ldg(a.grad_losses) : 0.0f;
   const float gz = (a.grad_losses ? __ldg(a.grad_losses + 1) : 0.0f) * 2.0f * inv_n;
   const float fs = gb * inv_n * inv_n * (float)a.E / (float)a.k;
-  for (int e = threadIdx.x; e < a.E; e += kLossThreads) s_f[e] = fs * (float)__ldg(a.counts + e);
+  for (int e = threadIdx.x; e < kWidth; e += kBwdThreads)
+    s_f[e] = e < a.E ? fs * (float)__ldg(a.counts + e) : 0.0f;
   __syncthreads();
-  float f[VPL];
+  auto f_of = [&](int i, float (&f)[VEC]) {   // the VEC shares from logit i on
+    if constexpr (VEC == 4) {
+      const float4 q = *reinterpret_cast<const float4*>(s_f + expert_of<G, VPL, VEC>(sub, i));
+      f[0] = q.x; f[1] = q.y; f[2] = q.z; f[3] = q.w;
+    } else {
+      f[0] = s_f[expert_of<G, VPL, VEC>(sub, i)];
+    }
+  };
+  while (t - lane / G < a.T) {   // the warp's first row decides
+    TokenRow<VPL> r;
+    const int64_t ahead = step * a.E;
+    if constexpr (kAhead) {
+      r = next;
+      load_row<G, VPL, VEC>(row + ahead, ids, a.mask, t + step, a.T, a.E, a.k, sub, next);
+    } else {
+      load_row<G, VPL, VEC>(row, ids, a.mask, t, a.T, a.E, a.k, sub, r);
+    }
+    // (E, k) slots of the row: the first per lane, with its logit and weight gradient
+    float l0 = -INFINITY, g0 = 0.0f;
+    if (ids && (uint32_t)r.id < (uint32_t)a.E) {
+      l0 = __ldg(row + r.id);
+      g0 = __ldg(a.grad_w + t * a.k + sub);
+    }
+    float top = r.v[0];
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = expert_of<G, VPL, VEC>(sub, i);
-    f[i] = e < a.E ? s_f[e] : 0.0f;
-  }
-  const int64_t step = (int64_t)gridDim.x * kLossWarps * R;
-  for (int64_t t0 = ((int64_t)blockIdx.x * kLossWarps + warp) * R; t0 < a.T; t0 += step) {
-    const int64_t t = t0 + lane / G;
-    bool live = t < a.T && (!a.mask || a.mask[t]);
-    float v[VPL], ex[VPL];
-    const float* row = a.logits + t * a.E;
-    load_row<G, VPL, VEC>(row, a.E, sub, live, v);
-    float top = v[0];
-#pragma unroll
-    for (int i = 1; i < VPL; ++i) top = nan_max(top, v[i]);
+    for (int i = 1; i < VPL; ++i) top = nan_max(top, r.v[i]);
     top = group_max<G>(top);
-    live = live && top != -INFINITY;
-    float sum = 0.0f, sc = 0.0f, fp = 0.0f;
+    const bool live = r.kept && top != -INFINITY;
+    float sum = 0.0f, sc = 0.0f, fp = 0.0f, slope[SQRTSP ? VPL : 1];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      ex[i] = expf(v[i] - top);
-      sum += ex[i];
-      if constexpr (SQRTSP) {
-        const float s = sqrtsp_score(v[i]);
-        sc += s;
-        fp = fmaf(f[i], s, fp);
-      } else {
-        fp = fmaf(f[i], ex[i], fp);
+    for (int i0 = 0; i0 < VPL; i0 += VEC) {
+      float f[VEC];
+      f_of(i0, f);
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) {
+        const int i = i0 + c;
+        const float ex = ex2((r.v[i] - top) * kLog2e);
+        sum += ex;
+        if constexpr (SQRTSP) {
+          const float s = sqrtsp_score(r.v[i], slope[i]);
+          sc += s;
+          fp = fmaf(f[c], s, fp);
+        } else {
+          fp = fmaf(f[c], ex, fp);
+        }
+        r.v[i] = ex;
       }
     }
     sum = group_sum<G>(sum);
     fp = group_sum<G>(fp);
     if constexpr (SQRTSP) sc = group_sum<G>(sc);
-    const float inv = 1.0f / sum;
-    const float zc = gz * (top + logf(sum)) * inv;
+    const float inv = rcp_approx(sum);
+    const float is = SQRTSP ? (sc == 0.0f ? 0.0f : rcp_approx(sc)) : inv;
+    const float zc = gz * fmaf(lg2_approx(sum), kLn2, top) * inv;
+    fp *= is;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      float d;
-      if constexpr (SQRTSP) {
-        const float s = sqrtsp_score(v[i]);
-        const float is = sc == 0.0f ? 0.0f : 1.0f / sc;
-        d = zc * ex[i] + (s == 0.0f ? 0.0f : (f[i] - fp * is) * is * sqrtsp_slope(v[i], s));
-      } else {
-        d = ex[i] * (zc + inv * (f[i] - fp * inv));
+    for (int i0 = 0; i0 < VPL; i0 += VEC) {
+      float f[VEC];
+      f_of(i0, f);
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) {
+        const int i = i0 + c;
+        const float d = SQRTSP ? fmaf(zc, r.v[i], (f[c] - fp) * is * slope[SQRTSP ? i : 0])
+                               : r.v[i] * fmaf(is, f[c] - fp, zc);
+        r.v[i] = live ? d : 0.0f;
       }
-      const int e = expert_of<G, VPL, VEC>(sub, i);
-      if (e < a.E) s_row[e] = live ? d : 0.0f;
     }
-    __syncwarp();
-    if (a.grad_w) {
+    if (ids) {
       // the top-k weights' own softmax (or normalised scores) over the valid ids
-      float mx = -INFINITY;
-      for (int j = sub; j < a.k; j += G) {
-        const int id = live ? __ldg(a.ids + t * a.k + j) : -1;
-        if ((uint32_t)id < (uint32_t)a.E) mx = nan_max(mx, __ldg(row + id));
+      auto slot = [&](int j, float& l, float& g) {   // slot j >= G of this row
+        const int id = live && j < a.k ? __ldg(ids + t * a.k + j) : -1;
+        const bool valid = (uint32_t)id < (uint32_t)a.E;
+        l = valid ? __ldg(row + id) : -INFINITY;
+        g = valid ? __ldg(a.grad_w + t * a.k + j) : 0.0f;
+        return valid ? id : -1;
+      };
+      auto weight = [&](float l, float mx, float& dl) {   // score and its slope by the logit
+        if constexpr (SQRTSP) return sqrtsp_score(l, dl);
+        const float w = l == -INFINITY ? 0.0f : ex2((l - mx) * kLog2e);
+        dl = w;
+        return w;
+      };
+      float mx = l0, l, g, dl0, dl;
+      if constexpr (!SQRTSP) {
+        for (int j = sub + G; j - sub < a.k; j += G) {
+          slot(j, l, g);
+          mx = nan_max(mx, l);
+        }
+        mx = group_max<G>(mx);
       }
-      mx = group_max<G>(mx);
-      float ws = 0.0f, wg = 0.0f;
-      for (int j = sub; j < a.k; j += G) {
-        const int id = live ? __ldg(a.ids + t * a.k + j) : -1;
-        if ((uint32_t)id >= (uint32_t)a.E) continue;
-        const float l = __ldg(row + id);
-        const float s = SQRTSP ? sqrtsp_score(l) : expf(l - mx);
-        ws += s;
-        wg = fmaf(s, __ldg(a.grad_w + t * a.k + j), wg);
+      float ws = weight(l0, mx, dl0), wg = ws * g0;
+      for (int j = sub + G; j - sub < a.k; j += G) {
+        slot(j, l, g);
+        const float w = weight(l, mx, dl);
+        ws += w;
+        wg = fmaf(w, g, wg);
       }
       ws = group_sum<G>(ws);
       wg = group_sum<G>(wg);
-      const float iw = ws == 0.0f ? 0.0f : 1.0f / ws;
-      // slot by slot, so that an id that stands twice in a row gets both shares in slot order
-      for (int j = 0; j < a.k; ++j) {
-        if (sub == j % G && live) {
-          const int id = __ldg(a.ids + t * a.k + j);
-          if ((uint32_t)id < (uint32_t)a.E) {
-            const float l = __ldg(row + id);
-            const float g = __ldg(a.grad_w + t * a.k + j) - wg * iw;
-            if constexpr (SQRTSP) {
-              const float s = sqrtsp_score(l);
-              if (s != 0.0f) s_row[id] += g * iw * sqrtsp_slope(l, s);
-            } else if (l != -INFINITY) {
-              s_row[id] += expf(l - mx) * iw * g;
-            }
+      const float iw = ws == 0.0f ? 0.0f : rcp_approx(ws);
+      wg *= iw;
+#pragma unroll
+      for (int i = 0; i < VPL; i += VEC) {
+        float* p = s_row + expert_of<G, VPL, VEC>(sub, i);
+        if constexpr (VEC == 4)
+          *reinterpret_cast<float4*>(p) = make_float4(r.v[i], r.v[i + 1], r.v[i + 2], r.v[i + 3]);
+        else
+          *p = r.v[i];
+      }
+      __syncwarp();
+      // G slots at a time; where an id stands twice among them, slot by slot, so that it gets both
+      // shares in slot order
+      int id = live && (uint32_t)r.id < (uint32_t)a.E ? r.id : -1;
+      float add = (g0 - wg) * iw * dl0;
+      for (int j = sub;;) {
+        const bool valid = id >= 0;
+        const uint32_t same = __match_any_sync(0xffffffffu, valid ? lane / G * kWidth + id : -1 - lane);
+        if (__all_sync(0xffffffffu, (same & (same - 1u)) == 0u)) {
+          if (valid) s_row[id] += add;
+        } else {
+          for (int q = 0; q < G; ++q) {
+            if (valid && sub == q) s_row[id] += add;
+            __syncwarp();
           }
         }
         __syncwarp();
+        j += G;
+        if (j - sub >= a.k) break;
+        id = slot(j, l, g);
+        weight(l, mx, dl);
+        add = (g - wg) * iw * dl;
       }
-    }
-    if (t < a.T) {
 #pragma unroll
       for (int i = 0; i < VPL; i += VEC) {
-        const int e = expert_of<G, VPL, VEC>(sub, i);
-        if (e >= a.E) continue;
-        if constexpr (VEC == 4)
-          *reinterpret_cast<float4*>(a.dlogits + t * a.E + e) =
-              *reinterpret_cast<const float4*>(s_row + e);
-        else
-          a.dlogits[t * a.E + e] = s_row[e];
+        const float* p = s_row + expert_of<G, VPL, VEC>(sub, i);
+        if constexpr (VEC == 4) {
+          const float4 q = *reinterpret_cast<const float4*>(p);
+          r.v[i] = q.x; r.v[i + 1] = q.y; r.v[i + 2] = q.z; r.v[i + 3] = q.w;
+        } else {
+          r.v[i] = *p;
+        }
       }
+      __syncwarp();
     }
-    __syncwarp();
+    const int left = t < a.T ? a.E - sub * VEC : 0;
+#pragma unroll
+    for (int i = 0; i < VPL; i += VEC) {
+      const int o = i / VEC * G * VEC;
+      if (o >= left) continue;
+      if constexpr (VEC == 4)
+        *reinterpret_cast<float4*>(out + o) =
+            make_float4(r.v[i], r.v[i + 1], r.v[i + 2], r.v[i + 3]);
+      else
+        out[o] = r.v[i];
+    }
+    t += step;
+    row += ahead;
+    out += ahead;
   }
 }
 
-int loss_blocks(int64_t T) {
-  // whole waves of two blocks per SM; a small batch takes a block per eight tokens
-  return (int)std::min<int64_t>(std::max<int64_t>((T + kLossWarps - 1) / kLossWarps, 1),
-                                2 * (int64_t)num_sms());
-}
+// Lanes of one token's row for E experts, and the blocks of the loss kernel.  A batch of at most four rounds of one block's warps stays in one block, which then needs no
+// second launch; above, one block per SM.
+struct LossGrid {
+  int lanes, blocks;
+  LossGrid(int64_t T, int E) {
+    lanes = E <= 64 ? 4 : E <= 128 ? 8 : E <= 256 ? 16 : 32;
+    const int64_t round = (E <= 512 ? loss_threads<16>() : loss_threads<32>()) / lanes;
+    const int64_t need = (T + round - 1) / round;
+    blocks = need <= 4 ? 1 : (int)std::min<int64_t>(need, num_sms());
+  }
+};
 
 // Calls f with the lane layout for E experts as template arguments.
 template <typename F>
@@ -409,9 +641,9 @@ cudaError_t with_layout(int E, bool vec, F&& f) {
        : f(integral_constant<int, G>{}, integral_constant<int, VPL>{},                           \
            integral_constant<int, 1>{}))
   if (E <= 32) return NVFP4MOE_LAYOUT(4, 8);
-  if (E <= 64) return NVFP4MOE_LAYOUT(8, 8);
-  if (E <= 128) return NVFP4MOE_LAYOUT(16, 8);
-  if (E <= 256) return NVFP4MOE_LAYOUT(32, 8);
+  if (E <= 64) return NVFP4MOE_LAYOUT(4, 16);
+  if (E <= 128) return NVFP4MOE_LAYOUT(8, 16);
+  if (E <= 256) return NVFP4MOE_LAYOUT(16, 16);
   if (E <= 512) return NVFP4MOE_LAYOUT(32, 16);
   return NVFP4MOE_LAYOUT(32, 32);
 #undef NVFP4MOE_LAYOUT
@@ -433,7 +665,7 @@ extern "C" {
 
 size_t moe_router_loss_workspace_size(int32_t T, int32_t E) {
   if (T < 0 || E < 1) return 0;
-  const size_t nb = (size_t)loss_blocks(T);
+  const size_t nb = (size_t)LossGrid(T, E).blocks;
   return kAlign + 2 * align_up(4 * nb * (size_t)E) + 3 * align_up(4 * nb);
 }
 
@@ -452,7 +684,8 @@ int moe_router_loss(const float* logits, const int32_t* topk_ids, const uint8_t*
                         (const void*)counts, (const void*)tokens, (const void*)probs})
     if (!is_aligned(p, 4)) return MOE_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int nb = loss_blocks(T);
+  const LossGrid lg(T, E);
+  const int nb = lg.blocks;
   uint8_t* w8 = static_cast<uint8_t*>(workspace);
   LossArgs a{};
   a.logits = logits;
@@ -473,16 +706,39 @@ int moe_router_loss(const float* logits, const int32_t* topk_ids, const uint8_t*
   a.part_bad = reinterpret_cast<int32_t*>(w8 + o);
   const bool vec = E % 4 == 0 && is_aligned(logits, 16);
   const bool sp = (flags & MOE_FLAG_ROUTER_SQRTSOFTPLUS) != 0u;
+  a.losses = losses;
+  a.counts = counts;
+  a.tokens = tokens;
+  a.probs = probs;
+  a.status = reinterpret_cast<int32_t*>(workspace);
   cudaError_t e = with_layout(E, vec, [&](auto g, auto vpl, auto v) {
-    auto kern = sp ? router_loss_kernel<decltype(g)::value, decltype(vpl)::value,
-                                        decltype(v)::value, true>
-                   : router_loss_kernel<decltype(g)::value, decltype(vpl)::value,
-                                        decltype(v)::value, false>;
-    return launch_pdl(kern, dim3(nb), dim3(kLossThreads), 8 * (size_t)E, s, a);
+    constexpr int G = decltype(g)::value, VPL = decltype(vpl)::value, VEC = decltype(v)::value;
+    auto kern = sp ? router_loss_kernel<G, VPL, VEC, true> : router_loss_kernel<G, VPL, VEC, false>;
+    constexpr int threads = loss_threads<VPL>();
+    const size_t smem = 4 * (size_t)E * (threads / 32 + 1);
+    if (smem > 48 * 1024) {
+      const cudaError_t ea = cudaFuncSetAttribute(
+          kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (ea != cudaSuccess) return ea;
+    }
+    return launch_pdl(kern, dim3(nb), dim3(threads), smem, s, a);
   });
-  if (e == cudaSuccess)
-    e = launch_pdl(router_loss_join_kernel, dim3(1), dim3(1024), 0, s, a, nb, losses, counts,
-                   tokens, probs, reinterpret_cast<int32_t*>(workspace));
+  if (e == cudaSuccess && nb > 1) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kJoinCtas);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kJoinCtas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, router_loss_join_kernel, a, nb);
+  }
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -504,13 +760,14 @@ int moe_router_loss_backward(const float* logits, const int32_t* topk_ids, const
   const bool vec = E % 4 == 0 && is_aligned(logits, 16) && is_aligned(dlogits, 16);
   const bool sp = (flags & MOE_FLAG_ROUTER_SQRTSOFTPLUS) != 0u;
   const cudaError_t e = with_layout(E, vec, [&](auto g, auto vpl, auto v) {
-    constexpr int G = decltype(g)::value;
-    auto kern = sp ? router_loss_backward_kernel<G, decltype(vpl)::value, decltype(v)::value, true>
-                   : router_loss_backward_kernel<G, decltype(vpl)::value, decltype(v)::value,
-                                                 false>;
-    const int rows = kLossWarps * (32 / G);
-    const int nb = (int)std::min<int64_t>(((int64_t)T + rows - 1) / rows, 4 * (int64_t)num_sms());
-    return launch_pdl(kern, dim3(nb), dim3(kLossThreads), 4 * (size_t)E * (1 + rows), (cudaStream_t)stream, a);
+    constexpr int G = decltype(g)::value, VPL = decltype(vpl)::value, VEC = decltype(v)::value;
+    auto kern = sp ? router_loss_backward_kernel<G, VPL, VEC, true>
+                   : router_loss_backward_kernel<G, VPL, VEC, false>;
+    constexpr int rows = kBwdWarps * (32 / G), width = G * VPL;
+    const int64_t most = (int64_t)kBwdBlocks * num_sms();
+    const int nb = (int)std::min<int64_t>(((int64_t)T + rows - 1) / rows, most);
+    return launch_pdl(kern, dim3(nb), dim3(kBwdThreads), 4 * (size_t)width * (1 + rows),
+                      reinterpret_cast<cudaStream_t>(stream), a);
   });
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
