@@ -2,14 +2,33 @@
 // in the canonical NVFP4 layout (E2M1 codes [N, K/2], E4M3 scales [N, K/16], one FP32 tensor
 // scale) or MXFP4 (codes [N, K/2], E8M0 scales [N, K/32]), x BF16 [T, K], y BF16 or FP32 [T, N].
 //
-// The weights are read once and decoded to BF16 in registers (exact: an E2M1 value times an
-// E4M3 scale has at most 6 significant bits), then multiplied on the tensor cores
-// (mma m16n8k16: 16 weight rows x 8 tokens, FP32 accumulators).  The sum over k may run in any
-// order as long as both operands agree, so lane t of a quad takes 32 consecutive codes (one
-// 16-byte load) of its row and the same 32 columns of x, with no shuffles.
+// The weights are read once, decoded in registers and multiplied on the tensor cores
+// (mma m16n8k16: 16 weight rows x 8 tokens, FP32 accumulators); x sits in shared memory.  The sum
+// over k may run in any order as long as both operands agree, so lane q of a quad takes
+// consecutive codes of its rows and the same columns of x, with no shuffles.
 //
-// A block owns 16 weight rows; its warps split K and join their accumulators in shared memory, in
-// warp order.
+// For few tokens the bound is the instruction stream of the decoding next to HBM: at the copy rate
+// an SM has 22 issue slots for 8 codes.  The conversion of two E2M1 codes to F16 is one
+// instruction (measured 27 T codes/s over the GPU, placing the bits of a BF16 by hand 13.7, HBM
+// delivers 13.4), so weights and x are F16:
+//   * an E2M1 value times an E4M3 scale is exact in F16 (at most 6 significant bits, 2^-10 to
+//     2688).  So is one times an E8M0 scale of 2^-23 .. 2^13; a tile that meets another scale is
+//     done again with each row's largest scale at 2^13: scales below 2^-36 of the row's largest
+//     become zero;
+//   * a row of x is multiplied by a power of two, 2^6 if its largest element is in [2^-6, 2^10),
+//     otherwise the one that brings it to [2^15, 2^16) (one more pass over x): elements down to
+//     2^-32 of the largest keep all of BF16's bits, smaller ones are rounded to a multiple of
+//     2^-30 (or 2^-39 of the largest), an error of at most half of that times sum |w| in a sum whose FP32
+//     roundings are of 2^-24 of its terms.
+// From 32 tokens on the MMAs are the bound (two cycles each on an SM's four tensor cores).
+//
+// K is split twice: over the blocks of a cluster, so that a block can keep its share of x in
+// shared memory, and over ks warps of a block.  A group of ks warps works on a tile of kMt * 16
+// weight rows; the partial sums are joined through (distributed) shared memory in a fixed order.
+#include <algorithm>
+#include <climits>
+#include <type_traits>
+
 #include "ops.h"
 #include "w4.cuh"
 
@@ -17,38 +36,104 @@ namespace nvfp4moe {
 
 namespace {
 
-constexpr int kLinWarps = 8;
-constexpr int kLinRows = 16;
 constexpr int kLinMaxTokens = 64;
+constexpr int kTopGuess = 9;         // exponent of a row's largest element: the first scale's
+constexpr int kTopLeast = -6;        // bounds
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+// Tiling by the number of 8-token columns NT.  One column: 16-row tiles, 16 warps of 64 registers
+// and two blocks an SM, whose many warps hide the latency of the loads.  More columns: x fills the
+// shared memory of an SM, so one block of 16 warps with 128 registers, 32-row tiles (each x
+// fragment is used twice) and more loads in flight a warp; eight columns' accumulators leave room
+// for half the step.
+template <int NT>
+struct LinTile {
+  static constexpr int kMt = NT == 1 ? 1 : 2;        // 16-row MMA tiles of a warp
+  static constexpr int kWarps = 16;
+  static constexpr int kPerSm = NT == 1 ? 2 : 1;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kRows = kMt * 16;
+  static constexpr int kHalves = NT <= 4 ? 2 : 1;    // 128-column parts of a step
+  static constexpr int kStep = kHalves * 128;        // columns of a step
+  // join buffer: kJoin of a warp's kMt * NT accumulator fragments at a time
+  static constexpr int kFrags = kMt * NT;
+  static constexpr int kJoin = kFrags < 8 ? kFrags : 8;
+  static constexpr int kJoinBytes = kWarps * kJoin * 512;
+};
+constexpr int kScaleWindow = 37;     // binades of E8M0 scales that are exact in F16 at one offset
+constexpr int kScaleLow = 104;       // lowest scale byte at offset 0
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Two E4M3 scale bytes -> each times 2^118 as BF16x2 (exact, see e2m1x8_to_bf16x2_scaled_down:
-// times an E2M1 value placed at 2^-126 the product is the weight times 2^-8).  NaN stays NaN.
-__device__ __forceinline__ void e4m3x2_scales(uint32_t b2, uint32_t (&s)[2]) {
-  const float2 f = e4m3x2_to_f32x2(b2);
-  const __nv_bfloat162 s0 = __float2bfloat162_rn(f.x * 0x1p118f);
-  const __nv_bfloat162 s1 = __float2bfloat162_rn(f.y * 0x1p118f);
-  s[0] = *reinterpret_cast<const uint32_t*>(&s0);
-  s[1] = *reinterpret_cast<const uint32_t*>(&s1);
+// Eight E2M1 codes -> four F16x2 words of their values, codes 2i and 2i+1 in word i.
+__device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t (&o)[4]) {
+  asm("{\n"
+      ".reg .b8 b0, b1, b2, b3;\n"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n"
+      "}"
+      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+      : "r"(w));
 }
 
-// Codes word -> four BF16x2 words of the weights (NVFP4: times 2^-8).
-template <bool kMx>
 __device__ __forceinline__ void decode8(uint32_t w, uint32_t scale, uint32_t (&o)[4]) {
-  e2m1x8_to_bf16x2_scaled_down(w, o);
+  e2m1x8_to_f16x2(w, o);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (kMx) o[i] = mul_bf16x2(o[i], kBf16x2Pow2_126);
-    o[i] = mul_bf16x2(o[i], scale);
+  for (int i = 0; i < 4; ++i) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(o[i]) : "r"(scale));
+}
+
+// One row's 32 codes of 128 columns in a lane, and their scale bytes (NVFP4 two, MXFP4 one).
+struct RowCodes {
+  uint4 c;
+  uint32_t s;
+  __device__ __forceinline__ uint32_t word(int i) const {
+    return i == 0 ? c.x : i == 1 ? c.y : i == 2 ? c.z : c.w;
   }
+};
+
+// Scale of unit i (8 codes) of 32 as F16x2, from their scale bytes; MXFP4: 2^(byte - 127 - down),
+// zero below 2^-24 and infinite above 2^15 (the tile is then done again), 255 NaN.
+template <bool kMx>
+__device__ __forceinline__ uint32_t unit_scale(uint32_t bytes, int i, int down) {
+  if constexpr (kMx) {
+    const int f = (int)bytes - 112 - down;   // F16 exponent field; subnormal below 1
+    uint32_t h = f > 0 ? (uint32_t)min(f, 31) << 10 : 0x200u >> min(-f, 31);
+    if (bytes == 255u) h = 0x7E00u;
+    return h | (h << 16);
+  } else {
+    uint32_t h2;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)bytes));
+    return __byte_perm(h2, 0u, (i & 2) ? 0x3232 : 0x1010);
+  }
+}
+
+// floor(log2) of a finite nonzero BF16 magnitude.
+__device__ __forceinline__ int bf16_exponent(uint32_t m) {
+  return m >= 0x80u ? (int)(m >> 7) - 127 : 31 - __clz(m) - 133;
+}
+
+// 2^e as two factors, e in [-252, 254].
+__device__ __forceinline__ float2 pow2_factors(int e) {
+  return make_float2(__uint_as_float((uint32_t)(e / 2 + 127) << 23),
+                     __uint_as_float((uint32_t)(e - e / 2 + 127) << 23));
+}
+
+__device__ __forceinline__ void st_dsmem_float4(const void* local_smem, uint32_t rank,
+                                                const float* v) {
+  uint32_t ra;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(smem_u32(local_smem)), "r"(rank));
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(ra), "f"(v[0]), "f"(v[1]),
+               "f"(v[2]), "f"(v[3])
+               : "memory");
 }
 
 struct LinearArgs {
@@ -60,87 +145,424 @@ struct LinearArgs {
   int64_t N;
   int K;
   void* y;
+  int ks;       // warps that split a tile's steps
+  int cluster;  // blocks that split K
+  int kslice;   // columns of a block, a multiple of the step
+  int kc;       // columns of x in shared memory at a time, a multiple of the step
+  int iters;    // tiles of a group of ks warps
 };
 
+// Columns [k0, k0 + kc) of x, row t times 2^shift[t], to shared memory as F16 (zeros from column ke
+// on), and the largest magnitude of each row (BF16 bits) to top[t].  A warp takes a row's units
+// (8 columns) 32 at a time, kFly loads in flight.  Inside 128 columns, lane q's i-th unit
+// (u = 4 q + i) sits at i * 64 + q * 16, so that a quad's loads of one i are 64 consecutive bytes;
+// rows are 64 bytes off a multiple of 128, so two rows fill all banks.  Not inlined: the kernel's
+// registers are the multiplication's.
+template <int kFly, int kWarps>
+__device__ __noinline__ void stage_x(const uint16_t* x, int T, int K, int k0, int kc, int ke,
+                                     uint8_t* xs, const int* shift, uint32_t* top) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int units = kc / 8, per = (units + kFly * 32 - 1) / (kFly * 32), stride = kc * 2 + 64;
+  for (int v = warp; v < T * per; v += kWarps) {
+    const int t = v / per, u0 = (v - t * per) * (kFly * 32) + lane;
+    const uint4* src = reinterpret_cast<const uint4*>(x + (int64_t)t * K + k0);
+    uint4 d[kFly];
+#pragma unroll
+    for (int b = 0; b < kFly; ++b) {
+      const int u = u0 + b * 32;
+      d[b] = u < units && k0 + u * 8 < ke ? __ldg(src + u) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    const float f = __uint_as_float((uint32_t)(shift[t] + 127) << 23);
+    uint32_t hi = 0u;
+#pragma unroll
+    for (int b = 0; b < kFly; ++b) {
+      const int u = u0 + b * 32;
+      if (u >= units) break;
+      uint32_t w[4] = {d[b].x, d[b].y, d[b].z, d[b].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        hi = __vmaxu2(hi, w[j] & 0x7FFF7FFFu);
+        const __half2 hh = __floats2half2_rn(__uint_as_float(w[j] << 16) * f,
+                                             __uint_as_float(w[j] & 0xFFFF0000u) * f);
+        w[j] = *reinterpret_cast<const uint32_t*>(&hh);
+      }
+      *reinterpret_cast<uint4*>(xs + (size_t)t * stride + (u >> 4) * 256 + (u & 3) * 64 +
+                                ((u >> 2) & 3) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    hi = __reduce_max_sync(0xffffffffu, max(hi >> 16, hi & 0xFFFFu));
+    if (lane == 0) atomicMax(top + t, hi);
+  }
+}
+
+// The largest finite exponent of each row of x over all of K, as the shift that brings it to 15.
+template <int kWarps>
+__device__ __noinline__ void find_shifts(const uint16_t* x, int T, int K, int* shift) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int t = warp; t < T; t += kWarps) {
+    const uint4* row = reinterpret_cast<const uint4*>(x + (int64_t)t * K);
+    uint32_t hi = 0u;
+#pragma unroll 4
+    for (int u = lane; u < K / 8; u += 32) {
+      const uint4 v = __ldg(row + u);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t m = (w[i >> 1] >> (16 * (i & 1))) & 0x7FFFu;
+        if (m < 0x7F80u) hi = max(hi, m);
+      }
+    }
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0) shift[t] = hi == 0u ? 0 : min(15 - bf16_exponent(hi), 127);
+  }
+}
+
+// The largest scale byte of a row (255, NaN, left out) for each lane of its quad.
+__device__ __noinline__ int row_scale_top(const uint8_t* sf, int n) {
+  int top = 0;
+  for (int i = threadIdx.x & 3; i < n; i += 4) {
+    const int b = __ldg(sf + i);
+    if (b != 255) top = max(top, b);
+  }
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  return max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+}
+
 template <int NT, bool kMx, bool kF32>
-__global__ void __launch_bounds__(kLinWarps * 32) linear_w4_kernel(LinearArgs a) {
-  __shared__ float red[kLinWarps][NT][32][4];
-  griddep_wait();
-  griddep_launch();
+__global__ void __launch_bounds__(LinTile<NT>::kThreads, LinTile<NT>::kPerSm)
+linear_w4_kernel(LinearArgs a) {
+  using L = LinTile<NT>;
+  constexpr int kMt = L::kMt, kHalves = L::kHalves, kStep = L::kStep, kWarps = L::kWarps;
+  constexpr int kBlk = kMx ? 32 : 16;
+  constexpr bool kRefill = NT > 1;   // load a part of the next step as soon as this one's is used up
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int s_shift[kLinMaxTokens];        // rows of x: the power of two they are times
+  __shared__ uint32_t s_top[kLinMaxTokens];     // their largest magnitude
+  __shared__ float2 s_unscale[kLinMaxTokens];   // takes a row's sums to y, in two factors
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, q = lane & 3;
-  const int64_t n0 = (int64_t)blockIdx.x * kLinRows;
-  // rows behind the last one read it again and are not stored
-  const int64_t r0 = min(n0 + g, a.N - 1), r1 = min(n0 + g + 8, a.N - 1);
-  constexpr int kBlk = kMx ? 32 : 16;
-  float c[NT][4];
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c[j][i] = 0.0f;
-  for (int k0 = warp * 128; k0 < a.K; k0 += kLinWarps * 128) {
-    const int k = k0 + q * 32;
-    uint4 w0 = make_uint4(0u, 0u, 0u, 0u), w1 = w0;
-    uint32_t s0[2] = {0u, 0u}, s1[2] = {0u, 0u};
-    const bool in = k < a.K;
-    if (in) {
-      w0 = __ldg(reinterpret_cast<const uint4*>(a.codes + r0 * (a.K / 2) + k / 2));
-      w1 = __ldg(reinterpret_cast<const uint4*>(a.codes + r1 * (a.K / 2) + k / 2));
-      const uint8_t* p0 = a.sf + r0 * (a.K / kBlk) + k / kBlk;
-      const uint8_t* p1 = a.sf + r1 * (a.K / kBlk) + k / kBlk;
-      if constexpr (kMx) {
-        const uint32_t b0 = __ldg(p0), b1 = __ldg(p1);
-        s0[0] = s0[1] = b0 == 255u ? 0x7FC07FC0u : e8m0_scale_bf16x2(b0);
-        s1[0] = s1[1] = b1 == 255u ? 0x7FC07FC0u : e8m0_scale_bf16x2(b1);
-      } else {
-        e4m3x2_scales(__ldg(reinterpret_cast<const uint16_t*>(p0)), s0);
-        e4m3x2_scales(__ldg(reinterpret_cast<const uint16_t*>(p1)), s1);
-      }
-    }
-    const uint32_t cw0[4] = {w0.x, w0.y, w0.z, w0.w}, cw1[4] = {w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t o0[4], o1[4];
-      decode8<kMx>(cw0[i], s0[i / 2], o0);
-      decode8<kMx>(cw1[i], s1[i / 2], o1);
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int t = j * 8 + g;
-        const uint4 xv = in && t < a.T
-                             ? __ldg(reinterpret_cast<const uint4*>(a.x + (int64_t)t * a.K + k + 8 * i))
-                             : make_uint4(0u, 0u, 0u, 0u);
-        mma_bf16(c[j], o0[0], o1[0], o0[1], o1[1], xv.x, xv.y);
-        mma_bf16(c[j], o0[2], o1[2], o0[3], o1[3], xv.z, xv.w);
-      }
-    }
+  const int slice = warp % a.ks, group = warp / a.ks, groups = kWarps / a.ks;
+  const int rank = (int)blockIdx.x % a.cluster, col = (int)blockIdx.x / a.cluster;
+  const int cols = (int)gridDim.x / a.cluster;
+  const int stride = a.kc * 2 + 64;
+  float4* join = reinterpret_cast<float4*>(smem);   // [warps][kJoin][32], if anything is joined
+  const bool joins = a.ks > 1 || a.cluster > 1;
+  uint8_t* xs = smem + (joins ? L::kJoinBytes : 0);
+  const int64_t tiles = (a.N + L::kRows - 1) / L::kRows;
+  const int64_t tile0 = (int64_t)col * groups + group;   // this group's first tile
+  const int kb = rank * a.kslice, ke = min(a.K, kb + a.kslice);   // this block's columns
+  if (threadIdx.x < kLinMaxTokens) {
+    s_shift[threadIdx.x] = 15 - kTopGuess;
+    s_top[threadIdx.x] = 0u;
   }
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-    *reinterpret_cast<float4*>(red[warp][j][lane]) = make_float4(c[j][0], c[j][1], c[j][2], c[j][3]);
+  {
+    // the first step's codes (and scales) on their way into L2 while the previous kernel ends and x
+    // is staged; a prefetch reads nothing, so it need not wait for that kernel
+    const int64_t row = min(tile0 * L::kRows + lane % L::kRows, a.N - 1);
+    const int64_t k = kb + min(slice * kStep, ke - kb - 32);
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.codes + row * (a.K / 2) + k / 2));
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.sf + row * (a.K / kBlk) + k / kBlk));
+  }
   __syncthreads();
-  // element (row r, token t) sits in lane (r % 8) * 4 + (t % 8) / 2, register (r / 8) * 2 + t % 2
-  const float scale = kMx ? 1.0f : __ldg(a.ts) * 256.0f;
-  for (int i = threadIdx.x; i < kLinRows * a.T; i += kLinWarps * 32) {
-    const int r = i % kLinRows, t = i / kLinRows;
-    const int src = (r & 7) * 4 + ((t & 7) >> 1), reg = (r >> 3) * 2 + (t & 1);
-    float s = 0.0f;
+  griddep_wait();
+  griddep_launch();
+
+  // x at the first scale; if a row's largest element (anywhere in the cluster's blocks) does not
+  // fit it, at the rows' own.  x that is too long for shared memory is staged again by chunks.
+  const int chunks = (a.kslice + a.kc - 1) / a.kc;
+  constexpr int kFly = NT == 1 ? 4 : 8;
+  for (int attempt = 0;; ++attempt) {
+    for (int chunk = chunks - 1; chunk >= 0; --chunk)
+      stage_x<kFly, kWarps>(a.x, a.T, a.K, kb + chunk * a.kc, a.kc, ke, xs, s_shift, s_top);
+    __syncthreads();
+    if (attempt == 1) break;
+    if (a.cluster > 1) cluster_sync();
+    bool fits = true;
+    if ((int)threadIdx.x < a.T) {
+      uint32_t top = s_top[threadIdx.x];
+      if (a.cluster > 1)
+        for (int b = 0; b < a.cluster; ++b) top = max(top, ld_dsmem_u32(s_top + threadIdx.x, b));
+      fits = top == 0u || (top >= (uint32_t)(kTopLeast + 127) << 7 && top < (uint32_t)(kTopGuess + 128) << 7);
+    }
+    fits = __syncthreads_and(fits);
+    if (a.cluster > 1) cluster_sync();   // (the others have read this block's maxima)
+    if (fits) break;
+    find_shifts<kWarps>(a.x, a.T, a.K, s_shift);
+    __syncthreads();
+  }
+  if (threadIdx.x < kLinMaxTokens) {   // half of the power of two on either side of the tensor scale
+    float2 u = pow2_factors(-s_shift[threadIdx.x]);
+    if constexpr (!kMx) u.y *= __ldg(a.ts);
+    s_unscale[threadIdx.x] = u;
+  }
+  __syncthreads();
+
+  // A tile's rows 8 r + g; rows behind the last one read it again and are not stored.
+  const uint8_t *pc, *ps;
+  int off[2 * kMt], down[kMx ? 2 * kMt : 1];
+  RowCodes st[kHalves][2 * kMt];
+  float c[kMt][NT][4];
+  // Part h of the step at column k behind k0: a lane's 32 of each 128 columns, so that a quad's
+  // 16-byte loads fill whole sectors.  Columns behind k1 read the row's last 32 again, against
+  // zeros of x (a NaN there is the row's anyway).
+  auto load = [&](int k0, int k1, int k, int h) {
+    const int at = min(k0 + k + q * 32 + h * 128, k1 - 32);
 #pragma unroll
-    for (int w = 0; w < kLinWarps; ++w) s += red[w][t >> 3][src][reg];
-    s *= scale;
-    if (n0 + r < a.N) {
-      const int64_t at = (int64_t)t * a.N + n0 + r;
-      if constexpr (kF32) static_cast<float*>(a.y)[at] = s;
-      else static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(s);
+    for (int r = 0; r < 2 * kMt; ++r) {
+      st[h][r].c = __ldg(reinterpret_cast<const uint4*>(pc + (int64_t)off[r] * (a.K / 2) + (at >> 1)));
+      const uint8_t* s = ps + (int64_t)off[r] * (a.K / kBlk) + at / kBlk;
+      if constexpr (kMx) st[h][r].s = __ldg(s);
+      else st[h][r].s = __ldg(reinterpret_cast<const uint16_t*>(s));
+    }
+  };
+  // Token 8 j + g, unit at byte `at`.  Lanes of tokens behind T read the last token (one column) or
+  // the uninitialised end of the last column's rows; they only reach sums that are not stored.
+  const uint8_t* xrow = xs + (NT == 1 ? min(g, a.T - 1) : g) * stride + q * 16;
+  auto x_frag = [&](int j, int at) {
+    return *reinterpret_cast<const uint4*>(xrow + j * 8 * stride + at);
+  };
+  // Adds columns k0 .. k1 of the tile (x of k0 at the start of shared memory) to c.  Returns
+  // whether this lane met a scale that F16 does not hold (kMx).
+  auto sweep = [&](int k0, int k1) {
+    bool odd = false;
+    if constexpr (kRefill) {
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) load(k0, k1, slice * kStep, h);
+    }
+    for (int k = slice * kStep; k < k1 - k0; k += a.ks * kStep) {
+      if constexpr (!kRefill) {
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) load(k0, k1, k, h);
+      }
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) {
+        uint32_t sc[2 * kMt];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t o[2 * kMt][4];
+#pragma unroll
+          for (int r = 0; r < 2 * kMt; ++r) {
+            if (i % (kMx ? 4 : 2) == 0) sc[r] = unit_scale<kMx>(st[h][r].s, i, down[kMx ? r : 0]);
+            if (kMx && i == 0)
+              odd = odd || (st[h][r].s - (uint32_t)kScaleLow >= (uint32_t)kScaleWindow &&
+                            st[h][r].s != 255u);
+            decode8(st[h][r].word(i), sc[r], o[r]);
+          }
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            if (NT > 1 && j * 8 >= a.T) break;
+            const uint4 xv = x_frag(j, k * 2 + h * 256 + i * 64);
+#pragma unroll
+            for (int m = 0; m < kMt; ++m) {
+              mma_f16(c[m][j], o[2 * m][0], o[2 * m + 1][0], o[2 * m][1], o[2 * m + 1][1], xv.x, xv.y);
+              mma_f16(c[m][j], o[2 * m][2], o[2 * m + 1][2], o[2 * m][3], o[2 * m + 1][3], xv.z, xv.w);
+            }
+          }
+        }
+        if constexpr (kRefill) load(k0, k1, k + a.ks * kStep, h);
+      }
+    }
+    return odd;
+  };
+  // One sum to y: token 8 j + t8, row r16 of MMA tile m.
+  auto store = [&](int64_t tile, int m, int j, int t8, int r16, float v) {
+    const int t = j * 8 + t8;
+    const int64_t n = tile * L::kRows + m * 16 + r16;
+    if (t >= a.T || n >= a.N) return;
+    if constexpr (kF32) static_cast<float*>(a.y)[(int64_t)t * a.N + n] = v;
+    else static_cast<__nv_bfloat16*>(a.y)[(int64_t)t * a.N + n] = __float2bfloat16_rn(v);
+  };
+  auto all = [&]() {   // the threads that join a tile
+    if (a.cluster > 1) cluster_sync();
+    else if (a.ks == kWarps) __syncthreads();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(a.ks * 32) : "memory");
+  };
+
+  for (int it = 0; it < a.iters; ++it) {
+    const int64_t tile = tile0 + (int64_t)it * cols * groups;
+    {
+      const int64_t row = min(tile * L::kRows + g, a.N - 1);
+      pc = a.codes + row * (a.K / 2);
+      ps = a.sf + row * (a.K / kBlk);
+#pragma unroll
+      for (int r = 0; r < 2 * kMt; ++r)
+        off[r] = (int)(min(tile * L::kRows + g + r * 8, a.N - 1) - row);
+    }
+#pragma unroll
+    for (int r = 0; r < (kMx ? 2 * kMt : 1); ++r) down[r] = 0;
+#pragma unroll 1
+    for (int attempt = 0;; ++attempt) {
+#pragma unroll
+      for (int m = 0; m < kMt; ++m)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) c[m][j][i] = 0.0f;
+      bool odd = false;
+#pragma unroll 1
+      for (int chunk = 0; chunk < chunks; ++chunk) {
+        const int k0 = kb + chunk * a.kc;
+        if (chunks > 1) {
+          __syncthreads();
+          stage_x<kFly, kWarps>(a.x, a.T, a.K, k0, a.kc, ke, xs, s_shift, s_top);
+          __syncthreads();
+        }
+        if (tile < tiles) odd = sweep(k0, min(ke, k0 + a.kc)) || odd;
+      }
+      if constexpr (!kMx) break;
+      odd = chunks > 1 ? __syncthreads_or(odd) : __any_sync(0xffffffffu, odd);
+      if (!odd || attempt == 1) break;
+#pragma unroll
+      for (int r = 0; r < 2 * kMt; ++r)
+        down[r] = row_scale_top(ps + (int64_t)off[r] * (a.K / kBlk), a.K / kBlk) - 140;
+    }
+    // to y's scale: the rows' (kMx) and x's powers of two and the tensor scale
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 u = s_unscale[j * 8 + q * 2 + (i & 1)];   // (rows behind T: any)
+#pragma unroll
+        for (int m = 0; m < kMt; ++m) {
+          float v = c[m][j][i];
+          if constexpr (kMx) {
+            if (down[2 * m + (i >> 1)] != 0) {   // one exponent for both
+              const float2 d = pow2_factors(
+                  max(down[2 * m + (i >> 1)] - s_shift[j * 8 + q * 2 + (i & 1)], -252));
+              c[m][j][i] = v * d.x * d.y;
+              continue;
+            }
+          }
+          c[m][j][i] = v * u.x * u.y;
+        }
+      }
+    if (!joins) {
+      if (tile < tiles) {
+#pragma unroll
+        for (int m = 0; m < kMt; ++m)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              store(tile, m, j, q * 2 + (i & 1), g + (i >> 1) * 8, c[m][j][i]);
+      }
+      continue;
+    }
+#pragma unroll
+    for (int f0 = 0; f0 < L::kFrags; f0 += L::kJoin) {
+      if (it > 0 || f0 > 0) all();   // the readers of what stands there are through
+      // fragments go round the cluster's blocks: [block][warp][fragments of a block][lane]
+      const int per = L::kJoin / a.cluster;
+#pragma unroll
+      for (int f = 0; f < L::kJoin; ++f) {
+        const float* v = c[(f0 + f) % kMt][(f0 + f) / kMt];
+        float4* slot = join + ((rank * kWarps + warp) * per + f / a.cluster) * 32 + lane;
+        if (a.cluster > 1) st_dsmem_float4(slot, f % a.cluster, v);
+        else *slot = make_float4(v[0], v[1], v[2], v[3]);
+      }
+      all();
+      // this block's sums go round the group's threads, neighbours on neighbouring rows: blocks,
+      // then warps in order.  Row r, token t of a fragment: lane (r % 8) * 4 + t / 2, register
+      // (r / 8) * 2 + t % 2
+      const float* base = reinterpret_cast<const float*>(join + group * a.ks * per * 32);
+      for (int e = slice * 32 + lane; e < per * 128; e += a.ks * 32) {
+        const int r = e & 15, t = (e >> 4) & 7, fl = e >> 7;
+        const float* at = base + fl * 128 + (r & 7) * 16 + (t >> 1) * 4 + (r >> 3) * 2 + (t & 1);
+        float sum = 0.0f;
+        for (int b = 0; b < a.cluster; ++b)
+#pragma unroll 4
+          for (int w = 0; w < a.ks; ++w) sum += at[(b * kWarps + w) * per * 128];
+        const int f = f0 + fl * a.cluster + rank;
+        if (tile < tiles) store(tile, f % kMt, f / kMt, t, r, sum);
+      }
     }
   }
 }
 
+// Time of a split in us, from measurements on GB300: a step of a warp takes kStepUs[0], or
+// kStepUs[1] for each warp of an SM if its warps are many; a join kJoinUs[0] (warps) or [1]
+// (cluster); x comes into shared memory at 16 elements a ns.
+template <int NT>
+struct LinCost {
+  static constexpr double kStepUs[2] = {NT <= 2 ? 1.1 : 1.5, NT == 1 ? 0.0625 : NT == 2 ? 0.15 : 0.25};
+  static constexpr double kJoinUs[2] = {NT == 1 ? 2.0 : 3.0, 5.0};
+};
+
+template <int NT, bool kMx, bool kF32>
+cudaError_t launch_linear(LinearArgs a, cudaStream_t s) {
+  using L = LinTile<NT>;
+  using C = LinCost<NT>;
+  auto kern = linear_w4_kernel<NT, kMx, kF32>;
+  const int64_t tiles = (a.N + L::kRows - 1) / L::kRows;
+  const int64_t steps = (a.K + L::kStep - 1) / L::kStep;
+  const int rows = NT == 1 ? a.T : (a.T + 7) / 8 * 8;   // of x in shared memory
+  // Columns of x that fit beside the join buffer, with `blocks` blocks an SM.
+  auto fitting = [&](bool joins, int blocks) {
+    const int room = (blocks == 2 ? 110 : 222) * 1024 - (joins ? L::kJoinBytes : 0);
+    return (room / rows - 64) / 2 / L::kStep * L::kStep;
+  };
+  // Larger clusters leave SMs of each GPC idle: on 152 SMs 36 clusters of four fit, 15 of eight
+  // (the occupancy query's numbers).
+  auto clusters = [](int cl) {
+    return cl == 8 ? num_sms() / 10 : num_sms() / cl - (cl == 4 ? 2 : 0);
+  };
+  // The split of K over cluster blocks and warps that should finish first.
+  double best = 0.0;
+  int cols = 1;
+  for (int cl = 1; cl <= 8 && cl <= L::kFrags && cl <= steps; cl *= 2) {
+    const int64_t sl = (steps + cl - 1) / cl;
+    for (int ks = 1; ks <= L::kWarps; ks *= 2) {
+      const int64_t groups = L::kWarps / ks, need = (tiles + groups - 1) / groups;
+      if (ks > 1 && groups > 15) continue;   // a named barrier for each group
+      const bool joins = ks > 1 || cl > 1;
+      const int blocks = fitting(joins, L::kPerSm) >= sl * L::kStep ? L::kPerSm : 1;
+      const int64_t slots = (int64_t)blocks * clusters(cl), busy = std::min(need, slots);
+      const int64_t rounds = (need + slots - 1) / slots;
+      const double warps = (double)(busy * cl * L::kWarps) / num_sms();
+      double stage = (double)a.T * sl * L::kStep / 16000.0 * (busy > clusters(cl) ? blocks : 1);
+      if (fitting(joins, blocks) < sl * L::kStep) stage *= 1 + rounds;
+      const double cost = stage + (cl > 1 ? 1.5 : 0.0) +
+                          rounds * ((double)((sl + ks - 1) / ks) *
+                                        std::max(C::kStepUs[0], C::kStepUs[1] * warps) +
+                                    (cl > 1 ? C::kJoinUs[1] : ks > 1 ? C::kJoinUs[0] : 0.0));
+      if (best == 0.0 || cost < best) {
+        best = cost;
+        a.ks = ks;
+        a.cluster = cl;
+        cols = (int)busy;
+        a.iters = (int)rounds;
+        a.kslice = (int)sl * L::kStep;
+        a.kc = std::min(a.kslice, fitting(joins, blocks));
+      }
+    }
+  }
+  const size_t smem = (size_t)rows * (a.kc * 2 + 64) +
+                      (a.ks > 1 || a.cluster > 1 ? L::kJoinBytes : 0);
+  if (smem > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(cols * a.cluster));
+  cfg.blockDim = dim3(L::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)a.cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
 template <int NT>
 cudaError_t launch_linear(const LinearArgs& a, bool mx, bool f32, cudaStream_t s) {
-  auto k = mx ? (f32 ? linear_w4_kernel<NT, true, true> : linear_w4_kernel<NT, true, false>)
-              : (f32 ? linear_w4_kernel<NT, false, true> : linear_w4_kernel<NT, false, false>);
-  return launch_pdl(k, dim3((unsigned)((a.N + kLinRows - 1) / kLinRows)), dim3(kLinWarps * 32), 0,
-                    s, a);
+  return mx ? (f32 ? launch_linear<NT, true, true>(a, s) : launch_linear<NT, true, false>(a, s))
+            : (f32 ? launch_linear<NT, false, true>(a, s) : launch_linear<NT, false, false>(a, s));
 }
 
 }  // namespace
@@ -161,7 +583,15 @@ extern "C" int moe_linear_w4(const void* x, const uint8_t* codes, const uint8_t*
   if (!is_aligned(x, 16) || !is_aligned(codes, 16) || !is_aligned(sf, 2) || !is_aligned(ts, 4) ||
       !is_aligned(y, f32 ? 4 : 2))
     return MOE_ERR_INVALID_ARG;
-  LinearArgs a{static_cast<const uint16_t*>(x), codes, sf, ts, T, N, (int)K, y};
+  LinearArgs a{};
+  a.x = static_cast<const uint16_t*>(x);
+  a.codes = codes;
+  a.sf = sf;
+  a.ts = ts;
+  a.T = T;
+  a.N = N;
+  a.K = (int)K;
+  a.y = y;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = T <= 8    ? launch_linear<1>(a, mx, f32, s)
                         : T <= 16 ? launch_linear<2>(a, mx, f32, s)

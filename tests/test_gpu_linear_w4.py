@@ -107,6 +107,54 @@ def test_quantised_matrix_and_every_code(moe):
     assert torch.equal(y.t().double(), decode(codes, b[:, None], None))
 
 
+LONG = [(64, 100, 16384), (8, 70, 16384), (12, 33, 32768), (33, 40, 20000 // 32 * 32), (1, 20, 131072)]
+
+
+@pytest.mark.parametrize("T,N,K", LONG)
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_exact_rows_longer_than_shared_memory(moe, T, N, K, fmt):
+    """|x| <= 1 keeps the whole-number sums of K terms exact: at most 24 K in units of 1/2 (NVFP4)
+    or 12 K in units of 1/4, below 2^24 up to K = 131072 / 1 with half of x zero."""
+    codes, sf, ts = random_weights(N, K, fmt, True, T + N + K)
+    g = torch.Generator(device="cuda").manual_seed(K)
+    x = (torch.rand(T, K, device="cuda", generator=g) < 0.1).bfloat16()
+    y = moe.linear_w4(x, codes, sf, ts, out_dtype=torch.float32)
+    assert torch.equal(y.double(), x.double() @ decode(codes, sf, ts).t())
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 50, 512), (8, 33, 4096), (16, 40, 7168), (30, 70, 2048), (64, 40, 16384)])
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_rows_of_any_magnitude(moe, T, N, K, fmt):
+    """Rows of x far from one, with outliers, of zeros, and MXFP4 rows whose scales span more than
+    F16.  Elements of x are at worst rounded to 2^-24 of their row's largest (half of 2^-30 where
+    that is at least 2^-6), scales below 2^-36 of a row's largest are zero."""
+    codes, sf, ts = random_weights(N, K, fmt, False, T + N + K)
+    g = torch.Generator(device="cuda").manual_seed(K)
+    if fmt == "mxfp4":
+        rows = torch.randint(0, 4, (N, 1), device="cuda", generator=g)
+        spread = torch.randint(0, 60, (N, K // 32), device="cuda", generator=g)
+        base = torch.tensor([110, 20, 180, 64], device="cuda")[rows]
+        sf = torch.where(rows == 0, base + spread % 8, base + spread).to(torch.uint8)
+    x = torch.randn(T, K, device="cuda", generator=g)
+    e = torch.tensor([0, 30, -60, 12, -14, 0, -100, 3], device="cuda")[torch.arange(T, device="cuda") % 8].double()
+    x = (x.double() * torch.exp2(e)[:, None]).float().bfloat16()
+    x[T // 2, 7] = 2.0 ** 20 * x[T // 2].abs().max()
+    if T > 3:
+        x[3] = 0
+    w = decode(codes, sf, ts)
+    want, size = x.double() @ w.t(), x.double().abs() @ w.abs().t()
+    top = x.double().abs().amax(1, keepdim=True)
+    tol = (K / 128 + 16) * 2.0 ** -21 * size + 2.0 ** -24 * top * w.abs().sum(1)
+    if fmt == "mxfp4":
+        tol = tol + x.double().abs().sum(1, keepdim=True) * 6 * 2.0 ** -36 * torch.exp2(sf.double().amax(1) - 127)
+    y = moe.linear_w4(x, codes, sf, ts, out_dtype=torch.float32).double()
+    # FP32 sums: a partial sum is bounded only by the sum of the magnitudes, so where that is beyond
+    # FP32's 3.4e38 a partial sum may be infinite although the whole one is not
+    over = size + tol > 3e38
+    under = 2.0 ** -140                        # FP32's own smallest steps
+    assert bool((((y - want).abs() <= tol + under) | over).all())
+
+
 @pytest.mark.parametrize("T", [1, 12, 40])
 def test_nonfinite(moe, T):
     codes, sf, ts = random_weights(40, 256, "nvfp4", False, 7)
