@@ -333,6 +333,18 @@ linear_w4_kernel(LinearArgs a) {
 #pragma unroll
         for (int h = 0; h < kHalves; ++h) load(k0, k1, k, h);
       }
+      // up to two columns, a step's MMAs sum from zero and are added with rounded FP32 additions:
+      // the tensor cores truncate, which a chain of 256 MMAs turns into a bias of 1e-6
+      constexpr bool kApart = NT <= 2;
+      float d[kApart ? kMt : 1][kApart ? NT : 1][4];
+      if constexpr (kApart) {
+#pragma unroll
+        for (int m = 0; m < kMt; ++m)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[m][j][i] = 0.0f;
+      }
 #pragma unroll
       for (int h = 0; h < kHalves; ++h) {
         uint32_t sc[2 * kMt];
@@ -353,12 +365,21 @@ linear_w4_kernel(LinearArgs a) {
             const uint4 xv = x_frag(j, k * 2 + h * 256 + i * 64);
 #pragma unroll
             for (int m = 0; m < kMt; ++m) {
-              mma_f16(c[m][j], o[2 * m][0], o[2 * m + 1][0], o[2 * m][1], o[2 * m + 1][1], xv.x, xv.y);
-              mma_f16(c[m][j], o[2 * m][2], o[2 * m + 1][2], o[2 * m][3], o[2 * m + 1][3], xv.z, xv.w);
+              float (&sum)[4] = kApart ? d[kApart ? m : 0][kApart ? j : 0] : c[m][j];
+              mma_f16(sum, o[2 * m][0], o[2 * m + 1][0], o[2 * m][1], o[2 * m + 1][1], xv.x, xv.y);
+              mma_f16(sum, o[2 * m][2], o[2 * m + 1][2], o[2 * m][3], o[2 * m + 1][3], xv.z, xv.w);
             }
           }
         }
         if constexpr (kRefill) load(k0, k1, k + a.ks * kStep, h);
+      }
+      if constexpr (kApart) {
+#pragma unroll
+        for (int m = 0; m < kMt; ++m)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c[m][j][i] += d[m][j][i];
       }
     }
     return odd;

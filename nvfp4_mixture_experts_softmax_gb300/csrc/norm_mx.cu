@@ -9,6 +9,7 @@
 // Backward, with a = gamma * dy:  dx = dh + r * a - h * r^3 * mean(a * h)  (the gradient of x and
 // of the residual alike),  dgamma_c = sum over rows of dy * (h * r).  The quantisation is passed
 // straight through: dy is the gradient of y.
+#include <algorithm>
 #include <cmath>
 
 #include "common.cuh"
@@ -39,70 +40,106 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Sum of one value per thread over the block, the same on every thread and in a fixed order.
-__device__ __forceinline__ float block_sum(float v, float* red) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+// How a row is laid over threads: W warps with J vectors of 8 columns a lane (vector c of lane t:
+// c = j * 32 W + t, so four neighbouring lanes share a 32-element block); a block holds G such row
+// groups, each of which takes every gridDim * G-th row.
+struct RowGrid {
+  int J, W, G, blocks;
+};
+
+// Sum of one value per thread over the W warps of a row group, the same on every thread and in a
+// fixed order.  One barrier: `red` holds two rows' partial sums in turn (a warp that writes a row's
+// has passed the barrier of the row before, behind the reads of the one before that).
+__device__ __forceinline__ float row_sum(float v, float* red, int W, int wrow, int group, int G,
+                                         int parity) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (lane == 0) red[warp] = v;
-  __syncthreads();
-  float s = lane < nw ? red[lane] : 0.0f;
+  if (W == 1) return v;
+  const int lane = threadIdx.x & 31;
+  float* mine = red + (parity * G + group) * 32;
+  if (lane == 0) mine[wrow] = v;
+  if (G == 1) __syncthreads();
+  else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(W * 32) : "memory");
+  float s = lane < W ? mine[lane] : 0.0f;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  __syncthreads();
   return s;
 }
 
-// One block per row; a thread owns J vectors of 8 columns, so four neighbouring threads share a
-// 32-element block.
+// h = bf16(x + residual) of one vector, and its squares added to sq.
+__device__ __forceinline__ uint4 add_vec(uint4 x, uint4 r, bool has_res, float& sq) {
+  float f[8];
+  unpack8(x, f);
+  if (has_res) {
+    float g[8];
+    unpack8(r, g);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] += g[i];
+    x = pack8(f);
+    unpack8(x, f);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sq = fmaf(f[i], f[i], sq);
+  return x;
+}
+
+// The next row's x and residual are loaded before the current row is reduced.  64 registers a
+// thread: 32 warps an SM with 2 KB each in flight.
 template <int J>
-__global__ void __launch_bounds__(512) add_rmsnorm_mx_kernel(
+__global__ void __launch_bounds__(512, J <= 2 ? 2 : 1) add_rmsnorm_mx_kernel(
     const uint4* x, const uint4* residual, const uint4* __restrict__ gamma, float eps,
-    int64_t rows, int cols, uint4* h, uint2* codes, uint8_t* sf, uint4* y, float* rrms) {
-  __shared__ float red[32];
+    int64_t rows, int cols, int W, int G, uint4* h, uint2* codes, uint8_t* sf, uint4* y,
+    float* rrms) {
+  __shared__ float red[2 * 16 * 32];
+  const int warp = threadIdx.x >> 5, group = warp / W, wrow = warp - group * W;
+  const int t = wrow * 32 + (threadIdx.x & 31), span = W * 32;   // thread of the row, vectors apart
+  const int nvec = cols / 8;
+  const float inv_cols = 1.0f / (float)cols;
   griddep_wait();
   griddep_launch();
-  const int nvec = cols / 8;
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  int64_t row = (int64_t)blockIdx.x * G + group;
+  const int64_t step = (int64_t)gridDim.x * G;
+  uint4 nx[J], nr[J];
+  auto load = [&](int64_t rw) {
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int c = j * span + t;
+      const bool in = rw < rows && c < nvec;
+      nx[j] = in ? x[rw * nvec + c] : zero;
+      nr[j] = in && residual ? residual[rw * nvec + c] : zero;
+    }
+  };
+  load(row);
+  for (int parity = 0; row < rows; row += step, parity ^= 1) {
     const int64_t base = row * nvec;
-    float v[J][8];
+    uint4 hv[J];
     float sq = 0.0f;
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const int c = j * blockDim.x + threadIdx.x;
+    for (int j = 0; j < J; ++j) hv[j] = add_vec(nx[j], nr[j], residual != nullptr, sq);
+    load(row + step);   // (rows are written by their own group only, after this group read them)
+    if (residual) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
-      if (c < nvec) {
-        unpack8(x[base + c], v[j]);
-        if (residual) {
-          float f[8];
-          unpack8(residual[base + c], f);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[j][i] += f[i];
-          const uint4 p = pack8(v[j]);
-          unpack8(p, v[j]);
-          if (h) h[base + c] = p;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sq = fmaf(v[j][i], v[j][i], sq);
-      }
+      for (int j = 0; j < J; ++j)
+        if (j * span + t < nvec) h[base + j * span + t] = hv[j];
     }
-    sq = block_sum(sq, red);
-    const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sq, (float)cols), eps)));
-    if (rrms && threadIdx.x == 0) rrms[row] = r;
+    sq = row_sum(sq, red, W, wrow, group, G, parity);
+    const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(sq * inv_cols, eps)));
+    if (rrms && t == 0) rrms[row] = r;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const int c = j * blockDim.x + threadIdx.x;
+      const int c = j * span + t;
       const bool in = c < nvec;
-      float g[8];
-      unpack8(in ? __ldg(gamma + c) : make_uint4(0u, 0u, 0u, 0u), g);
+      float v[8], g[8];
+      unpack8(hv[j], v);
+      unpack8(in ? __ldg(gamma + c) : zero, g);
       uint32_t top = 0u;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        v[j][i] = __fmul_rn(__fmul_rn(v[j][i], r), g[i]);
-        top = max(top, __float_as_uint(fabsf(v[j][i])));   // NaN orders above infinity
+        v[i] = __fmul_rn(__fmul_rn(v[i], r), g[i]);
+        top = max(top, __float_as_uint(fabsf(v[i])));   // NaN orders above infinity
       }
-      if (y && in) y[base + c] = pack8(v[j]);
+      if (y && in) y[base + c] = pack8(v);
       if (!codes) continue;
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -114,10 +151,8 @@ __global__ void __launch_bounds__(512) add_rmsnorm_mx_kernel(
         lo = hi = 0x7F7F7F7Fu;
       } else {
         const float inv = e8m0_to_f32(254u - sb);   // 2^(127 - sb)
-        lo = f32_to_e4m3x2(v[j][0] * inv, v[j][1] * inv) |
-             f32_to_e4m3x2(v[j][2] * inv, v[j][3] * inv) << 16;
-        hi = f32_to_e4m3x2(v[j][4] * inv, v[j][5] * inv) |
-             f32_to_e4m3x2(v[j][6] * inv, v[j][7] * inv) << 16;
+        lo = f32_to_e4m3x2(v[0] * inv, v[1] * inv) | f32_to_e4m3x2(v[2] * inv, v[3] * inv) << 16;
+        hi = f32_to_e4m3x2(v[4] * inv, v[5] * inv) | f32_to_e4m3x2(v[6] * inv, v[7] * inv) << 16;
       }
       codes[base + c] = make_uint2(lo, hi);
       if ((c & 3) == 0) sf[(base + c) >> 2] = (uint8_t)sb;
@@ -125,67 +160,112 @@ __global__ void __launch_bounds__(512) add_rmsnorm_mx_kernel(
   }
 }
 
-// One block takes rows blockIdx, blockIdx + gridDim, ...; a thread owns the same J vectors of 8
-// columns in all of them and keeps their share of dgamma in registers.
-template <int J>
-__global__ void __launch_bounds__(512) add_rmsnorm_backward_kernel(
+// A thread owns the same J vectors of 8 columns in all rows of its group and keeps their share of
+// dgamma in registers; the groups of a block are joined in order at the end, the blocks by
+// dgamma_kernel.  The next row's dy and h are loaded before the current row is reduced (kAhead).
+template <int J, bool kAhead>
+__global__ void __launch_bounds__(kAhead ? 512 : 1024, 1) add_rmsnorm_backward_kernel(
     const uint4* dy, const uint4* dh, const uint4* __restrict__ h,
-    const float* __restrict__ rrms, const uint4* __restrict__ gamma, int64_t rows, int cols,
-    uint4* dx, float4* __restrict__ partial) {
-  __shared__ float red[32];
-  griddep_wait();
-  griddep_launch();
+    const float* __restrict__ rrms, const uint4* __restrict__ gamma, int64_t rows, int cols, int W,
+    int G, uint4* dx, float4* __restrict__ partial) {
+  extern __shared__ float4 s_dg[];   // [cols / 4] if G > 1
+  __shared__ float red[2 * 16 * 32];
+  const int warp = threadIdx.x >> 5, group = warp / W, wrow = warp - group * W;
+  const int t = wrow * 32 + (threadIdx.x & 31), span = W * 32;
   const int nvec = cols / 8;
   const float inv_cols = __fdiv_rn(1.0f, (float)cols);
+  griddep_wait();
+  griddep_launch();
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   float dg[J][8];
 #pragma unroll
   for (int j = 0; j < J; ++j)
 #pragma unroll
     for (int i = 0; i < 8; ++i) dg[j][i] = 0.0f;
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-    const int64_t base = row * nvec;
-    const float r = __ldg(rrms + row);
-    float s = 0.0f;
-    uint4 qd[J], qh[J];
+  int64_t row = (int64_t)blockIdx.x * G + group;
+  const int64_t step = (int64_t)gridDim.x * G;
+  uint4 nd[J], nh[J], ne[J];
+  float nr = 0.0f;
+  auto load = [&](int64_t rw) {
+    nr = rw < rows ? __ldg(rrms + rw) : 0.0f;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const int c = j * blockDim.x + threadIdx.x;
-      const bool in = c < nvec;
-      qd[j] = in ? dy[base + c] : make_uint4(0u, 0u, 0u, 0u);
-      qh[j] = in ? __ldg(h + base + c) : make_uint4(0u, 0u, 0u, 0u);
+      const int c = j * span + t;
+      const bool in = rw < rows && c < nvec;
+      nd[j] = in ? dy[rw * nvec + c] : zero;
+      nh[j] = in ? __ldg(h + rw * nvec + c) : zero;
+      ne[j] = in && dh ? dh[rw * nvec + c] : zero;
+    }
+  };
+  if constexpr (kAhead) load(row);
+  for (int parity = 0; row < rows; row += step, parity ^= 1) {
+    if constexpr (!kAhead) load(row);
+    const float r = nr;
+    uint4 qd[J], qh[J], qe[J];
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int c = j * span + t;
+      qd[j] = nd[j];
+      qh[j] = nh[j];
+      qe[j] = ne[j];
       float d[8], hv[8], g[8];
       unpack8(qd[j], d);
       unpack8(qh[j], hv);
-      unpack8(in ? __ldg(gamma + c) : make_uint4(0u, 0u, 0u, 0u), g);
+      unpack8(c < nvec ? __ldg(gamma + c) : zero, g);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         s = fmaf(d[i] * g[i], hv[i], s);
-        if (in) dg[j][i] = fmaf(d[i], hv[i] * r, dg[j][i]);
+        if (c < nvec) dg[j][i] = fmaf(d[i], hv[i] * r, dg[j][i]);
       }
     }
-    s = block_sum(s, red);
+    if constexpr (kAhead) load(row + step);
+    s = row_sum(s, red, W, wrow, group, G, parity);
     const float m = r * r * (s * inv_cols);
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const int c = j * blockDim.x + threadIdx.x;
+      const int c = j * span + t;
       if (c >= nvec) continue;
-      float d[8], hv[8], g[8], o[8];
+      float d[8], hv[8], g[8], e[8], o[8];
       unpack8(qd[j], d);
       unpack8(qh[j], hv);
       unpack8(__ldg(gamma + c), g);
-      float e[8];
-      if (dh) unpack8(dh[base + c], e);
+      unpack8(qe[j], e);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         o[i] = r * fmaf(-hv[i], m, d[i] * g[i]);
         if (dh) o[i] += e[i];
       }
-      dx[base + c] = pack8(o);
+      dx[row * nvec + c] = pack8(o);
     }
   }
+  for (int k = 1; k < G; ++k) {   // the other groups' sums to the first's, in order
+    __syncthreads();
+    if (group == k) {
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const int c = j * span + t;
+        if (c >= nvec) continue;
+        s_dg[2 * c] = make_float4(dg[j][0], dg[j][1], dg[j][2], dg[j][3]);
+        s_dg[2 * c + 1] = make_float4(dg[j][4], dg[j][5], dg[j][6], dg[j][7]);
+      }
+    }
+    __syncthreads();
+    if (group == 0) {
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const int c = j * span + t;
+        if (c >= nvec) continue;
+        const float4 u = s_dg[2 * c], v = s_dg[2 * c + 1];
+        dg[j][0] += u.x; dg[j][1] += u.y; dg[j][2] += u.z; dg[j][3] += u.w;
+        dg[j][4] += v.x; dg[j][5] += v.y; dg[j][6] += v.z; dg[j][7] += v.w;
+      }
+    }
+  }
+  if (group != 0) return;
 #pragma unroll
   for (int j = 0; j < J; ++j) {
-    const int c = j * blockDim.x + threadIdx.x;
+    const int c = j * span + t;
     if (c >= nvec) continue;
     float4* p = partial + (int64_t)blockIdx.x * (cols / 4) + 2 * c;
     p[0] = make_float4(dg[j][0], dg[j][1], dg[j][2], dg[j][3]);
@@ -193,31 +273,47 @@ __global__ void __launch_bounds__(512) add_rmsnorm_backward_kernel(
   }
 }
 
-// dgamma = sum of the blocks' partial rows, in block order.
-__global__ void __launch_bounds__(256) dgamma_kernel(const float* __restrict__ partial, int nb,
-                                                     int cols, float* __restrict__ dgamma) {
-  __shared__ float red[8][32];
+// dgamma = sum of the blocks' partial rows: warp w takes rows w, w + 32, ..., then the warps in order.
+__global__ void __launch_bounds__(1024) dgamma_kernel(const float* __restrict__ partial, int nb,
+                                                      int cols, float* __restrict__ dgamma) {
+  __shared__ float red[32][33];
   griddep_wait();
   griddep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float s = 0.0f;
-  for (int b = warp; b < nb; b += 8) s += __ldcg(partial + (int64_t)b * cols + c);
+#pragma unroll 10
+  for (int b = warp; b < nb; b += 32) s += __ldcg(partial + (int64_t)b * cols + c);
   red[warp][lane] = s;
   __syncthreads();
-  if (warp == 0) {
+  // lane w of warp c adds warp w's share of column c
+  s = red[lane][warp];
 #pragma unroll
-    for (int w = 1; w < 8; ++w) s += red[w][lane];
-    dgamma[c] = s;
-  }
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane == 0) dgamma[blockIdx.x * 32 + warp] = s;
 }
 
-// Threads for a row of nvec vectors with J of them each: whole warps.
-int row_threads(int nvec, int J) { return ((nvec + J - 1) / J + 31) / 32 * 32; }
+// Few rows: as many warps a row as its vectors fill, for the latency.  Many rows: two vectors a
+// lane, at least eight warps a block, 32 warps an SM.
+RowGrid forward_grid(int64_t rows, int nvec) {
+  RowGrid g;
+  const bool few = rows <= 2 * (int64_t)num_sms();
+  g.J = nvec > 1024 ? 4 : nvec > 512 || (!few && nvec > 32) ? 2 : 1;
+  g.W = (nvec + 32 * g.J - 1) / (32 * g.J);
+  g.G = few ? 1 : std::max(1, 8 / g.W);
+  const int64_t need = (rows + g.G - 1) / g.G, most = (int64_t)num_sms() * std::max(1, (g.J <= 2 ? 32 : 16) / (g.W * g.G));
+  g.blocks = (int)std::min(need, most);
+  return g;
+}
 
-int backward_blocks(int64_t rows) {
-  const int64_t most = 2 * (int64_t)num_sms();
-  return (int)(rows < most ? rows : most);
+RowGrid backward_grid(int64_t rows, int nvec) {
+  RowGrid g;
+  g.J = nvec > 512 ? 2 : 1;
+  g.W = (nvec + 32 * g.J - 1) / (32 * g.J);
+  g.G = std::max(1, 8 / g.W);
+  const int64_t need = (rows + g.G - 1) / g.G, most = (int64_t)num_sms() * std::max(1, 16 / (g.W * g.G));
+  g.blocks = (int)std::max<int64_t>(1, std::min(need, most));
+  return g;
 }
 
 }  // namespace
@@ -240,21 +336,21 @@ int moe_add_rmsnorm_quantize_mx(const void* x, const void* residual, const void*
   for (const void* p : {x, residual, gamma, (const void*)h, (const void*)y})
     if (!is_aligned(p, 16)) return MOE_ERR_INVALID_ARG;
   if (!is_aligned(codes, 8) || !is_aligned(rrms, 4)) return MOE_ERR_INVALID_ARG;
-  const int nvec = (int)(cols / 8);
-  const int J = nvec <= 512 ? 1 : nvec <= 1024 ? 2 : 4;
-  const dim3 grid((unsigned)rows), block(row_threads(nvec, J));
-  auto k = J == 1 ? add_rmsnorm_mx_kernel<1> : J == 2 ? add_rmsnorm_mx_kernel<2>
-                                                       : add_rmsnorm_mx_kernel<4>;
+  const RowGrid g = forward_grid(rows, (int)(cols / 8));
+  auto k = g.J == 1 ? add_rmsnorm_mx_kernel<1> : g.J == 2 ? add_rmsnorm_mx_kernel<2>
+                                                           : add_rmsnorm_mx_kernel<4>;
   const cudaError_t e = launch_pdl(
-      k, grid, block, 0, reinterpret_cast<cudaStream_t>(stream), static_cast<const uint4*>(x),
-      static_cast<const uint4*>(residual), static_cast<const uint4*>(gamma), eps, rows, (int)cols,
-      static_cast<uint4*>(h), reinterpret_cast<uint2*>(codes), sf, static_cast<uint4*>(y), rrms);
+      k, dim3((unsigned)g.blocks), dim3(g.W * g.G * 32), 0, reinterpret_cast<cudaStream_t>(stream),
+      static_cast<const uint4*>(x), static_cast<const uint4*>(residual),
+      static_cast<const uint4*>(gamma), eps, rows, (int)cols, g.W, g.G, static_cast<uint4*>(h),
+      reinterpret_cast<uint2*>(codes), sf, static_cast<uint4*>(y), rrms);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 size_t moe_add_rmsnorm_backward_workspace_size(int64_t rows, int64_t cols) {
-  if (rows < 0 || cols <= 0) return 0;
-  return align_up(sizeof(float) * (size_t)backward_blocks(rows) * (size_t)cols);
+  if (rows < 0 || cols <= 0 || cols > kMaxCols) return 0;
+  return align_up(sizeof(float) * (size_t)backward_grid(rows, (int)((cols + 7) / 8)).blocks *
+                  (size_t)cols);
 }
 
 int moe_add_rmsnorm_backward(const void* dy, const void* dh, const void* h, const float* rrms,
@@ -274,19 +370,19 @@ int moe_add_rmsnorm_backward(const void* dy, const void* dh, const void* h, cons
   for (const void* p : {dy, dh, h, gamma, (const void*)dx})
     if (!is_aligned(p, 16)) return MOE_ERR_INVALID_ARG;
   if (!is_aligned(rrms, 4)) return MOE_ERR_INVALID_ARG;
-  const int nvec = (int)(cols / 8);
-  const int J = nvec <= 512 ? 1 : nvec <= 1024 ? 2 : 4;
-  const int nb = backward_blocks(rows);
-  auto k = J == 1 ? add_rmsnorm_backward_kernel<1> : J == 2 ? add_rmsnorm_backward_kernel<2>
-                                                             : add_rmsnorm_backward_kernel<4>;
+  const RowGrid g = backward_grid(rows, (int)(cols / 8));
+  const bool ahead = g.W * g.G <= 16;
+  auto k = g.J == 1 ? add_rmsnorm_backward_kernel<1, true>
+           : ahead  ? add_rmsnorm_backward_kernel<2, true>
+                    : add_rmsnorm_backward_kernel<2, false>;
   cudaError_t e = launch_pdl(
-      k, dim3(nb), dim3(row_threads(nvec, J)), 0, s, static_cast<const uint4*>(dy),
-      static_cast<const uint4*>(dh), static_cast<const uint4*>(h), rrms,
-      static_cast<const uint4*>(gamma), rows, (int)cols, static_cast<uint4*>(dx),
+      k, dim3(g.blocks), dim3(g.W * g.G * 32), g.G > 1 ? sizeof(float) * (size_t)cols : 0, s,
+      static_cast<const uint4*>(dy), static_cast<const uint4*>(dh), static_cast<const uint4*>(h),
+      rrms, static_cast<const uint4*>(gamma), rows, (int)cols, g.W, g.G, static_cast<uint4*>(dx),
       static_cast<float4*>(workspace));
   if (e == cudaSuccess)
-    e = launch_pdl(dgamma_kernel, dim3((unsigned)(cols / 32)), dim3(256), 0, s,
-                   static_cast<const float*>(workspace), nb, (int)cols, dgamma);
+    e = launch_pdl(dgamma_kernel, dim3((unsigned)(cols / 32)), dim3(1024), 0, s,
+                   static_cast<const float*>(workspace), g.blocks, (int)cols, dgamma);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
