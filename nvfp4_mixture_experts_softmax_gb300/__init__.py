@@ -397,6 +397,12 @@ def run(cfg: MoeConfig, wbuf, x, logits, k=None, y=None, workspace=None, debug=F
 
 # ---- operators around the layer ----
 
+# The current stream's handle of a device: torch's own accessor where it has it (0.1 us; the Stream
+# object costs 1.1 us of a call's 9)
+_stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream",
+                         lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _scoped(fn):
     """Calls fn(stream handle, ...) with its first tensor's device current, on `stream` if that is
     passed (what fn allocates then belongs to that stream) or on the device's current stream."""
@@ -406,12 +412,12 @@ def _scoped(fn):
             raise ValueError(f"{fn.__name__} needs CUDA tensors, got one on {first.device}")
         dev = first.get_device()
         if stream is None and dev == torch.cuda.current_device():
-            return fn(torch.cuda.current_stream(dev).cuda_stream, first, *args, **kw)
+            return fn(_stream_handle(dev), first, *args, **kw)
         if stream is not None and stream.device != first.device:
             raise ValueError(f"{fn.__name__}: the stream is on {stream.device}, the tensors on "
                              f"{first.device}")
         with torch.cuda.device(dev), torch.cuda.stream(stream):
-            return fn(torch.cuda.current_stream(dev).cuda_stream, first, *args, **kw)
+            return fn(_stream_handle(dev), first, *args, **kw)
     return call
 
 

@@ -324,6 +324,26 @@ linear_w4_kernel(LinearArgs a) {
   // whether this lane met a scale that F16 does not hold (kMx).
   auto sweep = [&](int k0, int k1) {
     bool odd = false;
+    // One column: the MMAs of four steps sum from zero and are added with rounded FP32 additions.
+    // The tensor cores truncate, which a chain of 256 MMAs turns into a bias of 1e-6; with more
+    // columns the second set of accumulators costs 15 to 25%, and their chains stay that long.
+    constexpr bool kApart = NT == 1;
+    float d[kApart ? kMt : 1][kApart ? NT : 1][4];
+    auto flush = [&](bool add) {
+      if constexpr (kApart) {
+#pragma unroll
+        for (int m = 0; m < kMt; ++m)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (add) c[m][j][i] += d[m][j][i];
+              d[m][j][i] = 0.0f;
+            }
+      }
+    };
+    flush(false);
+    int chain = 0;
     if constexpr (kRefill) {
 #pragma unroll
       for (int h = 0; h < kHalves; ++h) load(k0, k1, slice * kStep, h);
@@ -332,18 +352,6 @@ linear_w4_kernel(LinearArgs a) {
       if constexpr (!kRefill) {
 #pragma unroll
         for (int h = 0; h < kHalves; ++h) load(k0, k1, k, h);
-      }
-      // up to two columns, a step's MMAs sum from zero and are added with rounded FP32 additions:
-      // the tensor cores truncate, which a chain of 256 MMAs turns into a bias of 1e-6
-      constexpr bool kApart = NT <= 2;
-      float d[kApart ? kMt : 1][kApart ? NT : 1][4];
-      if constexpr (kApart) {
-#pragma unroll
-        for (int m = 0; m < kMt; ++m)
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) d[m][j][i] = 0.0f;
       }
 #pragma unroll
       for (int h = 0; h < kHalves; ++h) {
@@ -373,15 +381,9 @@ linear_w4_kernel(LinearArgs a) {
         }
         if constexpr (kRefill) load(k0, k1, k + a.ks * kStep, h);
       }
-      if constexpr (kApart) {
-#pragma unroll
-        for (int m = 0; m < kMt; ++m)
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) c[m][j][i] += d[m][j][i];
-      }
+      if (kApart && (++chain & 3) == 0) flush(true);
     }
+    flush(true);
     return odd;
   };
   // One sum to y: token 8 j + t8, row r16 of MMA tile m.

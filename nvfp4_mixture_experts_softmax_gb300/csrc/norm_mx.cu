@@ -162,12 +162,14 @@ __global__ void __launch_bounds__(512, J <= 2 ? 2 : 1) add_rmsnorm_mx_kernel(
 
 // A thread owns the same J vectors of 8 columns in all rows of its group and keeps their share of
 // dgamma in registers; the groups of a block are joined in order at the end, the blocks by
-// dgamma_kernel.  The next row's dy and h are loaded before the current row is reduced (kAhead).
-template <int J, bool kAhead>
-__global__ void __launch_bounds__(kAhead ? 512 : 1024, 1) add_rmsnorm_backward_kernel(
+// dgamma_kernel.  Up to two vectors the next row's dy, h and dh are loaded before the current row is
+// reduced (J = 1: 24 warps an SM, J = 2: 16); four vectors (above 8192 columns) fill the registers.
+template <int J>
+__global__ void __launch_bounds__(J == 1 ? 256 : 512, J == 1 ? 3 : 1) add_rmsnorm_backward_kernel(
     const uint4* dy, const uint4* dh, const uint4* __restrict__ h,
     const float* __restrict__ rrms, const uint4* __restrict__ gamma, int64_t rows, int cols, int W,
     int G, uint4* dx, float4* __restrict__ partial) {
+  constexpr bool kAhead = J <= 2;
   extern __shared__ float4 s_dg[];   // [cols / 4] if G > 1
   __shared__ float red[2 * 16 * 32];
   const int warp = threadIdx.x >> 5, group = warp / W, wrow = warp - group * W;
@@ -184,8 +186,22 @@ __global__ void __launch_bounds__(kAhead ? 512 : 1024, 1) add_rmsnorm_backward_k
     for (int i = 0; i < 8; ++i) dg[j][i] = 0.0f;
   int64_t row = (int64_t)blockIdx.x * G + group;
   const int64_t step = (int64_t)gridDim.x * G;
-  uint4 nd[J], nh[J], ne[J];
+  uint4 nd[J], nh[J], ne[J], ng[kAhead ? J : 1];
   float nr = 0.0f;
+  auto gamma_of = [&](int j) {
+    return j * span + t < nvec ? __ldg(gamma + j * span + t) : zero;
+  };
+  if constexpr (kAhead) {
+#pragma unroll
+    for (int j = 0; j < J; ++j) ng[j] = gamma_of(j);
+  }
+  auto load_dh = [&](int64_t rw) {
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int c = j * span + t;
+      ne[j] = rw < rows && c < nvec && dh ? dh[rw * nvec + c] : zero;
+    }
+  };
   auto load = [&](int64_t rw) {
     nr = rw < rows ? __ldg(rrms + rw) : 0.0f;
 #pragma unroll
@@ -194,47 +210,63 @@ __global__ void __launch_bounds__(kAhead ? 512 : 1024, 1) add_rmsnorm_backward_k
       const bool in = rw < rows && c < nvec;
       nd[j] = in ? dy[rw * nvec + c] : zero;
       nh[j] = in ? __ldg(h + rw * nvec + c) : zero;
-      ne[j] = in && dh ? dh[rw * nvec + c] : zero;
     }
+    if (kAhead) load_dh(rw);
   };
   if constexpr (kAhead) load(row);
   for (int parity = 0; row < rows; row += step, parity ^= 1) {
     if constexpr (!kAhead) load(row);
     const float r = nr;
     uint4 qd[J], qh[J], qe[J];
+    float a[kAhead ? J : 1][8];   // gamma dy, or computed again from qd
     float s = 0.0f;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const int c = j * span + t;
       qd[j] = nd[j];
       qh[j] = nh[j];
-      qe[j] = ne[j];
+      if (kAhead) qe[j] = ne[j];
       float d[8], hv[8], g[8];
       unpack8(qd[j], d);
       unpack8(qh[j], hv);
-      unpack8(c < nvec ? __ldg(gamma + c) : zero, g);
+      unpack8(kAhead ? ng[kAhead ? j : 0] : gamma_of(j), g);
+      const bool in = j * span + t < nvec;   // (an infinite 1/rms must not meet the zeros outside)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        s = fmaf(d[i] * g[i], hv[i], s);
-        if (c < nvec) dg[j][i] = fmaf(d[i], hv[i] * r, dg[j][i]);
+        const float ai = d[i] * g[i];
+        if constexpr (kAhead) a[j][i] = ai;
+        s = fmaf(ai, hv[i], s);
+        if (in) dg[j][i] = fmaf(d[i], hv[i] * r, dg[j][i]);
       }
     }
-    if constexpr (kAhead) load(row + step);
+    if constexpr (kAhead) {
+      load(row + step);
+    } else {   // dh is not part of the row's sum
+      load_dh(row);
+#pragma unroll
+      for (int j = 0; j < J; ++j) qe[j] = ne[j];
+    }
     s = row_sum(s, red, W, wrow, group, G, parity);
     const float m = r * r * (s * inv_cols);
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int c = j * span + t;
       if (c >= nvec) continue;
-      float d[8], hv[8], g[8], e[8], o[8];
-      unpack8(qd[j], d);
+      float hv[8], e[8], o[8];
       unpack8(qh[j], hv);
-      unpack8(__ldg(gamma + c), g);
       unpack8(qe[j], e);
+      if constexpr (kAhead) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        o[i] = r * fmaf(-hv[i], m, d[i] * g[i]);
-        if (dh) o[i] += e[i];
+        for (int i = 0; i < 8; ++i) o[i] = r * fmaf(-hv[i], m, a[j][i]);
+      } else {
+        float d[8], g[8];
+        unpack8(qd[j], d);
+        unpack8(gamma_of(j), g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = r * fmaf(-hv[i], m, d[i] * g[i]);
+      }
+      if (dh) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] += e[i];
       }
       dx[row * nvec + c] = pack8(o);
     }
@@ -308,10 +340,11 @@ RowGrid forward_grid(int64_t rows, int nvec) {
 
 RowGrid backward_grid(int64_t rows, int nvec) {
   RowGrid g;
-  g.J = nvec > 512 ? 2 : 1;
+  g.J = nvec > 1024 ? 4 : nvec > 256 ? 2 : 1;
   g.W = (nvec + 32 * g.J - 1) / (32 * g.J);
   g.G = std::max(1, 8 / g.W);
-  const int64_t need = (rows + g.G - 1) / g.G, most = (int64_t)num_sms() * std::max(1, 16 / (g.W * g.G));
+  const int64_t need = (rows + g.G - 1) / g.G;
+  const int64_t most = (int64_t)num_sms() * std::max(1, (g.J == 1 ? 24 : 16) / (g.W * g.G));
   g.blocks = (int)std::max<int64_t>(1, std::min(need, most));
   return g;
 }
@@ -371,10 +404,9 @@ int moe_add_rmsnorm_backward(const void* dy, const void* dh, const void* h, cons
     if (!is_aligned(p, 16)) return MOE_ERR_INVALID_ARG;
   if (!is_aligned(rrms, 4)) return MOE_ERR_INVALID_ARG;
   const RowGrid g = backward_grid(rows, (int)(cols / 8));
-  const bool ahead = g.W * g.G <= 16;
-  auto k = g.J == 1 ? add_rmsnorm_backward_kernel<1, true>
-           : ahead  ? add_rmsnorm_backward_kernel<2, true>
-                    : add_rmsnorm_backward_kernel<2, false>;
+  auto k = g.J == 1   ? add_rmsnorm_backward_kernel<1>
+           : g.J == 2 ? add_rmsnorm_backward_kernel<2>
+                      : add_rmsnorm_backward_kernel<4>;
   cudaError_t e = launch_pdl(
       k, dim3(g.blocks), dim3(g.W * g.G * 32), g.G > 1 ? sizeof(float) * (size_t)cols : 0, s,
       static_cast<const uint4*>(dy), static_cast<const uint4*>(dh), static_cast<const uint4*>(h),
