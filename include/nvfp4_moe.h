@@ -286,7 +286,7 @@ int moe_plan(const float* logits, int32_t T, int32_t E, int32_t k, int32_t* topk
  * chosen logits, or s / sum of the k chosen s), NULL: none.  dlogits [T,E] is overwritten; tokens
  * that do not count get zeros; ids outside [0, E) are left out; an id that stands twice gets both
  * shares.
- * 1 <= E <= 1024, 1 <= k <= min(E, 32); FP32 pointers 4-byte aligned.
+ * 1 <= E <= 1024, 1 <= k <= min(E, 32), T * k < 2^31; FP32 pointers 4-byte aligned.
  * ------------------------------------------------------------------------------------------- */
 size_t moe_router_loss_workspace_size(int32_t T, int32_t E);
 int moe_router_loss(const float* logits, const int32_t* topk_ids, const uint8_t* mask, int32_t T,

@@ -9,28 +9,33 @@
 //
 // For few tokens the bound is the instruction stream of the decoding next to HBM: at the copy rate
 // an SM has 22 issue slots for 8 codes.  The conversion of two E2M1 codes to F16 is one
-// instruction (measured 27 T codes/s over the GPU, placing the bits of a BF16 by hand 13.7, HBM
+// instruction (measured 27 T codes/s over the GPU; placing the bits of a BF16 by hand 13.7; HBM
 // delivers 13.4), so weights and x are F16:
 //   * an E2M1 value times an E4M3 scale is exact in F16 (at most 6 significant bits, 2^-10 to
 //     2688).  So is one times an E8M0 scale of 2^-23 .. 2^13; a tile that meets another scale is
 //     done again with each row's largest scale at 2^13: scales below 2^-36 of the row's largest
 //     become zero;
-//   * a row of x is multiplied by a power of two, 2^6 if its largest element is in [2^-6, 2^10),
-//     otherwise the one that brings it to [2^15, 2^16) (one more pass over x): elements down to
-//     2^-32 of the largest keep all of BF16's bits, smaller ones are rounded to a multiple of
-//     2^-30 (or 2^-39 of the largest), an error of at most half of that times sum |w| in a sum whose FP32
-//     roundings are of 2^-24 of its terms.
-// From 32 tokens on the MMAs are the bound (two cycles each on an SM's four tensor cores).
+//   * a row of x is multiplied by a power of two: 2^6 if its largest element is in [2^-6, 2^10),
+//     otherwise the one that brings it to [2^15, 2^16) (one more pass over x).  Elements down to
+//     2^-32 of the F16 top keep all of BF16's bits; smaller ones are rounded to a multiple of
+//     2^-30 (2^-39 of the row's largest in the second case).  Half of that times sum |w| is below
+//     the roundings of an FP32 sum of the row's terms, 2^-24 of each.
+// From 32 tokens on the MMAs weigh most (two cycles each on an SM's four tensor cores: 14 us for
+// 18432 x 7168 at 32 tokens, 27 us at 64).
 //
 // K is split twice: over the blocks of a cluster, so that a block can keep its share of x in
 // shared memory, and over ks warps of a block.  A group of ks warps works on a tile of kMt * 16
 // weight rows; the partial sums are joined through (distributed) shared memory in a fixed order.
+//
+// Measured (device time of a call, inputs larger than L2 where the weights are): 131072 x 4096
+// NVFP4, 1 token 63.9 us (4.7 TB/s; a pure read of HBM reaches 5.8), 16 tokens 83 us; 18431 x 7168
+// MXFP4, 15 tokens 26 us; 18432 x 7168 NVFP4, 1 / 32 / 64 tokens 19.4 / 40.6 / 84 us; 2048 x 2048, 1
+// token 4.5 us.  A block of 16 rows whose eight warps read x from L1 in BF16, without staging, took
+// 77.6, 166, 39.6, 22.2 / 77 / 138 and 2.8 us.
 #include <algorithm>
-#include <climits>
-#include <type_traits>
 
+#include "common.cuh"
 #include "ops.h"
-#include "w4.cuh"
 
 namespace nvfp4moe {
 
@@ -395,6 +400,7 @@ linear_w4_kernel(LinearArgs a) {
     else static_cast<__nv_bfloat16*>(a.y)[(int64_t)t * a.N + n] = __float2bfloat16_rn(v);
   };
   auto all = [&]() {   // the threads that join a tile
+    __syncwarp();
     if (a.cluster > 1) cluster_sync();
     else if (a.ks == kWarps) __syncthreads();
     else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(a.ks * 32) : "memory");
@@ -424,7 +430,7 @@ linear_w4_kernel(LinearArgs a) {
 #pragma unroll 1
       for (int chunk = 0; chunk < chunks; ++chunk) {
         const int k0 = kb + chunk * a.kc;
-        if (chunks > 1) {
+        if (chunks > 1 && (it > 0 || attempt > 0 || chunk > 0)) {   // (the first is there)
           __syncthreads();
           stage_x<kFly, kWarps>(a.x, a.T, a.K, k0, a.kc, ke, xs, s_shift, s_top);
           __syncthreads();

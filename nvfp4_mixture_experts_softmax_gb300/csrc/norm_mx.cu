@@ -9,6 +9,13 @@
 // Backward, with a = gamma * dy:  dx = dh + r * a - h * r^3 * mean(a * h)  (the gradient of x and
 // of the residual alike),  dgamma_c = sum over rows of dy * (h * r).  The quantisation is passed
 // straight through: dy is the gradient of y.
+//
+// Both are bound by HBM: every element is read and written once (7.03 bytes an element forward, 9.03
+// with y; 6 or 8 backward).  Measured (device time of a call): forward 16384 x 4096 74.6 us = 93% of
+// the copy rate, 4096 x 7168 with y 46.9 us (84%), 20000 x 256 9.3 us (74%), 1 x 2048 1.9 us;
+// backward 8192 x 2048 with dh 27.8 us (71%), 1999 x 7168 22.2 us (57%), 3906 x 16384 118 us
+// (64%).  One block per row, reduced before the next row's loads, took 108, 53.9, 20.6, 2.0 us and
+// 50, 33, 134 us.
 #include <algorithm>
 #include <cmath>
 

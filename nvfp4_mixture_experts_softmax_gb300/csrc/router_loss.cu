@@ -18,6 +18,11 @@
 // G lanes of a warp hold one token's row in registers (VPL logits each), so a warp takes 32 / G
 // tokens at a time and each row is read once; the next row's loads are issued before the current
 // one is reduced.
+// Bound by HBM for softmax and many tokens (the logits once, in the backward pass the gradient once),
+// by the instruction stream for the sqrt-softplus router (26 instructions a score), by launches and
+// the join for small batches.  Measured (device time of a call): losses 131072 x 256 30.4 us (67% of
+// the copy rate; sqrt-softplus 43.6), 8192 x 256 8.4 us, 64 x 128 3.3 us; gradient 131072 x 256 54 us
+// (75%; sqrt-softplus 68), 100003 x 60 14.4 us, 8192 x 256 sqrt-softplus 6.7 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -653,6 +658,7 @@ int check_loss(int32_t T, int32_t E, int32_t k, uint32_t flags) {
   if (T < 0 || E < 1 || k < 1 || k > E) return MOE_ERR_INVALID_ARG;
   if (flags & ~MOE_FLAG_ROUTER_SQRTSOFTPLUS) return MOE_ERR_INVALID_ARG;
   if (E > 1024 || k > 32) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if ((int64_t)T * k > INT32_MAX) return MOE_ERR_UNSUPPORTED_SHAPE;   // counts are 32 bits
   return MOE_OK;
 }
 

@@ -43,7 +43,7 @@ def test_norm_backward_rejections(moe, kw, want):
 
 @pytest.mark.parametrize("kw,want", [
     (dict(T=-1), -1), (dict(E=0), -1), (dict(k=0), -1), (dict(k=9), -1), (dict(E=1025, k=8), -2), (dict(E=64, k=33), -2),
-    (dict(flags=2), -1), (dict(losses=None), -1), (dict(counts=None), -1), (dict(tokens=None), -1), (dict(probs=None), -1),
+    (dict(T=1 << 30, k=2), -2), (dict(flags=2), -1), (dict(losses=None), -1), (dict(counts=None), -1), (dict(tokens=None), -1), (dict(probs=None), -1),
     (dict(ws=None), -3), (dict(n=64), -3), (dict(ws=P + 16), -1), (dict(logits=None), -1), (dict(ids=None), -1),
     (dict(logits=P + 2), -1), (dict(ids=P + 2), -1), (dict(losses=P + 1), -1)])
 def test_loss_rejections(moe, kw, want):
@@ -54,7 +54,8 @@ def test_loss_rejections(moe, kw, want):
 
 
 @pytest.mark.parametrize("kw,want", [
-    (dict(T=0), 0), (dict(T=-1), -1), (dict(k=9), -1), (dict(E=1025), -2), (dict(flags=4), -1), (dict(logits=None), -1),
+    (dict(T=0), 0), (dict(T=-1), -1), (dict(k=9), -1), (dict(E=1025), -2), (dict(T=1 << 30, k=2), -2), (dict(flags=4), -1),
+    (dict(logits=None), -1),
     (dict(counts=None), -1), (dict(tokens=None), -1), (dict(dl=None), -1), (dict(ids=None, gw=P), -1), (dict(gw=P + 2), -1),
     (dict(gl=P + 1), -1), (dict(dl=P + 2), -1)])
 def test_loss_backward_rejections(moe, kw, want):
