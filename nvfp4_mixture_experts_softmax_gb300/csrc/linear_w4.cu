@@ -163,12 +163,12 @@ struct LinearArgs {
 // (u = 4 q + i) sits at i * 64 + q * 16, so that a quad's loads of one i are 64 consecutive bytes;
 // rows are 64 bytes off a multiple of 128, so two rows fill all banks.  Not inlined: the kernel's
 // registers are the multiplication's.
-template <int kFly, int kWarps>
+template <int kFly>
 __device__ __noinline__ void stage_x(const uint16_t* x, int T, int K, int k0, int kc, int ke,
                                      uint8_t* xs, const int* shift, uint32_t* top) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int units = kc / 8, per = (units + kFly * 32 - 1) / (kFly * 32), stride = kc * 2 + 64;
-  for (int v = warp; v < T * per; v += kWarps) {
+  for (int v = warp; v < T * per; v += warps) {
     const int t = v / per, u0 = (v - t * per) * (kFly * 32) + lane;
     const uint4* src = reinterpret_cast<const uint4*>(x + (int64_t)t * K + k0);
     uint4 d[kFly];
@@ -200,10 +200,9 @@ __device__ __noinline__ void stage_x(const uint16_t* x, int T, int K, int k0, in
 }
 
 // The largest finite exponent of each row of x over all of K, as the shift that brings it to 15.
-template <int kWarps>
 __device__ __noinline__ void find_shifts(const uint16_t* x, int T, int K, int* shift) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int t = warp; t < T; t += kWarps) {
+  for (int t = warp; t < T; t += blockDim.x >> 5) {
     const uint4* row = reinterpret_cast<const uint4*>(x + (int64_t)t * K);
     uint32_t hi = 0u;
 #pragma unroll 4
@@ -236,7 +235,7 @@ template <int NT, bool kMx, bool kF32>
 __global__ void __launch_bounds__(LinTile<NT>::kThreads, LinTile<NT>::kPerSm)
 linear_w4_kernel(LinearArgs a) {
   using L = LinTile<NT>;
-  constexpr int kMt = L::kMt, kHalves = L::kHalves, kStep = L::kStep, kWarps = L::kWarps;
+  constexpr int kMt = L::kMt, kHalves = L::kHalves, kStep = L::kStep;
   constexpr int kBlk = kMx ? 32 : 16;
   constexpr bool kRefill = NT > 1;   // load a part of the next step as soon as this one's is used up
   extern __shared__ __align__(16) uint8_t smem[];
@@ -245,7 +244,8 @@ linear_w4_kernel(LinearArgs a) {
   __shared__ float2 s_unscale[kLinMaxTokens];   // takes a row's sums to y, in two factors
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, q = lane & 3;
-  const int slice = warp % a.ks, group = warp / a.ks, groups = kWarps / a.ks;
+  const int warps = blockDim.x >> 5;
+  const int slice = warp % a.ks, group = warp / a.ks, groups = warps / a.ks;
   const int rank = (int)blockIdx.x % a.cluster, col = (int)blockIdx.x / a.cluster;
   const int cols = (int)gridDim.x / a.cluster;
   const int stride = a.kc * 2 + 64;
@@ -255,17 +255,9 @@ linear_w4_kernel(LinearArgs a) {
   const int64_t tiles = (a.N + L::kRows - 1) / L::kRows;
   const int64_t tile0 = (int64_t)col * groups + group;   // this group's first tile
   const int kb = rank * a.kslice, ke = min(a.K, kb + a.kslice);   // this block's columns
-  if (threadIdx.x < kLinMaxTokens) {
-    s_shift[threadIdx.x] = 15 - kTopGuess;
-    s_top[threadIdx.x] = 0u;
-  }
-  {
-    // the first step's codes (and scales) on their way into L2 while the previous kernel ends and x
-    // is staged; a prefetch reads nothing, so it need not wait for that kernel
-    const int64_t row = min(tile0 * L::kRows + lane % L::kRows, a.N - 1);
-    const int64_t k = kb + min(slice * kStep, ke - kb - 32);
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.codes + row * (a.K / 2) + k / 2));
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.sf + row * (a.K / kBlk) + k / kBlk));
+  for (int t = threadIdx.x; t < kLinMaxTokens; t += blockDim.x) {   // (blocks of one warp exist)
+    s_shift[t] = 15 - kTopGuess;
+    s_top[t] = 0u;
   }
   __syncthreads();
   griddep_wait();
@@ -277,27 +269,28 @@ linear_w4_kernel(LinearArgs a) {
   constexpr int kFly = NT == 1 ? 4 : 8;
   for (int attempt = 0;; ++attempt) {
     for (int chunk = chunks - 1; chunk >= 0; --chunk)
-      stage_x<kFly, kWarps>(a.x, a.T, a.K, kb + chunk * a.kc, a.kc, ke, xs, s_shift, s_top);
+      stage_x<kFly>(a.x, a.T, a.K, kb + chunk * a.kc, a.kc, ke, xs, s_shift, s_top);
     __syncthreads();
     if (attempt == 1) break;
     if (a.cluster > 1) cluster_sync();
     bool fits = true;
-    if ((int)threadIdx.x < a.T) {
-      uint32_t top = s_top[threadIdx.x];
+    for (int t = threadIdx.x; t < a.T; t += blockDim.x) {
+      uint32_t top = s_top[t];
       if (a.cluster > 1)
-        for (int b = 0; b < a.cluster; ++b) top = max(top, ld_dsmem_u32(s_top + threadIdx.x, b));
-      fits = top == 0u || (top >= (uint32_t)(kTopLeast + 127) << 7 && top < (uint32_t)(kTopGuess + 128) << 7);
+        for (int b = 0; b < a.cluster; ++b) top = max(top, ld_dsmem_u32(s_top + t, b));
+      fits = fits && (top == 0u || (top >= (uint32_t)(kTopLeast + 127) << 7 &&
+                                    top < (uint32_t)(kTopGuess + 128) << 7));
     }
     fits = __syncthreads_and(fits);
     if (a.cluster > 1) cluster_sync();   // (the others have read this block's maxima)
     if (fits) break;
-    find_shifts<kWarps>(a.x, a.T, a.K, s_shift);
+    find_shifts(a.x, a.T, a.K, s_shift);
     __syncthreads();
   }
-  if (threadIdx.x < kLinMaxTokens) {   // half of the power of two on either side of the tensor scale
-    float2 u = pow2_factors(-s_shift[threadIdx.x]);
+  for (int t = threadIdx.x; t < kLinMaxTokens; t += blockDim.x) {
+    float2 u = pow2_factors(-s_shift[t]);   // half on either side of the tensor scale
     if constexpr (!kMx) u.y *= __ldg(a.ts);
-    s_unscale[threadIdx.x] = u;
+    s_unscale[t] = u;
   }
   __syncthreads();
 
@@ -402,7 +395,7 @@ linear_w4_kernel(LinearArgs a) {
   auto all = [&]() {   // the threads that join a tile
     __syncwarp();
     if (a.cluster > 1) cluster_sync();
-    else if (a.ks == kWarps) __syncthreads();
+    else if (a.ks == warps) __syncthreads();
     else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(a.ks * 32) : "memory");
   };
 
@@ -432,7 +425,7 @@ linear_w4_kernel(LinearArgs a) {
         const int k0 = kb + chunk * a.kc;
         if (chunks > 1 && (it > 0 || attempt > 0 || chunk > 0)) {   // (the first is there)
           __syncthreads();
-          stage_x<kFly, kWarps>(a.x, a.T, a.K, k0, a.kc, ke, xs, s_shift, s_top);
+          stage_x<kFly>(a.x, a.T, a.K, k0, a.kc, ke, xs, s_shift, s_top);
           __syncthreads();
         }
         if (tile < tiles) odd = sweep(k0, min(ke, k0 + a.kc)) || odd;
@@ -484,7 +477,7 @@ linear_w4_kernel(LinearArgs a) {
 #pragma unroll
       for (int f = 0; f < L::kJoin; ++f) {
         const float* v = c[(f0 + f) % kMt][(f0 + f) / kMt];
-        float4* slot = join + ((rank * kWarps + warp) * per + f / a.cluster) * 32 + lane;
+        float4* slot = join + ((rank * warps + warp) * per + f / a.cluster) * 32 + lane;
         if (a.cluster > 1) st_dsmem_float4(slot, f % a.cluster, v);
         else *slot = make_float4(v[0], v[1], v[2], v[3]);
       }
@@ -499,7 +492,7 @@ linear_w4_kernel(LinearArgs a) {
         float sum = 0.0f;
         for (int b = 0; b < a.cluster; ++b)
 #pragma unroll 4
-          for (int w = 0; w < a.ks; ++w) sum += at[(b * kWarps + w) * per * 128];
+          for (int w = 0; w < a.ks; ++w) sum += at[(b * warps + w) * per * 128];
         const int f = f0 + fl * a.cluster + rank;
         if (tile < tiles) store(tile, f % kMt, f / kMt, t, r, sum);
       }
@@ -534,36 +527,41 @@ cudaError_t launch_linear(LinearArgs a, cudaStream_t s) {
   auto clusters = [](int cl) {
     return cl == 8 ? num_sms() / 10 : num_sms() / cl - (cl == 4 ? 2 : 0);
   };
-  // The split of K over cluster blocks and warps that should finish first.
+  // The split of K over cluster blocks and warps, and the blocks an SM, that should finish first.
   double best = 0.0;
-  int cols = 1;
-  for (int cl = 1; cl <= 8 && cl <= L::kFrags && cl <= steps; cl *= 2) {
-    const int64_t sl = (steps + cl - 1) / cl;
+  int cols = 1, warps_used = 1;
+  auto consider = [&](int cl, int ks, int blocks) {
+    const bool joins = ks > 1 || cl > 1;
+    const int64_t sl = (steps + cl - 1) / cl, groups = L::kWarps / ks;
+    const int64_t slots = (int64_t)blocks * clusters(cl);
+    const int64_t rounds = (tiles + groups * slots - 1) / (groups * slots);
+    // no more groups a block than these rounds need: the tiles spread over the SMs
+    const int64_t even = (tiles + slots * rounds - 1) / (slots * rounds);
+    const int64_t busy = (tiles + even * rounds - 1) / (even * rounds);
+    const bool fits = fitting(joins, blocks) >= sl * L::kStep;
+    if (!fits && blocks > 1) return;
+    const double warps = (double)(busy * cl * even * ks) / num_sms();
+    double stage = (double)a.T * sl * L::kStep / 16000.0 * (busy > clusters(cl) ? blocks : 1);
+    if (!fits) stage *= 1 + rounds;
+    const double cost = stage + (cl > 1 ? 1.5 : 0.0) +
+                        rounds * ((double)((sl + ks - 1) / ks) *
+                                      std::max(C::kStepUs[0], C::kStepUs[1] * warps) +
+                                  (cl > 1 ? C::kJoinUs[1] : ks > 1 ? C::kJoinUs[0] : 0.0));
+    if (best != 0.0 && cost >= best) return;
+    best = cost;
+    a.ks = ks;
+    a.cluster = cl;
+    a.iters = (int)rounds;
+    a.kslice = (int)sl * L::kStep;
+    a.kc = std::min(a.kslice, fitting(joins, blocks));
+    cols = (int)busy;
+    warps_used = (int)even * ks;
+  };
+  for (int cl = 1; cl <= 8 && cl <= L::kFrags && cl <= steps; cl *= 2)
     for (int ks = 1; ks <= L::kWarps; ks *= 2) {
-      const int64_t groups = L::kWarps / ks, need = (tiles + groups - 1) / groups;
-      if (ks > 1 && groups > 15) continue;   // a named barrier for each group
-      const bool joins = ks > 1 || cl > 1;
-      const int blocks = fitting(joins, L::kPerSm) >= sl * L::kStep ? L::kPerSm : 1;
-      const int64_t slots = (int64_t)blocks * clusters(cl), busy = std::min(need, slots);
-      const int64_t rounds = (need + slots - 1) / slots;
-      const double warps = (double)(busy * cl * L::kWarps) / num_sms();
-      double stage = (double)a.T * sl * L::kStep / 16000.0 * (busy > clusters(cl) ? blocks : 1);
-      if (fitting(joins, blocks) < sl * L::kStep) stage *= 1 + rounds;
-      const double cost = stage + (cl > 1 ? 1.5 : 0.0) +
-                          rounds * ((double)((sl + ks - 1) / ks) *
-                                        std::max(C::kStepUs[0], C::kStepUs[1] * warps) +
-                                    (cl > 1 ? C::kJoinUs[1] : ks > 1 ? C::kJoinUs[0] : 0.0));
-      if (best == 0.0 || cost < best) {
-        best = cost;
-        a.ks = ks;
-        a.cluster = cl;
-        cols = (int)busy;
-        a.iters = (int)rounds;
-        a.kslice = (int)sl * L::kStep;
-        a.kc = std::min(a.kslice, fitting(joins, blocks));
-      }
+      if (ks > 1 && L::kWarps / ks > 15) continue;   // a named barrier for each group
+      for (int blocks = 1; blocks <= L::kPerSm; ++blocks) consider(cl, ks, blocks);
     }
-  }
   const size_t smem = (size_t)rows * (a.kc * 2 + 64) +
                       (a.ks > 1 || a.cluster > 1 ? L::kJoinBytes : 0);
   if (smem > 40 * 1024) {
@@ -573,7 +571,7 @@ cudaError_t launch_linear(LinearArgs a, cudaStream_t s) {
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(cols * a.cluster));
-  cfg.blockDim = dim3(L::kThreads);
+  cfg.blockDim = dim3((unsigned)warps_used * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];

@@ -1,5 +1,5 @@
-// Launchers of the operators around the layer (norm_mx.cu, router_loss.cu, linear_w4.cu) and of
-// the W4A8 layer's entry for already quantised activations.
+// What the operators around the layer (norm_mx.cu, router_loss.cu, linear_w4.cu) share, and the
+// launcher of the W4A8 layer's entry for already quantised activations.
 #pragma once
 #include "internal.h"
 
