@@ -27,11 +27,10 @@
 // shared memory, and over ks warps of a block.  A group of ks warps works on a tile of kMt * 16
 // weight rows; the partial sums are joined through (distributed) shared memory in a fixed order.
 //
-// Measured (device time of a call, inputs larger than L2 where the weights are): 131072 x 4096
-// NVFP4, 1 token 63.9 us (4.7 TB/s; a pure read of HBM reaches 5.8), 16 tokens 83 us; 18431 x 7168
-// MXFP4, 15 tokens 26 us; 18432 x 7168 NVFP4, 1 / 32 / 64 tokens 19.4 / 40.6 / 84 us; 2048 x 2048, 1
-// token 4.5 us.  A block of 16 rows whose eight warps read x from L1 in BF16, without staging, took
-// 77.6, 166, 39.6, 22.2 / 77 / 138 and 2.8 us.
+// Measured (device time of a call): 131072 x 4096 NVFP4, 1 token 60 us (5.0 TB/s; a pure read of HBM
+// reaches 5.8), 16 tokens 80 us; 18431 x 7168 MXFP4, 15 tokens 26 us; 18432 x 7168 NVFP4, 1 / 32 / 64
+// tokens 19.5 / 41 / 86 us; 2048 x 2048, 1 token 4.0 us.  A block of 16 rows whose eight warps read x
+// from L1 in BF16, without staging, took 77.6, 166, 39.6, 22.2 / 77 / 138 and 2.8 us.
 #include <algorithm>
 
 #include "common.cuh"
@@ -58,6 +57,7 @@ struct LinTile {
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kRows = kMt * 16;
   static constexpr int kHalves = NT <= 4 ? 2 : 1;    // 128-column parts of a step
+  static constexpr int kFly = NT == 1 ? 4 : 8;       // loads of x in flight in a lane
   static constexpr int kStep = kHalves * 128;        // columns of a step
   // join buffer: kJoin of a warp's kMt * NT accumulator fragments at a time
   static constexpr int kFrags = kMt * NT;
@@ -150,6 +150,7 @@ struct LinearArgs {
   int64_t N;
   int K;
   void* y;
+  int warps;    // warps of a block that multiply; further ones only bring x into shared memory
   int ks;       // warps that split a tile's steps
   int cluster;  // blocks that split K
   int kslice;   // columns of a block, a multiple of the step
@@ -244,8 +245,7 @@ linear_w4_kernel(LinearArgs a) {
   __shared__ float2 s_unscale[kLinMaxTokens];   // takes a row's sums to y, in two factors
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, q = lane & 3;
-  const int warps = blockDim.x >> 5;
-  const int slice = warp % a.ks, group = warp / a.ks, groups = warps / a.ks;
+  const int slice = warp % a.ks, group = warp / a.ks, groups = a.warps / a.ks;
   const int rank = (int)blockIdx.x % a.cluster, col = (int)blockIdx.x / a.cluster;
   const int cols = (int)gridDim.x / a.cluster;
   const int stride = a.kc * 2 + 64;
@@ -266,10 +266,9 @@ linear_w4_kernel(LinearArgs a) {
   // x at the first scale; if a row's largest element (anywhere in the cluster's blocks) does not
   // fit it, at the rows' own.  x that is too long for shared memory is staged again by chunks.
   const int chunks = (a.kslice + a.kc - 1) / a.kc;
-  constexpr int kFly = NT == 1 ? 4 : 8;
   for (int attempt = 0;; ++attempt) {
     for (int chunk = chunks - 1; chunk >= 0; --chunk)
-      stage_x<kFly>(a.x, a.T, a.K, kb + chunk * a.kc, a.kc, ke, xs, s_shift, s_top);
+      stage_x<L::kFly>(a.x, a.T, a.K, kb + chunk * a.kc, a.kc, ke, xs, s_shift, s_top);
     __syncthreads();
     if (attempt == 1) break;
     if (a.cluster > 1) cluster_sync();
@@ -392,15 +391,17 @@ linear_w4_kernel(LinearArgs a) {
     if constexpr (kF32) static_cast<float*>(a.y)[(int64_t)t * a.N + n] = v;
     else static_cast<__nv_bfloat16*>(a.y)[(int64_t)t * a.N + n] = __float2bfloat16_rn(v);
   };
+  // One column: no clusters, and further warps only if x is staged once, so they are done.
+  if (NT == 1 && warp >= a.warps) return;
+  const bool active = NT == 1 || warp < a.warps;
   auto all = [&]() {   // the threads that join a tile
     __syncwarp();
     if (a.cluster > 1) cluster_sync();
-    else if (a.ks == warps) __syncthreads();
-    else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(a.ks * 32) : "memory");
+    else if (active) asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(a.ks * 32) : "memory");
   };
 
   for (int it = 0; it < a.iters; ++it) {
-    const int64_t tile = tile0 + (int64_t)it * cols * groups;
+    const int64_t tile = active ? tile0 + (int64_t)it * cols * groups : tiles;
     {
       const int64_t row = min(tile * L::kRows + g, a.N - 1);
       pc = a.codes + row * (a.K / 2);
@@ -425,7 +426,7 @@ linear_w4_kernel(LinearArgs a) {
         const int k0 = kb + chunk * a.kc;
         if (chunks > 1 && (it > 0 || attempt > 0 || chunk > 0)) {   // (the first is there)
           __syncthreads();
-          stage_x<kFly>(a.x, a.T, a.K, k0, a.kc, ke, xs, s_shift, s_top);
+          stage_x<L::kFly>(a.x, a.T, a.K, k0, a.kc, ke, xs, s_shift, s_top);
           __syncthreads();
         }
         if (tile < tiles) odd = sweep(k0, min(ke, k0 + a.kc)) || odd;
@@ -476,8 +477,9 @@ linear_w4_kernel(LinearArgs a) {
       const int per = L::kJoin / a.cluster;
 #pragma unroll
       for (int f = 0; f < L::kJoin; ++f) {
+        if (!active) break;
         const float* v = c[(f0 + f) % kMt][(f0 + f) / kMt];
-        float4* slot = join + ((rank * warps + warp) * per + f / a.cluster) * 32 + lane;
+        float4* slot = join + ((rank * a.warps + warp) * per + f / a.cluster) * 32 + lane;
         if (a.cluster > 1) st_dsmem_float4(slot, f % a.cluster, v);
         else *slot = make_float4(v[0], v[1], v[2], v[3]);
       }
@@ -486,13 +488,13 @@ linear_w4_kernel(LinearArgs a) {
       // then warps in order.  Row r, token t of a fragment: lane (r % 8) * 4 + t / 2, register
       // (r / 8) * 2 + t % 2
       const float* base = reinterpret_cast<const float*>(join + group * a.ks * per * 32);
-      for (int e = slice * 32 + lane; e < per * 128; e += a.ks * 32) {
+      for (int e = slice * 32 + lane; active && e < per * 128; e += a.ks * 32) {
         const int r = e & 15, t = (e >> 4) & 7, fl = e >> 7;
         const float* at = base + fl * 128 + (r & 7) * 16 + (t >> 1) * 4 + (r >> 3) * 2 + (t & 1);
         float sum = 0.0f;
         for (int b = 0; b < a.cluster; ++b)
 #pragma unroll 4
-          for (int w = 0; w < a.ks; ++w) sum += at[(b * warps + w) * per * 128];
+          for (int w = 0; w < a.ks; ++w) sum += at[(b * a.warps + w) * per * 128];
         const int f = f0 + fl * a.cluster + rank;
         if (tile < tiles) store(tile, f % kMt, f / kMt, t, r, sum);
       }
@@ -529,7 +531,7 @@ cudaError_t launch_linear(LinearArgs a, cudaStream_t s) {
   };
   // The split of K over cluster blocks and warps, and the blocks an SM, that should finish first.
   double best = 0.0;
-  int cols = 1, warps_used = 1;
+  int cols = 1;
   auto consider = [&](int cl, int ks, int blocks) {
     const bool joins = ks > 1 || cl > 1;
     const int64_t sl = (steps + cl - 1) / cl, groups = L::kWarps / ks;
@@ -555,7 +557,7 @@ cudaError_t launch_linear(LinearArgs a, cudaStream_t s) {
     a.kslice = (int)sl * L::kStep;
     a.kc = std::min(a.kslice, fitting(joins, blocks));
     cols = (int)busy;
-    warps_used = (int)even * ks;
+    a.warps = (int)even * ks;
   };
   for (int cl = 1; cl <= 8 && cl <= L::kFrags && cl <= steps; cl *= 2)
     for (int ks = 1; ks <= L::kWarps; ks *= 2) {
@@ -571,7 +573,10 @@ cudaError_t launch_linear(LinearArgs a, cudaStream_t s) {
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(cols * a.cluster));
-  cfg.blockDim = dim3((unsigned)warps_used * 32);
+  // a warp for each of a row's visits of stage_x, up to the block's size
+  // (one column: only if it is staged once)
+  const int visits = NT == 1 && a.kc < a.kslice ? 1 : a.T * ((a.kc / 8 + L::kFly * 32 - 1) / (L::kFly * 32));
+  cfg.blockDim = dim3((unsigned)std::max(a.warps, std::min(visits, L::kWarps)) * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
