@@ -21,8 +21,8 @@
 // Bound by HBM for softmax and many tokens (the logits once, in the backward pass the gradient once),
 // by the instruction stream for the sqrt-softplus router (26 instructions a score), by launches and
 // the join for small batches.  Measured (device time of a call): losses 131072 x 256 30.4 us (67% of
-// the copy rate; sqrt-softplus 43.6), 8192 x 256 8.4 us, 64 x 128 3.3 us; gradient 131072 x 256 54 us
-// (75%; sqrt-softplus 68), 100003 x 60 14.4 us, 8192 x 256 sqrt-softplus 6.7 us.
+// the copy rate; sqrt-softplus 43.6), 8192 x 256 8.4 us, 64 x 128 3.3 us; gradient 131072 x 256 48 us
+// (85%; sqrt-softplus 68), 100003 x 60 13.9 us, 8192 x 256 sqrt-softplus 6.7 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -432,10 +432,14 @@ struct LossBwdArgs {
 
 constexpr int kBwdThreads = 256;
 constexpr int kBwdWarps = kBwdThreads / 32;
-constexpr int kBwdBlocks = 2;   // per SM: 128 registers a thread
+// Blocks per SM: 80 registers a thread hold a softmax row of up to 16 logits a lane and its successor,
+// 128 the slopes of the sqrt-softplus scores as well, or 32 logits.  (131072 x 256 softmax: 2, 3
+// blocks 54.5, 48.6 us; sqrt-softplus 68.0, 69.1; 32000 x 1021: 71, 89.)
+template <int VPL, bool SQRTSP>
+constexpr int bwd_blocks() { return VPL <= 16 && !SQRTSP ? 3 : 2; }
 
 template <int G, int VPL, int VEC, bool SQRTSP>
-__global__ void __launch_bounds__(kBwdThreads, kBwdBlocks)
+__global__ void __launch_bounds__(kBwdThreads, (bwd_blocks<VPL, SQRTSP>()))
 router_loss_backward_kernel(LossBwdArgs a) {
   extern __shared__ float dyn[];
   constexpr int R = 32 / G;
@@ -770,7 +774,7 @@ int moe_router_loss_backward(const float* logits, const int32_t* topk_ids, const
     auto kern = sp ? router_loss_backward_kernel<G, VPL, VEC, true>
                    : router_loss_backward_kernel<G, VPL, VEC, false>;
     constexpr int rows = kBwdWarps * (32 / G), width = G * VPL;
-    const int64_t most = (int64_t)kBwdBlocks * num_sms();
+    const int64_t most = (int64_t)(sp ? bwd_blocks<VPL, true>() : bwd_blocks<VPL, false>()) * num_sms();
     const int nb = (int)std::min<int64_t>(((int64_t)T + rows - 1) / rows, most);
     return launch_pdl(kern, dim3(nb), dim3(kBwdThreads), 4 * (size_t)width * (1 + rows),
                       reinterpret_cast<cudaStream_t>(stream), a);
