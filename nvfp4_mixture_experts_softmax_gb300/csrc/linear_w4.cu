@@ -20,8 +20,8 @@
 //     2^-32 of the F16 top keep all of BF16's bits; smaller ones are rounded to a multiple of
 //     2^-30 (2^-39 of the row's largest in the second case).  Half of that times sum |w| is below
 //     the roundings of an FP32 sum of the row's terms, 2^-24 of each.
-// From 32 tokens on the MMAs weigh most (two cycles each on an SM's four tensor cores: 14 us for
-// 18432 x 7168 at 32 tokens, 27 us at 64).
+// With more tokens the MMAs weigh most (two cycles each on an SM's four tensor cores: 14 us for
+// 18432 x 7168 at 32 tokens), so from 17 on linear_w4_tc.cu takes over.
 //
 // K is split twice: over the blocks of a cluster, so that a block can keep its share of x in
 // shared memory, and over ks warps of a block.  A group of ks warps works on a tile of kMt * 16
@@ -41,6 +41,7 @@ namespace nvfp4moe {
 namespace {
 
 constexpr int kLinMaxTokens = 64;
+constexpr int kLinTcTokens = 17;     // rows of x from which linear_w4_tc.cu is faster
 constexpr int kTopGuess = 9;         // exponent of a row's largest element: the first scale's
 constexpr int kTopLeast = -6;        // bounds
 
@@ -625,7 +626,9 @@ extern "C" int moe_linear_w4(const void* x, const uint8_t* codes, const uint8_t*
   a.K = (int)K;
   a.y = y;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = T <= 8    ? launch_linear<1>(a, mx, f32, s)
+  const cudaError_t e = T >= kLinTcTokens
+                            ? launch_linear_w4_tc(x, codes, sf, ts, T, N, (int)K, f32, y, s)
+                        : T <= 8  ? launch_linear<1>(a, mx, f32, s)
                         : T <= 16 ? launch_linear<2>(a, mx, f32, s)
                         : T <= 32 ? launch_linear<4>(a, mx, f32, s)
                                   : launch_linear<8>(a, mx, f32, s);

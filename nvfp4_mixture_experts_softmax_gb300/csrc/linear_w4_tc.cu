@@ -1,0 +1,504 @@
+// 4-bit matrix-vector product for 17 to 64 rows of x on the fifth-generation tensor cores: 128
+// weight rows are an MMA's M, the rows of x (rounded up to 16) its N.
+//
+// The weights are decoded to BF16 in registers and handed to tcgen05.mma through tensor memory as
+// its A operand; x comes into shared memory by TMA as B, as it is.  (A through shared memory would
+// put 128 x 64 BF16 weights there twice for every 64 columns, written and read: 22 us for 18432 x
+// 7168 before anything else.)  An E2M1 value times an E4M3 scale is exact in BF16 (at most 6
+// significant bits), and so is one times an E8M0 scale with the power of two set aside: a quarter of
+// it is at least 2^-130 and at most 1.5 * 2^127.  The sums are the tensor core's, FP32.
+//
+// A block works on 256 weight rows (two accumulators) in steps of 128 columns; a thread decodes half
+// of its row's share: 64 bytes of codes a step.  Warps 0-15 decode (w % 4: tensor memory's lane
+// quadrant, w / 4 % 2: the accumulator, w / 8: every second step), 16 loads x, 17 allocates tensor
+// memory and issues the MMAs, 18 loads the codes.  Three rings join them: codes and x in shared
+// memory, decoded weights in tensor memory.  256 rows, because x is read from L2 once a block: at
+// 128 rows (two blocks an SM) it was twice the bytes of the codes.
+// With few tiles the blocks of a cluster split K; each sums its share of the rows from all blocks'
+// accumulators, which they store into its shared memory, in block order.
+// Every wait is bounded; a block whose wait ran out stores NaN.
+//
+// Measured (device time of a call, NVFP4; in brackets the kernel for fewer rows): 18432 x 7168, 32
+// rows 26 us (41), 64 rows 28 us (86); 36864 x 7168, 64 rows 44 us (165); 2048 x 2048, 64 rows 8.9 us
+// (17.5).  The decoding bounds it: 11 of an SM sub-core's half-rate ALU instructions for 8 codes are
+// 0.37 us a step of the 0.64 us that one takes.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+
+#include "ops.h"
+#include "w4.cuh"
+
+namespace nvfp4moe {
+
+namespace {
+
+constexpr int kTcRows = 256;           // two accumulators of 128 rows
+constexpr int kTcCodeStages = 5;       // ring of codes: 128 columns each
+constexpr int kTcXStages = 4;          // ring of x: 128 columns each, as two swizzled tiles of 64
+constexpr int kTcAStages = 3;          // ring of decoded weights in tensor memory: 128 columns each
+constexpr int kTcCodeBytes = kTcRows * 64;
+constexpr int kTcDecWarps = 16;
+constexpr int kTcXWarp = 16;
+constexpr int kTcMmaWarp = 17;
+constexpr int kTcCodeWarp = 18;
+constexpr int kTcThreads = 608;
+constexpr uint32_t kTcCols = 512;      // tensor memory: accumulators, then the A ring
+constexpr uint32_t kTcACol = 128;
+constexpr uint32_t kTcPow2_124 = 0x7D807D80u;   // 2^124 in both halves
+
+// kind::f16 with FP32 accumulators, BF16 operands, K-major: see the grouped GEMM's descriptor.
+__device__ __forceinline__ uint32_t tc_idesc(int n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// D (+)= A B over 64 columns of K for both halves of the tile (128 rows each), by one lane of a
+// converged warp.  A in tensor memory: lane = row, 32-bit column = two elements of K, so K = 16 is 8
+// columns; the second half's is 64 columns on, its accumulators too.  B: 32 bytes of a 128-byte
+// row.  The whole warp runs the loop around this and one lane is elected here: the operands stay in
+// uniform registers (issued by a single lane of a diverged warp an MMA costs 43 cycles).
+__device__ __forceinline__ void tc_mma_64(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n"
+      ".reg .pred p, q, t;\n"
+      ".reg .b32 d1, a1, a2, a3, e0, e1, e2, e3;\n"
+      ".reg .b64 b1, b2, b3;\n"
+      "elect.sync _|q, 0xffffffff;\n"
+      "setp.ne.u32 p, %4, 0;\n"
+      "setp.eq.u32 t, %3, %3;\n"
+      "add.u32 d1, %0, 64;\n"
+      "add.u32 a1, %1, 8;\n"
+      "add.u32 a2, %1, 16;\n"
+      "add.u32 a3, %1, 24;\n"
+      "add.u32 e0, %1, 64;\n"
+      "add.u32 e1, %1, 72;\n"
+      "add.u32 e2, %1, 80;\n"
+      "add.u32 e3, %1, 88;\n"
+      "add.u64 b1, %2, 2;\n"
+      "add.u64 b2, %2, 4;\n"
+      "add.u64 b3, %2, 6;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [d1], [e0], %2, %3, p;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [d1], [e1], b1, %3, t;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [d1], [e2], b2, %3, t;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [d1], [e3], b3, %3, t;\n"
+      "}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tc_commit_elected(const uint64_t* bar) {
+  asm volatile(
+      "{\n"
+      ".reg .pred q;\n"
+      "elect.sync _|q, 0xffffffff;\n"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n"
+      "}" ::"r"(smem_u32(bar))
+      : "memory");
+}
+
+// 32 registers of each thread -> 32 consecutive columns of its lane.
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0],"
+      " {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16,"
+      " %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t dsmem_addr(const void* local_smem, uint32_t rank) {
+  uint32_t ra;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(smem_u32(local_smem)), "r"(rank));
+  return ra;
+}
+__device__ __forceinline__ void st_dsmem_f32x4(uint32_t addr, float a, float b, float c, float d) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c),
+               "f"(d)
+               : "memory");
+}
+
+// A wait of at most about a second.  The timer is read only once the first tries have failed: its
+// latency would be the ring's.
+__device__ __forceinline__ bool tc_wait(const uint64_t* bar, uint32_t parity) {
+  const uint32_t b = smem_u32(bar);
+  for (int i = 0; i < 128; ++i)
+    if (mbar_try_wait(b, parity)) return true;
+  return mbar_wait_bounded(b, parity, 1000000000ull, nullptr);
+}
+
+struct TcArgs {
+  const uint8_t* sf;
+  const float* ts;
+  int T, tn;        // rows of x, and rounded up to 16
+  int64_t N;
+  int K;
+  int cluster;      // blocks that split K
+  int kslice;       // columns of a block, a multiple of 128
+  bool wide;        // the scales of 128 columns are one aligned load
+  void* y;
+};
+
+template <bool kMx, bool kF32>
+__global__ void __launch_bounds__(kTcThreads, 1)
+linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tmap_x,
+                    const __grid_constant__ CUtensorMap tmap_c, const TcArgs a) {
+  constexpr int kBlk = kMx ? 32 : 16;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  __shared__ uint64_t c_full[kTcCodeStages], c_empty[kTcCodeStages], x_full[kTcXStages],
+      x_empty[kTcXStages], a_full[kTcAStages], a_empty[kTcAStages], acc_full;
+  __shared__ uint32_t s_tmem, s_issued_x, s_issued_c;
+  __shared__ volatile uint32_t s_abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)blockIdx.x % a.cluster;
+  const int64_t row0 = (int64_t)((int)blockIdx.x / a.cluster) * kTcRows;
+  const int kb = rank * a.kslice, ke = min(a.K, kb + a.kslice);
+  const int np = max(0, (ke - kb + 127) / 128);   // steps of 128 columns; behind K all are zeros
+  const uint32_t x_bytes = (uint32_t)a.tn * 256u;
+  uint8_t* x_ring = smem + kTcCodeStages * kTcCodeBytes;
+  // Met before the stores into other blocks, which only then need them to have started: a block
+  // that holds tensor memory waits for no other block (one that waits for tensor memory on its SM
+  // could hold it up).
+  if (a.cluster > 1) cluster_arrive();
+  if (warp == kTcMmaWarp) {
+    tmem_alloc(smem_u32(&s_tmem), kTcCols);
+    tmem_relinquish();
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kTcCodeStages; ++i) {
+      mbar_init(smem_u32(c_full + i), 1);    // the TMA load (expect_tx)
+      mbar_init(smem_u32(c_empty + i), 8);   // the eight warps that read it
+    }
+    for (int i = 0; i < kTcXStages; ++i) {
+      mbar_init(smem_u32(x_full + i), 1);
+      mbar_init(smem_u32(x_empty + i), 1);   // the MMA commit
+    }
+    for (int i = 0; i < kTcAStages; ++i) {
+      mbar_init(smem_u32(a_full + i), 8);    // the eight warps that decode it
+      mbar_init(smem_u32(a_empty + i), 1);
+    }
+    mbar_init(smem_u32(&acc_full), 1);
+    s_issued_x = s_issued_c = 0u;
+    s_abort = 0u;
+    fence_barrier_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
+  griddep_wait();
+  griddep_launch();
+
+  if (warp < kTcDecWarps) {
+    // ---- decode: one weight row a thread ----
+    const int quad = warp & 3, half = (warp >> 2) & 1, set = warp >> 3;
+    const int r = half * 128 + quad * 32 + lane;
+    const int64_t row = min(row0 + r, a.N - 1);   // rows behind the last: not stored
+    const uint8_t* ps = a.sf + row * (a.K / kBlk);
+    const uint32_t a_lane = tmem + kTcACol + (uint32_t)half * 64u + ((uint32_t)(quad * 32) << 16);
+    const uint8_t* c_lane = smem + r * 64;
+    const int swz = (r >> 1) & 3;   // the 64-byte swizzle: a row's chunk index xor (row / 2) % 4
+    // The scales of 128 columns: 8 or 4 bytes.  Behind K (where x and the codes are zeros) the row's
+    // last ones: a NaN there is the row's anyway.
+    uint32_t s[kMx ? 1 : 2];
+    auto load_scales = [&](int p) {
+      const int at = kb + p * 128;
+      if (a.wide) {
+        const uint8_t* q = ps + min(at, a.K - 128) / kBlk;
+        if constexpr (kMx) s[0] = __ldg(reinterpret_cast<const uint32_t*>(q));
+        else {
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(q));
+          s[0] = v.x;
+          s[1] = v.y;
+        }
+      } else {
+        uint32_t b[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const uint8_t* q = ps + min(at + u * 32, a.K - 32) / kBlk;
+          if constexpr (kMx) b[u] = __ldg(q);
+          else b[u] = __ldg(reinterpret_cast<const uint16_t*>(q));
+        }
+        if constexpr (kMx) s[0] = b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24);
+        else {
+          s[0] = b[0] | (b[1] << 16);
+          s[1] = b[2] | (b[3] << 16);
+        }
+      }
+    };
+    int slot = set, cslot = set;
+    uint32_t ph = 0u, cph = 0u;
+    bool ok = true;
+    if (set < np) load_scales(set);
+    for (int p = set; p < np; p += 2) {
+      uint32_t ss[kMx ? 1 : 2];
+#pragma unroll
+      for (int u = 0; u < (kMx ? 1 : 2); ++u) ss[u] = s[u];
+      load_scales(p + 2);
+      ok = __all_sync(0xffffffffu, tc_wait(c_full + cslot, cph));
+      if (!ok) break;
+      uint4 cc[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        cc[u] = *reinterpret_cast<const uint4*>(c_lane + cslot * kTcCodeBytes + ((u ^ swz) << 4));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(c_empty + cslot));
+      cslot += 2;
+      if (cslot >= kTcCodeStages) { cslot -= kTcCodeStages; cph ^= 1u; }
+      ok = __all_sync(0xffffffffu, tc_wait(a_empty + slot, ph ^ 1u));
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t out[32];
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const uint4 w4 = cc[2 * q + v];
+          const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+          uint32_t sc[2];
+          if constexpr (kMx) {
+            const uint32_t e = (ss[0] >> ((2 * q + v) * 8)) & 0xFFu;
+            sc[0] = sc[1] = e == 255u ? 0x7FC07FC0u : e8m0_scale_bf16x2(e);
+          } else {
+            const float2 f = e4m3x2_to_f32x2((ss[q] >> (v * 16)) & 0xFFFFu);   // NaN stays NaN
+            const __nv_bfloat162 s0 = __float2bfloat162_rn(f.x * 0x1p118f);
+            const __nv_bfloat162 s1 = __float2bfloat162_rn(f.y * 0x1p118f);
+            sc[0] = *reinterpret_cast<const uint32_t*>(&s0);
+            sc[1] = *reinterpret_cast<const uint32_t*>(&s1);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t o[4];
+            e2m1x8_to_bf16x2_scaled_down(w[i], o);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if constexpr (kMx) o[j] = mul_bf16x2(o[j], kTcPow2_124);
+              out[v * 16 + i * 4 + j] = mul_bf16x2(o[j], sc[i >> 1]);
+            }
+          }
+        }
+        tmem_st_32x32b_x32(a_lane + (uint32_t)slot * 128u + q * 32u, out);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(a_full + slot));
+      slot += 2;
+      if (slot >= kTcAStages) { slot -= kTcAStages; ph ^= 1u; }
+    }
+    if (!ok && lane == 0) s_abort = 1u;
+  } else if (warp == kTcXWarp || warp == kTcCodeWarp) {
+    if (lane == 0) {
+      const bool x = warp == kTcXWarp;
+      const int stages = x ? kTcXStages : kTcCodeStages;
+      uint64_t* full = x ? x_full : c_full;
+      uint64_t* empty = x ? x_empty : c_empty;
+      int slot = 0;
+      uint32_t ph = 0u;
+      for (int i = 0; i < np; ++i) {
+        if (!tc_wait(empty + slot, ph ^ 1u)) {
+          s_abort = 1u;
+          break;
+        }
+        const uint32_t fb = smem_u32(full + slot);
+        mbar_arrive_expect_tx(fb, x ? x_bytes : (uint32_t)kTcCodeBytes);
+        if (x) {
+          const uint32_t to = smem_u32(x_ring) + slot * x_bytes;
+          tma_load_2d(to, &tmap_x, kb + i * 128, 0, fb);
+          tma_load_2d(to + x_bytes / 2, &tmap_x, kb + i * 128 + 64, 0, fb);
+          s_issued_x = (uint32_t)i + 1u;
+        } else {
+          tma_load_2d(smem_u32(smem) + slot * kTcCodeBytes, &tmap_c, kb / 2 + i * 64, (int)row0, fb);
+          s_issued_c = (uint32_t)i + 1u;
+        }
+        if (++slot == stages) { slot = 0; ph ^= 1u; }
+      }
+    }
+    __syncwarp();
+  } else {
+    const uint32_t idesc = tc_idesc(a.tn);
+    const uint64_t db = smem_desc(smem_u32(x_ring), 16, 1024, kLayoutSwizzle128B);
+    int slot = 0, xs = 0;
+    uint32_t ph = 0u, xph = 0u;
+    bool ok = true;
+    for (int i = 0; i < np; ++i) {
+      ok = __all_sync(0xffffffffu, tc_wait(x_full + xs, xph)) &&
+           __all_sync(0xffffffffu, tc_wait(a_full + slot, ph));
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t b0 = db + (uint64_t)((xs * x_bytes) >> 4);
+      const uint32_t a0 = tmem + kTcACol + (uint32_t)slot * 128u;
+      tc_mma_64(tmem, a0, b0, idesc, i != 0 ? 1u : 0u);
+      tc_mma_64(tmem, a0 + 32u, b0 + (x_bytes >> 5), idesc, 1u);
+      tc_commit_elected(x_empty + xs);
+      tc_commit_elected(a_empty + slot);
+      if (++slot == kTcAStages) { slot = 0; ph ^= 1u; }
+      if (++xs == kTcXStages) { xs = 0; xph ^= 1u; }
+    }
+    // (after an expired wait this still waits for the MMAs issued before)
+    tc_commit_elected(&acc_full);
+    if (!__all_sync(0xffffffffu, tc_wait(&acc_full, 0u))) ok = false;
+    if (!ok && lane == 0) s_abort = 1u;
+  }
+
+  // ---- epilogue: lane = weight row, column = token ----
+  tc_fence_before();
+  __syncthreads();   // the MMA thread has seen the accumulators complete (or gave up)
+  tc_fence_after();
+  const bool bad = s_abort != 0u;
+  // The factors that undo the decoding's power of two, the exact one first where it cannot overflow
+  const float ts = kMx ? 4.0f : __ldg(a.ts);
+  const float up = kMx || fabsf(ts) > 1.0f ? ts : ts * 256.0f, up0 = !kMx && fabsf(ts) > 1.0f ? 256.0f : 1.0f;
+  auto store = [&](int t, int64_t n, float v) {
+    if (t >= a.T || n >= a.N) return;
+    if constexpr (kF32) static_cast<float*>(a.y)[(int64_t)t * a.N + n] = v;
+    else static_cast<__nv_bfloat16*>(a.y)[(int64_t)t * a.N + n] = __float2bfloat16_rn(v);
+  };
+  // A cluster's block sums 128 / cluster of the rows: join[block][row][token].  Rows of tn + 4
+  // words put a warp's 16-byte stores in all banks.
+  const int rows = kTcRows / a.cluster, stride = a.tn + 4;
+  float* join = reinterpret_cast<float*>(x_ring + kTcXStages * x_bytes);
+  if (a.cluster > 1) cluster_wait();
+  if (warp < kTcDecWarps) {
+    const int half = (warp >> 2) & 1, r = half * 128 + (warp & 3) * 32 + lane;
+    const uint32_t to = a.cluster > 1 ? dsmem_addr(join + (rank * rows + r % rows) * stride, r / rows) : 0u;
+    for (int c0 = (warp >> 3) * 16; c0 < a.tn; c0 += 32) {
+      uint32_t v[16];
+      tmem_ld_32x32b_x16(tmem + half * 64 + c0 + ((uint32_t)((warp & 3) * 32) << 16), v);
+      tmem_ld_wait();
+      float f[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        f[i] = np == 0 ? 0.0f : __uint_as_float(v[i]) * up0 * up;
+        if (bad) f[i] = __uint_as_float(0x7FC00000u);
+      }
+      if (a.cluster > 1) {
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+          st_dsmem_f32x4(to + (uint32_t)(c0 + i) * 4u, f[i], f[i + 1], f[i + 2], f[i + 3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) store(c0 + i, row0 + r, f[i]);
+      }
+    }
+  }
+  // After an expired wait TMA loads may still be in flight: the last ring's worth is waited for.
+  if (bad && (warp == kTcXWarp || warp == kTcCodeWarp) && lane == 0) {
+    const bool x = warp == kTcXWarp;
+    const uint32_t n = x ? s_issued_x : s_issued_c, stages = x ? kTcXStages : kTcCodeStages;
+    for (uint32_t i = n > stages ? n - stages : 0u; i < n; ++i)
+      if (!tc_wait((x ? x_full : c_full) + i % stages, (i / stages) & 1u))
+        break;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kTcMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTcCols);
+  }
+  if (a.cluster > 1) {
+    __syncwarp();
+    cluster_sync();
+    for (int e = threadIdx.x; e < rows * (a.tn / 4); e += kTcThreads) {
+      const int r = e % rows, t = e / rows * 4;
+      float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int b = 0; b < a.cluster; ++b) {
+        const float4 v = *reinterpret_cast<const float4*>(join + (b * rows + r) * stride + t);
+        sum.x += v.x;
+        sum.y += v.y;
+        sum.z += v.z;
+        sum.w += v.w;
+      }
+      const int64_t n = row0 + rank * rows + r;
+      store(t, n, sum.x);
+      store(t + 1, n, sum.y);
+      store(t + 2, n, sum.z);
+      store(t + 3, n, sum.w);
+    }
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn_linear() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
+                                                     cudaEnableDefault, &q) == cudaSuccess &&
+                    q == cudaDriverEntryPointSuccess;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ok ? ptr : nullptr);
+  }();
+  return fn;
+}
+
+}  // namespace
+
+cudaError_t launch_linear_w4_tc(const void* x, const uint8_t* codes, const uint8_t* sf,
+                                const float* ts, int T, int64_t N, int K, bool f32, void* y,
+                                cudaStream_t s) {
+  auto encode = encode_fn_linear();
+  if (!encode) return cudaErrorNotSupported;
+  TcArgs a{sf, ts, T, (T + 15) / 16 * 16, N, K, 1, 0, false, y};
+  a.wide = K % 128 == 0 && is_aligned(sf, ts ? 8 : 4);
+  CUtensorMap tmap_x, tmap_c;
+  const cuuint32_t estr[2] = {1u, 1u};
+  {
+    const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)T};
+    const cuuint64_t strides[1] = {(cuuint64_t)K * 2};
+    const cuuint32_t box[2] = {64u, (cuuint32_t)a.tn};   // rows and columns outside are zeros
+    if (encode(&tmap_x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(x), dims, strides,
+               box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  {
+    const cuuint64_t dims[2] = {(cuuint64_t)K / 2, (cuuint64_t)N};
+    const cuuint64_t strides[1] = {(cuuint64_t)K / 2};
+    const cuuint32_t box[2] = {64u, (cuuint32_t)kTcRows};
+    if (encode(&tmap_c, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides,
+               box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  // K over a cluster while all clusters are resident at once: of 4 blocks 36, of 8 blocks 15 on 152 SMs
+  const int64_t tiles = (N + kTcRows - 1) / kTcRows;
+  const int64_t steps = (K + 127) / 128;
+  const int most[4] = {num_sms(), num_sms() / 2, num_sms() * 36 / 152, num_sms() * 15 / 152};
+  for (int l = 1; l < 4 && tiles <= most[l] && steps >= 2 << l; ++l) a.cluster = 1 << l;
+  a.kslice = (int)((steps + a.cluster - 1) / a.cluster) * 128;
+  auto kern = ts ? (f32 ? linear_w4_tc_kernel<false, true> : linear_w4_tc_kernel<false, false>)
+                 : (f32 ? linear_w4_tc_kernel<true, true> : linear_w4_tc_kernel<true, false>);
+  const size_t smem = 1024 + (size_t)kTcCodeStages * kTcCodeBytes +
+                      (size_t)kTcXStages * a.tn * 256 +
+                      (a.cluster > 1 ? (size_t)(a.tn + 4) * kTcRows * 4 : 0u);
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * a.cluster));
+  cfg.blockDim = dim3(kTcThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)a.cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, tmap_x, tmap_c, a);
+}
+
+}  // namespace nvfp4moe
