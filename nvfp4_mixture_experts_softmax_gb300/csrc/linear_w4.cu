@@ -21,16 +21,16 @@
 //     2^-30 (2^-39 of the row's largest in the second case).  Half of that times sum |w| is below
 //     the roundings of an FP32 sum of the row's terms, 2^-24 of each.
 // With more tokens the MMAs weigh most (two cycles each on an SM's four tensor cores: 14 us for
-// 18432 x 7168 at 32 tokens), so from 17 on linear_w4_tc.cu takes over.
+// 18432 x 7168 at 32 tokens), so linear_w4_tc.cu takes over.
 //
 // K is split twice: over the blocks of a cluster, so that a block can keep its share of x in
 // shared memory, and over ks warps of a block.  A group of ks warps works on a tile of kMt * 16
 // weight rows; the partial sums are joined through (distributed) shared memory in a fixed order.
 //
 // Measured (device time of a call): 131072 x 4096 NVFP4, 1 token 60 us (5.0 TB/s; a pure read of HBM
-// reaches 5.8), 16 tokens 80 us; 18431 x 7168 MXFP4, 15 tokens 26 us; 18432 x 7168 NVFP4, 1 / 32 / 64
-// tokens 19.5 / 41 / 86 us; 2048 x 2048, 1 token 4.0 us.  A block of 16 rows whose eight warps read x
-// from L1 in BF16, without staging, took 77.6, 166, 39.6, 22.2 / 77 / 138 and 2.8 us.
+// reaches 5.8), 16 tokens 78 us; 18432 x 7168, 1 / 8 tokens 19.5 / 25.5 us; 2048 x 2048, 1 token 4.0
+// us.  A block of 16 rows whose eight warps read x from L1 in BF16, without staging, took 77.6, 166,
+// 22.2 / 39 and 2.8 us.
 #include <algorithm>
 
 #include "common.cuh"
@@ -41,15 +41,14 @@ namespace nvfp4moe {
 namespace {
 
 constexpr int kLinMaxTokens = 64;
-constexpr int kLinTcTokens = 17;     // rows of x from which linear_w4_tc.cu is faster
+constexpr int kLinRows = 16;          // of x in this kernel
 constexpr int kTopGuess = 9;         // exponent of a row's largest element: the first scale's
 constexpr int kTopLeast = -6;        // bounds
 
 // Tiling by the number of 8-token columns NT.  One column: 16-row tiles, 16 warps of 64 registers
-// and two blocks an SM, whose many warps hide the latency of the loads.  More columns: x fills the
+// and two blocks an SM, whose many warps hide the latency of the loads.  Two columns: x fills the
 // shared memory of an SM, so one block of 16 warps with 128 registers, 32-row tiles (each x
-// fragment is used twice) and more loads in flight a warp; eight columns' accumulators leave room
-// for half the step.
+// fragment is used twice) and more loads in flight a warp.
 template <int NT>
 struct LinTile {
   static constexpr int kMt = NT == 1 ? 1 : 2;        // 16-row MMA tiles of a warp
@@ -57,13 +56,12 @@ struct LinTile {
   static constexpr int kPerSm = NT == 1 ? 2 : 1;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kRows = kMt * 16;
-  static constexpr int kHalves = NT <= 4 ? 2 : 1;    // 128-column parts of a step
+  static constexpr int kHalves = 2;                  // 128-column parts of a step
   static constexpr int kFly = NT == 1 ? 4 : 8;       // loads of x in flight in a lane
   static constexpr int kStep = kHalves * 128;        // columns of a step
-  // join buffer: kJoin of a warp's kMt * NT accumulator fragments at a time
+  // join buffer: a warp's kMt * NT accumulator fragments
   static constexpr int kFrags = kMt * NT;
-  static constexpr int kJoin = kFrags < 8 ? kFrags : 8;
-  static constexpr int kJoinBytes = kWarps * kJoin * 512;
+  static constexpr int kJoinBytes = kWarps * kFrags * 512;
 };
 constexpr int kScaleWindow = 37;     // binades of E8M0 scales that are exact in F16 at one offset
 constexpr int kScaleLow = 104;       // lowest scale byte at offset 0
@@ -241,22 +239,22 @@ linear_w4_kernel(LinearArgs a) {
   constexpr int kBlk = kMx ? 32 : 16;
   constexpr bool kRefill = NT > 1;   // load a part of the next step as soon as this one's is used up
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int s_shift[kLinMaxTokens];        // rows of x: the power of two they are times
-  __shared__ uint32_t s_top[kLinMaxTokens];     // their largest magnitude
-  __shared__ float2 s_unscale[kLinMaxTokens];   // takes a row's sums to y, in two factors
+  __shared__ int s_shift[kLinRows];        // rows of x: the power of two they are times
+  __shared__ uint32_t s_top[kLinRows];     // their largest magnitude
+  __shared__ float2 s_unscale[kLinRows];   // takes a row's sums to y, in two factors
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, q = lane & 3;
   const int slice = warp % a.ks, group = warp / a.ks, groups = a.warps / a.ks;
   const int rank = (int)blockIdx.x % a.cluster, col = (int)blockIdx.x / a.cluster;
   const int cols = (int)gridDim.x / a.cluster;
   const int stride = a.kc * 2 + 64;
-  float4* join = reinterpret_cast<float4*>(smem);   // [warps][kJoin][32], if anything is joined
+  float4* join = reinterpret_cast<float4*>(smem);   // [warps][kFrags][32], if anything is joined
   const bool joins = a.ks > 1 || a.cluster > 1;
   uint8_t* xs = smem + (joins ? L::kJoinBytes : 0);
   const int64_t tiles = (a.N + L::kRows - 1) / L::kRows;
   const int64_t tile0 = (int64_t)col * groups + group;   // this group's first tile
   const int kb = rank * a.kslice, ke = min(a.K, kb + a.kslice);   // this block's columns
-  for (int t = threadIdx.x; t < kLinMaxTokens; t += blockDim.x) {   // (blocks of one warp exist)
+  for (int t = threadIdx.x; t < kLinRows; t += blockDim.x) {   // (blocks of one warp exist)
     s_shift[t] = 15 - kTopGuess;
     s_top[t] = 0u;
   }
@@ -287,7 +285,7 @@ linear_w4_kernel(LinearArgs a) {
     find_shifts(a.x, a.T, a.K, s_shift);
     __syncthreads();
   }
-  for (int t = threadIdx.x; t < kLinMaxTokens; t += blockDim.x) {
+  for (int t = threadIdx.x; t < kLinRows; t += blockDim.x) {
     float2 u = pow2_factors(-s_shift[t]);   // half on either side of the tensor scale
     if constexpr (!kMx) u.y *= __ldg(a.ts);
     s_unscale[t] = u;
@@ -471,44 +469,43 @@ linear_w4_kernel(LinearArgs a) {
       }
       continue;
     }
+    if (it > 0) all();   // the readers of what stands there are through
+    // fragments go round the cluster's blocks: [block][warp][fragments of a block][lane]
+    const int per = L::kFrags / a.cluster;
 #pragma unroll
-    for (int f0 = 0; f0 < L::kFrags; f0 += L::kJoin) {
-      if (it > 0 || f0 > 0) all();   // the readers of what stands there are through
-      // fragments go round the cluster's blocks: [block][warp][fragments of a block][lane]
-      const int per = L::kJoin / a.cluster;
-#pragma unroll
-      for (int f = 0; f < L::kJoin; ++f) {
-        if (!active) break;
-        const float* v = c[(f0 + f) % kMt][(f0 + f) / kMt];
-        float4* slot = join + ((rank * a.warps + warp) * per + f / a.cluster) * 32 + lane;
-        if (a.cluster > 1) st_dsmem_float4(slot, f % a.cluster, v);
-        else *slot = make_float4(v[0], v[1], v[2], v[3]);
-      }
-      all();
-      // this block's sums go round the group's threads, neighbours on neighbouring rows: blocks,
-      // then warps in order.  Row r, token t of a fragment: lane (r % 8) * 4 + t / 2, register
-      // (r / 8) * 2 + t % 2
-      const float* base = reinterpret_cast<const float*>(join + group * a.ks * per * 32);
-      for (int e = slice * 32 + lane; active && e < per * 128; e += a.ks * 32) {
-        const int r = e & 15, t = (e >> 4) & 7, fl = e >> 7;
-        const float* at = base + fl * 128 + (r & 7) * 16 + (t >> 1) * 4 + (r >> 3) * 2 + (t & 1);
-        float sum = 0.0f;
-        for (int b = 0; b < a.cluster; ++b)
+    for (int f = 0; f < L::kFrags; ++f) {
+      if (!active) break;
+      const float* v = c[f % kMt][f / kMt];
+      float4* slot = join + ((rank * a.warps + warp) * per + f / a.cluster) * 32 + lane;
+      if (a.cluster > 1) st_dsmem_float4(slot, f % a.cluster, v);
+      else *slot = make_float4(v[0], v[1], v[2], v[3]);
+    }
+    all();
+    // this block's sums go round the group's threads, neighbours on neighbouring rows: blocks,
+    // then warps in order.  Row r, token t of a fragment: lane (r % 8) * 4 + t / 2, register
+    // (r / 8) * 2 + t % 2
+    const float* base = reinterpret_cast<const float*>(join + group * a.ks * per * 32);
+    for (int e = slice * 32 + lane; active && e < per * 128; e += a.ks * 32) {
+      const int r = e & 15, t = (e >> 4) & 7, fl = e >> 7;
+      const float* at = base + fl * 128 + (r & 7) * 16 + (t >> 1) * 4 + (r >> 3) * 2 + (t & 1);
+      float sum = 0.0f;
+      for (int b = 0; b < a.cluster; ++b)
 #pragma unroll 4
-          for (int w = 0; w < a.ks; ++w) sum += at[(b * a.warps + w) * per * 128];
-        const int f = f0 + fl * a.cluster + rank;
-        if (tile < tiles) store(tile, f % kMt, f / kMt, t, r, sum);
-      }
+        for (int w = 0; w < a.ks; ++w) sum += at[(b * a.warps + w) * per * 128];
+      const int f = fl * a.cluster + rank;
+      if (tile < tiles) store(tile, f % kMt, f / kMt, t, r, sum);
     }
   }
 }
 
 // Time of a split in us, from measurements on GB300: a step of a warp takes kStepUs[0], or
 // kStepUs[1] for each warp of an SM if its warps are many; a join kJoinUs[0] (warps) or [1]
-// (cluster); x comes into shared memory at 16 elements a ns.
+// (cluster); x comes into shared memory at 16 elements a ns.  A split whose x does not fit is taken
+// only if none does: windows of x cost more than the split saves (131072 x 7168 at 12 rows 247 us,
+// with a cluster 152).
 template <int NT>
 struct LinCost {
-  static constexpr double kStepUs[2] = {NT <= 2 ? 1.1 : 1.5, NT == 1 ? 0.0625 : NT == 2 ? 0.15 : 0.25};
+  static constexpr double kStepUs[2] = {1.1, NT == 1 ? 0.0625 : 0.15};
   static constexpr double kJoinUs[2] = {NT == 1 ? 2.0 : 3.0, 5.0};
 };
 
@@ -520,9 +517,10 @@ cudaError_t launch_linear(LinearArgs a, cudaStream_t s) {
   const int64_t tiles = (a.N + L::kRows - 1) / L::kRows;
   const int64_t steps = (a.K + L::kStep - 1) / L::kStep;
   const int rows = NT == 1 ? a.T : (a.T + 7) / 8 * 8;   // of x in shared memory
-  // Columns of x that fit beside the join buffer, with `blocks` blocks an SM.
+  // Columns of x that fit beside the join buffer, with `blocks` blocks an SM.  Two blocks leave L1
+  // some 30 KB: with 110 KB each 36864 x 7168 at 7 rows takes 66 us, with one block an SM 41.
   auto fitting = [&](bool joins, int blocks) {
-    const int room = (blocks == 2 ? 110 : 222) * 1024 - (joins ? L::kJoinBytes : 0);
+    const int room = (blocks == 2 ? 96 : 222) * 1024 - (joins ? L::kJoinBytes : 0);
     return (room / rows - 64) / 2 / L::kStep * L::kStep;
   };
   // Larger clusters leave SMs of each GPC idle: on 152 SMs 36 clusters of four fit, 15 of eight
@@ -532,7 +530,7 @@ cudaError_t launch_linear(LinearArgs a, cudaStream_t s) {
   };
   // The split of K over cluster blocks and warps, and the blocks an SM, that should finish first.
   double best = 0.0;
-  int cols = 1;
+  int cols = 1, per_sm = 1;
   auto consider = [&](int cl, int ks, int blocks) {
     const bool joins = ks > 1 || cl > 1;
     const int64_t sl = (steps + cl - 1) / cl, groups = L::kWarps / ks;
@@ -545,7 +543,7 @@ cudaError_t launch_linear(LinearArgs a, cudaStream_t s) {
     if (!fits && blocks > 1) return;
     const double warps = (double)(busy * cl * even * ks) / num_sms();
     double stage = (double)a.T * sl * L::kStep / 16000.0 * (busy > clusters(cl) ? blocks : 1);
-    if (!fits) stage *= 1 + rounds;
+    if (!fits) stage *= 100.0 + (double)rounds;
     const double cost = stage + (cl > 1 ? 1.5 : 0.0) +
                         rounds * ((double)((sl + ks - 1) / ks) *
                                       std::max(C::kStepUs[0], C::kStepUs[1] * warps) +
@@ -558,6 +556,7 @@ cudaError_t launch_linear(LinearArgs a, cudaStream_t s) {
     a.kslice = (int)sl * L::kStep;
     a.kc = std::min(a.kslice, fitting(joins, blocks));
     cols = (int)busy;
+    per_sm = blocks;
     a.warps = (int)even * ks;
   };
   for (int cl = 1; cl <= 8 && cl <= L::kFrags && cl <= steps; cl *= 2)
@@ -570,6 +569,14 @@ cudaError_t launch_linear(LinearArgs a, cudaStream_t s) {
   if (smem > 40 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  // Shared memory for these blocks only, the rest is L1: the codes of a row come in 16-byte loads, and
+  // a small L1 loses their lines between them.
+  {
+    const size_t used = per_sm * (smem + 2048);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                               (int)std::min<size_t>(100, (used * 100 + 233471) / 233472));
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
@@ -626,11 +633,13 @@ extern "C" int moe_linear_w4(const void* x, const uint8_t* codes, const uint8_t*
   a.K = (int)K;
   a.y = y;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = T >= kLinTcTokens
+  // One column of tokens while x leaves L1 its room; two, whose blocks split K in a cluster, where
+  // it does not and a quarter of K fits (18432 x 16384 at 5 / 6 / 8 rows: 48 / 61 / 73 us and 45;
+  // 8192 x 28672 at 3 / 4: 43 / 70 and 40; 8192 x 49152 at 4: 103 and 113).
+  const bool one = T == 1 || (T <= 8 && ((int64_t)T * K <= 88 * 1024 || K > 40 * 1024));
+  const cudaError_t e = linear_w4_tc_faster(T, N, (int)K)
                             ? launch_linear_w4_tc(x, codes, sf, ts, T, N, (int)K, f32, y, s)
-                        : T <= 8  ? launch_linear<1>(a, mx, f32, s)
-                        : T <= 16 ? launch_linear<2>(a, mx, f32, s)
-                        : T <= 32 ? launch_linear<4>(a, mx, f32, s)
-                                  : launch_linear<8>(a, mx, f32, s);
+                        : one ? launch_linear<1>(a, mx, f32, s)
+                              : launch_linear<2>(a, mx, f32, s);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

@@ -1,27 +1,28 @@
-// 4-bit matrix-vector product for 17 to 64 rows of x on the fifth-generation tensor cores: 128
-// weight rows are an MMA's M, the rows of x (rounded up to 16) its N.
+// 4-bit matrix-vector product for many rows of x (9 or 17 to 64) on the fifth-generation tensor
+// cores: 128 weight rows are an MMA's M, the rows of x (rounded up to 16) its N.
 //
 // The weights are decoded to BF16 in registers and handed to tcgen05.mma through tensor memory as
 // its A operand; x comes into shared memory by TMA as B, as it is.  (A through shared memory would
-// put 128 x 64 BF16 weights there twice for every 64 columns, written and read: 22 us for 18432 x
-// 7168 before anything else.)  An E2M1 value times an E4M3 scale is exact in BF16 (at most 6
-// significant bits), and so is one times an E8M0 scale with the power of two set aside: a quarter of
-// it is at least 2^-130 and at most 1.5 * 2^127.  The sums are the tensor core's, FP32.
+// put 128 x 64 BF16 weights there for every 64 columns, written and read: 22 us for 18432 x 7168
+// before anything else.)  An E2M1 value times an E4M3 scale is exact in BF16 (at most 6 significant
+// bits), and so is one times an E8M0 scale with a power of two set aside: a quarter of it is at least
+// 2^-130 and at most 1.5 * 2^127.  The sums are the tensor core's, FP32.
 //
-// A block works on 256 weight rows (two accumulators) in steps of 128 columns; a thread decodes half
-// of its row's share: 64 bytes of codes a step.  Warps 0-15 decode (w % 4: tensor memory's lane
-// quadrant, w / 4 % 2: the accumulator, w / 8: every second step), 16 loads x, 17 allocates tensor
-// memory and issues the MMAs, 18 loads the codes.  Three rings join them: codes and x in shared
-// memory, decoded weights in tensor memory.  256 rows, because x is read from L2 once a block: at
-// 128 rows (two blocks an SM) it was twice the bytes of the codes.
+// A block works on 256 weight rows (two accumulators) in steps of 128 columns; a thread decodes its
+// row's 64 bytes of a step.  Warps 0-23 decode (w % 4: tensor memory's lane quadrant, w / 4 % 2: the
+// accumulator, w / 8: every third step), 24 loads x, 25 allocates tensor memory and issues the MMAs,
+// 26 loads the codes.  Three rings join them: codes and x in shared memory, decoded weights in
+// tensor memory.  256 rows, because x is read from L2 once a block: at 128 rows (two blocks an SM)
+// it was twice the bytes of the codes.
 // With few tiles the blocks of a cluster split K; each sums its share of the rows from all blocks'
 // accumulators, which they store into its shared memory, in block order.
 // Every wait is bounded; a block whose wait ran out stores NaN.
 //
-// Measured (device time of a call, NVFP4; in brackets the kernel for fewer rows): 18432 x 7168, 32
-// rows 26 us (41), 64 rows 28 us (86); 36864 x 7168, 64 rows 44 us (165); 2048 x 2048, 64 rows 8.9 us
-// (17.5).  The decoding bounds it: 11 of an SM sub-core's half-rate ALU instructions for 8 codes are
-// 0.37 us a step of the 0.64 us that one takes.
+// Measured (device time of a call, NVFP4; in brackets warp-level MMAs): 18432 x 7168, 32 rows 25 us
+// (41), 64 rows 29 us (86); 36864 x 7168, 64 rows 43 us (165); 2048 x 2048, 64 rows 9.1 us (17.5);
+// 18431 x 7168 MXFP4, 15 rows 23.8 us (26.2).  A step of a block takes 0.62 us.  Alone the decoding
+// takes 0.59 (some 20 instructions for 8 codes), the MMAs 0.53 at 64 rows (67 cycles each), the loads
+// 0.39 (from L2, 32 KB); 16 decoding warps 0.64; a warp whose single lane issues the MMAs 1.11.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -39,11 +40,11 @@ constexpr int kTcCodeStages = 5;       // ring of codes: 128 columns each
 constexpr int kTcXStages = 4;          // ring of x: 128 columns each, as two swizzled tiles of 64
 constexpr int kTcAStages = 3;          // ring of decoded weights in tensor memory: 128 columns each
 constexpr int kTcCodeBytes = kTcRows * 64;
-constexpr int kTcDecWarps = 16;
-constexpr int kTcXWarp = 16;
-constexpr int kTcMmaWarp = 17;
-constexpr int kTcCodeWarp = 18;
-constexpr int kTcThreads = 608;
+constexpr int kTcDecWarps = 24;
+constexpr int kTcXWarp = 24;
+constexpr int kTcMmaWarp = 25;
+constexpr int kTcCodeWarp = 26;
+constexpr int kTcThreads = 864;
 constexpr uint32_t kTcCols = 512;      // tensor memory: accumulators, then the A ring
 constexpr uint32_t kTcACol = 128;
 constexpr uint32_t kTcPow2_124 = 0x7D807D80u;   // 2^124 in both halves
@@ -242,61 +243,68 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tmap_x,
     uint32_t ph = 0u, cph = 0u;
     bool ok = true;
     if (set < np) load_scales(set);
-    for (int p = set; p < np; p += 2) {
+    for (int p = set; p < np; p += 3) {
       uint32_t ss[kMx ? 1 : 2];
 #pragma unroll
       for (int u = 0; u < (kMx ? 1 : 2); ++u) ss[u] = s[u];
-      load_scales(p + 2);
+      load_scales(p + 3);
       ok = __all_sync(0xffffffffu, tc_wait(c_full + cslot, cph));
       if (!ok) break;
-      uint4 cc[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        cc[u] = *reinterpret_cast<const uint4*>(c_lane + cslot * kTcCodeBytes + ((u ^ swz) << 4));
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(c_empty + cslot));
-      cslot += 2;
+      const uint8_t* cp = c_lane + cslot * kTcCodeBytes;
+      const int cold = cslot;
+      cslot += 3;
       if (cslot >= kTcCodeStages) { cslot -= kTcCodeStages; cph ^= 1u; }
       ok = __all_sync(0xffffffffu, tc_wait(a_empty + slot, ph ^ 1u));
       if (!ok) break;
       tc_fence_after();
+      // A placed code times its scale: NVFP4 one product (the scale in BF16 times 2^118).  MXFP4 one if
+      // the scale times 2^124 is a BF16 (up to 2^3), otherwise (`big`) two.
+      auto decode = [&](const bool big) {
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t out[32];
+        for (int q = 0; q < 2; ++q) {
+          uint32_t out[32];
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const uint4 w4 = cc[2 * q + v];
-          const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-          uint32_t sc[2];
-          if constexpr (kMx) {
-            const uint32_t e = (ss[0] >> ((2 * q + v) * 8)) & 0xFFu;
-            sc[0] = sc[1] = e == 255u ? 0x7FC07FC0u : e8m0_scale_bf16x2(e);
-          } else {
-            const float2 f = e4m3x2_to_f32x2((ss[q] >> (v * 16)) & 0xFFFFu);   // NaN stays NaN
-            const __nv_bfloat162 s0 = __float2bfloat162_rn(f.x * 0x1p118f);
-            const __nv_bfloat162 s1 = __float2bfloat162_rn(f.y * 0x1p118f);
-            sc[0] = *reinterpret_cast<const uint32_t*>(&s0);
-            sc[1] = *reinterpret_cast<const uint32_t*>(&s1);
-          }
+          for (int v = 0; v < 2; ++v) {
+            const uint4 w4 = *reinterpret_cast<const uint4*>(cp + (((2 * q + v) ^ swz) << 4));
+            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+            uint32_t sc[2];
+            if constexpr (kMx) {
+              const uint32_t e = (ss[0] >> ((2 * q + v) * 8)) & 0xFFu;
+              sc[0] = sc[1] = !big ? (e + 124u) * 0x00800080u
+                                   : e == 255u ? 0x7FC07FC0u : e8m0_scale_bf16x2(e);
+            } else {
+              const float2 f = e4m3x2_to_f32x2((ss[q] >> (v * 16)) & 0xFFFFu);   // NaN stays NaN
+              const __nv_bfloat162 s0 = __float2bfloat162_rn(f.x * 0x1p118f);
+              const __nv_bfloat162 s1 = __float2bfloat162_rn(f.y * 0x1p118f);
+              sc[0] = *reinterpret_cast<const uint32_t*>(&s0);
+              sc[1] = *reinterpret_cast<const uint32_t*>(&s1);
+            }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t o[4];
-            e2m1x8_to_bf16x2_scaled_down(w[i], o);
+            for (int i = 0; i < 4; ++i) {
+              uint32_t o[4];
+              e2m1x8_to_bf16x2_scaled_down(w[i], o);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if constexpr (kMx) o[j] = mul_bf16x2(o[j], kTcPow2_124);
-              out[v * 16 + i * 4 + j] = mul_bf16x2(o[j], sc[i >> 1]);
+              for (int j = 0; j < 4; ++j) {
+                if (big) o[j] = mul_bf16x2(o[j], kTcPow2_124);
+                out[v * 16 + i * 4 + j] = mul_bf16x2(o[j], sc[i >> 1]);
+              }
             }
           }
+          tmem_st_32x32b_x32(a_lane + (uint32_t)slot * 128u + q * 32u, out);
         }
-        tmem_st_32x32b_x32(a_lane + (uint32_t)slot * 128u + q * 32u, out);
-      }
+      };
+      bool big = false;
+      if constexpr (kMx)
+        big = __any_sync(0xffffffffu, (ss[0] & ((ss[0] & 0x7F7F7F7Fu) + 0x7D7D7D7Du) & 0x80808080u) != 0u);
+      if (kMx && big) decode(true);
+      else decode(false);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(c_empty + cold));
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(a_full + slot));
-      slot += 2;
-      if (slot >= kTcAStages) { slot -= kTcAStages; ph ^= 1u; }
+      ph ^= 1u;
     }
     if (!ok && lane == 0) s_abort = 1u;
   } else if (warp == kTcXWarp || warp == kTcCodeWarp) {
@@ -374,7 +382,7 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tmap_x,
   if (warp < kTcDecWarps) {
     const int half = (warp >> 2) & 1, r = half * 128 + (warp & 3) * 32 + lane;
     const uint32_t to = a.cluster > 1 ? dsmem_addr(join + (rank * rows + r % rows) * stride, r / rows) : 0u;
-    for (int c0 = (warp >> 3) * 16; c0 < a.tn; c0 += 32) {
+    for (int c0 = (warp >> 3) * 16; c0 < a.tn; c0 += 48) {
       uint32_t v[16];
       tmem_ld_32x32b_x16(tmem + half * 64 + c0 + ((uint32_t)((warp & 3) * 32) << 16), v);
       tmem_ld_wait();
@@ -442,7 +450,25 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn_linear() {
   return fn;
 }
 
+// Blocks that split K: while all clusters are resident at once (of 4 blocks 36, of 8 blocks 15 on 152
+// SMs: the occupancy query's numbers) and each has two steps.
+int tc_cluster(int64_t tiles, int64_t steps) {
+  const int most[4] = {num_sms(), num_sms() / 2, num_sms() * 36 / 152, num_sms() * 15 / 152};
+  int cluster = 1;
+  for (int l = 1; l < 4 && tiles <= most[l] && steps >= 2 << l; ++l) cluster = 1 << l;
+  return cluster;
+}
+
 }  // namespace
+
+// From 17 rows always.  From 9 rows where one round of blocks has work for half the SMs, or K is
+// short (us, this kernel and the other one at 16 rows: 2048 x 2048 6.1 and 7.4, 18432 x 7168 24 and
+// 27, 4096 x 7168 13.2 and 12.0, 131072 x 4096 97 and 78).
+bool linear_w4_tc_faster(int T, int64_t N, int K) {
+  if (T <= 8 || T > 16) return T > 16;
+  const int64_t tiles = (N + kTcRows - 1) / kTcRows;
+  return tiles <= num_sms() && (K <= 2048 || 2 * tiles * tc_cluster(tiles, (K + 127) / 128) >= num_sms());
+}
 
 cudaError_t launch_linear_w4_tc(const void* x, const uint8_t* codes, const uint8_t* sf,
                                 const float* ts, int T, int64_t N, int K, bool f32, void* y,
@@ -471,11 +497,9 @@ cudaError_t launch_linear_w4_tc(const void* x, const uint8_t* codes, const uint8
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  // K over a cluster while all clusters are resident at once: of 4 blocks 36, of 8 blocks 15 on 152 SMs
   const int64_t tiles = (N + kTcRows - 1) / kTcRows;
   const int64_t steps = (K + 127) / 128;
-  const int most[4] = {num_sms(), num_sms() / 2, num_sms() * 36 / 152, num_sms() * 15 / 152};
-  for (int l = 1; l < 4 && tiles <= most[l] && steps >= 2 << l; ++l) a.cluster = 1 << l;
+  a.cluster = tc_cluster(tiles, steps);
   a.kslice = (int)((steps + a.cluster - 1) / a.cluster) * 128;
   auto kern = ts ? (f32 ? linear_w4_tc_kernel<false, true> : linear_w4_tc_kernel<false, false>)
                  : (f32 ? linear_w4_tc_kernel<true, true> : linear_w4_tc_kernel<true, false>);

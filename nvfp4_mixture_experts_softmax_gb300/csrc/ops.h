@@ -14,7 +14,9 @@ cudaError_t launch_mx_decode_perm(const uint8_t* codes, const uint8_t* sf, int T
                                   int shared, int Rt, const int32_t* inv, void* xb_perm,
                                   int32_t* status, cudaStream_t s);
 
-// The 4-bit matrix-vector product for many rows of x (linear_w4_tc.cu); ts null: MXFP4.
+// The 4-bit matrix-vector product for many rows of x (linear_w4_tc.cu), whether it is the faster one,
+// and its launch; ts null: MXFP4.
+bool linear_w4_tc_faster(int T, int64_t N, int K);
 cudaError_t launch_linear_w4_tc(const void* x, const uint8_t* codes, const uint8_t* sf,
                                 const float* ts, int T, int64_t N, int K, bool f32, void* y,
                                 cudaStream_t s);

@@ -176,6 +176,67 @@ def test_nonfinite(moe, T):
     assert bool(y[T - 1].isnan().all()) and torch.equal(y[:T - 1], clean[:T - 1])
 
 
+# N and K around the splits of the kernel for many rows: tiles of 256 weight rows, blocks of a cluster
+# that split K in steps of 128 (one of them with nothing left), scales that are not loaded in one piece
+MANY = [(9, 1, 32), (10, 255, 1184), (16, 257, 2048), (17, 300, 2144), (24, 256, 2176), (31, 520, 96), (33, 2000, 1056),
+        (40, 2049, 4096), (48, 3841, 2080), (49, 9217, 512), (64, 10001, 640), (63, 19457, 288), (20, 40000, 160)]
+
+
+@pytest.mark.parametrize("T,N,K", MANY)
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_exact_many_rows(moe, T, N, K, fmt):
+    """|x| <= 2: terms of at most 96 units of 1/4, whole sums of up to 4096 of them below 2^24."""
+    codes, sf, ts = random_weights(N, K, fmt, True, T + N + K)
+    g = torch.Generator(device="cuda").manual_seed(K)
+    x = torch.randint(-2, 3, (T, K), device="cuda", generator=g).bfloat16()
+    want = (x.double() @ decode(codes, sf, ts).t()).float()
+    buf = torch.full((T + 2, N), 7.0, device="cuda")
+    assert torch.equal(moe.linear_w4(x, codes, sf, ts, y=buf[1:T + 1]), want)
+    assert bool((buf[0] == 7).all()) and bool((buf[T + 1] == 7).all())
+    # scales that start two bytes into an allocation
+    off = torch.empty(sf.numel() + 2, dtype=torch.uint8, device="cuda")[2:].view(sf.shape)
+    off.copy_(sf)
+    assert torch.equal(moe.linear_w4(x, codes, off, ts, out_dtype=torch.float32), want)
+
+
+@pytest.mark.parametrize("T", [12, 50])
+def test_many_rows_captured_and_on_two_streams(moe, T):
+    """Calls that follow one another on a stream, in a graph, and beside another stream's."""
+    codes, sf, ts = random_weights(1024, 1024, "nvfp4", True, 3)
+    ts.fill_(2.0 ** -6)
+    w = decode(codes, sf, ts)
+    x = torch.randint(-1, 2, (T, 1024), device="cuda").bfloat16()
+
+    def chain(x):
+        return moe.linear_w4(moe.linear_w4(x, codes, sf, ts), codes, sf, ts, out_dtype=torch.float32)
+
+    def formula(x):
+        mid = (x.double() @ w.t()).float().bfloat16().double()
+        return mid @ w.t(), mid.abs() @ w.abs().t()
+
+    def close(y, x):
+        want, size = formula(x)   # the first product is exact; K / 128 + 16 roundings as above
+        return bool(((y.double() - want).abs() <= (1024 / 128 + 16) * 2.0 ** -21 * size).all())
+
+    chain(x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = chain(x)
+    for seed in range(3):
+        x.copy_(torch.randint(-1, 2, (T, 1024), device="cuda", generator=torch.Generator(device="cuda").manual_seed(seed)))
+        graph.replay()
+        assert close(y, x)
+    side, other = torch.cuda.Stream(), torch.randint(-1, 2, (T, 1024), device="cuda").bfloat16()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        b = [chain(other) for _ in range(20)]
+    a = [chain(x) for _ in range(20)]
+    torch.cuda.synchronize()
+    assert all(close(t, x) for t in a) and all(close(t, other) for t in b)
+    assert all(torch.equal(t, a[0]) for t in a) and all(torch.equal(t, b[0]) for t in b)
+
+
 def test_large_offsets(moe):
     """More than 2^32 bytes of codes: the last rows."""
     N, K = 70000, 131072
@@ -185,6 +246,18 @@ def test_large_offsets(moe):
     sf = torch.full((N, K // 32), 127, dtype=torch.uint8, device="cuda")
     codes[-3:] = 0x22                     # ones
     x = torch.ones(2, K, dtype=torch.bfloat16, device="cuda")
+    y = moe.linear_w4(x, codes, sf, out_dtype=torch.float32)
+    assert bool((y[:, -3:] == K).all()) and not y[:, :-3].any()
+
+
+def test_large_offsets_many_rows(moe):
+    N, K = 70000, 131072
+    if torch.cuda.mem_get_info()[0] < (12 << 30):
+        pytest.skip("not enough memory")
+    codes = torch.zeros(N, K // 2, dtype=torch.uint8, device="cuda")
+    sf = torch.full((N, K // 32), 127, dtype=torch.uint8, device="cuda")
+    codes[-3:] = 0x22                     # ones
+    x = torch.ones(17, K, dtype=torch.bfloat16, device="cuda")
     y = moe.linear_w4(x, codes, sf, out_dtype=torch.float32)
     assert bool((y[:, -3:] == K).all()) and not y[:, :-3].any()
 
