@@ -32,6 +32,7 @@
 // us.  A block of 16 rows whose eight warps read x from L1 in BF16, without staging, took 77.6, 166,
 // 22.2 / 39 and 2.8 us.
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "ops.h"
@@ -41,6 +42,7 @@ namespace nvfp4moe {
 namespace {
 
 constexpr int kLinMaxTokens = 64;
+constexpr int kLinSmem = 222 * 1024;  // dynamic shared memory of a block, at most
 constexpr int kLinRows = 16;          // of x in this kernel
 constexpr int kTopGuess = 9;         // exponent of a row's largest element: the first scale's
 constexpr int kTopLeast = -6;        // bounds
@@ -520,7 +522,7 @@ cudaError_t launch_linear(LinearArgs a, cudaStream_t s) {
   // Columns of x that fit beside the join buffer, with `blocks` blocks an SM.  Two blocks leave L1
   // some 30 KB: with 110 KB each 36864 x 7168 at 7 rows takes 66 us, with one block an SM 41.
   auto fitting = [&](bool joins, int blocks) {
-    const int room = (blocks == 2 ? 96 : 222) * 1024 - (joins ? L::kJoinBytes : 0);
+    const int room = (blocks == 2 ? 96 * 1024 : kLinSmem) - (joins ? L::kJoinBytes : 0);
     return (room / rows - 64) / 2 / L::kStep * L::kStep;
   };
   // Larger clusters leave SMs of each GPC idle: on 152 SMs 36 clusters of four fit, 15 of eight
@@ -566,18 +568,24 @@ cudaError_t launch_linear(LinearArgs a, cudaStream_t s) {
     }
   const size_t smem = (size_t)rows * (a.kc * 2 + 64) +
                       (a.ks > 1 || a.cluster > 1 ? L::kJoinBytes : 0);
-  if (smem > 40 * 1024) {
+  if (smem > 40 * 1024) {   // always to the most: another thread's launch may need more than this one's
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)smem);
+                                               kLinSmem);
     if (e != cudaSuccess) return e;
   }
   // Shared memory for these blocks only, the rest is L1: the codes of a row come in 16-byte loads, and
-  // a small L1 loses their lines between them.
-  {
-    const size_t used = per_sm * (smem + 2048);
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                               (int)std::min<size_t>(100, (used * 100 + 233471) / 233472));
+  // a small L1 loses their lines between them (36864 x 7168 at 8 rows: 68 us where the driver makes
+  // room for two blocks, 41 with room for one).  The setting stays with the function, so it is made
+  // anew only where another is wanted (0.8 us of host time at 2048 x 2048).
+  static std::atomic<int> carved[64];   // by device; 0: never set
+  const int percent = (int)std::min<size_t>(100, (per_sm * (smem + 2048) * 100 + 233471) / 233472);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || carved[dev].load(std::memory_order_relaxed) != percent) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, percent);
     if (e != cudaSuccess) return e;
+    if (dev < 64) carved[dev].store(percent, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(cols * a.cluster));

@@ -35,6 +35,7 @@ namespace nvfp4moe {
 
 namespace {
 
+constexpr int kTcMaxTokens = 64;
 constexpr int kTcRows = 256;           // two accumulators of 128 rows
 constexpr int kTcCodeStages = 5;       // ring of codes: 128 columns each
 constexpr int kTcXStages = 4;          // ring of x: 128 columns each, as two swizzled tiles of 64
@@ -459,6 +460,12 @@ int tc_cluster(int64_t tiles, int64_t steps) {
   return cluster;
 }
 
+// Alignment, the rings of codes and x, and a cluster's join buffer.
+size_t tc_smem(int tn, bool joins) {
+  return 1024 + (size_t)kTcCodeStages * kTcCodeBytes + (size_t)kTcXStages * tn * 256 +
+         (joins ? (size_t)(tn + 4) * kTcRows * 4 : 0u);
+}
+
 }  // namespace
 
 // From 17 rows always.  From 9 rows where one round of blocks has work for half the SMs, or K is
@@ -503,10 +510,10 @@ cudaError_t launch_linear_w4_tc(const void* x, const uint8_t* codes, const uint8
   a.kslice = (int)((steps + a.cluster - 1) / a.cluster) * 128;
   auto kern = ts ? (f32 ? linear_w4_tc_kernel<false, true> : linear_w4_tc_kernel<false, false>)
                  : (f32 ? linear_w4_tc_kernel<true, true> : linear_w4_tc_kernel<true, false>);
-  const size_t smem = 1024 + (size_t)kTcCodeStages * kTcCodeBytes +
-                      (size_t)kTcXStages * a.tn * 256 +
-                      (a.cluster > 1 ? (size_t)(a.tn + 4) * kTcRows * 4 : 0u);
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const size_t smem = tc_smem(a.tn, a.cluster > 1);
+  // (always to the most: another thread's launch may need more than this one's)
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)tc_smem(kTcMaxTokens, true));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * a.cluster));

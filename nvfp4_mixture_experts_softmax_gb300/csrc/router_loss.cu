@@ -726,9 +726,9 @@ int moe_router_loss(const float* logits, const int32_t* topk_ids, const uint8_t*
     auto kern = sp ? router_loss_kernel<G, VPL, VEC, true> : router_loss_kernel<G, VPL, VEC, false>;
     constexpr int threads = loss_threads<VPL>();
     const size_t smem = 4 * (size_t)E * (threads / 32 + 1);
-    if (smem > 48 * 1024) {
+    if (smem > 48 * 1024) {   // always to the layout's most: another thread's launch may need more
       const cudaError_t ea = cudaFuncSetAttribute(
-          kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+          kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * G * VPL * (threads / 32 + 1));
       if (ea != cudaSuccess) return ea;
     }
     return launch_pdl(kern, dim3(nb), dim3(threads), smem, s, a);

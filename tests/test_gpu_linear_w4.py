@@ -250,6 +250,34 @@ def test_large_offsets(moe):
     assert bool((y[:, -3:] == K).all()) and not y[:, :-3].any()
 
 
+def test_threads_with_different_sizes(moe):
+    """Two host threads whose launches of one kernel need different shared memory."""
+    import threading
+    sizes = [[(8, 64, 13312), (8, 64, 4096)], [(16, 64, 6656), (16, 64, 4480)], [(64, 512, 4096), (20, 512, 4096)]]
+    work = {s: random_weights(s[1], s[2], "nvfp4", True, 1) for pair in sizes for s in pair}
+    x = {s: torch.ones(s[0], s[2], device="cuda").bfloat16() for s in work}
+    want = {s: moe.linear_w4(x[s], *work[s]) for s in work}
+    for pair in sizes:
+        wrong = []
+
+        def run(s):
+            try:
+                with torch.cuda.stream(torch.cuda.Stream()):
+                    out = [moe.linear_w4(x[s], *work[s]) for _ in range(300)]
+                    torch.cuda.current_stream().synchronize()
+                wrong.extend(1 for o in out if not torch.equal(o, want[s]))
+            except Exception as error:
+                wrong.append(error)
+
+        torch.cuda.synchronize()
+        threads = [threading.Thread(target=run, args=(s,)) for s in pair]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        assert not wrong
+
+
 def test_large_offsets_many_rows(moe):
     N, K = 70000, 131072
     if torch.cuda.mem_get_info()[0] < (12 << 30):
