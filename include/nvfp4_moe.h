@@ -313,7 +313,8 @@ int moe_router_loss_backward(const float* logits, const int32_t* topk_ids, const
  * [2^-6, 2^10)), an E8M0 scale is exact down to 2^-36 of its row's largest and zero below.  Rows of x
  * whose largest element is in [2^-6, 2^10), and E8M0 scales in [2^-23, 2^13], are the fast case
  * there; others cost a second pass over x or over that tile.  NaN and infinities of x stay in their
- * row of y, NaN scales in their column.
+ * row of y, NaN scales in their column.  A block whose wait for its own copies runs out (about a
+ * second) leaves NaN.
  * K a multiple of 32, at most 2^20; N at most 2^30; x and codes 16-byte aligned, sf 2.  More than
  * 64 rows: MOE_ERR_UNSUPPORTED_SHAPE.  No workspace, one launch.
  * ------------------------------------------------------------------------------------------- */

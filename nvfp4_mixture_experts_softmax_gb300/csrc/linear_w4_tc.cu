@@ -364,18 +364,19 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tmap_x,
 
   // ---- epilogue: lane = weight row, column = token ----
   tc_fence_before();
-  __syncthreads();   // the MMA thread has seen the accumulators complete (or gave up)
+  __syncthreads();   // the MMA warp has seen the accumulators complete (or gave up)
   tc_fence_after();
   const bool bad = s_abort != 0u;
   // The factors that undo the decoding's power of two, the exact one first where it cannot overflow
   const float ts = kMx ? 4.0f : __ldg(a.ts);
-  const float up = kMx || fabsf(ts) > 1.0f ? ts : ts * 256.0f, up0 = !kMx && fabsf(ts) > 1.0f ? 256.0f : 1.0f;
+  const bool large = !kMx && fabsf(ts) > 1.0f;
+  const float up0 = large ? 256.0f : 1.0f, up = kMx || large ? ts : ts * 256.0f;
   auto store = [&](int t, int64_t n, float v) {
     if (t >= a.T || n >= a.N) return;
     if constexpr (kF32) static_cast<float*>(a.y)[(int64_t)t * a.N + n] = v;
     else static_cast<__nv_bfloat16*>(a.y)[(int64_t)t * a.N + n] = __float2bfloat16_rn(v);
   };
-  // A cluster's block sums 128 / cluster of the rows: join[block][row][token].  Rows of tn + 4
+  // A cluster's block sums 256 / cluster of the rows: join[block][row][token].  Rows of tn + 4
   // words put a warp's 16-byte stores in all banks.
   const int rows = kTcRows / a.cluster, stride = a.tn + 4;
   float* join = reinterpret_cast<float*>(x_ring + kTcXStages * x_bytes);
