@@ -15,7 +15,9 @@
 // tensor memory.  256 rows, because x is read from L2 once a block: at 128 rows (two blocks an SM)
 // it was twice the bytes of the codes.
 // With few tiles the blocks of a cluster split K; each sums its share of the rows from all blocks'
-// accumulators, which they store into its shared memory, in block order.
+// accumulators, which they store into its shared memory, in block order.  With more tiles than SMs a
+// block works through several; its rings run on, and the warps that decode store a tile before they
+// go on to the next.
 // Every wait is bounded; a block whose wait ran out stores NaN.
 //
 // Measured (device time of a call, NVFP4; in brackets warp-level MMAs): 18432 x 7168, 32 rows 25 us
@@ -27,6 +29,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "ops.h"
 #include "w4.cuh"
@@ -148,11 +151,15 @@ struct TcArgs {
   int K;
   int cluster;      // blocks that split K
   int kslice;       // columns of a block, a multiple of 128
+  int tiles;        // of 256 weight rows
   bool wide;        // the scales of 128 columns are one aligned load
   void* y;
 };
 
-template <bool kMx, bool kF32>
+// kMany: a block works through several tiles (its rings run on from one to the next).  The steps of a
+// block with one tile are 2 to 4% shorter without that; a block for each tile takes 106 us for 131072
+// x 4096 at 64 rows (102 so), 31.7 for 146704 x 640 at 24 (23.5).
+template <bool kMx, bool kF32, bool kMany>
 __global__ void __launch_bounds__(kTcThreads, 1)
 linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tmap_x,
                     const __grid_constant__ CUtensorMap tmap_c, const TcArgs a) {
@@ -160,12 +167,14 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tmap_x,
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ uint64_t c_full[kTcCodeStages], c_empty[kTcCodeStages], x_full[kTcXStages],
-      x_empty[kTcXStages], a_full[kTcAStages], a_empty[kTcAStages], acc_full;
+      x_empty[kTcXStages], a_full[kTcAStages], a_empty[kTcAStages], acc_full, acc_empty, drained;
   __shared__ uint32_t s_tmem, s_issued_x, s_issued_c;
   __shared__ volatile uint32_t s_abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)blockIdx.x % a.cluster;
-  const int64_t row0 = (int64_t)((int)blockIdx.x / a.cluster) * kTcRows;
+  const int first = (int)blockIdx.x / a.cluster;   // tiles first, + gridDim.x, ..
+  const int ntile = kMany ? (a.tiles - first + (int)gridDim.x - 1) / (int)gridDim.x : 1;
+  auto row0 = [&](int t) { return ((int64_t)first + (int64_t)t * gridDim.x) * kTcRows; };
   const int kb = rank * a.kslice, ke = min(a.K, kb + a.kslice);
   const int np = max(0, (ke - kb + 127) / 128);   // steps of 128 columns; behind K all are zeros
   const uint32_t x_bytes = (uint32_t)a.tn * 256u;
@@ -191,7 +200,9 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tmap_x,
       mbar_init(smem_u32(a_full + i), 8);    // the eight warps that decode it
       mbar_init(smem_u32(a_empty + i), 1);
     }
-    mbar_init(smem_u32(&acc_full), 1);
+    mbar_init(smem_u32(&acc_full), 1);              // a tile's MMAs
+    mbar_init(smem_u32(&acc_empty), kTcDecWarps);   // its accumulators have been read
+    mbar_init(smem_u32(&drained), 1);
     s_issued_x = s_issued_c = 0u;
     s_abort = 0u;
     fence_barrier_init();
@@ -203,12 +214,28 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tmap_x,
   griddep_wait();
   griddep_launch();
 
+  // The factors that undo the decoding's power of two, the exact one first where it cannot overflow
+  const float ts = kMx ? 4.0f : __ldg(a.ts);
+  const bool large = !kMx && fabsf(ts) > 1.0f;
+  const float up0 = large ? 256.0f : 1.0f, up = kMx || large ? ts : ts * 256.0f;
+  auto store = [&](int t, int64_t n, float v) {
+    if (t >= a.T || n >= a.N) return;
+    if constexpr (kF32) static_cast<float*>(a.y)[(int64_t)t * a.N + n] = v;
+    else static_cast<__nv_bfloat16*>(a.y)[(int64_t)t * a.N + n] = __float2bfloat16_rn(v);
+  };
+  // A cluster's block sums 256 / cluster of the rows: join[block][row][token].  Rows of tn + 4
+  // words put a warp's 16-byte stores in all banks.
+  const int rows = kTcRows / a.cluster, stride = a.tn + 4;
+  float* join = reinterpret_cast<float*>(x_ring + kTcXStages * x_bytes);
+
   if (warp < kTcDecWarps) {
-    // ---- decode: one weight row a thread ----
+    // ---- decode: one weight row a thread; after a tile's steps its accumulators' store ----
     const int quad = warp & 3, half = (warp >> 2) & 1, set = warp >> 3;
     const int r = half * 128 + quad * 32 + lane;
-    const int64_t row = min(row0 + r, a.N - 1);   // rows behind the last: not stored
-    const uint8_t* ps = a.sf + row * (a.K / kBlk);
+    auto scales_of = [&](int t) {   // (rows behind the last are not stored)
+      return a.sf + min(row0(t) + r, a.N - 1) * (a.K / kBlk);
+    };
+    const uint8_t* ps = a.sf;
     const uint32_t a_lane = tmem + kTcACol + (uint32_t)half * 64u + ((uint32_t)(quad * 32) << 16);
     const uint8_t* c_lane = smem + r * 64;
     const int swz = (r >> 1) & 3;   // the 64-byte swizzle: a row's chunk index xor (row / 2) % 4
@@ -240,15 +267,67 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tmap_x,
         }
       }
     };
+    bool ok = true;
+    // lane = weight row, column = token
+    auto epilogue = [&](int t) {
+      if (np > 0 && ok) ok = __all_sync(0xffffffffu, tc_wait(&acc_full, (uint32_t)t & 1u));
+      tc_fence_after();
+      if (a.cluster > 1) cluster_wait();
+      const uint32_t to =
+          a.cluster > 1 ? dsmem_addr(join + (rank * rows + r % rows) * stride, r / rows) : 0u;
+      for (int c0 = set * 16; c0 < a.tn; c0 += 48) {
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(tmem + half * 64 + c0 + ((uint32_t)(quad * 32) << 16), v);
+        tmem_ld_wait();
+        float f[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          f[i] = np == 0 ? 0.0f : __uint_as_float(v[i]) * up0 * up;
+          if (!ok) f[i] = __uint_as_float(0x7FC00000u);
+        }
+        if (a.cluster > 1) {
+#pragma unroll
+          for (int i = 0; i < 16; i += 4)
+            st_dsmem_f32x4(to + (uint32_t)(c0 + i) * 4u, f[i], f[i + 1], f[i + 2], f[i + 3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) store(c0 + i, row0(t) + r, f[i]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0 && ok) mbar_arrive(smem_u32(&acc_empty));
+    };
     int slot = set, cslot = set;
     uint32_t ph = 0u, cph = 0u;
-    bool ok = true;
-    if (set < np) load_scales(set);
-    for (int p = set; p < np; p += 3) {
+    // this warp's steps are every third of all its block's; tile t, its step p; the next one's
+    // scales are loaded a step ahead
+    int t = 0, p = 0, done = 0;
+    auto advance = [&](int by) {
+      p += by;
+      if constexpr (kMany) {
+        const int was = t;
+        for (; p >= np && t < ntile; ++t) p -= np;
+        if (t != was && t < ntile) ps = scales_of(t);
+      } else {
+        t = p >= np ? 1 : 0;
+      }
+    };
+    if (np > 0) {
+      ps = scales_of(0);
+      advance(set);
+      if (t < ntile) load_scales(p);
+    }
+    while (np > 0 && t < ntile) {
+      if constexpr (kMany) {
+        for (; done < t; ++done) epilogue(done);
+        if (!ok) break;
+      }
       uint32_t ss[kMx ? 1 : 2];
 #pragma unroll
       for (int u = 0; u < (kMx ? 1 : 2); ++u) ss[u] = s[u];
-      load_scales(p + 3);
+      advance(3);
+      if (!kMany || t < ntile) load_scales(p);   // (one tile: behind the last step the last ones again)
       ok = __all_sync(0xffffffffu, tc_wait(c_full + cslot, cph));
       if (!ok) break;
       const uint8_t* cp = c_lane + cslot * kTcCodeBytes;
@@ -307,6 +386,7 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tmap_x,
       if (lane == 0) mbar_arrive(smem_u32(a_full + slot));
       ph ^= 1u;
     }
+    for (; done < ntile; ++done) epilogue(done);
     if (!ok && lane == 0) s_abort = 1u;
   } else if (warp == kTcXWarp || warp == kTcCodeWarp) {
     if (lane == 0) {
@@ -316,24 +396,26 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tmap_x,
       uint64_t* empty = x ? x_empty : c_empty;
       int slot = 0;
       uint32_t ph = 0u;
-      for (int i = 0; i < np; ++i) {
-        if (!tc_wait(empty + slot, ph ^ 1u)) {
-          s_abort = 1u;
-          break;
+      uint32_t issued = 0u;
+      bool ok = true;
+      for (int t = 0; t < ntile && ok; ++t)
+        for (int i = 0; i < np; ++i) {
+          ok = tc_wait(empty + slot, ph ^ 1u);
+          if (!ok) break;
+          const uint32_t fb = smem_u32(full + slot);
+          mbar_arrive_expect_tx(fb, x ? x_bytes : (uint32_t)kTcCodeBytes);
+          if (x) {
+            const uint32_t to = smem_u32(x_ring) + slot * x_bytes;
+            tma_load_2d(to, &tmap_x, kb + i * 128, 0, fb);
+            tma_load_2d(to + x_bytes / 2, &tmap_x, kb + i * 128 + 64, 0, fb);
+          } else {
+            tma_load_2d(smem_u32(smem) + slot * kTcCodeBytes, &tmap_c, kb / 2 + i * 64, (int)row0(t), fb);
+          }
+          ++issued;
+          if (++slot == stages) { slot = 0; ph ^= 1u; }
         }
-        const uint32_t fb = smem_u32(full + slot);
-        mbar_arrive_expect_tx(fb, x ? x_bytes : (uint32_t)kTcCodeBytes);
-        if (x) {
-          const uint32_t to = smem_u32(x_ring) + slot * x_bytes;
-          tma_load_2d(to, &tmap_x, kb + i * 128, 0, fb);
-          tma_load_2d(to + x_bytes / 2, &tmap_x, kb + i * 128 + 64, 0, fb);
-          s_issued_x = (uint32_t)i + 1u;
-        } else {
-          tma_load_2d(smem_u32(smem) + slot * kTcCodeBytes, &tmap_c, kb / 2 + i * 64, (int)row0, fb);
-          s_issued_c = (uint32_t)i + 1u;
-        }
-        if (++slot == stages) { slot = 0; ph ^= 1u; }
-      }
+      if (!ok) s_abort = 1u;
+      (x ? s_issued_x : s_issued_c) = issued;
     }
     __syncwarp();
   } else {
@@ -342,78 +424,45 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tmap_x,
     int slot = 0, xs = 0;
     uint32_t ph = 0u, xph = 0u;
     bool ok = true;
-    for (int i = 0; i < np; ++i) {
-      ok = __all_sync(0xffffffffu, tc_wait(x_full + xs, xph)) &&
-           __all_sync(0xffffffffu, tc_wait(a_full + slot, ph));
+    for (int t = 0; t < ntile && np > 0 && ok; ++t) {
+      ok = __all_sync(0xffffffffu, tc_wait(&acc_empty, ((uint32_t)t & 1u) ^ 1u));
       if (!ok) break;
       tc_fence_after();
-      const uint64_t b0 = db + (uint64_t)((xs * x_bytes) >> 4);
-      const uint32_t a0 = tmem + kTcACol + (uint32_t)slot * 128u;
-      tc_mma_64(tmem, a0, b0, idesc, i != 0 ? 1u : 0u);
-      tc_mma_64(tmem, a0 + 32u, b0 + (x_bytes >> 5), idesc, 1u);
-      tc_commit_elected(x_empty + xs);
-      tc_commit_elected(a_empty + slot);
-      if (++slot == kTcAStages) { slot = 0; ph ^= 1u; }
-      if (++xs == kTcXStages) { xs = 0; xph ^= 1u; }
+      for (int i = 0; i < np; ++i) {
+        ok = __all_sync(0xffffffffu, tc_wait(x_full + xs, xph)) &&
+             __all_sync(0xffffffffu, tc_wait(a_full + slot, ph));
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t b0 = db + (uint64_t)((xs * x_bytes) >> 4);
+        const uint32_t a0 = tmem + kTcACol + (uint32_t)slot * 128u;
+        tc_mma_64(tmem, a0, b0, idesc, i != 0 ? 1u : 0u);
+        tc_mma_64(tmem, a0 + 32u, b0 + (x_bytes >> 5), idesc, 1u);
+        tc_commit_elected(x_empty + xs);
+        tc_commit_elected(a_empty + slot);
+        if (++slot == kTcAStages) { slot = 0; ph ^= 1u; }
+        if (++xs == kTcXStages) { xs = 0; xph ^= 1u; }
+      }
+      if (ok) tc_commit_elected(&acc_full);
     }
-    // (after an expired wait this still waits for the MMAs issued before)
-    tc_commit_elected(&acc_full);
-    if (!__all_sync(0xffffffffu, tc_wait(&acc_full, 0u))) ok = false;
+    if (!ok) {   // the MMAs issued before the wait that ran out
+      tc_commit_elected(&drained);
+      tc_wait(&drained, 0u);
+    }
     if (!ok && lane == 0) s_abort = 1u;
   }
 
-  // ---- epilogue: lane = weight row, column = token ----
+  __syncwarp();
+  if (a.cluster > 1 && warp >= kTcDecWarps) cluster_wait();
   tc_fence_before();
-  __syncthreads();   // the MMA warp has seen the accumulators complete (or gave up)
-  tc_fence_after();
-  const bool bad = s_abort != 0u;
-  // The factors that undo the decoding's power of two, the exact one first where it cannot overflow
-  const float ts = kMx ? 4.0f : __ldg(a.ts);
-  const bool large = !kMx && fabsf(ts) > 1.0f;
-  const float up0 = large ? 256.0f : 1.0f, up = kMx || large ? ts : ts * 256.0f;
-  auto store = [&](int t, int64_t n, float v) {
-    if (t >= a.T || n >= a.N) return;
-    if constexpr (kF32) static_cast<float*>(a.y)[(int64_t)t * a.N + n] = v;
-    else static_cast<__nv_bfloat16*>(a.y)[(int64_t)t * a.N + n] = __float2bfloat16_rn(v);
-  };
-  // A cluster's block sums 256 / cluster of the rows: join[block][row][token].  Rows of tn + 4
-  // words put a warp's 16-byte stores in all banks.
-  const int rows = kTcRows / a.cluster, stride = a.tn + 4;
-  float* join = reinterpret_cast<float*>(x_ring + kTcXStages * x_bytes);
-  if (a.cluster > 1) cluster_wait();
-  if (warp < kTcDecWarps) {
-    const int half = (warp >> 2) & 1, r = half * 128 + (warp & 3) * 32 + lane;
-    const uint32_t to = a.cluster > 1 ? dsmem_addr(join + (rank * rows + r % rows) * stride, r / rows) : 0u;
-    for (int c0 = (warp >> 3) * 16; c0 < a.tn; c0 += 48) {
-      uint32_t v[16];
-      tmem_ld_32x32b_x16(tmem + half * 64 + c0 + ((uint32_t)((warp & 3) * 32) << 16), v);
-      tmem_ld_wait();
-      float f[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        f[i] = np == 0 ? 0.0f : __uint_as_float(v[i]) * up0 * up;
-        if (bad) f[i] = __uint_as_float(0x7FC00000u);
-      }
-      if (a.cluster > 1) {
-#pragma unroll
-        for (int i = 0; i < 16; i += 4)
-          st_dsmem_f32x4(to + (uint32_t)(c0 + i) * 4u, f[i], f[i + 1], f[i + 2], f[i + 3]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) store(c0 + i, row0 + r, f[i]);
-      }
-    }
-  }
+  __syncthreads();   // every accumulator has been read, every MMA is done (or a wait ran out)
   // After an expired wait TMA loads may still be in flight: the last ring's worth is waited for.
-  if (bad && (warp == kTcXWarp || warp == kTcCodeWarp) && lane == 0) {
+  if (s_abort != 0u && (warp == kTcXWarp || warp == kTcCodeWarp) && lane == 0) {
     const bool x = warp == kTcXWarp;
     const uint32_t n = x ? s_issued_x : s_issued_c, stages = x ? kTcXStages : kTcCodeStages;
     for (uint32_t i = n > stages ? n - stages : 0u; i < n; ++i)
       if (!tc_wait((x ? x_full : c_full) + i % stages, (i / stages) & 1u))
         break;
   }
-  tc_fence_before();
-  __syncthreads();
   if (warp == kTcMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTcCols);
@@ -431,7 +480,7 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tmap_x,
         sum.z += v.z;
         sum.w += v.w;
       }
-      const int64_t n = row0 + rank * rows + r;
+      const int64_t n = row0(0) + rank * rows + r;
       store(t, n, sum.x);
       store(t + 1, n, sum.y);
       store(t + 2, n, sum.z);
@@ -483,7 +532,7 @@ cudaError_t launch_linear_w4_tc(const void* x, const uint8_t* codes, const uint8
                                 cudaStream_t s) {
   auto encode = encode_fn_linear();
   if (!encode) return cudaErrorNotSupported;
-  TcArgs a{sf, ts, T, (T + 15) / 16 * 16, N, K, 1, 0, false, y};
+  TcArgs a{sf, ts, T, (T + 15) / 16 * 16, N, K, 1, 0, 0, false, y};
   a.wide = K % 128 == 0 && is_aligned(sf, ts ? 8 : 4);
   CUtensorMap tmap_x, tmap_c;
   const cuuint32_t estr[2] = {1u, 1u};
@@ -508,16 +557,21 @@ cudaError_t launch_linear_w4_tc(const void* x, const uint8_t* codes, const uint8
   const int64_t tiles = (N + kTcRows - 1) / kTcRows;
   const int64_t steps = (K + 127) / 128;
   a.cluster = tc_cluster(tiles, steps);
+  a.tiles = (int)tiles;
   a.kslice = (int)((steps + a.cluster - 1) / a.cluster) * 128;
-  auto kern = ts ? (f32 ? linear_w4_tc_kernel<false, true> : linear_w4_tc_kernel<false, false>)
-                 : (f32 ? linear_w4_tc_kernel<true, true> : linear_w4_tc_kernel<true, false>);
+  auto pick = [&](auto many) {
+    constexpr bool kMany = decltype(many)::value;
+    return ts ? (f32 ? linear_w4_tc_kernel<false, true, kMany> : linear_w4_tc_kernel<false, false, kMany>)
+              : (f32 ? linear_w4_tc_kernel<true, true, kMany> : linear_w4_tc_kernel<true, false, kMany>);
+  };
+  auto kern = tiles > num_sms() ? pick(std::true_type{}) : pick(std::false_type{});
   const size_t smem = tc_smem(a.tn, a.cluster > 1);
   // (always to the most: another thread's launch may need more than this one's)
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)tc_smem(kTcMaxTokens, true));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * a.cluster));
+  cfg.gridDim = dim3((unsigned)(a.cluster > 1 ? tiles * a.cluster : std::min<int64_t>(tiles, num_sms())));
   cfg.blockDim = dim3(kTcThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;

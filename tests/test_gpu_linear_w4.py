@@ -179,7 +179,8 @@ def test_nonfinite(moe, T):
 # N and K around the splits of the kernel for many rows: tiles of 256 weight rows, blocks of a cluster
 # that split K in steps of 128 (one of them with nothing left), scales that are not loaded in one piece
 MANY = [(9, 1, 32), (10, 255, 1184), (16, 257, 2048), (17, 300, 2144), (24, 256, 2176), (31, 520, 96), (33, 2000, 1056),
-        (40, 2049, 4096), (48, 3841, 2080), (49, 9217, 512), (64, 10001, 640), (63, 19457, 288), (20, 40000, 160)]
+        (40, 2049, 4096), (48, 3841, 2080), (49, 9217, 512), (64, 10001, 640), (63, 19457, 288), (20, 40000, 160),
+        (17, 120001, 32), (64, 99999, 224), (33, 79900, 416)]   # several tiles a block, fewer steps than warp groups
 
 
 @pytest.mark.parametrize("T,N,K", MANY)
