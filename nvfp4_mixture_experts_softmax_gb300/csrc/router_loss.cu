@@ -726,7 +726,9 @@ int moe_router_loss(const float* logits, const int32_t* topk_ids, const uint8_t*
     auto kern = sp ? router_loss_kernel<G, VPL, VEC, true> : router_loss_kernel<G, VPL, VEC, false>;
     constexpr int threads = loss_threads<VPL>();
     const size_t smem = 4 * (size_t)E * (threads / 32 + 1);
-    if (smem > 48 * 1024) {   // always to the layout's most: another thread's launch may need more
+    // 48 KB hold the kernel's own few hundred bytes too.  (Always to the layout's most: another
+    // thread's launch may need more.)
+    if (smem > 40 * 1024) {
       const cudaError_t ea = cudaFuncSetAttribute(
           kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * G * VPL * (threads / 32 + 1));
       if (ea != cudaSuccess) return ea;
