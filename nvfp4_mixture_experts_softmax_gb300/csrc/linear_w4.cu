@@ -12,9 +12,9 @@
 // instruction (measured 27 T codes/s over the GPU; placing the bits of a BF16 by hand 13.7; HBM
 // delivers 13.4), so weights and x are F16:
 //   * an E2M1 value times an E4M3 scale is exact in F16 (at most 6 significant bits, 2^-10 to
-//     2688).  So is one times an E8M0 scale of 2^-23 .. 2^13; a tile that meets another scale is
-//     done again with each row's largest scale at 2^13: scales below 2^-36 of the row's largest
-//     become zero;
+//     2688).  So is one times an E8M0 scale of 2^-23 .. 2^13; a warp that meets another scale, in a
+//     block that is not all zeros, does its part of the tile again in BF16, where every scale is
+//     exact;
 //   * a row of x is multiplied by a power of two: 2^6 if its largest element is in [2^-6, 2^10),
 //     otherwise the one that brings it to [2^15, 2^16) (one more pass over x).  Elements down to
 //     2^-32 of the F16 top keep all of BF16's bits; smaller ones are rounded to a multiple of
@@ -36,6 +36,7 @@
 
 #include "common.cuh"
 #include "ops.h"
+#include "w4.cuh"
 
 namespace nvfp4moe {
 
@@ -65,13 +66,22 @@ struct LinTile {
   static constexpr int kFrags = kMt * NT;
   static constexpr int kJoinBytes = kWarps * kFrags * 512;
 };
-constexpr int kScaleWindow = 37;     // binades of E8M0 scales that are exact in F16 at one offset
-constexpr int kScaleLow = 104;       // lowest scale byte at offset 0
+constexpr int kScaleWindow = 37;     // binades of E8M0 scales that are exact in F16
+constexpr int kScaleLow = 104;       // scale byte of the lowest
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -106,13 +116,13 @@ struct RowCodes {
   }
 };
 
-// Scale of unit i (8 codes) of 32 as F16x2, from their scale bytes; MXFP4: 2^(byte - 127 - down),
-// zero below 2^-24 and infinite above 2^15 (the tile is then done again), 255 NaN.
+// Scale of unit i (8 codes) of 32 as F16x2, from their scale bytes; MXFP4: 2^(byte - 127), outside
+// F16's range some finite value (codes that are not zero are then done again), 255 NaN.
 template <bool kMx>
-__device__ __forceinline__ uint32_t unit_scale(uint32_t bytes, int i, int down) {
+__device__ __forceinline__ uint32_t unit_scale(uint32_t bytes, int i) {
   if constexpr (kMx) {
-    const int f = (int)bytes - 112 - down;   // F16 exponent field; subnormal below 1
-    uint32_t h = f > 0 ? (uint32_t)min(f, 31) << 10 : 0x200u >> min(-f, 31);
+    const int f = (int)bytes - 112;   // F16 exponent field; subnormal below 1
+    uint32_t h = f > 0 ? (uint32_t)min(f, 30) << 10 : 0x200u >> min(-f, 31);
     if (bytes == 255u) h = 0x7E00u;
     return h | (h << 16);
   } else {
@@ -222,15 +232,67 @@ __device__ __noinline__ void find_shifts(const uint16_t* x, int T, int K, int* s
   }
 }
 
-// The largest scale byte of a row (255, NaN, left out) for each lane of its quad.
-__device__ __noinline__ int row_scale_top(const uint8_t* sf, int n) {
-  int top = 0;
-  for (int i = threadIdx.x & 3; i < n; i += 4) {
-    const int b = __ldg(sf + i);
-    if (b != 255) top = max(top, b);
-  }
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  return max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+// A warp's part of a tile in BF16: rows row0 + 8 r + g, and of each kc columns from kb to ke those from
+// `first` on, 256 at every `step`, as the kernel's sweeps divide them among warps and with their layout of
+// lanes; the sums times up0 and up1 to out (kMt * NT fragments).  x comes from global memory as it is.
+// A placed code times 2^124 is a quarter of its value; times an E8M0 scale that is exact in BF16 (2^-130
+// to 1.5 * 2^127).  Not inlined, for the same reason as stage_x.
+template <int NT>
+__device__ __noinline__ void sweep_bf16(const uint16_t* x, const uint8_t* codes, const uint8_t* sf,
+                                        int T, int64_t N, int K, int64_t row0, int kb, int ke,
+                                        int kc, int first, int step, float up0, float up1,
+                                        float* out) {
+  using L = LinTile<NT>;
+  constexpr int kMt = L::kMt;
+  const int g = (threadIdx.x & 31) >> 2, q = threadIdx.x & 3;
+  float c[kMt][NT][4];
+#pragma unroll
+  for (int f = 0; f < L::kFrags * 4; ++f) c[f / (NT * 4)][f / 4 % NT][f % 4] = 0.0f;
+  for (int k0 = kb; k0 < ke; k0 += kc)
+    for (int k = k0 + first, k1 = min(ke, k0 + kc); k < k1; k += step)
+#pragma unroll 1
+      for (int h = 0; h < L::kHalves; ++h) {
+        const int at = min(k + h * 128 + q * 32, k1 - 32);   // (as in the kernel's load)
+        const bool in = k + h * 128 + q * 32 < k1;
+        RowCodes w[2 * kMt];
+#pragma unroll
+        for (int r = 0; r < 2 * kMt; ++r) {
+          const int64_t n = min(row0 + r * 8 + g, N - 1);
+          w[r].c = __ldg(reinterpret_cast<const uint4*>(codes + n * (K / 2) + (at >> 1)));
+          w[r].s = __ldg(sf + n * (K / 32) + at / 32);
+          w[r].s = w[r].s == 255u ? 0x7FC07FC0u : e8m0_scale_bf16x2(w[r].s);
+        }
+        float d[kMt][NT][4];   // (see the kernel's kApart)
+#pragma unroll
+        for (int f = 0; f < L::kFrags * 4; ++f) d[f / (NT * 4)][f / 4 % NT][f % 4] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t o[2 * kMt][4];
+#pragma unroll
+          for (int r = 0; r < 2 * kMt; ++r) {
+            e2m1x8_to_bf16x2_scaled_down(w[r].word(i), o[r]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[r][e] = mul_bf16x2(mul_bf16x2(o[r][e], kBf16x2Pow2_124), w[r].s);
+          }
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            if (j * 8 >= T) break;
+            const int t = min(j * 8 + g, T - 1);   // (sums of tokens behind T are not stored)
+            const uint4 xv = in ? __ldg(reinterpret_cast<const uint4*>(x + (int64_t)t * K + at + i * 8))
+                                : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int m = 0; m < kMt; ++m) {
+              mma_bf16(d[m][j], o[2 * m][0], o[2 * m + 1][0], o[2 * m][1], o[2 * m + 1][1], xv.x, xv.y);
+              mma_bf16(d[m][j], o[2 * m][2], o[2 * m + 1][2], o[2 * m][3], o[2 * m + 1][3], xv.z, xv.w);
+            }
+          }
+        }
+#pragma unroll
+        for (int f = 0; f < L::kFrags * 4; ++f)
+          c[f / (NT * 4)][f / 4 % NT][f % 4] += d[f / (NT * 4)][f / 4 % NT][f % 4];
+      }
+#pragma unroll
+  for (int f = 0; f < L::kFrags * 4; ++f) out[f] = c[f / (NT * 4)][f / 4 % NT][f % 4] * up0 * up1;
 }
 
 template <int NT, bool kMx, bool kF32>
@@ -296,7 +358,7 @@ linear_w4_kernel(LinearArgs a) {
 
   // A tile's rows 8 r + g; rows behind the last one read it again and are not stored.
   const uint8_t *pc, *ps;
-  int off[2 * kMt], down[kMx ? 2 * kMt : 1];
+  int off[2 * kMt];
   RowCodes st[kHalves][2 * kMt];
   float c[kMt][NT][4];
   // Part h of the step at column k behind k0: a lane's 32 of each 128 columns, so that a quad's
@@ -319,7 +381,8 @@ linear_w4_kernel(LinearArgs a) {
     return *reinterpret_cast<const uint4*>(xrow + j * 8 * stride + at);
   };
   // Adds columns k0 .. k1 of the tile (x of k0 at the start of shared memory) to c.  Returns
-  // whether this lane met a scale that F16 does not hold (kMx).
+  // whether this lane met a scale that F16 does not hold (kMx), in a block that is not all zeros (those
+  // may carry any scale).
   auto sweep = [&](int k0, int k1) {
     bool odd = false;
     // One column: the MMAs of four steps sum from zero and are added with rounded FP32 additions.
@@ -359,10 +422,10 @@ linear_w4_kernel(LinearArgs a) {
           uint32_t o[2 * kMt][4];
 #pragma unroll
           for (int r = 0; r < 2 * kMt; ++r) {
-            if (i % (kMx ? 4 : 2) == 0) sc[r] = unit_scale<kMx>(st[h][r].s, i, down[kMx ? r : 0]);
-            if (kMx && i == 0)
-              odd = odd || (st[h][r].s - (uint32_t)kScaleLow >= (uint32_t)kScaleWindow &&
-                            st[h][r].s != 255u);
+            if (i % (kMx ? 4 : 2) == 0) sc[r] = unit_scale<kMx>(st[h][r].s, i);
+            if (kMx && i == 0 && st[h][r].s - (uint32_t)kScaleLow >= (uint32_t)kScaleWindow &&
+                st[h][r].s != 255u)
+              odd = odd || ((st[h][r].c.x | st[h][r].c.y | st[h][r].c.z | st[h][r].c.w) & 0x77777777u) != 0u;
             decode8(st[h][r].word(i), sc[r], o[r]);
           }
 #pragma unroll
@@ -412,53 +475,40 @@ linear_w4_kernel(LinearArgs a) {
         off[r] = (int)(min(tile * L::kRows + g + r * 8, a.N - 1) - row);
     }
 #pragma unroll
-    for (int r = 0; r < (kMx ? 2 * kMt : 1); ++r) down[r] = 0;
+    for (int m = 0; m < kMt; ++m)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[m][j][i] = 0.0f;
+    bool odd = false;
 #pragma unroll 1
-    for (int attempt = 0;; ++attempt) {
-#pragma unroll
-      for (int m = 0; m < kMt; ++m)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) c[m][j][i] = 0.0f;
-      bool odd = false;
-#pragma unroll 1
-      for (int chunk = 0; chunk < chunks; ++chunk) {
-        const int k0 = kb + chunk * a.kc;
-        if (chunks > 1 && (it > 0 || attempt > 0 || chunk > 0)) {   // (the first is there)
-          __syncthreads();
-          stage_x<L::kFly>(a.x, a.T, a.K, k0, a.kc, ke, xs, s_shift, s_top);
-          __syncthreads();
-        }
-        if (tile < tiles) odd = sweep(k0, min(ke, k0 + a.kc)) || odd;
+    for (int chunk = 0; chunk < chunks; ++chunk) {
+      const int k0 = kb + chunk * a.kc;
+      if (chunks > 1 && (it > 0 || chunk > 0)) {   // (the first is there)
+        __syncthreads();
+        stage_x<L::kFly>(a.x, a.T, a.K, k0, a.kc, ke, xs, s_shift, s_top);
+        __syncthreads();
       }
-      if constexpr (!kMx) break;
-      odd = chunks > 1 ? __syncthreads_or(odd) : __any_sync(0xffffffffu, odd);
-      if (!odd || attempt == 1) break;
-#pragma unroll
-      for (int r = 0; r < 2 * kMt; ++r)
-        down[r] = row_scale_top(ps + (int64_t)off[r] * (a.K / kBlk), a.K / kBlk) - 140;
+      if (tile < tiles) odd = sweep(k0, min(ke, k0 + a.kc)) || odd;
     }
-    // to y's scale: the rows' (kMx) and x's powers of two and the tensor scale
+    // to y's scale: x's powers of two and the tensor scale
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 u = s_unscale[j * 8 + q * 2 + (i & 1)];   // (rows behind T: any)
 #pragma unroll
-        for (int m = 0; m < kMt; ++m) {
-          float v = c[m][j][i];
-          if constexpr (kMx) {
-            if (down[2 * m + (i >> 1)] != 0) {   // one exponent for both
-              const float2 d = pow2_factors(
-                  max(down[2 * m + (i >> 1)] - s_shift[j * 8 + q * 2 + (i & 1)], -252));
-              c[m][j][i] = v * d.x * d.y;
-              continue;
-            }
-          }
-          c[m][j][i] = v * u.x * u.y;
-        }
+        for (int m = 0; m < kMt; ++m) c[m][j][i] = c[m][j][i] * u.x * u.y;
       }
+    if constexpr (kMx) {
+      if (__any_sync(0xffffffffu, odd)) {
+        float again[L::kFrags * 4];
+        sweep_bf16<NT>(a.x, a.codes, a.sf, a.T, a.N, a.K, tile * L::kRows, kb, ke, a.kc,
+                       slice * kStep, a.ks * kStep, 4.0f, 1.0f, again);
+#pragma unroll
+        for (int f = 0; f < L::kFrags * 4; ++f) c[f / (NT * 4)][f / 4 % NT][f % 4] = again[f];
+      }
+    }
     if (!joins) {
       if (tile < tiles) {
 #pragma unroll

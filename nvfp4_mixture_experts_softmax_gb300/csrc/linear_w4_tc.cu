@@ -51,7 +51,6 @@ constexpr int kTcCodeWarp = 26;
 constexpr int kTcThreads = 864;
 constexpr uint32_t kTcCols = 512;      // tensor memory: accumulators, then the A ring
 constexpr uint32_t kTcACol = 128;
-constexpr uint32_t kTcPow2_124 = 0x7D807D80u;   // 2^124 in both halves
 
 // kind::f16 with FP32 accumulators, BF16 operands, K-major: see the grouped GEMM's descriptor.
 __device__ __forceinline__ uint32_t tc_idesc(int n) {
@@ -365,7 +364,7 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tmap_x,
               e2m1x8_to_bf16x2_scaled_down(w[i], o);
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                if (big) o[j] = mul_bf16x2(o[j], kTcPow2_124);
+                if (big) o[j] = mul_bf16x2(o[j], kBf16x2Pow2_124);
                 out[v * 16 + i * 4 + j] = mul_bf16x2(o[j], sc[i >> 1]);
               }
             }

@@ -35,6 +35,7 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 }
 
 constexpr uint32_t kBf16x2Pow2_126 = 0x7E807E80u;   // 2^126 in both halves
+constexpr uint32_t kBf16x2Pow2_124 = 0x7D807D80u;   // 2^124 in both halves
 constexpr uint32_t kBf16x2Pow2_120 = 0x7B807B80u;   // 2^120 in both halves
 
 constexpr uint32_t kBf16x2Pow2_118 = 0x7A807A80u;   // 2^118 in both halves
