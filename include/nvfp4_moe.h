@@ -306,14 +306,14 @@ int moe_router_loss_backward(const float* logits, const int32_t* topk_ids, const
  *     moe_quantize_act (of the BF16 matrix [N,K]) and moe_weights_export write them;
  *   MXFP4 (MOE_LINEAR_MXFP4): codes [N,K/2], sf [N,K/32] E8M0, ts NULL.
  * y [T,N] is BF16, or FP32 with MOE_LINEAR_F32_OUT (router logits).  The sums are FP32 in an order
- * that is fixed for a shape.  Every weight is exact: E2M1 x E4M3, and E2M1 x any E8M0 scale; a block of
- * zeros may carry any scale.  From 17 rows on, and for some matrices from 9, x is multiplied as it is.
- * Otherwise in F16, x scaled by a power of two for each row: an element of x keeps all its bits down
- * to 2^-32 of its row's largest (2^-24 of it at worst: smaller elements are rounded to half of 2^-39
- * of it, or of 2^-30 where it is in [2^-6, 2^10)).  Rows of x whose largest element is in
- * [2^-6, 2^10), and E8M0 scales in [2^-23, 2^13], are the fast case there; others cost a second pass
- * over x or over that tile.  NaN and infinities of x stay in their row of y, NaN scales in their
- * column.  A block whose wait for its own copies runs out (about a second) leaves NaN.
+ * that is fixed for a shape.  Every product is exact: E2M1 x E4M3 weights, E2M1 x any E8M0 scale (a
+ * block of zeros may carry any scale), times x as it is.  Of NVFP4 weights only those elements of x
+ * can lose bits that are 2^-176 of their row's largest.  Up to 16 rows, for most matrices, the fast
+ * case are rows of x whose elements are zero or in [2^-23, 2^10) and E8M0 scales in [2^-23, 2^13];
+ * other rows cost a second pass over x if none of their elements is below 2^-32 of their row's
+ * largest, otherwise the whole product takes about twice the time, as does a tile with other
+ * scales.  NaN and infinities of x stay in their row of y, NaN scales in their column.  A block whose
+ * wait for its own copies runs out (about a second) leaves NaN.
  * K a multiple of 32, at most 2^20; N at most 2^30; x and codes 16-byte aligned, sf 2.  More than
  * 64 rows: MOE_ERR_UNSUPPORTED_SHAPE.  No workspace, one launch.
  * ------------------------------------------------------------------------------------------- */

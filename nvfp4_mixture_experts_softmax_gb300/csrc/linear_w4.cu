@@ -15,11 +15,12 @@
 //     2688).  So is one times an E8M0 scale of 2^-23 .. 2^13; a warp that meets another scale, in a
 //     block that is not all zeros, does its part of the tile again in BF16, where every scale is
 //     exact;
-//   * a row of x is multiplied by a power of two: 2^6 if its largest element is in [2^-6, 2^10),
-//     otherwise the one that brings it to [2^15, 2^16) (one more pass over x).  Elements down to
-//     2^-32 of the F16 top keep all of BF16's bits; smaller ones are rounded to a multiple of
-//     2^-30 (2^-39 of the row's largest in the second case).  Half of that times sum |w| is below
-//     the roundings of an FP32 sum of the row's terms, 2^-24 of each.
+//   * a row of x is multiplied by a power of two: 2^6 if its elements are zero or in [2^-23, 2^10),
+//     otherwise the one that brings its largest to [2^15, 2^16) (one more pass over x).  From 2^-17 on
+//     F16 holds all of BF16's 8 bits; if an element lies lower even so, 2^32 below its row's largest,
+//     the whole product is done in BF16, whose exponents are FP32's, without staging x (18432 x 7168,
+//     1 / 8 rows 33 / 50 us).
+// So every product is exact, whichever type it takes.
 // With more tokens the MMAs weigh most (two cycles each on an SM's four tensor cores: 14 us for
 // 18432 x 7168 at 32 tokens), so linear_w4_tc.cu takes over.
 //
@@ -45,8 +46,10 @@ namespace {
 constexpr int kLinMaxTokens = 64;
 constexpr int kLinSmem = 222 * 1024;  // dynamic shared memory of a block, at most
 constexpr int kLinRows = 16;          // of x in this kernel
-constexpr int kTopGuess = 9;         // exponent of a row's largest element: the first scale's
-constexpr int kTopLeast = -6;        // bounds
+constexpr int kTopGuess = 9;         // largest exponent of an element of x at the first power of two
+constexpr int kF16Top = 15;          // exponents of F16
+constexpr int kF16Exact = -17;       // from which on it holds 8 significant bits
+constexpr int kBf16Top = 60;         // a row's largest in BF16 with NVFP4 weights
 
 // Tiling by the number of 8-token columns NT.  One column: 16-row tiles, 16 warps of 64 registers
 // and two blocks an SM, whose many warps hide the latency of the loads.  Two columns: x fills the
@@ -170,14 +173,14 @@ struct LinearArgs {
 };
 
 // Columns [k0, k0 + kc) of x, row t times 2^shift[t], to shared memory as F16 (zeros from column ke
-// on), and the largest magnitude of each row (BF16 bits) to top[t].  A warp takes a row's units
-// (8 columns) 32 at a time, kFly loads in flight.  Inside 128 columns, lane q's i-th unit
+// on); sets *bad if an element is not exact there at the first power of two.  A warp takes a row's
+// units (8 columns) 32 at a time, kFly loads in flight.  Inside 128 columns, lane q's i-th unit
 // (u = 4 q + i) sits at i * 64 + q * 16, so that a quad's loads of one i are 64 consecutive bytes;
 // rows are 64 bytes off a multiple of 128, so two rows fill all banks.  Not inlined: the kernel's
 // registers are the multiplication's.
 template <int kFly>
 __device__ __noinline__ void stage_x(const uint16_t* x, int T, int K, int k0, int kc, int ke,
-                                     uint8_t* xs, const int* shift, uint32_t* top) {
+                                     uint8_t* xs, const int* shift, uint32_t* bad) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int units = kc / 8, per = (units + kFly * 32 - 1) / (kFly * 32), stride = kc * 2 + 64;
   for (int v = warp; v < T * per; v += warps) {
@@ -190,7 +193,7 @@ __device__ __noinline__ void stage_x(const uint16_t* x, int T, int K, int k0, in
       d[b] = u < units && k0 + u * 8 < ke ? __ldg(src + u) : make_uint4(0u, 0u, 0u, 0u);
     }
     const float f = __uint_as_float((uint32_t)(shift[t] + 127) << 23);
-    uint32_t hi = 0u;
+    uint32_t hi = 0u, lo = 0x7FFF7FFFu;
 #pragma unroll
     for (int b = 0; b < kFly; ++b) {
       const int u = u0 + b * 32;
@@ -198,7 +201,10 @@ __device__ __noinline__ void stage_x(const uint16_t* x, int T, int K, int k0, in
       uint32_t w[4] = {d[b].x, d[b].y, d[b].z, d[b].w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        hi = __vmaxu2(hi, w[j] & 0x7FFF7FFFu);
+        // per half 0x8000 + magnitude - 1: unsigned, zeros are below all others; signed, above
+        const uint32_t m = (w[j] | 0x80008000u) - 0x00010001u;
+        hi = __vmaxu2(hi, m);
+        lo = __vmins2(lo, m);
         const __half2 hh = __floats2half2_rn(__uint_as_float(w[j] << 16) * f,
                                              __uint_as_float(w[j] & 0xFFFF0000u) * f);
         w[j] = *reinterpret_cast<const uint32_t*>(&hh);
@@ -206,48 +212,83 @@ __device__ __noinline__ void stage_x(const uint16_t* x, int T, int K, int k0, in
       *reinterpret_cast<uint4*>(xs + (size_t)t * stride + (u >> 4) * 256 + (u & 3) * 64 +
                                 ((u >> 2) & 3) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    hi = __reduce_max_sync(0xffffffffu, max(hi >> 16, hi & 0xFFFFu));
-    if (lane == 0) atomicMax(top + t, hi);
+    constexpr uint32_t kBelow = 0x8000u + ((uint32_t)(kTopGuess + 128) << 7) - 1u;
+    constexpr int kFrom = ((kF16Exact + kTopGuess - kF16Top + 127) << 7) - 1 - 0x8000;
+    const bool fits = max(hi >> 16, hi & 0xFFFFu) < kBelow &&
+                      min((int)(int16_t)(lo >> 16), (int)(int16_t)(lo & 0xFFFFu)) >= kFrom;
+    if (!__all_sync(0xffffffffu, fits) && lane == 0) *bad = 1u;   // (every writer writes the same)
   }
 }
 
-// The largest finite exponent of each row of x over all of K, as the shift that brings it to 15.
-__device__ __noinline__ void find_shifts(const uint16_t* x, int T, int K, int* shift) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int t = warp; t < T; t += blockDim.x >> 5) {
+// The largest finite magnitude of each row of x over all of K to hi[t] (BF16 bits, 0 before), the
+// smallest that is not zero to lo[t] (0xFFFF before).
+__device__ __noinline__ void find_range(const uint16_t* x, int T, int K, uint32_t* hi, uint32_t* lo) {
+  constexpr int kFly = 4;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int units = K / 8, per = (units + kFly * 32 - 1) / (kFly * 32);
+  for (int v = warp; v < T * per; v += warps) {
+    const int t = v / per, u0 = (v - t * per) * (kFly * 32) + lane;
     const uint4* row = reinterpret_cast<const uint4*>(x + (int64_t)t * K);
-    uint32_t hi = 0u;
-#pragma unroll 4
-    for (int u = lane; u < K / 8; u += 32) {
-      const uint4 v = __ldg(row + u);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint4 d[kFly];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t m = (w[i >> 1] >> (16 * (i & 1))) & 0x7FFFu;
-        if (m < 0x7F80u) hi = max(hi, m);
+    for (int b = 0; b < kFly; ++b)
+      d[b] = u0 + b * 32 < units ? __ldg(row + u0 + b * 32) : make_uint4(0u, 0u, 0u, 0u);
+    uint32_t top = 0u, low = 0x7FFF7FFFu;
+#pragma unroll
+    for (int b = 0; b < kFly; ++b) {
+      const uint32_t w[4] = {d[b].x, d[b].y, d[b].z, d[b].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        top = __vmaxu2(top, w[j] & 0x7FFF7FFFu);
+        low = __vmins2(low, (w[j] | 0x80008000u) - 0x00010001u);   // (see stage_x)
       }
     }
-    hi = __reduce_max_sync(0xffffffffu, hi);
-    if (lane == 0) shift[t] = hi == 0u ? 0 : min(15 - bf16_exponent(hi), 127);
+    top = max(top >> 16, top & 0xFFFFu);
+    if (top >= 0x7F80u) {   // without the infinities and NaN
+      top = 0u;
+#pragma unroll
+      for (int b = 0; b < kFly; ++b) {
+        const uint32_t w[4] = {d[b].x, d[b].y, d[b].z, d[b].w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t m = (w[i >> 1] >> (16 * (i & 1))) & 0x7FFFu;
+          if (m < 0x7F80u) top = max(top, m);
+        }
+      }
+    }
+    const int least = min((int)(int16_t)(low >> 16), (int)(int16_t)(low & 0xFFFFu));
+    top = __reduce_max_sync(0xffffffffu, top);
+    low = __reduce_min_sync(0xffffffffu, (uint32_t)(least + 0x8001));   // 0x10000: zeros only
+    if (lane == 0) {
+      atomicMax(hi + t, top);
+      atomicMin(lo + t, low);
+    }
   }
 }
 
 // A warp's part of a tile in BF16: rows row0 + 8 r + g, and of each kc columns from kb to ke those from
 // `first` on, 256 at every `step`, as the kernel's sweeps divide them among warps and with their layout of
-// lanes; the sums times up0 and up1 to out (kMt * NT fragments).  x comes from global memory as it is.
-// A placed code times 2^124 is a quarter of its value; times an E8M0 scale that is exact in BF16 (2^-130
-// to 1.5 * 2^127).  Not inlined, for the same reason as stage_x.
-template <int NT>
+// lanes; the sums to out (kMt * NT fragments).  x comes from global memory.
+// MXFP4: x as it is.  A placed code times 2^124 is a quarter of its value, times an E8M0 scale that is
+// exact in BF16 (2^-130 to 1.5 * 2^127): sums are a quarter of y, in range as far as y is.
+// NVFP4: a placed code times its scale and 2^118 is 2^-8 of the weight.  A row of x is multiplied by
+// 2^shift, which brings its largest to 2^60: sums of 2^20 terms are finite, and only elements 2^-176 of
+// the row's largest meet the end of FP32's range.
+// Not inlined, for the same reason as stage_x.
+template <int NT, bool kMx>
 __device__ __noinline__ void sweep_bf16(const uint16_t* x, const uint8_t* codes, const uint8_t* sf,
                                         int T, int64_t N, int K, int64_t row0, int kb, int ke,
-                                        int kc, int first, int step, float up0, float up1,
-                                        float* out) {
+                                        int kc, int first, int step, const int* shift, float* out) {
   using L = LinTile<NT>;
   constexpr int kMt = L::kMt;
   const int g = (threadIdx.x & 31) >> 2, q = threadIdx.x & 3;
   float c[kMt][NT][4];
 #pragma unroll
   for (int f = 0; f < L::kFrags * 4; ++f) c[f / (NT * 4)][f / 4 % NT][f % 4] = 0.0f;
+  uint32_t xscale[NT];   // 2^shift of this lane's rows of x, in both halves
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+    xscale[j] = kMx ? 0u : (uint32_t)(shift[min(j * 8 + g, T - 1)] + 127) * 0x00800080u;
   for (int k0 = kb; k0 < ke; k0 += kc)
     for (int k = k0 + first, k1 = min(ke, k0 + kc); k < k1; k += step)
 #pragma unroll 1
@@ -259,8 +300,15 @@ __device__ __noinline__ void sweep_bf16(const uint16_t* x, const uint8_t* codes,
         for (int r = 0; r < 2 * kMt; ++r) {
           const int64_t n = min(row0 + r * 8 + g, N - 1);
           w[r].c = __ldg(reinterpret_cast<const uint4*>(codes + n * (K / 2) + (at >> 1)));
-          w[r].s = __ldg(sf + n * (K / 32) + at / 32);
-          w[r].s = w[r].s == 255u ? 0x7FC07FC0u : e8m0_scale_bf16x2(w[r].s);
+          if constexpr (kMx) {
+            const uint32_t b = __ldg(sf + n * (K / 32) + at / 32);
+            w[r].s = b == 255u ? 0x7FC07FC0u : e8m0_scale_bf16x2(b);
+          } else {   // both scales, exact in BF16
+            const float2 f = e4m3x2_to_f32x2(
+                __ldg(reinterpret_cast<const uint16_t*>(sf + n * (K / 16) + at / 16)));
+            const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * 0x1p118f, f.y * 0x1p118f);
+            w[r].s = *reinterpret_cast<const uint32_t*>(&b);
+          }
         }
         float d[kMt][NT][4];   // (see the kernel's kApart)
 #pragma unroll
@@ -272,14 +320,19 @@ __device__ __noinline__ void sweep_bf16(const uint16_t* x, const uint8_t* codes,
           for (int r = 0; r < 2 * kMt; ++r) {
             e2m1x8_to_bf16x2_scaled_down(w[r].word(i), o[r]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[r][e] = mul_bf16x2(mul_bf16x2(o[r][e], kBf16x2Pow2_124), w[r].s);
+            for (int e = 0; e < 4; ++e)
+              o[r][e] = kMx ? mul_bf16x2(mul_bf16x2(o[r][e], kBf16x2Pow2_124), w[r].s)
+                            : mul_bf16x2(o[r][e], __byte_perm(w[r].s, 0u, (i & 2) ? 0x3232 : 0x1010));
           }
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
             if (j * 8 >= T) break;
             const int t = min(j * 8 + g, T - 1);   // (sums of tokens behind T are not stored)
-            const uint4 xv = in ? __ldg(reinterpret_cast<const uint4*>(x + (int64_t)t * K + at + i * 8))
-                                : make_uint4(0u, 0u, 0u, 0u);
+            uint4 xv = in ? __ldg(reinterpret_cast<const uint4*>(x + (int64_t)t * K + at + i * 8))
+                          : make_uint4(0u, 0u, 0u, 0u);
+            if constexpr (!kMx)
+              xv = make_uint4(mul_bf16x2(xv.x, xscale[j]), mul_bf16x2(xv.y, xscale[j]),
+                              mul_bf16x2(xv.z, xscale[j]), mul_bf16x2(xv.w, xscale[j]));
 #pragma unroll
             for (int m = 0; m < kMt; ++m) {
               mma_bf16(d[m][j], o[2 * m][0], o[2 * m + 1][0], o[2 * m][1], o[2 * m + 1][1], xv.x, xv.y);
@@ -292,7 +345,7 @@ __device__ __noinline__ void sweep_bf16(const uint16_t* x, const uint8_t* codes,
           c[f / (NT * 4)][f / 4 % NT][f % 4] += d[f / (NT * 4)][f / 4 % NT][f % 4];
       }
 #pragma unroll
-  for (int f = 0; f < L::kFrags * 4; ++f) out[f] = c[f / (NT * 4)][f / 4 % NT][f % 4] * up0 * up1;
+  for (int f = 0; f < L::kFrags * 4; ++f) out[f] = c[f / (NT * 4)][f / 4 % NT][f % 4];
 }
 
 template <int NT, bool kMx, bool kF32>
@@ -304,7 +357,8 @@ linear_w4_kernel(LinearArgs a) {
   constexpr bool kRefill = NT > 1;   // load a part of the next step as soon as this one's is used up
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int s_shift[kLinRows];        // rows of x: the power of two they are times
-  __shared__ uint32_t s_top[kLinRows];     // their largest magnitude
+  __shared__ uint32_t s_bad;               // x is not exact in F16 at the first power of two
+  __shared__ uint32_t s_hi[kLinRows], s_lo[kLinRows];   // then: a row's largest and smallest magnitude
   __shared__ float2 s_unscale[kLinRows];   // takes a row's sums to y, in two factors
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, q = lane & 3;
@@ -319,36 +373,52 @@ linear_w4_kernel(LinearArgs a) {
   const int64_t tile0 = (int64_t)col * groups + group;   // this group's first tile
   const int kb = rank * a.kslice, ke = min(a.K, kb + a.kslice);   // this block's columns
   for (int t = threadIdx.x; t < kLinRows; t += blockDim.x) {   // (blocks of one warp exist)
-    s_shift[t] = 15 - kTopGuess;
-    s_top[t] = 0u;
+    s_shift[t] = kF16Top - kTopGuess;
+    s_hi[t] = 0u;
+    s_lo[t] = 0xFFFFu;
   }
+  if (threadIdx.x == 0) s_bad = 0u;
   __syncthreads();
   griddep_wait();
   griddep_launch();
 
-  // x at the first scale; if a row's largest element (anywhere in the cluster's blocks) does not
-  // fit it, at the rows' own.  x that is too long for shared memory is staged again by chunks.
+  // x at the first power of two; if an element (in any of the cluster's blocks) is not exact there, at
+  // the rows' own; if one is not exact there either, not at all.  x that is too long for shared memory
+  // is staged again by chunks.
   const int chunks = (a.kslice + a.kc - 1) / a.kc;
+  bool direct = false;   // BF16, x from global memory; the same in all blocks of a cluster
   for (int attempt = 0;; ++attempt) {
     for (int chunk = chunks - 1; chunk >= 0; --chunk)
-      stage_x<L::kFly>(a.x, a.T, a.K, kb + chunk * a.kc, a.kc, ke, xs, s_shift, s_top);
+      stage_x<L::kFly>(a.x, a.T, a.K, kb + chunk * a.kc, a.kc, ke, xs, s_shift, &s_bad);
     __syncthreads();
     if (attempt == 1) break;
-    if (a.cluster > 1) cluster_sync();
-    bool fits = true;
-    for (int t = threadIdx.x; t < a.T; t += blockDim.x) {
-      uint32_t top = s_top[t];
-      if (a.cluster > 1)
-        for (int b = 0; b < a.cluster; ++b) top = max(top, ld_dsmem_u32(s_top + t, b));
-      fits = fits && (top == 0u || (top >= (uint32_t)(kTopLeast + 127) << 7 &&
-                                    top < (uint32_t)(kTopGuess + 128) << 7));
+    bool fits = s_bad == 0u;
+    if (a.cluster > 1) {
+      cluster_sync();
+      fits = (int)threadIdx.x >= a.cluster || ld_dsmem_u32(&s_bad, threadIdx.x) == 0u;
+      fits = __syncthreads_and(fits);
+      cluster_sync();   // (the others have read this block's flag)
     }
-    fits = __syncthreads_and(fits);
-    if (a.cluster > 1) cluster_sync();   // (the others have read this block's maxima)
     if (fits) break;
-    find_shifts(a.x, a.T, a.K, s_shift);
+    find_range(a.x, a.T, a.K, s_hi, s_lo);
     __syncthreads();
+    bool exact = true;   // infinities and NaN are
+    for (int t = threadIdx.x; t < a.T; t += blockDim.x) {
+      const uint32_t hi = s_hi[t];
+      const int up = hi == 0u ? 0 : min(kF16Top - bf16_exponent(hi), 127);
+      s_shift[t] = up;
+      exact = exact && (hi == 0u || bf16_exponent(s_lo[t]) + up >= kF16Exact);
+    }
+    direct = !__syncthreads_and(exact);
+    if (direct) {
+      if constexpr (!kMx) {
+        for (int t = threadIdx.x; t < a.T; t += blockDim.x)
+          s_shift[t] = min(s_shift[t] + kBf16Top - kF16Top, 127);
+      }
+      break;
+    }
   }
+  // (the thread that writes a row's shift reads it here)
   for (int t = threadIdx.x; t < kLinRows; t += blockDim.x) {
     float2 u = pow2_factors(-s_shift[t]);   // half on either side of the tensor scale
     if constexpr (!kMx) u.y *= __ldg(a.ts);
@@ -481,15 +551,27 @@ linear_w4_kernel(LinearArgs a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) c[m][j][i] = 0.0f;
     bool odd = false;
+    if (!direct) {
 #pragma unroll 1
-    for (int chunk = 0; chunk < chunks; ++chunk) {
-      const int k0 = kb + chunk * a.kc;
-      if (chunks > 1 && (it > 0 || chunk > 0)) {   // (the first is there)
-        __syncthreads();
-        stage_x<L::kFly>(a.x, a.T, a.K, k0, a.kc, ke, xs, s_shift, s_top);
-        __syncthreads();
+      for (int chunk = 0; chunk < chunks; ++chunk) {
+        const int k0 = kb + chunk * a.kc;
+        if (chunks > 1 && (it > 0 || chunk > 0)) {   // (the first is there)
+          __syncthreads();
+          stage_x<L::kFly>(a.x, a.T, a.K, k0, a.kc, ke, xs, s_shift, &s_bad);
+          __syncthreads();
+        }
+        if (tile < tiles) odd = sweep(k0, min(ke, k0 + a.kc)) || odd;
       }
-      if (tile < tiles) odd = sweep(k0, min(ke, k0 + a.kc)) || odd;
+    }
+    auto again = [&](float up) {   // this warp's part in BF16, times up
+      float sums[L::kFrags * 4];
+      sweep_bf16<NT, kMx>(a.x, a.codes, a.sf, a.T, a.N, a.K, tile * L::kRows, kb, ke, a.kc,
+                          slice * kStep, a.ks * kStep, s_shift, sums);
+#pragma unroll
+      for (int f = 0; f < L::kFrags * 4; ++f) c[f / (NT * 4)][f / 4 % NT][f % 4] = sums[f] * up;
+    };
+    if constexpr (!kMx) {
+      if (direct && tile < tiles) again(256.0f);
     }
     // to y's scale: x's powers of two and the tensor scale
 #pragma unroll
@@ -501,13 +583,7 @@ linear_w4_kernel(LinearArgs a) {
         for (int m = 0; m < kMt; ++m) c[m][j][i] = c[m][j][i] * u.x * u.y;
       }
     if constexpr (kMx) {
-      if (__any_sync(0xffffffffu, odd)) {
-        float again[L::kFrags * 4];
-        sweep_bf16<NT>(a.x, a.codes, a.sf, a.T, a.N, a.K, tile * L::kRows, kb, ke, a.kc,
-                       slice * kStep, a.ks * kStep, 4.0f, 1.0f, again);
-#pragma unroll
-        for (int f = 0; f < L::kFrags * 4; ++f) c[f / (NT * 4)][f / 4 % NT][f % 4] = again[f];
-      }
+      if (direct ? tile < tiles : __any_sync(0xffffffffu, odd)) again(4.0f);
     }
     if (!joins) {
       if (tile < tiles) {

@@ -82,3 +82,64 @@ def test_mxfp4_scales_far_apart(moe, T, N, K):
     y = moe.linear_w4(x, codes, sf, out_dtype=torch.float32).double()
     assert torch.equal(y[1::2], want[1::2])               # ordinary blocks only
     assert torch.equal(y[::2, N // 3], want[::2, N // 3])   # the odd one only
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("N,K", SHAPES)
+@pytest.mark.parametrize("T", ROWS)
+def test_elements_of_x_far_apart(moe, T, N, K, fmt):
+    """Each row of x has columns of two magnitudes; each row of weights is zero at one of the two, so
+    that the small elements stand alone in half of the outputs."""
+    codes, sf, g = mx_weights(N, K, N + K + 3)
+    ts = None
+    if fmt == "nvfp4":
+        sf = torch.exp2(torch.randint(0, 3, (N, K // 16), device="cuda", generator=g).float()).to(torch.float8_e4m3fn).view(torch.uint8)
+        ts = torch.tensor([0.25], device="cuda")
+    small = torch.rand(K // 2, device="cuda", generator=g).repeat_interleave(2) < 0.5        # columns
+    drop = small[None, ::2] == (torch.arange(N, device="cuda")[:, None] % 2 == 0)            # code bytes
+    codes = torch.where(drop, 0, codes).to(torch.uint8)
+    x = whole((T, K), 1, K + 5).double()
+    large_e = torch.tensor([0.0, -6, 60, -90, 3, 20, 120, 0], device="cuda", dtype=torch.float64)
+    small_e = torch.tensor([0.0, -26, -20, -130, -40, -13, 70, 0], device="cuda", dtype=torch.float64)
+    for first in range(8 if T == 1 else 1):                # which pairs meet in one call
+        row = (torch.arange(T, device="cuda") + first) % 8
+        xs = (x * torch.exp2(torch.where(small, small_e[row][:, None], large_e[row][:, None]))).bfloat16()
+        w = decode(codes, sf, ts)
+        want = (xs.double() @ w.t()).float()
+        # a partial sum is bounded only by the sum of the magnitudes: where that is beyond FP32 (some
+        # sums of 2^120), a partial sum may be infinite although the whole one is not
+        inside = xs.double().abs() @ w.abs().t() < torch.finfo(torch.float32).max
+        y = moe.linear_w4(xs, codes, sf, ts, out_dtype=torch.float32)
+        assert bool(((y == want) | ~inside).all()), first
+        y = moe.linear_w4(xs, codes, sf, ts)
+        assert bool(((y == want.bfloat16()) | ~inside).all()), first
+
+
+@pytest.mark.parametrize("T", [1, 8, 12, 20])
+def test_one_outlier_whose_weight_is_zero(moe, T):
+    """The outlier decides the power of two of its row, and then has no part in the sums."""
+    codes, sf, _ = mx_weights(64, 512, 5)
+    codes[:, 100] = 0
+    ordinary = whole((T, 512), 3, 6)
+    for outlier, rest in ((-6, -26), (9, -30), (10, 0), (30, -5), (-60, -133)):
+        x = (ordinary.double() * 2.0 ** rest).bfloat16()
+        x[:, 200] = 2.0 ** outlier
+        want = (x.double() @ decode(codes, sf).t()).float()
+        assert torch.equal(moe.linear_w4(x, codes, sf, out_dtype=torch.float32), want), (outlier, rest)
+
+
+@pytest.mark.parametrize("T", [1, 8, 12])
+def test_nonfinite_x_beside_a_wide_row(moe, T):
+    """NaN and infinity stay in their row of y where the product takes BF16."""
+    codes, sf, _ = mx_weights(64, 512, 7)
+    nv = torch.full((64, 32), 0x38, dtype=torch.uint8, device="cuda")     # ones
+    x = whole((T + 2, 512), 2, 8)[:T + 2].contiguous()
+    x = x[:T]
+    x[0, ::2] *= 2.0 ** -50
+    for args in ((codes, sf), (codes, nv, torch.ones(1, device="cuda"))):
+        clean = moe.linear_w4(x, *args, out_dtype=torch.float32)
+        for v in (float("nan"), float("inf")):
+            bad = x.clone()
+            bad[T - 1, 17] = v
+            y = moe.linear_w4(bad, *args, out_dtype=torch.float32)
+            assert torch.equal(y[:T - 1], clean[:T - 1]) and not bool(y[T - 1].isfinite().any())
