@@ -268,8 +268,8 @@ int moe_plan(const float* logits, int32_t T, int32_t E, int32_t k, int32_t* topk
 /* ---------------------------------------------------------------------------------------------
  * Router losses.  Per-expert counts, the balance loss and the z loss of one batch of routed
  * tokens, and the gradient of the logits.  A token counts unless mask (uint8 [T], may be NULL) is
- * 0 there - its logits and ids are then not read - or all its logits are -infinity; n tokens
- * count.  p are the token's expert probabilities over all E: softmax(logits), or with
+ * 0 there - its logits, ids and grad_topk_w are then not read - or all its logits are -infinity;
+ * n tokens count.  p are the token's expert probabilities over all E: softmax(logits), or with
  * MOE_FLAG_ROUTER_SQRTSOFTPLUS in flags s / sum(s), s = sqrt(softplus(logit)); lse = log sum
  * exp(logits) for either router.
  *   counts_e (int32 [E]): how often e stands in topk_ids [T,k];  tokens (int32 [1]): n;

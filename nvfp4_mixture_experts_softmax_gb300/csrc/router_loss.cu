@@ -44,26 +44,27 @@ __device__ __forceinline__ int expert_of(int sub, int i) {
   return (i / VEC) * G * VEC + sub * VEC + i % VEC;
 }
 
-// What a lane holds of one token: its logits, whether the mask keeps the token, its first slot's
-// id.
+// What a lane holds of one token: its logits and its first slot's id.
 template <int VPL>
 struct TokenRow {
   float v[VPL];
-  bool kept;
   int32_t id;
 };
 
-// Loads of one token's row (t < T, otherwise nothing is kept); row: logits + t * E.  Experts behind
-// E are -infinity.
+// Whether token t counts as far as the mask (if there is one: MASK) says.
+template <bool MASK>
+__device__ __forceinline__ bool kept_token(const uint8_t* __restrict__ mask, int64_t t, int64_t T) {
+  return t < T && (!MASK || __ldg(mask + t));
+}
+
+// Loads of one token's row if it is kept; row: logits + t * E.  Experts behind E, and all of a token
+// that is not kept (whose memory is not touched), are -infinity.
 template <int G, int VPL, int VEC>
 __device__ __forceinline__ void load_row(const float* __restrict__ row,
-                                         const int32_t* __restrict__ ids,
-                                         const uint8_t* __restrict__ mask, int64_t t, int64_t T,
+                                         const int32_t* __restrict__ ids, bool kept, int64_t t,
                                          int E, int k, int sub, TokenRow<VPL>& r) {
-  const bool in = t < T;
-  r.kept = in && (!mask || __ldg(mask + t));
-  r.id = in && ids && sub < k ? __ldg(ids + t * k + sub) : -1;
-  const int left = in ? E - sub * VEC : 0;   // experts from this lane's first on
+  r.id = kept && ids && sub < k ? __ldg(ids + t * k + sub) : -1;
+  const int left = kept ? E - sub * VEC : 0;   // experts from this lane's first on
   const float* p = row + sub * VEC;
 #pragma unroll
   for (int i = 0; i < VPL; i += VEC) {
@@ -175,7 +176,7 @@ constexpr int loss_threads() { return VPL <= 16 ? 640 : 512; }
 
 // One block takes every gridDim-th group of rows; its sums go to partials, or, if it is the only
 // block, straight to the outputs.
-template <int G, int VPL, int VEC, bool SQRTSP>
+template <int G, int VPL, int VEC, bool SQRTSP, bool MASK>
 __global__ void __launch_bounds__(loss_threads<VPL>(), 1) router_loss_kernel(LossArgs a) {
   constexpr int kThreads = loss_threads<VPL>(), kWarps = kThreads / 32;
   constexpr int R = 32 / G;   // rows of a warp at a time
@@ -221,7 +222,7 @@ __global__ void __launch_bounds__(loss_threads<VPL>(), 1) router_loss_kernel(Los
     sum = group_sum<G>(sum);
     if constexpr (SQRTSP) sc = group_sum<G>(sc);
     else sc = sum;
-    if (r.kept && top != -INFINITY) {
+    if (top != -INFINITY) {   // (also not if the mask took the token out)
       const float lse = fmaf(lg2_approx(sum), kLn2, top);
       z = fmaf(lse, lse, z);   // (the same on the G lanes; one of them is added up)
       ++n;
@@ -242,13 +243,20 @@ __global__ void __launch_bounds__(loss_threads<VPL>(), 1) router_loss_kernel(Los
     row += step * a.E;
   };
   TokenRow<VPL> r0, r1;
-  load_row<G, VPL, VEC>(row, a.ids, a.mask, t, a.T, a.E, a.k, sub, r0);
+  // The mask is read a round ahead of the row whose loads depend on it.
+  bool kept = MASK && kept_token<MASK>(a.mask, t, a.T);
+  auto load_next = [&](int64_t ahead, TokenRow<VPL>& r) {
+    load_row<G, VPL, VEC>(row + ahead * a.E, a.ids, MASK ? kept : t + ahead < a.T, t + ahead, a.E, a.k,
+                          sub, r);
+    if constexpr (MASK) kept = kept_token<MASK>(a.mask, t + ahead + step, a.T);
+  };
+  load_next(0, r0);
   while (true) {   // the warp's first row decides: t - lane / G
     if (t - lane / G >= a.T) break;
-    load_row<G, VPL, VEC>(row + step * a.E, a.ids, a.mask, t + step, a.T, a.E, a.k, sub, r1);
+    load_next(step, r1);
     take(r0);
     if (t - lane / G >= a.T) break;
-    load_row<G, VPL, VEC>(row + step * a.E, a.ids, a.mask, t + step, a.T, a.E, a.k, sub, r0);
+    load_next(step, r0);
     take(r1);
   }
   if (sub != 0) z = 0.0f, n = 0;
@@ -438,7 +446,7 @@ constexpr int kBwdWarps = kBwdThreads / 32;
 template <int VPL, bool SQRTSP>
 constexpr int bwd_blocks() { return VPL <= 16 && !SQRTSP ? 3 : 2; }
 
-template <int G, int VPL, int VEC, bool SQRTSP>
+template <int G, int VPL, int VEC, bool SQRTSP, bool MASK>
 __global__ void __launch_bounds__(kBwdThreads, (bwd_blocks<VPL, SQRTSP>()))
 router_loss_backward_kernel(LossBwdArgs a) {
   extern __shared__ float dyn[];
@@ -457,8 +465,13 @@ router_loss_backward_kernel(LossBwdArgs a) {
   const int32_t* ids = a.grad_w ? a.ids : nullptr;
   constexpr bool kAhead = VPL <= 16;   // two rows of 32 logits a lane would spill
   TokenRow<VPL> next;
-  if constexpr (kAhead)
-    load_row<G, VPL, VEC>(row, ids, a.mask, t, a.T, a.E, a.k, sub, next);
+  bool kept = kAhead && MASK && kept_token<MASK>(a.mask, t, a.T);   // (a round ahead, as above)
+  auto load_next = [&](int64_t rows_on) {
+    load_row<G, VPL, VEC>(row + rows_on * a.E, ids, MASK ? kept : t + rows_on < a.T, t + rows_on, a.E,
+                          a.k, sub, next);
+    if constexpr (MASK) kept = kept_token<MASK>(a.mask, t + rows_on + step, a.T);
+  };
+  if constexpr (kAhead) load_next(0);
   const int32_t n = __ldg(a.tokens);
   const float inv_n = n > 0 ? 1.0f / (float)n : 0.0f;
   const float gb = a.grad_losses ? __ldg(a.grad_losses) : 0.0f;
@@ -480,9 +493,13 @@ router_loss_backward_kernel(LossBwdArgs a) {
     const int64_t ahead = step * a.E;
     if constexpr (kAhead) {
       r = next;
-      load_row<G, VPL, VEC>(row + ahead, ids, a.mask, t + step, a.T, a.E, a.k, sub, next);
+      load_next(step);
     } else {
-      load_row<G, VPL, VEC>(row, ids, a.mask, t, a.T, a.E, a.k, sub, r);
+      load_row<G, VPL, VEC>(row, ids, kept_token<MASK>(a.mask, t, a.T), t, a.E, a.k, sub, r);
+      // Without a mask always true: the branch keeps the compiler from moving the arithmetic of the
+      // first logits between the loads of the others (32000 x 1024, softmax 51.7 us without it, 48.4
+      // with it; sqrt-softplus 64.7 and 61.9).
+      kept = MASK || !a.mask || __ldg(a.mask + t);
     }
     // (E, k) slots of the row: the first per lane, with its logit and weight gradient
     float l0 = -INFINITY, g0 = 0.0f;
@@ -494,7 +511,8 @@ router_loss_backward_kernel(LossBwdArgs a) {
 #pragma unroll
     for (int i = 1; i < VPL; ++i) top = nan_max(top, r.v[i]);
     top = group_max<G>(top);
-    const bool live = r.kept && top != -INFINITY;
+    // (not if the mask took the token out)
+    const bool live = (kAhead || kept) && top != -INFINITY;
     float sum = 0.0f, sc = 0.0f, fp = 0.0f, slope[SQRTSP ? VPL : 1];
 #pragma unroll
     for (int i0 = 0; i0 < VPL; i0 += VEC) {
@@ -723,7 +741,10 @@ int moe_router_loss(const float* logits, const int32_t* topk_ids, const uint8_t*
   a.status = reinterpret_cast<int32_t*>(workspace);
   cudaError_t e = with_layout(E, vec, [&](auto g, auto vpl, auto v) {
     constexpr int G = decltype(g)::value, VPL = decltype(vpl)::value, VEC = decltype(v)::value;
-    auto kern = sp ? router_loss_kernel<G, VPL, VEC, true> : router_loss_kernel<G, VPL, VEC, false>;
+    auto kern = sp ? (mask ? router_loss_kernel<G, VPL, VEC, true, true>
+                           : router_loss_kernel<G, VPL, VEC, true, false>)
+                   : (mask ? router_loss_kernel<G, VPL, VEC, false, true>
+                           : router_loss_kernel<G, VPL, VEC, false, false>);
     constexpr int threads = loss_threads<VPL>();
     const size_t smem = 4 * (size_t)E * (threads / 32 + 1);
     // 48 KB hold the kernel's own few hundred bytes too.  (Always to the layout's most: another
@@ -773,8 +794,10 @@ int moe_router_loss_backward(const float* logits, const int32_t* topk_ids, const
   const bool sp = (flags & MOE_FLAG_ROUTER_SQRTSOFTPLUS) != 0u;
   const cudaError_t e = with_layout(E, vec, [&](auto g, auto vpl, auto v) {
     constexpr int G = decltype(g)::value, VPL = decltype(vpl)::value, VEC = decltype(v)::value;
-    auto kern = sp ? router_loss_backward_kernel<G, VPL, VEC, true>
-                   : router_loss_backward_kernel<G, VPL, VEC, false>;
+    auto kern = sp ? (mask ? router_loss_backward_kernel<G, VPL, VEC, true, true>
+                           : router_loss_backward_kernel<G, VPL, VEC, true, false>)
+                   : (mask ? router_loss_backward_kernel<G, VPL, VEC, false, true>
+                           : router_loss_backward_kernel<G, VPL, VEC, false, false>);
     constexpr int rows = kBwdWarps * (32 / G), width = G * VPL;
     const int64_t most = (int64_t)(sp ? bwd_blocks<VPL, true>() : bwd_blocks<VPL, false>()) * num_sms();
     const int nb = (int)std::min<int64_t>(((int64_t)T + rows - 1) / rows, most);
