@@ -33,7 +33,6 @@
 // us.  A block of 16 rows whose eight warps read x from L1 in BF16, without staging, took 77.6, 166,
 // 22.2 / 39 and 2.8 us.
 #include <algorithm>
-#include <atomic>
 
 #include "common.cuh"
 #include "ops.h"
@@ -699,20 +698,6 @@ cudaError_t launch_linear(LinearArgs a, cudaStream_t s) {
                                                kLinSmem);
     if (e != cudaSuccess) return e;
   }
-  // Shared memory for these blocks only, the rest is L1: the codes of a row come in 16-byte loads, and
-  // a small L1 loses their lines between them (36864 x 7168 at 8 rows: 68 us where the driver makes
-  // room for two blocks, 41 with room for one).  The setting stays with the function, so it is made
-  // anew only where another is wanted (0.8 us of host time at 2048 x 2048).
-  static std::atomic<int> carved[64];   // by device; 0: never set
-  const int percent = (int)std::min<size_t>(100, (per_sm * (smem + 2048) * 100 + 233471) / 233472);
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev >= 64 || carved[dev].load(std::memory_order_relaxed) != percent) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, percent);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) carved[dev].store(percent, std::memory_order_relaxed);
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(cols * a.cluster));
   // a warp for each of a row's visits of stage_x, up to the block's size
@@ -721,15 +706,22 @@ cudaError_t launch_linear(LinearArgs a, cudaStream_t s) {
   cfg.blockDim = dim3((unsigned)std::max(a.warps, std::min(visits, L::kWarps)) * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[3];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)a.cluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
+  // Shared memory for these blocks only, the rest is L1: the codes of a row come in 16-byte loads, and
+  // a small L1 loses their lines between them (36864 x 7168 at 8 rows: 68 us where the driver makes
+  // room for two blocks, 41 with room for one).  Set with the launch, not with the function, whose
+  // other launches (another thread's, a graph's) want other sizes.
+  attr[1].id = cudaLaunchAttributePreferredSharedMemoryCarveout;
+  attr[1].val.sharedMemCarveout =
+      (unsigned)std::min<size_t>(100, (per_sm * (smem + 2048) * 100 + 233471) / 233472);
+  attr[2].id = cudaLaunchAttributeClusterDimension;
+  attr[2].val.clusterDim.x = (unsigned)a.cluster;
+  attr[2].val.clusterDim.y = 1;
+  attr[2].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = a.cluster > 1 ? 2 : 1;
+  cfg.numAttrs = a.cluster > 1 ? 3 : 2;
   return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
