@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes as C
 import functools
+import inspect
 import os
 
 import torch
@@ -406,18 +407,28 @@ _stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream",
 def _scoped(fn):
     """Calls fn(stream handle, ...) with its first tensor's device current, on `stream` if that is
     passed (what fn allocates then belongs to that stream) or on the device's current stream."""
+    sig = inspect.signature(fn)
+    params = list(sig.parameters.values())[1:]   # without the stream handle
+    name = params[0].name
+
     @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
+    def call(*args, stream=None, **kw):
+        first = args[0] if args else kw.get(name)
+        if first is None:
+            raise ValueError(f"{fn.__name__}: {name} is required")
         if not first.is_cuda:
             raise ValueError(f"{fn.__name__} needs CUDA tensors, got one on {first.device}")
         dev = first.get_device()
         if stream is None and dev == torch.cuda.current_device():
-            return fn(_stream_handle(dev), first, *args, **kw)
+            return fn(_stream_handle(dev), *args, **kw)
         if stream is not None and stream.device != first.device:
             raise ValueError(f"{fn.__name__}: the stream is on {stream.device}, the tensors on "
                              f"{first.device}")
         with torch.cuda.device(dev), torch.cuda.stream(stream):
-            return fn(_stream_handle(dev), first, *args, **kw)
+            return fn(_stream_handle(dev), *args, **kw)
+
+    call.__signature__ = sig.replace(parameters=params + [
+        inspect.Parameter("stream", inspect.Parameter.KEYWORD_ONLY, default=None)])
     return call
 
 
