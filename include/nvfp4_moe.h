@@ -236,7 +236,8 @@ int moe_rmsnorm_quantize_act(const void* x, const void* gamma, float eps, int64_
  *   residual or of x (in place); no other two buffers may overlap.  codes and sf are both given
  *   or both NULL; y may be NULL if they are given.
  * A 32-element block of y that holds an infinity or NaN gets scale byte 255 (NaN) and codes 0x7F
- * (NaN); the sum of squares is FP32, so rows with elements above 2^63 can overflow it (r = 0).
+ * (NaN); the sum of squares is FP32, so rows with elements above 2^63 can overflow it (r = 0), and
+ * with eps below 2^-100 rows whose elements are all below 2^-50 can underflow it (r infinite).
  * No workspace, one launch.  rows == 0 is MOE_OK. */
 int moe_add_rmsnorm_quantize_mx(const void* x, const void* residual, const void* gamma, float eps,
                                 int64_t rows, int64_t cols, void* h, uint8_t* codes, uint8_t* sf,
@@ -278,7 +279,8 @@ int moe_plan(const float* logits, int32_t T, int32_t E, int32_t k, int32_t* topk
  *                      [1] z = (1/n) sum_t lse_t^2.   n = 0: zeros.
  * An id outside [0, E) is not counted and leaves MOE_ERR_INVALID_ARG in the device status (first
  * word of the workspace).  NaN or +infinity logits of a token that counts make the losses NaN.
- * Sums run in a fixed order: the same call gives the same bits.
+ * Sums are FP32 and run in a fixed order: the same call gives the same bits.  Scores s below 2^-126
+ * (logits below -174) are zero.
  *
  * Backward: counts and tokens as moe_router_loss wrote them (constants of the gradient);
  * grad_losses: device FP32 [2], the gradients of the two losses (NULL: zeros); grad_topk_w: FP32
@@ -305,15 +307,20 @@ int moe_router_loss_backward(const float* logits, const int32_t* topk_ids, const
  *   NVFP4 (default): codes [N,K/2], sf [N,K/16] E4M3, ts: device FP32 tensor scale, as
  *     moe_quantize_act (of the BF16 matrix [N,K]) and moe_weights_export write them;
  *   MXFP4 (MOE_LINEAR_MXFP4): codes [N,K/2], sf [N,K/32] E8M0, ts NULL.
- * y [T,N] is BF16, or FP32 with MOE_LINEAR_F32_OUT (router logits).  The sums are FP32 in an order
- * that is fixed for a shape.  Every product is exact: E2M1 x E4M3 weights, E2M1 x any E8M0 scale (a
- * block of zeros may carry any scale), times x as it is.  Of NVFP4 weights only those elements of x
- * can lose bits that are 2^-176 of their row's largest.  Up to 16 rows, for most matrices, the fast
- * case are rows of x whose elements are zero or in [2^-23, 2^10) and E8M0 scales in [2^-23, 2^13];
- * other rows cost a second pass over x if none of their elements is below 2^-32 of their row's
- * largest, otherwise the whole product takes about twice the time, as does a tile with other
- * scales.  NaN and infinities of x stay in their row of y, NaN scales in their column.  A block whose
- * wait for its own copies runs out (about a second) leaves NaN.
+ * y [T,N] is BF16, or FP32 with MOE_LINEAR_F32_OUT (router logits).
+ * Every product is exact: E2M1 x E4M3 weights, E2M1 x any E8M0 scale (a block of zeros may carry any
+ * scale), times x as it is.  Of NVFP4 weights only those elements of x can lose bits that are 2^-176
+ * of their row's largest.  Up to 16 rows, for most matrices, the fast case are rows of x whose
+ * elements are zero or in [2^-23, 2^10) and E8M0 scales in [2^-23, 2^13]; other rows cost a second
+ * pass over x if none of their elements is below 2^-32 of their row's largest, otherwise the whole
+ * product takes about twice the time, as does a tile with other scales.
+ * The sums are FP32 in an order that is fixed for a shape, and the tensor cores truncate where they
+ * add: for chains of up to K / 16 additions from 9 rows on (fewer where few tiles leave K to several
+ * blocks), and of long rows from 2 (T K above 90112), otherwise 32 to 128.  Measured in FP32 output,
+ * relative to y, K = 2048 / 7168 / 16384: one row 2e-7 throughout, 64 rows 5e-7 / 2e-6 / 7e-6 with
+ * normal data and 2e-6 / 1e-5 / 3e-5 with all terms of one sign.
+ * NaN and infinities of x stay in their row of y, NaN scales in their column.  A block whose wait for
+ * its own copies runs out (about a second) leaves NaN.
  * K a multiple of 32, at most 2^20; N at most 2^30; x and codes 16-byte aligned, sf 2.  More than
  * 64 rows: MOE_ERR_UNSUPPORTED_SHAPE.  No workspace, one launch.
  * ------------------------------------------------------------------------------------------- */

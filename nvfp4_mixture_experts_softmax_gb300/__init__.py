@@ -397,6 +397,9 @@ def run(cfg: MoeConfig, wbuf, x, logits, k=None, y=None, workspace=None, debug=F
 
 
 # ---- operators around the layer ----
+#
+# Every function takes stream=, the torch.cuda.Stream to launch on (default: the current one).  None of
+# them records anything for autograd: a backward pass is a call of its own.
 
 # The current stream's handle of a device: torch's own accessor where it has it (0.1 us; the Stream
 # object costs 1.1 us of a call's 9)
@@ -405,8 +408,9 @@ _stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream",
 
 
 def _scoped(fn):
-    """Calls fn(stream handle, ...) with its first tensor's device current, on `stream` if that is
-    passed (what fn allocates then belongs to that stream) or on the device's current stream."""
+    """Calls fn(stream handle, ...) with its first tensor's device current, on `stream` (a
+    torch.cuda.Stream) if that is passed, which then owns what fn allocates, or on the device's
+    current stream."""
     sig = inspect.signature(fn)
     params = list(sig.parameters.values())[1:]   # without the stream handle
     name = params[0].name
@@ -465,7 +469,7 @@ def add_rmsnorm_quantize_mx(handle, x, residual, gamma, eps: float = 1e-6, want_
     h (absent without a residual), codes [rows, cols] u8 (E4M3) and sf [rows, cols/32] u8 (E8M0)
     unless quantize is False, y [rows, cols] BF16 (want_y) and rrms [rows] FP32 (want_rrms).
     out: a dict of preallocated tensors that takes the place of those switches; out["h"] may be
-    residual or x itself (in place).  stream: see run."""
+    residual or x itself (in place).  stream: a torch.cuda.Stream to launch on."""
     if x.dim() != 2 or x.shape[1] % 32:
         raise ValueError(f"x must be [rows, cols] with cols a multiple of 32, got {tuple(x.shape)}")
     rows, cols = shape = x.shape
@@ -505,7 +509,7 @@ def add_rmsnorm_backward(handle, dy, h, rrms, gamma, dh=None, out=None, workspac
     dy, h [rows, cols] BF16, rrms [rows] FP32, gamma [cols] BF16 as in the forward pass; dh: the
     gradient that reaches h over the residual stream (BF16, or None).  Returns a dict of dx
     [rows, cols] BF16 (the gradient of x and of the residual alike; out["dx"] may be dy or dh) and
-    dgamma [cols] FP32.  stream: see run."""
+    dgamma [cols] FP32.  stream: a torch.cuda.Stream to launch on."""
     if dy.dim() != 2 or dy.shape[1] % 32:
         raise ValueError(f"dy must be [rows, cols] with cols a multiple of 32, got {tuple(dy.shape)}")
     rows, cols = shape = dy.shape
@@ -560,7 +564,8 @@ def router_loss(handle, logits, topk_ids, mask=None, router: str = "softmax", ou
 
     Returns a dict of losses [2] FP32 (balance, z), counts [E] int32, tokens [1] int32 and probs
     [E] FP32 (mean expert probabilities); pass it to router_loss_backward.  An id outside [0, E)
-    is reported in the workspace's device status (last_device_status).  stream: see run."""
+    is reported in the workspace's device status (pass a workspace to read it with
+    last_device_status).  stream: a torch.cuda.Stream to launch on."""
     T, E, k = _routing_shape(logits, topk_ids)
     dev = logits.get_device()
     if out is None:
@@ -589,7 +594,9 @@ def router_loss_backward(handle, logits, topk_ids, stats, grad_losses=None, grad
                          router: str = "softmax", dlogits=None):
     """Gradient [T, E] FP32 of the logits from grad_losses [2] FP32 (on the device; the gradients
     of the balance and z losses) and grad_topk_w [T, k] FP32 (of the top-k weights); either may be
-    None.  stats: what router_loss returned for the same logits, ids, mask and router."""
+    None.  The latter comes from the caller's own backward pass through the experts, which this library
+    does not have.  stats: what router_loss returned for the same logits, ids, mask and router.
+    stream: a torch.cuda.Stream to launch on."""
     T, E, k = _routing_shape(logits, topk_ids)
     dev = logits.get_device()
     if dlogits is None:
@@ -614,10 +621,11 @@ LINEAR_MAX_TOKENS = 64
 
 @_scoped
 def linear_w4(handle, x, codes, sf, ts=None, out_dtype=torch.bfloat16, y=None):
-    """x [T, K] BF16 (T <= 64) times a 4-bit matrix: y [T, N] in out_dtype (bfloat16 or float32).
+    """x [T, K] BF16 (T <= LINEAR_MAX_TOKENS) times a 4-bit matrix: y [T, N] in out_dtype (bfloat16 or float32).
 
     codes [N, K/2] u8 with sf [N, K/16] u8 (E4M3) and ts [1] FP32: NVFP4, as quantize_act(W) gives
-    them; with sf [N, K/32] u8 (E8M0) and no ts: MXFP4.  stream: see run."""
+    them; with sf [N, K/32] u8 (E8M0) and no ts: MXFP4.
+    stream: a torch.cuda.Stream to launch on."""
     if x.dim() != 2 or codes.dim() != 2 or sf.dim() != 2:
         raise ValueError("x must be [T, K], codes [N, K/2] and sf [N, K/16] or [N, K/32]")
     (T, K), N, dev = x.shape, codes.shape[0], x.get_device()

@@ -650,11 +650,8 @@ cudaError_t launch_linear(LinearArgs a, cudaStream_t s) {
     const int room = (blocks == 2 ? 96 * 1024 : kLinSmem) - (joins ? L::kJoinBytes : 0);
     return (room / rows - 64) / 2 / L::kStep * L::kStep;
   };
-  // Larger clusters leave SMs of each GPC idle: on 152 SMs 36 clusters of four fit, 15 of eight
-  // (the occupancy query's numbers).
-  auto clusters = [](int cl) {
-    return cl == 8 ? num_sms() / 10 : num_sms() / cl - (cl == 4 ? 2 : 0);
-  };
+  // Clusters of four leave SMs of each GPC idle: on 152 SMs 36 fit (the occupancy query's number).
+  auto clusters = [](int cl) { return num_sms() / cl - (cl == 4 ? 2 : 0); };
   // The split of K over cluster blocks and warps, and the blocks an SM, that should finish first.
   double best = 0.0;
   int cols = 1, per_sm = 1;
@@ -686,11 +683,10 @@ cudaError_t launch_linear(LinearArgs a, cudaStream_t s) {
     per_sm = blocks;
     a.warps = (int)even * ks;
   };
-  for (int cl = 1; cl <= 8 && cl <= L::kFrags && cl <= steps; cl *= 2)
-    for (int ks = 1; ks <= L::kWarps; ks *= 2) {
-      if (ks > 1 && L::kWarps / ks > 15) continue;   // a named barrier for each group
+  // (a named barrier for each group: at most 8 of them if ks > 1)
+  for (int cl = 1; cl <= L::kFrags && cl <= steps; cl *= 2)
+    for (int ks = 1; ks <= L::kWarps; ks *= 2)
       for (int blocks = 1; blocks <= L::kPerSm; ++blocks) consider(cl, ks, blocks);
-    }
   const size_t smem = (size_t)rows * (a.kc * 2 + 64) +
                       (a.ks > 1 || a.cluster > 1 ? L::kJoinBytes : 0);
   if (smem > 40 * 1024) {   // always to the most: another thread's launch may need more than this one's

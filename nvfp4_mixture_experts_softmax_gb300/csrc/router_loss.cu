@@ -646,8 +646,9 @@ router_loss_backward_kernel(LossBwdArgs a) {
   }
 }
 
-// Lanes of one token's row for E experts, and the blocks of the loss kernel.  A batch of at most four rounds of one block's warps stays in one block, which then needs no
-// second launch; above, one block per SM.
+// Lanes of one token's row for E experts, and the blocks of the loss kernel.  A batch of at most four
+// rounds of one block's warps stays in one block, which then needs no second launch; above, one block
+// per SM.
 struct LossGrid {
   int lanes, blocks;
   LossGrid(int64_t T, int E) {
