@@ -315,10 +315,9 @@ int moe_router_loss_backward(const float* logits, const int32_t* topk_ids, const
  * pass over x if none of their elements is below 2^-32 of their row's largest, otherwise the whole
  * product takes about twice the time, as does a tile with other scales.
  * The sums are FP32 in an order that is fixed for a shape, and the tensor cores truncate where they
- * add: for chains of up to K / 16 additions from 9 rows on (fewer where few tiles leave K to several
- * blocks), and of long rows from 2 (T K above 90112), otherwise 32 to 128.  Measured in FP32 output,
- * relative to y, K = 2048 / 7168 / 16384: one row 2e-7 throughout, 64 rows 5e-7 / 2e-6 / 7e-6 with
- * normal data and 2e-6 / 1e-5 / 3e-5 with all terms of one sign.
+ * add.  FP32 output: chains of at most 256 additions up to K = 229376, then rounded ones, which leave
+ * 1e-6 of y with normal data and 8e-6 with all terms of one sign.  BF16 output from 9 rows on (and of long
+ * rows from 2): up to K / 16, of which 64 rows of K = 16384 lose 7e-6 and 3e-5 before the rounding.
  * NaN and infinities of x stay in their row of y, NaN scales in their column.  A block whose wait for
  * its own copies runs out (about a second) leaves NaN.
  * K a multiple of 32, at most 2^20; N at most 2^30; x and codes 16-byte aligned, sf 2.  More than

@@ -454,9 +454,9 @@ linear_w4_kernel(LinearArgs a) {
   // may carry any scale).
   auto sweep = [&](int k0, int k1) {
     bool odd = false;
-    // One column: the MMAs of four steps sum from zero and are added with rounded FP32 additions.
-    // The tensor cores truncate, which a chain of 256 MMAs turns into a bias of 1e-6; with more
-    // columns the second set of accumulators costs 15 to 25%, and their chains stay that long.
+    // The tensor cores truncate, which a chain of 256 MMAs turns into a bias of 1e-6 of the sum.  One
+    // column: the MMAs of four steps sum from zero and are added with rounded FP32 additions.  Two: a
+    // second set of accumulators costs 15 to 25%, so the split keeps the chains of FP32 output short.
     constexpr bool kApart = NT == 1;
     float d[kApart ? kMt : 1][kApart ? NT : 1][4];
     auto flush = [&](bool add) {
@@ -636,6 +636,10 @@ struct LinCost {
   static constexpr double kJoinUs[2] = {NT == 1 ? 2.0 : 3.0, 5.0};
 };
 
+// Two columns with FP32 output: steps of a warp, at most.  16 are 256 MMAs in one chain, whose truncation
+// leaves 1e-6 of y with normal data (32 3e-6, 64 6e-6); BF16 output does not need it.
+constexpr int kLinChain = 16;
+
 template <int NT, bool kMx, bool kF32>
 cudaError_t launch_linear(LinearArgs a, cudaStream_t s) {
   using L = LinTile<NT>;
@@ -655,9 +659,11 @@ cudaError_t launch_linear(LinearArgs a, cudaStream_t s) {
   // The split of K over cluster blocks and warps, and the blocks an SM, that should finish first.
   double best = 0.0;
   int cols = 1, per_sm = 1;
+  const int64_t chain = std::max<int64_t>(kLinChain, (steps + 4 * L::kWarps - 1) / (4 * L::kWarps));
   auto consider = [&](int cl, int ks, int blocks) {
     const bool joins = ks > 1 || cl > 1;
     const int64_t sl = (steps + cl - 1) / cl, groups = L::kWarps / ks;
+    if (NT > 1 && kF32 && (sl + ks - 1) / ks > chain) return;
     const int64_t slots = (int64_t)blocks * clusters(cl);
     const int64_t rounds = (tiles + groups * slots - 1) / (groups * slots);
     // no more groups a block than these rounds need: the tiles spread over the SMs

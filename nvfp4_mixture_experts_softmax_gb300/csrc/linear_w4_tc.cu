@@ -18,6 +18,12 @@
 // accumulators, which they store into its shared memory, in block order.  With more tiles than SMs a
 // block works through several; its rings run on, and the warps that decode store a tile before they
 // go on to the next.
+// The tensor core truncates where it adds: chains of 128 / 256 / 448 / 1024 MMAs of normal data end 4e-7 /
+// 1e-6 / 2e-6 / 6e-6 of y off.  FP32 output stays at 1e-6: above kTcChain steps they take turns on two or
+// four accumulators (up to 32 or 16 rows: what 64 columns hold), and a tile's K is worked through in parts,
+// like further tiles, that are added in FP32 in shared memory; the blocks of a cluster then read one
+// another's sums.  BF16 output does not need it.  (36864 x 7168, 24 / 64 rows: 42.9 / 49.4 us, one chain
+// 41.2 / 44.)
 // Every wait is bounded; a block whose wait ran out stores NaN.
 //
 // Measured (device time of a call, NVFP4; in brackets warp-level MMAs): 18432 x 7168, 32 rows 25 us
@@ -44,6 +50,8 @@ constexpr int kTcCodeStages = 5;       // ring of codes: 128 columns each
 constexpr int kTcXStages = 4;          // ring of x: 128 columns each, as two swizzled tiles of 64
 constexpr int kTcAStages = 3;          // ring of decoded weights in tensor memory: 128 columns each
 constexpr int kTcCodeBytes = kTcRows * 64;
+constexpr int kTcChain = 32;           // steps of an accumulator with FP32 output: 256 MMAs in a chain,
+constexpr int kTcPart = 28;            // and where that is not enough, 224
 constexpr int kTcDecWarps = 24;
 constexpr int kTcXWarp = 24;
 constexpr int kTcMmaWarp = 25;
@@ -133,6 +141,15 @@ __device__ __forceinline__ void st_dsmem_f32x4(uint32_t addr, float a, float b, 
                : "memory");
 }
 
+__device__ __forceinline__ float4 ld_dsmem_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
 // A wait of at most about a second.  The timer is read only once the first tries have failed: its
 // latency would be the ring's.
 __device__ __forceinline__ bool tc_wait(const uint64_t* bar, uint32_t parity) {
@@ -150,19 +167,25 @@ struct TcArgs {
   int K;
   int cluster;      // blocks that split K
   int kslice;       // columns of a block, a multiple of 128
+  int turns;        // accumulators that the steps take turns on (kTcParts; 1, 2 or 4)
+  int parts;        // in which a tile's share of K is worked through (kTcParts)
+  int kpart;        // columns of a part, a multiple of 128
   int tiles;        // of 256 weight rows
   bool wide;        // the scales of 128 columns are one aligned load
   void* y;
 };
 
-// kMany: a block works through several tiles (its rings run on from one to the next).  The steps of a
-// block with one tile are 2 to 4% shorter without that; a block for each tile takes 106 us for 131072
-// x 4096 at 64 rows (102 so), 31.7 for 146704 x 640 at 24 (23.5).
-template <bool kMx, bool kF32, bool kMany>
+// What a block works through: one tile; several tiles (its rings run on from one to the next); several
+// tiles or one, each in parts of its K or with accumulators that take turns (FP32 output of long rows).
+// The steps of a block with one tile are 2 to 4% shorter in the kernel for one; a block for each tile
+// takes 106 us for 131072 x 4096 at 64 rows (kTcTiles 102), 31.7 for 146704 x 640 at 24 (23.5).
+enum TcWork { kTcTile, kTcTiles, kTcParts };
+template <bool kMx, bool kF32, TcWork kWork>
 __global__ void __launch_bounds__(kTcThreads, 1)
 linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tmap_x,
                     const __grid_constant__ CUtensorMap tmap_c, const TcArgs a) {
   constexpr int kBlk = kMx ? 32 : 16;
+  constexpr bool kMany = kWork != kTcTile, kParts = kWork == kTcParts;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ uint64_t c_full[kTcCodeStages], c_empty[kTcCodeStages], x_full[kTcXStages],
@@ -174,8 +197,11 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tmap_x,
   const int first = (int)blockIdx.x / a.cluster;   // tiles first, + gridDim.x, ..
   const int ntile = kMany ? (a.tiles - first + (int)gridDim.x - 1) / (int)gridDim.x : 1;
   auto row0 = [&](int t) { return ((int64_t)first + (int64_t)t * gridDim.x) * kTcRows; };
+  // units of work: tiles or their parts
+  const int parts = kParts ? a.parts : 1, turns = kParts ? a.turns : 1, nunit = ntile * parts;
   const int kb = rank * a.kslice, ke = min(a.K, kb + a.kslice);
-  const int np = max(0, (ke - kb + 127) / 128);   // steps of 128 columns; behind K all are zeros
+  // steps of 128 columns in a unit; behind K all are zeros
+  const int np = parts > 1 ? (kb < a.K ? a.kpart / 128 : 0) : max(0, (ke - kb + 127) / 128);
   const uint32_t x_bytes = (uint32_t)a.tn * 256u;
   uint8_t* x_ring = smem + kTcCodeStages * kTcCodeBytes;
   // Met before the stores into other blocks, which only then need them to have started: a block
@@ -222,8 +248,9 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tmap_x,
     if constexpr (kF32) static_cast<float*>(a.y)[(int64_t)t * a.N + n] = v;
     else static_cast<__nv_bfloat16*>(a.y)[(int64_t)t * a.N + n] = __float2bfloat16_rn(v);
   };
-  // A cluster's block sums 256 / cluster of the rows: join[block][row][token].  Rows of tn + 4
-  // words put a warp's 16-byte stores in all banks.
+  // A cluster's block sums 256 / cluster of the rows: join[block][row][token], stored by their blocks.
+  // Of a tile with parts: this block's sums, [row][token], from which a cluster's blocks load theirs.
+  // Rows of tn + 4 words put a warp's 16-byte stores in all banks.
   const int rows = kTcRows / a.cluster, stride = a.tn + 4;
   float* join = reinterpret_cast<float*>(x_ring + kTcXStages * x_bytes);
 
@@ -241,8 +268,9 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tmap_x,
     // The scales of 128 columns: 8 or 4 bytes.  Behind K (where x and the codes are zeros) the row's
     // last ones: a NaN there is the row's anyway.
     uint32_t s[kMx ? 1 : 2];
+    int k0 = kb;   // first column of the unit that the scales are loaded of
     auto load_scales = [&](int p) {
-      const int at = kb + p * 128;
+      const int at = k0 + p * 128;
       if (a.wide) {
         const uint8_t* q = ps + min(at, a.K - 128) / kBlk;
         if constexpr (kMx) s[0] = __ldg(reinterpret_cast<const uint32_t*>(q));
@@ -267,44 +295,77 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tmap_x,
       }
     };
     bool ok = true;
-    // lane = weight row, column = token
-    auto epilogue = [&](int t) {
-      if (np > 0 && ok) ok = __all_sync(0xffffffffu, tc_wait(&acc_full, (uint32_t)t & 1u));
+    // The next unit (`done` before it): lane = weight row, column = token.
+    int done = 0;
+    auto epilogue = [&]() {
+      if (np > 0 && ok) ok = __all_sync(0xffffffffu, tc_wait(&acc_full, (uint32_t)done & 1u));
       tc_fence_after();
-      if (a.cluster > 1) cluster_wait();
+      const bool push = a.cluster > 1 && parts == 1;
+      if (push) cluster_wait();
+      const int part = kParts ? done % parts : 0, t = kParts ? done / parts : done;
       const uint32_t to =
-          a.cluster > 1 ? dsmem_addr(join + (rank * rows + r % rows) * stride, r / rows) : 0u;
+          push ? dsmem_addr(join + (rank * rows + r % rows) * stride, r / rows) : 0u;
       for (int c0 = set * 16; c0 < a.tn; c0 += 48) {
         uint32_t v[16];
-        tmem_ld_32x32b_x16(tmem + half * 64 + c0 + ((uint32_t)(quad * 32) << 16), v);
+        const uint32_t at = tmem + half * 64 + c0 + ((uint32_t)(quad * 32) << 16);
+        tmem_ld_32x32b_x16(at, v);
         tmem_ld_wait();
         float f[16];
 #pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(v[i]);
+        if constexpr (kParts) {
+          for (int j = 1; j < min(turns, np); ++j) {
+            tmem_ld_32x32b_x16(at + (uint32_t)(j * a.tn), v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) f[i] += __uint_as_float(v[i]);
+          }
+        }
+#pragma unroll
         for (int i = 0; i < 16; ++i) {
-          f[i] = np == 0 ? 0.0f : __uint_as_float(v[i]) * up0 * up;
+          f[i] = np == 0 ? 0.0f : f[i] * up0 * up;
           if (!ok) f[i] = __uint_as_float(0x7FC00000u);
         }
-        if (a.cluster > 1) {
+        if (push) {
 #pragma unroll
           for (int i = 0; i < 16; i += 4)
             st_dsmem_f32x4(to + (uint32_t)(c0 + i) * 4u, f[i], f[i + 1], f[i + 2], f[i + 3]);
         } else {
+          if (parts > 1) {
+            float4* sum = reinterpret_cast<float4*>(join + r * stride + c0);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) store(c0 + i, row0(t) + r, f[i]);
+            for (int i = 0; i < 4; ++i) {
+              if (part > 0) {
+                const float4 v4 = sum[i];
+                f[4 * i] += v4.x;
+                f[4 * i + 1] += v4.y;
+                f[4 * i + 2] += v4.z;
+                f[4 * i + 3] += v4.w;
+              }
+              if (part < parts - 1 || a.cluster > 1)
+                sum[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+            }
+          }
+          if (part == parts - 1 && a.cluster == 1) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) store(c0 + i, row0(t) + r, f[i]);
+          }
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0 && ok) mbar_arrive(smem_u32(&acc_empty));
+      ++done;
     };
     int slot = set, cslot = set;
     uint32_t ph = 0u, cph = 0u;
-    // this warp's steps are every third of all its block's; tile t, its step p; the next one's
+    // this warp's steps are every third of all its block's; unit t, its step p; the next one's
     // scales are loaded a step ahead
-    int t = 0, p = 0, done = 0;
+    int t = 0, p = 0;
     auto advance = [&](int by) {
       p += by;
-      if constexpr (kMany) {
+      if constexpr (kParts) {
+      } else if constexpr (kMany) {
         const int was = t;
         for (; p >= np && t < ntile; ++t) p -= np;
         if (t != was && t < ntile) ps = scales_of(t);
@@ -315,77 +376,92 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tmap_x,
     if (np > 0) {
       ps = scales_of(0);
       advance(set);
-      if (t < ntile) load_scales(p);
+      if (t < nunit) load_scales(p);
     }
-    while (np > 0 && t < ntile) {
-      if constexpr (kMany) {
-        for (; done < t; ++done) epilogue(done);
+    // kParts: unit by unit, so that the loop over steps is that of a single tile
+    for (int unit = 0; unit < (kParts ? nunit : 1);) {
+      while (np > 0 && (kParts ? p < np && ok : t < nunit)) {
+        if constexpr (kWork == kTcTiles) {
+          while (done < t) epilogue();
+          if (!ok) break;
+        }
+        uint32_t ss[kMx ? 1 : 2];
+#pragma unroll
+        for (int u = 0; u < (kMx ? 1 : 2); ++u) ss[u] = s[u];
+        advance(3);
+        // (behind the last step the last ones again)
+        if (kWork != kTcTiles || t < nunit) load_scales(p);
+        ok = __all_sync(0xffffffffu, tc_wait(c_full + cslot, cph));
         if (!ok) break;
-      }
-      uint32_t ss[kMx ? 1 : 2];
+        const uint8_t* cp = c_lane + cslot * kTcCodeBytes;
+        const int cold = cslot;
+        cslot += 3;
+        if (cslot >= kTcCodeStages) { cslot -= kTcCodeStages; cph ^= 1u; }
+        ok = __all_sync(0xffffffffu, tc_wait(a_empty + slot, ph ^ 1u));
+        if (!ok) break;
+        tc_fence_after();
+        // A placed code times its scale: NVFP4 one product (the scale in BF16 times 2^118).  MXFP4 one if
+        // the scale times 2^124 is a BF16 (up to 2^3), otherwise (`big`) two.
+        auto decode = [&](const bool big) {
 #pragma unroll
-      for (int u = 0; u < (kMx ? 1 : 2); ++u) ss[u] = s[u];
-      advance(3);
-      if (!kMany || t < ntile) load_scales(p);   // (one tile: behind the last step the last ones again)
-      ok = __all_sync(0xffffffffu, tc_wait(c_full + cslot, cph));
-      if (!ok) break;
-      const uint8_t* cp = c_lane + cslot * kTcCodeBytes;
-      const int cold = cslot;
-      cslot += 3;
-      if (cslot >= kTcCodeStages) { cslot -= kTcCodeStages; cph ^= 1u; }
-      ok = __all_sync(0xffffffffu, tc_wait(a_empty + slot, ph ^ 1u));
-      if (!ok) break;
-      tc_fence_after();
-      // A placed code times its scale: NVFP4 one product (the scale in BF16 times 2^118).  MXFP4 one if
-      // the scale times 2^124 is a BF16 (up to 2^3), otherwise (`big`) two.
-      auto decode = [&](const bool big) {
+          for (int q = 0; q < 2; ++q) {
+            uint32_t out[32];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t out[32];
+            for (int v = 0; v < 2; ++v) {
+              const uint4 w4 = *reinterpret_cast<const uint4*>(cp + (((2 * q + v) ^ swz) << 4));
+              const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+              uint32_t sc[2];
+              if constexpr (kMx) {
+                const uint32_t e = (ss[0] >> ((2 * q + v) * 8)) & 0xFFu;
+                sc[0] = sc[1] = !big ? (e + 124u) * 0x00800080u
+                                     : e == 255u ? 0x7FC07FC0u : e8m0_scale_bf16x2(e);
+              } else {
+                const float2 f = e4m3x2_to_f32x2((ss[q] >> (v * 16)) & 0xFFFFu);   // NaN stays NaN
+                const __nv_bfloat162 s0 = __float2bfloat162_rn(f.x * 0x1p118f);
+                const __nv_bfloat162 s1 = __float2bfloat162_rn(f.y * 0x1p118f);
+                sc[0] = *reinterpret_cast<const uint32_t*>(&s0);
+                sc[1] = *reinterpret_cast<const uint32_t*>(&s1);
+              }
 #pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            const uint4 w4 = *reinterpret_cast<const uint4*>(cp + (((2 * q + v) ^ swz) << 4));
-            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-            uint32_t sc[2];
-            if constexpr (kMx) {
-              const uint32_t e = (ss[0] >> ((2 * q + v) * 8)) & 0xFFu;
-              sc[0] = sc[1] = !big ? (e + 124u) * 0x00800080u
-                                   : e == 255u ? 0x7FC07FC0u : e8m0_scale_bf16x2(e);
-            } else {
-              const float2 f = e4m3x2_to_f32x2((ss[q] >> (v * 16)) & 0xFFFFu);   // NaN stays NaN
-              const __nv_bfloat162 s0 = __float2bfloat162_rn(f.x * 0x1p118f);
-              const __nv_bfloat162 s1 = __float2bfloat162_rn(f.y * 0x1p118f);
-              sc[0] = *reinterpret_cast<const uint32_t*>(&s0);
-              sc[1] = *reinterpret_cast<const uint32_t*>(&s1);
-            }
+              for (int i = 0; i < 4; ++i) {
+                uint32_t o[4];
+                e2m1x8_to_bf16x2_scaled_down(w[i], o);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t o[4];
-              e2m1x8_to_bf16x2_scaled_down(w[i], o);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                if (big) o[j] = mul_bf16x2(o[j], kBf16x2Pow2_124);
-                out[v * 16 + i * 4 + j] = mul_bf16x2(o[j], sc[i >> 1]);
+                for (int j = 0; j < 4; ++j) {
+                  if (big) o[j] = mul_bf16x2(o[j], kBf16x2Pow2_124);
+                  out[v * 16 + i * 4 + j] = mul_bf16x2(o[j], sc[i >> 1]);
+                }
               }
             }
+            tmem_st_32x32b_x32(a_lane + (uint32_t)slot * 128u + q * 32u, out);
           }
-          tmem_st_32x32b_x32(a_lane + (uint32_t)slot * 128u + q * 32u, out);
+        };
+        bool big = false;
+        if constexpr (kMx)
+          big = __any_sync(0xffffffffu, (ss[0] & ((ss[0] & 0x7F7F7F7Fu) + 0x7D7D7D7Du) & 0x80808080u) != 0u);
+        if (kMx && big) decode(true);
+        else decode(false);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(c_empty + cold));
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(a_full + slot));
+        ph ^= 1u;
+      }
+      if constexpr (kParts) {
+        p -= np;
+        if (++unit < nunit) {   // the next unit's first scales come during the epilogue
+          ps = scales_of(unit / parts);
+          k0 = kb + unit % parts * a.kpart;
+          load_scales(p);
         }
-      };
-      bool big = false;
-      if constexpr (kMx)
-        big = __any_sync(0xffffffffu, (ss[0] & ((ss[0] & 0x7F7F7F7Fu) + 0x7D7D7D7Du) & 0x80808080u) != 0u);
-      if (kMx && big) decode(true);
-      else decode(false);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(c_empty + cold));
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(a_full + slot));
-      ph ^= 1u;
+        epilogue();
+      } else {
+        while (done < nunit) epilogue();
+        break;
+      }
     }
-    for (; done < ntile; ++done) epilogue(done);
     if (!ok && lane == 0) s_abort = 1u;
   } else if (warp == kTcXWarp || warp == kTcCodeWarp) {
     if (lane == 0) {
@@ -397,7 +473,8 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tmap_x,
       uint32_t ph = 0u;
       uint32_t issued = 0u;
       bool ok = true;
-      for (int t = 0; t < ntile && ok; ++t)
+      for (int u = 0, t = 0, part = 0; u < nunit && ok; ++u) {
+        const int k0 = kb + part * a.kpart;
         for (int i = 0; i < np; ++i) {
           ok = tc_wait(empty + slot, ph ^ 1u);
           if (!ok) break;
@@ -405,14 +482,16 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tmap_x,
           mbar_arrive_expect_tx(fb, x ? x_bytes : (uint32_t)kTcCodeBytes);
           if (x) {
             const uint32_t to = smem_u32(x_ring) + slot * x_bytes;
-            tma_load_2d(to, &tmap_x, kb + i * 128, 0, fb);
-            tma_load_2d(to + x_bytes / 2, &tmap_x, kb + i * 128 + 64, 0, fb);
+            tma_load_2d(to, &tmap_x, k0 + i * 128, 0, fb);
+            tma_load_2d(to + x_bytes / 2, &tmap_x, k0 + i * 128 + 64, 0, fb);
           } else {
-            tma_load_2d(smem_u32(smem) + slot * kTcCodeBytes, &tmap_c, kb / 2 + i * 64, (int)row0(t), fb);
+            tma_load_2d(smem_u32(smem) + slot * kTcCodeBytes, &tmap_c, k0 / 2 + i * 64, (int)row0(t), fb);
           }
           ++issued;
           if (++slot == stages) { slot = 0; ph ^= 1u; }
         }
+        if (++part == parts) { part = 0; ++t; }
+      }
       if (!ok) s_abort = 1u;
       (x ? s_issued_x : s_issued_c) = issued;
     }
@@ -423,7 +502,7 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tmap_x,
     int slot = 0, xs = 0;
     uint32_t ph = 0u, xph = 0u;
     bool ok = true;
-    for (int t = 0; t < ntile && np > 0 && ok; ++t) {
+    for (int t = 0; t < nunit && np > 0 && ok; ++t) {
       ok = __all_sync(0xffffffffu, tc_wait(&acc_empty, ((uint32_t)t & 1u) ^ 1u));
       if (!ok) break;
       tc_fence_after();
@@ -434,8 +513,9 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tmap_x,
         tc_fence_after();
         const uint64_t b0 = db + (uint64_t)((xs * x_bytes) >> 4);
         const uint32_t a0 = tmem + kTcACol + (uint32_t)slot * 128u;
-        tc_mma_64(tmem, a0, b0, idesc, i != 0 ? 1u : 0u);
-        tc_mma_64(tmem, a0 + 32u, b0 + (x_bytes >> 5), idesc, 1u);
+        const uint32_t d = tmem + (kParts ? (uint32_t)(i & (turns - 1)) * (uint32_t)a.tn : 0u);
+        tc_mma_64(d, a0, b0, idesc, i >= turns ? 1u : 0u);
+        tc_mma_64(d, a0 + 32u, b0 + (x_bytes >> 5), idesc, 1u);
         tc_commit_elected(x_empty + xs);
         tc_commit_elected(a_empty + slot);
         if (++slot == kTcAStages) { slot = 0; ph ^= 1u; }
@@ -451,7 +531,7 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tmap_x,
   }
 
   __syncwarp();
-  if (a.cluster > 1 && warp >= kTcDecWarps) cluster_wait();
+  if (a.cluster > 1 && (warp >= kTcDecWarps || parts > 1)) cluster_wait();
   tc_fence_before();
   __syncthreads();   // every accumulator has been read, every MMA is done (or a wait ran out)
   // After an expired wait TMA loads may still be in flight: the last ring's worth is waited for.
@@ -471,13 +551,21 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tmap_x,
     cluster_sync();
     for (int e = threadIdx.x; e < rows * (a.tn / 4); e += kTcThreads) {
       const int r = e % rows, t = e / rows * 4;
-      float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      for (int b = 0; b < a.cluster; ++b) {
-        const float4 v = *reinterpret_cast<const float4*>(join + (b * rows + r) * stride + t);
-        sum.x += v.x;
-        sum.y += v.y;
-        sum.z += v.z;
-        sum.w += v.w;
+      float4 v[8];
+#pragma unroll
+      for (int b = 0; b < 8; ++b) {
+        v[b] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (b >= a.cluster) continue;
+        v[b] = parts > 1 ? ld_dsmem_f32x4(dsmem_addr(join + (rank * rows + r) * stride + t, b))
+                         : *reinterpret_cast<const float4*>(join + (b * rows + r) * stride + t);
+      }
+      float4 sum = v[0];
+#pragma unroll
+      for (int b = 1; b < 8; ++b) {
+        sum.x += v[b].x;
+        sum.y += v[b].y;
+        sum.z += v[b].z;
+        sum.w += v[b].w;
       }
       const int64_t n = row0(0) + rank * rows + r;
       store(t, n, sum.x);
@@ -485,6 +573,7 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tmap_x,
       store(t + 2, n, sum.z);
       store(t + 3, n, sum.w);
     }
+    if (parts > 1) cluster_sync();   // (the others have read this block's sums)
   }
 }
 
@@ -509,7 +598,7 @@ int tc_cluster(int64_t tiles, int64_t steps) {
   return cluster;
 }
 
-// Alignment, the rings of codes and x, and a cluster's join buffer.
+// Alignment, the rings of codes and x, and the buffer of a cluster or of a tile's parts.
 size_t tc_smem(int tn, bool joins) {
   return 1024 + (size_t)kTcCodeStages * kTcCodeBytes + (size_t)kTcXStages * tn * 256 +
          (joins ? (size_t)(tn + 4) * kTcRows * 4 : 0u);
@@ -531,7 +620,7 @@ cudaError_t launch_linear_w4_tc(const void* x, const uint8_t* codes, const uint8
                                 cudaStream_t s) {
   auto encode = encode_fn_linear();
   if (!encode) return cudaErrorNotSupported;
-  TcArgs a{sf, ts, T, (T + 15) / 16 * 16, N, K, 1, 0, 0, false, y};
+  TcArgs a{sf, ts, T, (T + 15) / 16 * 16, N, K, 1, 0, 1, 1, 0, 0, false, y};
   a.wide = K % 128 == 0 && is_aligned(sf, ts ? 8 : 4);
   CUtensorMap tmap_x, tmap_c;
   const cuuint32_t estr[2] = {1u, 1u};
@@ -557,14 +646,23 @@ cudaError_t launch_linear_w4_tc(const void* x, const uint8_t* codes, const uint8
   const int64_t steps = (K + 127) / 128;
   a.cluster = tc_cluster(tiles, steps);
   a.tiles = (int)tiles;
-  a.kslice = (int)((steps + a.cluster - 1) / a.cluster) * 128;
-  auto pick = [&](auto many) {
-    constexpr bool kMany = decltype(many)::value;
-    return ts ? (f32 ? linear_w4_tc_kernel<false, true, kMany> : linear_w4_tc_kernel<false, false, kMany>)
-              : (f32 ? linear_w4_tc_kernel<true, true, kMany> : linear_w4_tc_kernel<true, false, kMany>);
+  const int mine = (int)((steps + a.cluster - 1) / a.cluster);
+  if (f32 && mine > kTcChain) {   // as many accumulators as needed and as fit into 64 columns, then parts
+    while (a.turns * a.tn <= 32 && a.turns * kTcPart < mine) a.turns *= 2;
+    a.parts = (mine + kTcPart * a.turns - 1) / (kTcPart * a.turns);
+  }
+  a.kpart = (mine + a.parts - 1) / a.parts * 128;
+  a.kslice = a.kpart * a.parts;   // (whole parts: none reaches into the next block's share)
+  auto pick = [&](auto work) {
+    constexpr TcWork kWork = decltype(work)::value;
+    return ts ? (f32 ? linear_w4_tc_kernel<false, true, kWork> : linear_w4_tc_kernel<false, false, kWork>)
+              : (f32 ? linear_w4_tc_kernel<true, true, kWork> : linear_w4_tc_kernel<true, false, kWork>);
   };
-  auto kern = tiles > num_sms() ? pick(std::true_type{}) : pick(std::false_type{});
-  const size_t smem = tc_smem(a.tn, a.cluster > 1);
+  auto kern = tiles > num_sms() ? pick(std::integral_constant<TcWork, kTcTiles>{})
+                                : pick(std::integral_constant<TcWork, kTcTile>{});
+  if (a.parts > 1 || a.turns > 1)
+    kern = ts ? linear_w4_tc_kernel<false, true, kTcParts> : linear_w4_tc_kernel<true, true, kTcParts>;
+  const size_t smem = tc_smem(a.tn, a.cluster > 1 || a.parts > 1);
   // (always to the most: another thread's launch may need more than this one's)
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)tc_smem(kTcMaxTokens, true));
