@@ -248,7 +248,8 @@ int moe_add_rmsnorm_quantize_mx(const void* x, const void* residual, const void*
  * residual alike - and dgamma = sum over rows of dy * (h * r).
  *   dy, h, dx: [rows, cols] BF16; dh: NULL or [rows, cols] BF16, the gradient that reaches h over
  *   the residual stream; rrms: [rows] FP32 of the forward pass; gamma: [cols] BF16; dgamma:
- *   [cols] FP32 (overwritten).  16-byte aligned (rrms, dgamma 4).  dx may be the buffer of dy or dh.
+ *   [cols] FP32 (overwritten).  16-byte aligned (rrms, dgamma 4).  dx may be the buffer of dy or dh,
+ *   not that of h (MOE_ERR_INVALID_ARG).
  * dgamma is summed in a fixed order: the same call gives the same bits.  workspace: 16-byte
  * aligned, of the size below; it carries no status word.  rows == 0 zeroes dgamma. */
 size_t moe_add_rmsnorm_backward_workspace_size(int64_t rows, int64_t cols);

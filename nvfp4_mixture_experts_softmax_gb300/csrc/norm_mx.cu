@@ -409,7 +409,7 @@ int moe_add_rmsnorm_backward(const void* dy, const void* dh, const void* h, cons
   if (!dy || !h || !rrms || !gamma || !dx) return MOE_ERR_INVALID_ARG;
   for (const void* p : {dy, dh, h, gamma, (const void*)dx})
     if (!is_aligned(p, 16)) return MOE_ERR_INVALID_ARG;
-  if (!is_aligned(rrms, 4)) return MOE_ERR_INVALID_ARG;
+  if (!is_aligned(rrms, 4) || dx == h) return MOE_ERR_INVALID_ARG;   // (h is read behind stores to dx)
   const RowGrid g = backward_grid(rows, (int)(cols / 8));
   auto k = g.J == 1   ? add_rmsnorm_backward_kernel<1>
            : g.J == 2 ? add_rmsnorm_backward_kernel<2>

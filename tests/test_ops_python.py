@@ -59,3 +59,10 @@ def test_by_name(moe):
     assert torch.equal(moe.router_loss_backward(lg, ids, sa, gl), moe.router_loss_backward(logits=lg, topk_ids=ids, stats=sa, grad_losses=gl))
     w = moe.quantize_act(n(48, 64).bfloat16())
     assert torch.equal(moe.linear_w4(x, *w), moe.linear_w4(x=x, codes=w[0], sf=w[1], ts=w[2]))
+
+
+def test_backward_over_h_is_refused(moe):
+    """dx may take the place of dy or dh; h is still read after the first rows of dx are written."""
+    P = 4096   # an address that no rejected call reads
+    call = moe.lib().moe_add_rmsnorm_backward
+    assert call(P, None, 2 * P, P, P, 4, 64, 2 * P, P, P, 1 << 24, None) == -1
