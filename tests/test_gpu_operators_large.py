@@ -88,3 +88,52 @@ def test_losses_and_gradient_of_many_tokens(moe, T, E, k, router, masked):
     assert bool(((got.double() - want).abs() <= G_REL * size + 1e-30).all())
     if masked:
         assert not got[~mask].any()
+
+
+def _room(gib):
+    if torch.cuda.mem_get_info()[0] < gib << 30:
+        pytest.skip("not enough memory")
+
+
+def test_norm_beyond_2_32_elements(moe):
+    """The last rows of 4.3 G elements, as a call of their own gives them."""
+    _room(80)
+    rows, cols = 263000, 16384
+    x, res = (torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    xs, rs, gamma = make_rows(400, cols, 1)
+    x[-400:], res[-400:] = xs, rs
+    want = moe.add_rmsnorm_quantize_mx(xs, rs, gamma, want_y=True, want_rrms=True)
+    o = moe.add_rmsnorm_quantize_mx(x, res, gamma, out={"h": x, "codes": torch.empty(rows, cols, dtype=torch.uint8, device="cuda"),
+                                                        "sf": torch.empty(rows, cols // 32, dtype=torch.uint8, device="cuda"),
+                                                        "rrms": torch.empty(rows, device="cuda")})
+    assert all(torch.equal(o[k][-400:], want[k]) for k in o) and not o["codes"][:1000].any()
+    del o["codes"], res
+    dy = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    dy[-400:] = rs
+    g = moe.add_rmsnorm_backward(dy, x, o["rrms"], gamma, out={"dx": dy, "dgamma": torch.empty(cols, device="cuda")})
+    dx, size, dg, dgsize = backward_reference(rs, want["h"], want["rrms"], gamma, None)
+    assert bool(((g["dx"][-400:].double() - dx).abs() <= BF16_HALF * dx.abs() + Y_REL * size).all()) and not g["dx"][:1000].any()
+    assert bool(((g["dgamma"].double() - dg).abs() <= (rows + 8) * 2.0 ** -24 * dgsize).all())
+
+
+@pytest.mark.parametrize("router", ROUTERS)
+def test_losses_beyond_2_32_elements(moe, router):
+    """4.3 G logits: sums over all tokens against the same token counted often, gradients of the last
+    tokens against a call of their own."""
+    _room(60)
+    T, E, k = 4200000, 1024, 4
+    l1, ids1, _, _ = make_logits(100, E, k, 3)
+    l = torch.empty(T, E, device="cuda")
+    l.view(T // 100, 100, E).copy_(l1.expand(T // 100, 100, E))
+    ids = ids1.repeat(T // 100, 1)
+    o = moe.router_loss(l, ids, router=router)
+    bal, z, counts, n, P = forward_reference(l1, ids1, None, router)
+    assert torch.equal(o["counts"].long(), counts * (T // 100)) and int(o["tokens"]) == T
+    # a warp's chain over T / (152 * 16) tokens, then sums over warps and blocks, each in FP32
+    tol = (T / (152 * 16) + 16 + 152 + 128) * U
+    assert bool(((o["probs"].double() - P).abs() <= tol * P).all())
+    assert abs(float(o["losses"][0]) - float(bal)) <= tol * float(bal) and abs(float(o["losses"][1]) - float(z)) <= 4 * tol * float(z)
+    gl, gw = torch.tensor([0.7, -0.3], device="cuda"), torch.randn(T, k, device="cuda")
+    d = moe.router_loss_backward(l, ids, o, gl, grad_topk_w=gw, router=router)
+    few = moe.router_loss_backward(l[-500:].clone(), ids[-500:].clone(), o, gl, grad_topk_w=gw[-500:].clone(), router=router)
+    assert torch.equal(d[-500:], few)
