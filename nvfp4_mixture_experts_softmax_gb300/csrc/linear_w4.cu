@@ -29,7 +29,7 @@
 // weight rows; the partial sums are joined through (distributed) shared memory in a fixed order.
 //
 // Measured (device time of a call): 131072 x 4096 NVFP4, 1 token 60 us (5.0 TB/s; a pure read of HBM
-// reaches 5.8), 16 tokens 78 us; 18432 x 7168, 1 / 8 tokens 19.5 / 25.5 us; 2048 x 2048, 1 token 4.0
+// reaches 5.8), 16 tokens 78 us; 18432 x 7168, 1 / 8 tokens 19.5 / 25.5 us; 2048 x 2048, 1 token 3.8
 // us.  A block of 16 rows whose eight warps read x from L1 in BF16, without staging, took 77.6, 166,
 // 22.2 / 39 and 2.8 us.
 #include <algorithm>

@@ -27,8 +27,8 @@
 // Every wait is bounded; a block whose wait ran out stores NaN.
 //
 // Measured (device time of a call, NVFP4; in brackets warp-level MMAs): 18432 x 7168, 32 rows 25 us
-// (41), 64 rows 29 us (86); 36864 x 7168, 64 rows 43 us (165); 2048 x 2048, 64 rows 9.1 us (17.5);
-// 18431 x 7168 MXFP4, 15 rows 23.8 us (26.2).  A step of a block takes 0.62 us.  Alone the decoding
+// (41), 64 rows 29 us (86); 36864 x 7168, 64 rows 44 us (165); 2048 x 2048, 64 rows 8.8 us (17.5);
+// 18431 x 7168 MXFP4, 15 rows 24.1 us (26.2).  A step of a block takes 0.62 us.  Alone the decoding
 // takes 0.59 (some 20 instructions for 8 codes), the MMAs 0.53 at 64 rows (67 cycles each), the loads
 // 0.39 (from L2, 32 KB); 16 decoding warps 0.64; a warp whose single lane issues the MMAs 1.11.
 #include <cuda.h>

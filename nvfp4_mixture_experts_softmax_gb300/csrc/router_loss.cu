@@ -20,9 +20,10 @@
 // one is reduced.
 // Bound by HBM for softmax and many tokens (the logits once, in the backward pass the gradient once),
 // by the instruction stream for the sqrt-softplus router (26 instructions a score), by launches and
-// the join for small batches.  Measured (device time of a call): losses 131072 x 256 30.4 us (67% of
-// the copy rate; sqrt-softplus 43.6), 8192 x 256 8.4 us, 64 x 128 3.3 us; gradient 131072 x 256 48 us
-// (85%; sqrt-softplus 68), 100003 x 60 13.9 us, 8192 x 256 sqrt-softplus 6.7 us.
+// the join for small batches.  Measured (device time of a call, 6% of the tokens masked): losses 131072 x
+// 256 30.0 us (67% of the copy rate; sqrt-softplus 43.2), 8192 x 256 8.6 us, 64 x 128 3.2 us; gradient
+// 131072 x 256 47.2 us (85%; sqrt-softplus 65.6), 100003 x 60 without a mask 13.7 us, 8192 x 256
+// sqrt-softplus 6.4 us.
 #include <algorithm>
 #include <type_traits>
 
