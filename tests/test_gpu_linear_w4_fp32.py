@@ -69,3 +69,55 @@ def test_exact_sums_of_parts(moe, T, N, K, fmt):
     bad[T - 1, K - 1] = float("nan")
     y2 = moe.linear_w4(bad, codes, sf, ts, out_dtype=torch.float32)
     assert torch.equal(y2[:T - 1], y[:T - 1]) and bool(y2[T - 1].isnan().all())
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("T", [1, 7, 12, 17, 64])
+def test_exact_longest_rows(moe, T, fmt):
+    """K = 2^20: ordinary x, and a row whose elements lie too far apart for F16 (the product in BF16)."""
+    N, K = 37, 1 << 20
+    codes, sf, ts = random_weights(N, K, fmt, True, T)
+    g = torch.Generator(device="cuda").manual_seed(K)
+    x = (torch.rand(T, K, device="cuda", generator=g) < 0.1).bfloat16()
+    w = decode(codes, sf, ts).t()
+    for dtype in (torch.float32, torch.bfloat16):
+        want = (x.double() @ w).to(torch.float32).to(dtype)
+        assert torch.equal(moe.linear_w4(x, codes, sf, ts, out_dtype=dtype), want)
+    x[0] *= 2.0 ** -60
+    x[0, 5:K:2] = 0
+    x[0, 4] = 1.0
+    codes[:, 2] &= 0xF0                                    # the weight of column 4: zero
+    want = (x.double() @ decode(codes, sf, ts).t()).float()
+    assert torch.equal(moe.linear_w4(x, codes, sf, ts, out_dtype=torch.float32), want)
+
+
+@pytest.mark.parametrize("T,N,K", [(64, 300, 45088), (64, 19713, 7168), (24, 19713, 7168), (12, 2048, 16384)])
+def test_parts_captured_and_on_two_streams(moe, T, N, K):
+    """Calls that follow one another, in a graph, and beside another stream's: exact each time."""
+    codes, sf, ts = random_weights(N, K, "nvfp4", True, 3)
+    w = decode(codes, sf, ts).float()
+
+    def rows(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        return (torch.rand(T, K, device="cuda", generator=g) < 0.1).bfloat16()
+
+    def exact(y, x):
+        return torch.equal(y.double(), torch.cat([x.double() @ p.double().t() for p in w.split(4096)], 1))
+
+    x, other, side = rows(0), rows(1), torch.cuda.Stream()
+    moe.linear_w4(x, codes, sf, ts, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = [moe.linear_w4(x, codes, sf, ts, out_dtype=torch.float32) for _ in range(3)]
+    for seed in (2, 3):
+        x.copy_(rows(seed))
+        graph.replay()
+        assert all(exact(t, x) for t in y)
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        b = [moe.linear_w4(other, codes, sf, ts, out_dtype=torch.float32) for _ in range(12)]
+    a = [moe.linear_w4(x, codes, sf, ts, out_dtype=torch.float32) for _ in range(12)]
+    torch.cuda.synchronize()
+    assert exact(a[0], x) and exact(b[0], other)
+    assert all(torch.equal(t, a[0]) for t in a) and all(torch.equal(t, b[0]) for t in b)
