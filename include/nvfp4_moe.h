@@ -257,6 +257,34 @@ int moe_add_rmsnorm_backward(const void* dy, const void* dh, const void* h, cons
                              const void* gamma, int64_t rows, int64_t cols, void* dx,
                              float* dgamma, void* workspace, size_t ws_bytes, moe_stream_t stream);
 
+/* Residual addition and layer norm: the norm of blocks that are not normalised by RMSNorm.  Per row:
+ * h = x + residual (in the tensors' type), m = mean(h), s = 1 / sqrt(mean((h - m)^2) + eps),
+ * y = (h - m) * s * gamma + beta, all in FP32 and rounded once.
+ *   x, residual, h, y: [rows, cols], gamma, beta: [cols], all BF16, or FP32 with MOE_ROWS_F32 in flags;
+ *   16-byte aligned, cols a multiple of 8, at most 16384; mean, rstd: NULL or device FP32 [rows] (m and s).
+ *   residual and h are both given or both NULL (then h is x itself); beta NULL: none.  h may be the buffer
+ *   of residual or of x (in place); no other two buffers may overlap.
+ * A NaN or infinity makes its own row NaN.  No workspace, one launch.  rows == 0 is MOE_OK. */
+#define MOE_ROWS_F32 1u
+int moe_add_layernorm(const void* x, const void* residual, const void* gamma, const void* beta,
+                      float eps, int64_t rows, int64_t cols, uint32_t flags, void* h, void* y,
+                      float* mean, float* rstd, moe_stream_t stream);
+
+/* Its backward pass.  With n = (h - mean) * rstd and a = gamma * dy:
+ * dx = dh + rstd * (a - mean(a) - n * mean(a * n)) - the gradient of x and of the residual alike -,
+ * dgamma = sum over rows of dy * n, dbeta = sum over rows of dy.
+ *   dy, h, dx: [rows, cols]; dh: NULL or [rows, cols], the gradient that reaches h over the residual
+ *   stream; gamma: [cols] (types as in the forward pass); mean, rstd: [rows] FP32 of the forward pass;
+ *   dgamma, dbeta: [cols] FP32 (overwritten; dbeta may be NULL).  16-byte aligned (FP32 vectors 4).  dx may
+ *   be the buffer of dy or dh, not that of h (MOE_ERR_INVALID_ARG).
+ * The sums over rows run in a fixed order: the same call gives the same bits.  workspace: 16-byte aligned,
+ * of the size below; it carries no status word.  rows == 0 zeroes dgamma and dbeta. */
+size_t moe_add_layernorm_backward_workspace_size(int64_t rows, int64_t cols);
+int moe_add_layernorm_backward(const void* dy, const void* dh, const void* h, const float* mean,
+                               const float* rstd, const void* gamma, int64_t rows, int64_t cols,
+                               uint32_t flags, void* dx, float* dgamma, float* dbeta, void* workspace,
+                               size_t ws_bytes, moe_stream_t stream);
+
 /* ---------------------------------------------------------------------------------------------
  * Router + plan.  logits [T,E] FP32 -> topk_ids [T,k] (slot 0 the largest), topk_w [T,k],
  * counts [E], offsets [E+1] (exclusive prefix sums, offsets[E] = T*k), perm_src [T*k]
@@ -266,6 +294,77 @@ size_t moe_plan_workspace_size(int32_t T, int32_t E, int32_t k);
 int moe_plan(const float* logits, int32_t T, int32_t E, int32_t k, int32_t* topk_ids,
              float* topk_w, int32_t* counts, int32_t* offsets, int32_t* perm_src, int32_t* inv,
              void* workspace, size_t ws_bytes, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Tokens to their experts and back, for callers that run the experts themselves (moe_experts_* below).
+ *
+ * moe_sort_tokens: the plan of given ids topk_ids [T,k] (any router's): counts, offsets, perm_src and inv
+ * as moe_plan writes them.  An assignment does not count if its token is masked (mask: uint8 [T], 0 =
+ * masked; may be NULL; a masked token's ids are not read) or its id is -1; any other id outside [0, E)
+ * does not count either and leaves MOE_ERR_INVALID_ARG in the device status.  Assignments that do not
+ * count have inv = -1, and perm_src is -1 from offsets[E] on.  1 <= E <= 1024, 1 <= k <= 32,
+ * T * k < 2^31; workspace 256-byte aligned, of the size below (its first word is the status).
+ *
+ * moe_permute_rows: rows[inv[t*k+j]] = x[t], for any element type: rows of row_bytes (a multiple of 16, at
+ * most 1 MB).  R: rows of `rows`.  Rows that no assignment names stay as they were.
+ * moe_combine_rows: y[t] = sum_j topk_w[t,j] * rows[inv[t*k+j]], FP32 in slot order, rounded once;
+ * topk_w NULL: weights 1, which is the gradient of moe_permute_rows.  x, y: [T, cols], rows: [R, cols], BF16 or,
+ * with MOE_ROWS_F32, FP32, cols a multiple of 8 (FP32: 4); topk_w: FP32 [T,k].  A token without rows gets zeros.
+ * moe_combine_rows_backward: drows[inv[t*k+j]] = topk_w[t,j] * dy[t] and dtopk_w[t,j] (FP32) = the product
+ * of dy[t] and rows[inv[t*k+j]], 0 without a row.  drows may be the buffer of rows; rows of drows that no
+ * assignment names stay as they were.
+ * In all three an inv outside [0, R) stands for no row (its weight is not read), and two assignments may
+ * not name the same row.  x, y, rows 16-byte aligned, the rest 4.  One launch each, no workspace.
+ * ------------------------------------------------------------------------------------------- */
+size_t moe_sort_tokens_workspace_size(int32_t T, int32_t E, int32_t k);
+int moe_sort_tokens(const int32_t* topk_ids, const uint8_t* mask, int32_t T, int32_t E, int32_t k,
+                    int32_t* counts, int32_t* offsets, int32_t* perm_src, int32_t* inv, void* workspace,
+                    size_t ws_bytes, moe_stream_t stream);
+int moe_permute_rows(const void* x, const int32_t* inv, int32_t T, int32_t k, int64_t row_bytes,
+                     int64_t R, void* rows, moe_stream_t stream);
+int moe_combine_rows(const void* rows, const int32_t* inv, const float* topk_w, int32_t T, int32_t k,
+                     int64_t cols, int64_t R, uint32_t flags, void* y, moe_stream_t stream);
+int moe_combine_rows_backward(const void* dy, const void* rows, const int32_t* inv, const float* topk_w,
+                              int32_t T, int32_t k, int64_t cols, int64_t R, uint32_t flags, void* drows,
+                              float* dtopk_w, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * The experts of a BF16 layer that is trained, on rows sorted by expert: expert e owns rows offsets[e] to
+ * offsets[e+1] of rows [R,H] (offsets: device int32 [E+1], as moe_plan and moe_sort_tokens write them;
+ * offsets that do not ascend within [0, R] leave MOE_ERR_INVALID_ARG in the device status, and nothing is
+ * computed).  w_gate, w_up [E,I,H], w_down [E,H,I] BF16, as moe_quantize_weights takes them.  Per row
+ *   g = x Wg^T, u = x Wu^T, h = bf16(act(g, u)) from the FP32 g and u, out = h Wd^T
+ * with the activation of flags (none: silu(g) * u; MOE_FLAG_SWIGLU_CLAMP, MOE_FLAG_ACT_SWIGLU_OAI with
+ * swiglu_limit and swiglu_alpha; MOE_FLAG_ACT_RELU2: no gate, w_gate and g are NULL or not read).
+ *   forward:  out [R,H]; g, u [R,I], what the backward pass reads (both NULL: not kept; relu2: u alone); h [R,I]
+ *             (NULL: kept in the workspace for the call), what the weights' gradient reads.
+ *   backward: from dout [R,H], g and u: dg, du [R,I] = bf16 of the gradients of g and u (a clamp's gradient
+ *             is 0 beyond its limit), and drows [R,H] = dg Wg + du Wu.
+ *   weights:  dw_gate = dg^T rows, dw_up = du^T rows [E,I,H], dw_down = dout^T h [E,H,I], FP32, per
+ *             segment; overwritten (zeros for an expert without rows) or, with MOE_EXPERTS_ACCUMULATE in
+ *             flags, added to.  relu2: dg and dw_gate NULL.
+ * All BF16 tensors: products accumulate in FP32, one rounding at the end.  The tensor cores truncate where they
+ * add; the weights' gradients are cut into chains of 64 such additions.  All sums run in a fixed order.
+ * Rows from offsets[E] on are neither used (they may hold anything) nor written; NaN and infinities
+ * stay in their row, in the weights' gradients in their segment.
+ * H, I multiples of 32, at most 65536; E <= 1024; R < 2^31.  Inputs 16-byte aligned, outputs, g and u 32-byte;
+ * no output may overlap an input.  workspace: 256-byte aligned, its first word the device status; 256 bytes,
+ * for a forward call without h moe_experts_workspace_size(R, I).  Two launches, the weights' gradients one.
+ * ------------------------------------------------------------------------------------------- */
+#define MOE_EXPERTS_ACCUMULATE 0x100u
+size_t moe_experts_workspace_size(int64_t R, int64_t I);
+int moe_experts_forward(const void* rows, const int32_t* offsets, int64_t R, int32_t E, int64_t H, int64_t I,
+                        const void* w_gate, const void* w_up, const void* w_down, uint32_t flags,
+                        float swiglu_limit, float swiglu_alpha, void* g, void* u, void* h, void* out,
+                        void* workspace, size_t ws_bytes, moe_stream_t stream);
+int moe_experts_backward(const void* dout, const int32_t* offsets, int64_t R, int32_t E, int64_t H, int64_t I,
+                         const void* w_gate, const void* w_up, const void* w_down, uint32_t flags,
+                         float swiglu_limit, float swiglu_alpha, const void* g, const void* u, void* dg, void* du,
+                         void* drows, void* workspace, size_t ws_bytes, moe_stream_t stream);
+int moe_experts_weight_grad(const void* rows, const void* dout, const void* h, const void* dg, const void* du,
+                            const int32_t* offsets, int64_t R, int32_t E, int64_t H, int64_t I, uint32_t flags,
+                            float* dw_gate, float* dw_up, float* dw_down, void* workspace, size_t ws_bytes,
+                            moe_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------------
  * Router losses.  Per-expert counts, the balance loss and the z loss of one batch of routed

@@ -30,7 +30,11 @@ EXPORTED = ["moe_status_string", "moe_config_check", "moe_weights_size", "moe_qu
             "moe_run_quantized", "moe_add_rmsnorm_quantize_mx",
             "moe_add_rmsnorm_backward_workspace_size", "moe_add_rmsnorm_backward",
             "moe_router_loss_workspace_size", "moe_router_loss", "moe_router_loss_backward",
-            "moe_linear_w4"]
+            "moe_linear_w4", "moe_add_layernorm", "moe_add_layernorm_backward_workspace_size",
+            "moe_add_layernorm_backward", "moe_sort_tokens_workspace_size", "moe_sort_tokens",
+            "moe_permute_rows", "moe_combine_rows", "moe_combine_rows_backward",
+            "moe_experts_workspace_size", "moe_experts_forward", "moe_experts_backward",
+            "moe_experts_weight_grad"]
 
 
 class MoeConfig(C.Structure):
@@ -104,6 +108,23 @@ def lib():
             "moe_router_loss_backward": (C.c_int, [vp, vp, vp, i32, i32, i32, u32, vp, vp, vp, vp,
                                                    vp, vp]),
             "moe_linear_w4": (C.c_int, [vp, vp, vp, vp, i32, i64, i64, u32, vp, vp]),
+            "moe_add_layernorm": (C.c_int, [vp, vp, vp, vp, f32, i64, i64, u32, vp, vp, vp, vp, vp]),
+            "moe_add_layernorm_backward_workspace_size": (sz, [i64, i64]),
+            "moe_add_layernorm_backward": (C.c_int, [vp, vp, vp, vp, vp, vp, i64, i64, u32, vp, vp, vp,
+                                                     vp, sz, vp]),
+            "moe_sort_tokens_workspace_size": (sz, [i32, i32, i32]),
+            "moe_sort_tokens": (C.c_int, [vp, vp, i32, i32, i32, vp, vp, vp, vp, vp, sz, vp]),
+            "moe_permute_rows": (C.c_int, [vp, vp, i32, i32, i64, i64, vp, vp]),
+            "moe_combine_rows": (C.c_int, [vp, vp, vp, i32, i32, i64, i64, u32, vp, vp]),
+            "moe_combine_rows_backward": (C.c_int, [vp, vp, vp, vp, i32, i32, i64, i64, u32, vp, vp,
+                                                    vp]),
+            "moe_experts_workspace_size": (sz, [i64, i64]),
+            "moe_experts_forward": (C.c_int, [vp, vp, i64, i32, i64, i64, vp, vp, vp, u32, f32, f32,
+                                              vp, vp, vp, vp, vp, sz, vp]),
+            "moe_experts_backward": (C.c_int, [vp, vp, i64, i32, i64, i64, vp, vp, vp, u32, f32, f32,
+                                               vp, vp, vp, vp, vp, vp, sz, vp]),
+            "moe_experts_weight_grad": (C.c_int, [vp, vp, vp, vp, vp, vp, i64, i32, i64, i64, u32, vp,
+                                                  vp, vp, vp, sz, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -140,6 +161,18 @@ FLAG_ACT_MXFP8 = 32
 ACTIVATIONS = ("swiglu", "relu2", "swiglu_oai")
 
 
+def _activation_flag(activation, swiglu_limit):
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {activation!r}")
+    if activation == "swiglu_oai" and swiglu_limit is None:
+        raise ValueError("swiglu_oai needs swiglu_limit")
+    if activation == "relu2":
+        return FLAG_ACT_RELU2
+    if activation == "swiglu_oai":
+        return FLAG_ACT_SWIGLU_OAI
+    return FLAG_SWIGLU_CLAMP if swiglu_limit is not None else 0
+
+
 def make_config(num_experts, hidden, inter, top_k, shared_inter=0, h_tensor_scale=1.0,
                 max_tokens=0, router="softmax", swiglu_limit=None, activation="swiglu",
                 swiglu_alpha=1.702, precision="nvfp4") -> MoeConfig:
@@ -153,17 +186,8 @@ def make_config(num_experts, hidden, inter, top_k, shared_inter=0, h_tensor_scal
     MXFP8 activations and h)."""
     if router not in ("softmax", "sqrtsoftplus"):
         raise ValueError(f"unknown router {router!r}")
-    if activation not in ACTIVATIONS:
-        raise ValueError(f"unknown activation {activation!r}")
-    if activation == "swiglu_oai" and swiglu_limit is None:
-        raise ValueError("swiglu_oai needs swiglu_limit")
     flags = FLAG_ROUTER_SQRTSOFTPLUS if router == "sqrtsoftplus" else 0
-    if activation == "relu2":
-        flags |= FLAG_ACT_RELU2
-    elif activation == "swiglu_oai":
-        flags |= FLAG_ACT_SWIGLU_OAI
-    elif swiglu_limit is not None:
-        flags |= FLAG_SWIGLU_CLAMP
+    flags |= _activation_flag(activation, swiglu_limit)
     if precision == "w4a16":
         flags |= FLAG_ACT_BF16
     elif precision == "w4a8":
@@ -647,6 +671,319 @@ def linear_w4(handle, x, codes, sf, ts=None, out_dtype=torch.bfloat16, y=None):
     if st:
         _check(st, "moe_linear_w4")
     return y
+
+
+# ---- the layer's training pass: layer norm, tokens to their experts and back, the experts ----
+
+ROWS_F32 = 1
+EXPERTS_ACCUMULATE = 0x100
+
+
+def _row_type(t, name):
+    if t.dtype is _BF16:
+        return 0
+    if t.dtype is _F32:
+        return ROWS_F32
+    raise ValueError(f"{name} must be bfloat16 or float32, not {t.dtype}")
+
+
+def _matrix(t, name, multiple):
+    if t.dim() != 2 or t.shape[1] % multiple or t.shape[1] == 0:
+        raise ValueError(f"{name} must be [rows, cols] with cols a multiple of {multiple}, got {tuple(t.shape)}")
+    return t.shape
+
+
+@_scoped
+def add_layernorm(handle, x, residual, gamma, beta=None, eps: float = 1e-5, want_stats: bool = False, out=None):
+    """h = x + residual and y = LayerNorm(h) * gamma + beta, in one launch.
+
+    x, residual [rows, cols] (residual None: h is x), gamma, beta [cols] (beta may be None), all
+    bfloat16 or all float32, cols a multiple of 8.  Returns a dict of h (absent without a residual), y
+    and, with want_stats, mean and rstd [rows] FP32, which add_layernorm_backward takes.  out: a dict
+    of preallocated tensors (y and, with a residual, h) that takes the place of the switch; out["h"] may be
+    residual or x itself (in place).  stream: a torch.cuda.Stream to launch on."""
+    rows, cols = shape = _matrix(x, "x", 8)
+    dt, dev, flags = x.dtype, x.get_device(), _row_type(x, "x")
+    if out is None:
+        out = {"y": torch.empty_like(x)}
+        if residual is not None:
+            out["h"] = torch.empty_like(x)
+        if want_stats:
+            out["mean"] = torch.empty(rows, dtype=_F32, device=dev)
+            out["rstd"] = torch.empty(rows, dtype=_F32, device=dev)
+    get = out.get
+    st = lib().moe_add_layernorm(
+        _given(x, "x", dt, shape, dev), _given(residual, "residual", dt, shape, dev),
+        _given(_need(gamma, "gamma"), "gamma", dt, (cols,), dev), _given(beta, "beta", dt, (cols,), dev), eps, rows,
+        cols, flags, _given(get("h"), "h", dt, shape, dev), _given(_need(get("y"), "y"), "y", dt, shape, dev),
+        _given(get("mean"), "mean", _F32, (rows,), dev), _given(get("rstd"), "rstd", _F32, (rows,), dev), handle)
+    if st:
+        _check(st, "moe_add_layernorm")
+    return out
+
+
+def add_layernorm_backward_workspace(rows: int, cols: int, device="cuda"):
+    return _bytes_on(lib().moe_add_layernorm_backward_workspace_size(rows, cols), device)
+
+
+@_scoped
+def add_layernorm_backward(handle, dy, h, mean, rstd, gamma, dh=None, out=None, workspace=None):
+    """Backward pass of add_layernorm.
+
+    dy, h [rows, cols], gamma [cols] (types as in the forward pass), mean, rstd [rows] FP32 as the forward
+    pass gives them; dh: the gradient that reaches h over the residual stream (or None).  Returns a dict
+    of dx [rows, cols] (the gradient of x and of the residual alike; out["dx"] may be dy or dh), dgamma
+    and dbeta [cols] FP32; an out without "dbeta" leaves that out.  stream: a torch.cuda.Stream to launch on."""
+    rows, cols = shape = _matrix(dy, "dy", 8)
+    dt, dev, flags = dy.dtype, dy.get_device(), _row_type(dy, "dy")
+    if out is None:
+        out = {"dx": torch.empty_like(dy), "dgamma": torch.empty(cols, dtype=_F32, device=dev),
+               "dbeta": torch.empty(cols, dtype=_F32, device=dev)}
+    if workspace is None:
+        workspace = add_layernorm_backward_workspace(rows, cols, dev)
+    st = lib().moe_add_layernorm_backward(
+        _given(dy, "dy", dt, shape, dev), _given(dh, "dh", dt, shape, dev),
+        _given(_need(h, "h"), "h", dt, shape, dev), _given(_need(mean, "mean"), "mean", _F32, (rows,), dev),
+        _given(_need(rstd, "rstd"), "rstd", _F32, (rows,), dev),
+        _given(_need(gamma, "gamma"), "gamma", dt, (cols,), dev), rows, cols, flags,
+        _given(out["dx"], "dx", dt, shape, dev), _given(out["dgamma"], "dgamma", _F32, (cols,), dev),
+        _given(out.get("dbeta"), "dbeta", _F32, (cols,), dev),
+        _given(workspace, "workspace", _U8, workspace.shape, dev), workspace.numel(), handle)
+    if st:
+        _check(st, "moe_add_layernorm_backward")
+    return out
+
+
+def sort_tokens_workspace(T: int, num_experts: int, k: int, device="cuda"):
+    return _bytes_on(lib().moe_sort_tokens_workspace_size(T, num_experts, k), device)
+
+
+@_scoped
+def sort_tokens(handle, topk_ids, num_experts: int, mask=None, out=None, workspace=None):
+    """The plan of given expert ids [T, k] int32 (any router's): a dict of counts [E], offsets [E+1],
+    perm_src [T*k] (row -> token) and inv [T*k] (assignment -> row), int32, as plan gives them.
+
+    mask [T] (bool or uint8) is 0 for tokens that are left out; ids of -1 are left out too (inv -1,
+    perm_src -1 from offsets[E] on).  Any other id outside [0, num_experts) is left out and reported in
+    the workspace's device status (pass a workspace to read it with last_device_status).  stream: a
+    torch.cuda.Stream to launch on."""
+    if topk_ids.dim() != 2:
+        raise ValueError(f"topk_ids must be [T, k], got {tuple(topk_ids.shape)}")
+    (T, k), E, dev = topk_ids.shape, num_experts, topk_ids.get_device()
+    if out is None:
+        out = {n: torch.empty(m, dtype=_I32, device=dev)
+               for n, m in (("counts", max(E, 0)), ("offsets", max(E, 0) + 1), ("perm_src", T * k), ("inv", T * k))}
+    if workspace is None:
+        workspace = sort_tokens_workspace(T, E, k, dev)
+    st = lib().moe_sort_tokens(
+        _given(topk_ids, "topk_ids", _I32, (T, k), dev), _mask_ptr(mask, T, dev), T, E, k,
+        _given(out["counts"], "counts", _I32, (E,), dev), _given(out["offsets"], "offsets", _I32, (E + 1,), dev),
+        _given(out["perm_src"], "perm_src", _I32, (T * k,), dev), _given(out["inv"], "inv", _I32, (T * k,), dev),
+        _given(workspace, "workspace", _U8, workspace.shape, dev), workspace.numel(), handle)
+    if st:
+        _check(st, "moe_sort_tokens")
+    return out
+
+
+def _inverse(plan, T, dev):
+    """Address of the plan's inv for T tokens, and k."""
+    inv = _need(_need(plan, "plan").get("inv"), "plan['inv']")
+    if T == 0:
+        return None, 1
+    if inv.numel() == 0 or inv.numel() % T:
+        raise ValueError(f"plan['inv'] has {inv.numel()} entries, which is no multiple of the {T} tokens")
+    return _given(inv, "plan['inv']", _I32, (inv.numel(),), dev), inv.numel() // T
+
+
+@_scoped
+def permute_tokens(handle, x, plan, out=None):
+    """Rows sorted by expert: rows[inv[t*k+j]] = x[t] for x [T, cols] of any type (rows of a multiple of
+    16 bytes) and a plan of plan or sort_tokens.  Returns rows [T*k, cols]; rows behind the last expert's stay
+    as they were in out (uninitialised without one).  stream: a torch.cuda.Stream to launch on."""
+    if x.dim() != 2:
+        raise ValueError(f"x must be [T, cols], got {tuple(x.shape)}")
+    (T, cols), dev = x.shape, x.get_device()
+    inv, k = _inverse(plan, T, dev)
+    if out is None:
+        out = torch.empty(T * k, cols, dtype=x.dtype, device=dev)
+    st = lib().moe_permute_rows(_given(x, "x", x.dtype, (T, cols), dev), inv, T, k, cols * x.element_size(), out.shape[0],
+                                _given(out, "out", x.dtype, (out.shape[0], cols), dev), handle)
+    if st:
+        _check(st, "moe_permute_rows")
+    return out
+
+
+@_scoped
+def permute_tokens_backward(handle, drows, plan, num_tokens: int, out=None):
+    """Gradient [num_tokens, cols] of permute_tokens's x: the sum of each token's rows of drows (bfloat16 or
+    float32), in FP32 and slot order.  stream: a torch.cuda.Stream to launch on."""
+    return _combine(handle, drows, "drows", plan, None, num_tokens, out)
+
+
+@_scoped
+def combine_tokens(handle, rows, plan, topk_w, out=None):
+    """y[t] = sum_j topk_w[t, j] * rows[inv[t*k+j]]: rows [T*k, cols] bfloat16 or float32 in expert order, topk_w
+    [T, k] FP32.  Returns y [T, cols] in the type of rows; assignments that were left out add nothing.
+    stream: a torch.cuda.Stream to launch on."""
+    if _need(topk_w, "topk_w").dim() != 2:
+        raise ValueError(f"topk_w must be [T, k], got {tuple(topk_w.shape)}")
+    return _combine(handle, rows, "rows", plan, topk_w, topk_w.shape[0], out)
+
+
+def _combine(handle, rows, name, plan, topk_w, T, out):
+    flags = _row_type(rows, name)
+    R, cols = _matrix(rows, name, 4 if flags else 8)
+    dev = rows.get_device()
+    inv, k = _inverse(plan, T, dev)
+    if out is None:
+        out = torch.empty(T, cols, dtype=rows.dtype, device=dev)
+    st = lib().moe_combine_rows(_given(rows, name, rows.dtype, (R, cols), dev), inv,
+                                _given(topk_w, "topk_w", _F32, (T, k), dev) if T else None, T, k, cols, R, flags,
+                                _given(out, "out", rows.dtype, (T, cols), dev), handle)
+    if st:
+        _check(st, "moe_combine_rows")
+    return out
+
+
+@_scoped
+def combine_tokens_backward(handle, dy, rows, plan, topk_w, out=None):
+    """Backward pass of combine_tokens: from dy [T, cols] a dict of drows [T*k, cols] (in the type of rows; rows
+    behind the last expert's stay as they were in out) and dtopk_w [T, k] FP32 (0 where there is no row),
+    which router_loss_backward takes as grad_topk_w.  out["drows"] may be rows itself.  stream: a
+    torch.cuda.Stream to launch on."""
+    flags = _row_type(dy, "dy")
+    T, cols = _matrix(dy, "dy", 4 if flags else 8)
+    if _need(rows, "rows").dim() != 2:
+        raise ValueError(f"rows must be [T*k, cols], got {tuple(rows.shape)}")
+    dt, dev, R = dy.dtype, dy.get_device(), rows.shape[0]
+    inv, k = _inverse(plan, T, dev)
+    if out is None:
+        out = {"drows": torch.empty_like(rows), "dtopk_w": torch.empty_like(_need(topk_w, "topk_w"))}
+    st = lib().moe_combine_rows_backward(
+        _given(dy, "dy", dt, (T, cols), dev), _given(rows, "rows", dt, (R, cols), dev), inv,
+        _given(_need(topk_w, "topk_w"), "topk_w", _F32, (T, k) if T else topk_w.shape, dev), T, k, cols, R, flags,
+        _given(out["drows"], "drows", dt, (R, cols), dev),
+        _given(out["dtopk_w"], "dtopk_w", _F32, topk_w.shape, dev), handle)
+    if st:
+        _check(st, "moe_combine_rows_backward")
+    return out
+
+
+def experts_workspace(R: int, inter: int, device="cuda"):
+    """Workspace of the three experts_* functions for up to R rows."""
+    return _bytes_on(lib().moe_experts_workspace_size(R, inter), device)
+
+
+def _experts_shapes(rows, name, plan, w_up, w_down):
+    if rows.dim() != 2 or _need(w_up, "w_up").dim() != 3 or _need(w_down, "w_down").dim() != 3:
+        raise ValueError(f"{name} must be [R, H], w_up [E, I, H] and w_down [E, H, I]")
+    (R, H), (E, I) = rows.shape, w_up.shape[:2]
+    if H % 32 or I % 32 or H == 0 or I == 0:
+        raise ValueError(f"H and I must be multiples of 32, got {H} and {I}")
+    return R, H, E, I
+
+
+def _offsets(plan, E, dev):
+    return _given(_need(_need(plan, "plan").get("offsets"), "plan['offsets']"), "plan['offsets']", _I32, (E + 1,), dev)
+
+
+@_scoped
+def experts_forward(handle, rows, plan, w_gate, w_up, w_down, activation: str = "swiglu", swiglu_limit=None,
+                    swiglu_alpha: float = 1.702, keep: bool = False, out=None, workspace=None):
+    """The experts on rows [R, H] BF16 sorted by expert (permute_tokens), plan["offsets"] their segments:
+    out = act(rows Wg^T, rows Wu^T) Wd^T per expert.
+
+    w_gate, w_up [E, I, H], w_down [E, H, I] BF16 (w_gate None for relu2); activation, swiglu_limit and
+    swiglu_alpha as in make_config.  Returns a dict of out [R, H] and, with keep, of what the backward pass
+    reads: g, u (relu2: u alone) and h [R, I].  out: a dict of preallocated tensors that takes the place of the
+    switch.  Rows behind the last expert's stay as they were.  stream: a torch.cuda.Stream to launch on."""
+    flags = _activation_flag(activation, swiglu_limit)
+    R, H, E, I = _experts_shapes(rows, "rows", plan, w_up, w_down)
+    dev, gated = rows.get_device(), activation != "relu2"
+    if out is None:
+        out = {"out": torch.empty_like(rows)}
+        if keep:
+            out.update({n: torch.empty(R, I, dtype=_BF16, device=dev) for n in (("g", "u", "h") if gated else ("u", "h"))})
+    get = out.get
+    if workspace is None:
+        workspace = experts_workspace(0 if get("h") is not None else R, I, dev)
+    st = lib().moe_experts_forward(
+        _given(rows, "rows", _BF16, (R, H), dev), _offsets(plan, E, dev), R, E, H, I,
+        _given(_need(w_gate, "w_gate"), "w_gate", _BF16, (E, I, H), dev) if gated else None,
+        _given(w_up, "w_up", _BF16, (E, I, H), dev), _given(w_down, "w_down", _BF16, (E, H, I), dev), flags,
+        0.0 if swiglu_limit is None else swiglu_limit, swiglu_alpha,
+        _given(get("g"), "g", _BF16, (R, I), dev), _given(get("u"), "u", _BF16, (R, I), dev),
+        _given(get("h"), "h", _BF16, (R, I), dev), _given(out["out"], "out", _BF16, (R, H), dev),
+        _given(workspace, "workspace", _U8, workspace.shape, dev), workspace.numel(), handle)
+    if st:
+        _check(st, "moe_experts_forward")
+    return out
+
+
+@_scoped
+def experts_backward(handle, dout, saved, plan, w_gate, w_up, w_down, activation: str = "swiglu", swiglu_limit=None,
+                     swiglu_alpha: float = 1.702, out=None, workspace=None):
+    """Gradients of experts_forward down to its rows, from dout [R, H] BF16 and saved, the forward pass's dict
+    (g and u): a dict of drows [R, H] (for permute_tokens_backward) and dg, du [R, I] BF16, the
+    gradients of g and u (relu2: du alone), which experts_weight_grad takes.  Rows behind the last
+    expert's stay as they were.  stream: a torch.cuda.Stream to launch on."""
+    flags = _activation_flag(activation, swiglu_limit)
+    R, H, E, I = _experts_shapes(dout, "dout", plan, w_up, w_down)
+    dev, gated = dout.get_device(), activation != "relu2"
+    if out is None:
+        out = {n: torch.empty(R, I, dtype=_BF16, device=dev) for n in (("dg", "du") if gated else ("du",))}
+        out["drows"] = torch.empty_like(dout)
+    if workspace is None:
+        workspace = experts_workspace(0, I, dev)
+    saved = _need(saved, "saved")
+    st = lib().moe_experts_backward(
+        _given(dout, "dout", _BF16, (R, H), dev), _offsets(plan, E, dev), R, E, H, I,
+        _given(_need(w_gate, "w_gate"), "w_gate", _BF16, (E, I, H), dev) if gated else None,
+        _given(w_up, "w_up", _BF16, (E, I, H), dev), _given(w_down, "w_down", _BF16, (E, H, I), dev), flags,
+        0.0 if swiglu_limit is None else swiglu_limit, swiglu_alpha,
+        _given(saved["g"], "g", _BF16, (R, I), dev) if gated else None, _given(saved["u"], "u", _BF16, (R, I), dev),
+        _given(out["dg"], "dg", _BF16, (R, I), dev) if gated else None, _given(out["du"], "du", _BF16, (R, I), dev),
+        _given(out["drows"], "drows", _BF16, (R, H), dev),
+        _given(workspace, "workspace", _U8, workspace.shape, dev), workspace.numel(), handle)
+    if st:
+        _check(st, "moe_experts_backward")
+    return out
+
+
+@_scoped
+def experts_weight_grad(handle, rows, dout, saved, grads, plan, accumulate: bool = False, out=None, workspace=None):
+    """Gradients of the experts' weights, FP32: a dict of w_gate, w_up [E, I, H] and w_down [E, H, I].
+
+    rows, dout [R, H] BF16: the forward pass's rows and the gradient of its out; saved: its dict (h);
+    grads: experts_backward's (dg, du; without dg, as relu2 has none, there is no w_gate).  accumulate: added
+    to out, the sums of earlier micro-batches, instead of taking its place.  stream: a torch.cuda.Stream to
+    launch on."""
+    if rows.dim() != 2 or _need(grads, "grads")["du"].dim() != 2:
+        raise ValueError("rows must be [R, H] and du [R, I]")
+    (R, H), I, dev = rows.shape, grads["du"].shape[1], rows.get_device()
+    if H % 32 or I % 32 or H == 0 or I == 0:
+        raise ValueError(f"H and I must be multiples of 32, got {H} and {I}")
+    E = _need(_need(plan, "plan").get("offsets"), "plan['offsets']").numel() - 1
+    gated = grads.get("dg") is not None
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out, the gradients to add to")
+        out = {"w_up": torch.empty(E, I, H, dtype=_F32, device=dev), "w_down": torch.empty(E, H, I, dtype=_F32, device=dev)}
+        if gated:
+            out["w_gate"] = torch.empty(E, I, H, dtype=_F32, device=dev)
+    if workspace is None:
+        workspace = experts_workspace(0, I, dev)
+    st = lib().moe_experts_weight_grad(
+        _given(rows, "rows", _BF16, (R, H), dev), _given(_need(dout, "dout"), "dout", _BF16, (R, H), dev),
+        _given(_need(saved, "saved")["h"], "h", _BF16, (R, I), dev),
+        _given(grads["dg"], "dg", _BF16, (R, I), dev) if gated else None, _given(grads["du"], "du", _BF16, (R, I), dev),
+        _offsets(plan, E, dev), R, E, H, I, (0 if gated else FLAG_ACT_RELU2) | (EXPERTS_ACCUMULATE if accumulate else 0),
+        _given(out["w_gate"], "w_gate", _F32, (E, I, H), dev) if gated else None,
+        _given(out["w_up"], "w_up", _F32, (E, I, H), dev), _given(out["w_down"], "w_down", _F32, (E, H, I), dev),
+        _given(workspace, "workspace", _U8, workspace.shape, dev), workspace.numel(), handle)
+    if st:
+        _check(st, "moe_experts_weight_grad")
+    return out
 
 
 def last_device_status(workspace) -> int:

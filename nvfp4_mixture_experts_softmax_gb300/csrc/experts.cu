@@ -1,0 +1,864 @@
+// The experts' products of a BF16 layer that is trained, on rows sorted by expert (segment e: rows
+// offsets[e] .. offsets[e+1]):
+//   forward      g = x Wg^T, u = x Wu^T, h = bf16(act(g, u)), out = h Wd^T
+//   backward     dh = dout Wd, (dg, du) = bf16(dh * act'(g, u)), dx = dg Wg + du Wu
+//   weights      dWg = dg^T x, dWu = du^T x, dWd = dout^T h   (FP32)
+// One kernel, a mode for each product.  The products accumulate in FP32 in tensor memory; h, dg and du
+// are rounded to BF16 because the tensor cores read them again (and the backward pass as tensors of
+// its own), everything else is rounded once, where it is stored.
+//
+// tcgen05.mma kind::f16 over pairs of CTAs (cta_group::2): a pair computes a tile of 256 x 256, each CTA
+// holding 128 rows of A and 128 of B, so that shared memory is written and read half as often as by
+// single CTAs with 128 x 256.  Operands come by TMA with the 128-byte swizzle in stages of K = 64, K-major
+// where the reduction runs along a row in memory (forward), MN-major where it runs across rows: no
+// product transposes anything in memory.  The gate and up products share a tile: CTA 0 brings 128 rows of
+// Wg, CTA 1 the same rows of Wu, so that each thread of the epilogue holds g and u of its row.
+//
+// Tiles of 256 rows of one segment: a tile's rows behind the segment are read and multiplied, but not
+// stored (rows do not mix).  In the weights' gradients the rows are the reduction: the last block of a
+// segment is zeroed behind the segment's end in shared memory, in both operands, before it is multiplied.
+//
+// Warps of a CTA: 0-7 epilogue (each a quarter of the rows and half of the columns), 8 copies, 9 tensor
+// memory and, in CTA 0, the MMAs of the pair, 10 the zeroing.  Two accumulators (2 x 256 columns) let
+// the epilogue run beside the next tile's products.  Every wait is bounded; one that runs out leaves
+// MOE_ERR_DEVICE_TIMEOUT in the status.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "common.cuh"
+#include "ops.h"
+
+namespace nvfp4moe {
+
+namespace {
+
+enum Mode { kUp, kUpSingle, kDown, kDgradAct, kDgradRows, kWgrad };
+
+constexpr int kTileM = 256, kTileN = 256;       // of a pair
+constexpr int kHalf = 128;                      // rows of A and of B a CTA holds
+constexpr int kBlockK = 64;
+constexpr int kOperandBytes = kHalf * kBlockK * 2;
+constexpr int kChunkBytes = kBlockK * 128;      // MN-major: 64 columns (128 bytes) of 64 rows
+constexpr int kStages = 6;
+constexpr int kStageBytes = 2 * kOperandBytes;
+constexpr int kEpiWarps = 8, kCopyWarp = 8, kMmaWarp = 9, kZeroWarp = 10;
+constexpr int kThreads = 11 * 32;
+constexpr int kMaxExperts = 1024;
+constexpr int kGroupM = 8;                      // row tiles that are worked through column by column
+constexpr int kSmallBox = 32;                   // rows of the small box
+constexpr uint64_t kLimitNs = 2000000000ull;
+
+// The tensor cores truncate where they add, so the FP32 gradients are cut into chains of this many
+// rows (64 additions), added in FP32 by the epilogue in order.
+constexpr int kChainRows = 1024;
+
+constexpr int kBarOff = kStages * kStageBytes;
+constexpr int kTableOff = kBarOff + 256;
+constexpr size_t kSmemBytes = 1024 + kTableOff + 2 * (kMaxExperts + 1) * sizeof(int32_t) + 8;
+static_assert(kSmemBytes <= 232448, "shared memory");
+
+constexpr bool a_mn_major(Mode m) { return m == kWgrad; }
+constexpr bool b_mn_major(Mode m) { return m == kDgradAct || m == kDgradRows || m == kWgrad; }
+
+// kind::f16: FP32 accumulator, BF16 operands, their major dimensions (bits 15 and 16: 1 = MN), N / 8, M / 16.
+constexpr uint32_t instr_desc(Mode m) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn_major(m) ? 1u : 0u) << 15) |
+         ((b_mn_major(m) ? 1u : 0u) << 16) | ((uint32_t)(kTileN >> 3) << 17) | ((uint32_t)(kTileM >> 4) << 24);
+}
+
+struct Maps {
+  CUtensorMap m[6];
+};
+
+struct Args {
+  const int32_t* offsets;
+  int32_t* status;
+  int E, R;
+  int N;          // columns of the output (gate/up: of each)
+  int M;          // kWgrad: H and N: I of the down matrix, the other way round for gate and up
+  int n_tiles;    // column tiles
+  int nkb;        // blocks of K = 64 of a tile (not kWgrad)
+  int half_kb;    // kDgradRows: blocks of the first source
+  int nmat;       // kWgrad: 3, or 2 without a gate
+  int act;
+  float limit, alpha;
+  const __nv_bfloat16 *g, *u;            // kDgradAct: the forward pass's
+  __nv_bfloat16 *o0, *o1, *o2;           // kUp: g, u (may be null), h; kDgradAct: dg, du; else out
+  float *dw0, *dw1, *dw2;                // kWgrad: gate, up, down
+  int accumulate;
+  int first;      // this launch clears the status
+};
+
+struct Tile {
+  int seg, m0, rows, n0;   // rows: of the tile (kWgrad: rows of the segment, the reduction)
+  int mat, row0;           // kWgrad
+};
+
+__device__ __forceinline__ uint32_t leader_addr(uint32_t bar) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(bar));
+  return r;
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ void arrive_expect_cluster(uint32_t addr, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(addr), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
+      "selp.u32 %0, 1, 0, p;\n"
+      "}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(kTryWaitSuspendNs)
+      : "memory");
+  return ok != 0;
+}
+// As mbar_wait_bounded, for barriers that both CTAs of the pair arrive on; gives up as soon as another
+// role of the CTA has.
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, int32_t* status,
+                                             volatile uint32_t* abort) {
+  if (try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (;;) {
+    if (try_wait_cluster(bar, parity)) return true;
+    if (*abort) return false;
+    if (global_timer_ns() - t0 > kLimitNs) {
+      set_status(status, MOE_ERR_DEVICE_TIMEOUT);
+      *abort = 1u;
+      return false;
+    }
+  }
+}
+
+// TMA loads into this CTA's shared memory that complete on a barrier of either CTA of the pair.
+__device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "setp.ne.u32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n"
+      "}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrives on the barrier at this address in both CTAs once the MMAs issued before are done.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+// 32 bytes a thread: whole sectors, although a warp's threads hold different rows.
+__device__ __forceinline__ void store_32b(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+__device__ __forceinline__ void load_32b(const void* p, uint32_t* v) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float low_bf16(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high_bf16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// 32 columns as BF16.
+__device__ __forceinline__ void store_bf16x32(__nv_bfloat16* p, const float (&f)[32]) {
+  uint32_t w[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) w[i] = pack2(f[2 * i], f[2 * i + 1]);
+  store_32b(p, w);
+  store_32b(p + 16, w + 8);
+}
+
+// The activation and its derivatives by g and u, the clamps passing NaN on.  The fast exponential and
+// division err by a few 2^-22, far below the BF16 rounding that follows; a very negative argument's
+// denominator overflows and the sigmoid is 0.
+__device__ __forceinline__ float clamp_up(float v, float L) { return v > L ? L : v; }
+__device__ __forceinline__ float clamp_both(float v, float L) { return v > L ? L : v < -L ? -L : v; }
+
+__device__ __forceinline__ float activation(float g, float u, int act, float L, float alpha) {
+  if (act == kActRelu2) return u <= 0.0f ? 0.0f : u * u;
+  if (act != kActSwiglu) {
+    g = clamp_up(g, L);
+    u = clamp_both(u, L);
+  }
+  if (act == kActSwigluOai) return (u + 1.0f) * __fdividef(g, 1.0f + __expf(-(alpha * g)));
+  return __fdividef(g, 1.0f + __expf(-g)) * u;
+}
+
+__device__ __forceinline__ void activation_grad(float g, float u, float dh, int act, float L, float alpha, float& dg,
+                                                float& du) {
+  if (act == kActRelu2) {
+    dg = 0.0f;
+    du = u <= 0.0f ? 0.0f : dh * (2.0f * u);
+    return;
+  }
+  float gc = g, uc = u, a = 1.0f;
+  if (act != kActSwiglu) {
+    gc = clamp_up(g, L);
+    uc = clamp_both(u, L);
+  }
+  if (act == kActSwigluOai) {
+    a = alpha;
+    uc += 1.0f;
+  }
+  const float s = __fdividef(1.0f, 1.0f + __expf(-(a * gc)));
+  dg = dh * (uc * (s * (1.0f + a * gc * (1.0f - s))));
+  du = dh * (gc * s);
+  if (act != kActSwiglu) {   // the clamps' gradient is 0 beyond them, 1 at them
+    if (g > L) dg = 0.0f;
+    if (fabsf(u) > L) du = 0.0f;
+  }
+}
+
+template <Mode kMode>
+__device__ __forceinline__ Tile tile_at(const Args& p, const int32_t* s_off, const int32_t* s_tile, int item) {
+  constexpr int kCols = kMode == kUp ? kHalf : kTileN;
+  Tile t;
+  int mt, local;   // row tiles of the group's matrix, item within it
+  if constexpr (kMode == kWgrad) {
+    const int mh = (p.M + kTileM - 1) / kTileM, ni = (p.N + kTileN - 1) / kTileN;   // of H and of I
+    const int per = mh * ni;
+    const int sm = item / per;
+    local = item - sm * per;
+    t.seg = sm / p.nmat;
+    t.mat = sm - t.seg * p.nmat + 3 - p.nmat;    // 0 gate, 1 up, 2 down
+    mt = t.mat == 2 ? mh : ni;
+    t.row0 = s_off[t.seg];
+    t.rows = s_off[t.seg + 1] - t.row0;
+  } else {
+    int lo = 0, hi = p.E - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_tile[mid] * p.n_tiles <= item) lo = mid;
+      else hi = mid - 1;
+    }
+    t.seg = lo;
+    t.mat = 0;
+    mt = s_tile[lo + 1] - s_tile[lo];
+    local = item - s_tile[lo] * p.n_tiles;
+  }
+  const int n_tiles = kMode == kWgrad ? (t.mat == 2 ? (p.N + kTileN - 1) / kTileN : (p.M + kTileN - 1) / kTileN) : p.n_tiles;
+  // kGroupM row tiles by all columns, rows fastest: the pairs that run at the same time share both operands
+  const int grp = local / (kGroupM * n_tiles);
+  const int rem = local - grp * kGroupM * n_tiles;
+  const int gm = min(kGroupM, mt - grp * kGroupM);
+  const int nt = rem / gm;
+  const int m = grp * kGroupM + rem - nt * gm;
+  t.n0 = nt * kCols;
+  if constexpr (kMode == kWgrad) {
+    t.m0 = m * kTileM;
+  } else {
+    t.m0 = s_off[t.seg] + m * kTileM;
+    t.rows = min(kTileM, s_off[t.seg + 1] - t.m0);
+    t.row0 = 0;
+  }
+  return t;
+}
+
+template <Mode kMode>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    experts_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBarOff);   // [stage], CTA 0's: both CTAs' data has landed
+  uint64_t* empty = full + kStages;                               // [stage]: the MMAs have read it
+  uint64_t* tail = empty + kStages;                               // [stage]: data that is to be zeroed has landed
+  uint64_t* acc_full = tail + kStages;                            // [2]
+  uint64_t* acc_empty = acc_full + 2;                             // [2], CTA 0's
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  volatile uint32_t* s_abort = tmem_slot + 1;
+  int32_t* s_bad = reinterpret_cast<int32_t*>(tmem_slot + 2);
+  int32_t* s_off = reinterpret_cast<int32_t*>(smem + kTableOff);
+  int32_t* s_tile = s_off + kMaxExperts + 1;
+  static_assert((3 * kStages + 4) * 8 + 12 <= 256, "barrier area");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(smem_u32(full + s), 2);    // one arrival of each CTA, and the bytes
+      mbar_init(smem_u32(empty + s), 1);
+      mbar_init(smem_u32(tail + s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(acc_full + b), 1);
+      mbar_init(smem_u32(acc_empty + b), 2 * kEpiWarps);
+    }
+    *s_abort = 0u;
+    *s_bad = 0;
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  griddep_wait();
+  griddep_launch();
+  for (int i = threadIdx.x; i <= p.E; i += kThreads) s_off[i] = p.offsets[i];
+  __syncthreads();
+  // offsets that do not ascend within the rows: no work, and the status says so
+  for (int i = threadIdx.x; i < p.E; i += kThreads)
+    if (s_off[i] < 0 || s_off[i + 1] < s_off[i] || s_off[i + 1] > p.R) *s_bad = 1;
+  __syncthreads();
+  const bool bad = *s_bad != 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    if (p.first) *p.status = bad ? MOE_ERR_INVALID_ARG : MOE_OK;
+  }
+  if (kMode != kWgrad && warp == 0 && !bad) {
+    // row tiles before each segment: lane l takes a run of segments
+    const int per = (p.E + 31) / 32, s0 = min(lane * per, p.E), s1 = min(s0 + per, p.E);
+    int c = 0;
+    for (int i = s0; i < s1; ++i) c += (s_off[i + 1] - s_off[i] + kTileM - 1) / kTileM;
+    int incl = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    int off = incl - c;
+    for (int i = s0; i < s1; ++i) {
+      s_tile[i] = off;
+      off += (s_off[i + 1] - s_off[i] + kTileM - 1) / kTileM;
+    }
+    if (lane == 31) s_tile[p.E] = incl;
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // the pair's barriers are ready
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t smem0 = smem_u32(smem);
+  int total = 0;
+  if (!bad)
+    total = kMode == kWgrad ? p.E * p.nmat * ((p.M + kTileM - 1) / kTileM) * ((p.N + kTileN - 1) / kTileN)
+                            : s_tile[p.E] * p.n_tiles;
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;   // pairs
+
+  // chains of a tile, and blocks of K of one of them
+  auto chains_of = [&](const Tile& t) { return kMode == kWgrad ? (t.rows + kChainRows - 1) / kChainRows : 1; };
+  auto blocks_of = [&](const Tile& t, int chain) {
+    return kMode == kWgrad ? (min(kChainRows, t.rows - chain * kChainRows) + kBlockK - 1) / kBlockK : p.nkb;
+  };
+
+  if (warp == kCopyWarp) {
+    // ---------------- copies ----------------
+    if (lane == 0) {
+      uint32_t st = 0, ph = 0, used = 0;
+      bool ok = true;
+      for (int item = first; item < total && ok; item += step) {
+        const Tile t = tile_at<kMode>(p, s_off, s_tile, item);
+        const int nch = chains_of(t);
+        for (int ch = 0; ch < nch && ok; ++ch) {
+          const int nkb = blocks_of(t, ch);
+          for (int kb = 0; kb < nkb; ++kb) {
+            if (!wait_bounded(smem_u32(empty + st), ph ^ 1u, p.status, s_abort)) {
+              ok = false;
+              break;
+            }
+            const uint32_t a = smem0 + st * kStageBytes, b = a + kOperandBytes;
+            uint32_t bar = leader_addr(smem_u32(full + st));
+            if constexpr (kMode == kWgrad) {
+              const int Mm = t.mat == 2 ? p.M : p.N, Nn = t.mat == 2 ? p.N : p.M;
+              const CUtensorMap* ma = maps.m + (t.mat == 0 ? 0 : t.mat == 1 ? 2 : 3);
+              const CUtensorMap* mb = maps.m + (t.mat == 2 ? 4 : 1);
+              const int row = t.row0 + ch * kChainRows + kb * kBlockK;
+              const int m = t.m0 + rank * kHalf, n = t.n0 + rank * kHalf;
+              const int na = m >= Mm ? 0 : m + 64 >= Mm ? 1 : 2, nb = n >= Nn ? 0 : n + 64 >= Nn ? 1 : 2;
+              const bool cut = row + kBlockK > t.row0 + t.rows;
+              if (cut) bar = smem_u32(tail + st);
+              if (cut) mbar_arrive_expect_tx(bar, (uint32_t)(na + nb) * kChunkBytes);
+              else arrive_expect_cluster(bar, (uint32_t)(na + nb) * kChunkBytes);
+              for (int i = 0; i < na; ++i) load_2d(a + i * kChunkBytes, ma, m + 64 * i, row, bar);
+              for (int i = 0; i < nb; ++i) load_2d(b + i * kChunkBytes, mb, n + 64 * i, row, bar);
+            } else {
+              const int mine = t.rows - (int)rank * kHalf;   // rows of this CTA's half
+              const uint32_t abytes = mine <= 0 ? 0u : mine <= kSmallBox ? kSmallBox * 128u : (uint32_t)kOperandBytes;
+              const bool second = kMode == kDgradRows && kb >= p.half_kb;
+              const int k0 = (second ? kb - p.half_kb : kb) * kBlockK;
+              const CUtensorMap* ma = maps.m + (abytes == kSmallBox * 128u ? (second ? 5 : 3) : (second ? 2 : 0));
+              if constexpr (b_mn_major(kMode)) {
+                const int n = t.n0 + rank * kHalf;
+                const int nb = n >= p.N ? 0 : n + 64 >= p.N ? 1 : 2;
+                arrive_expect_cluster(bar, abytes + (uint32_t)nb * kChunkBytes);
+                if (abytes) load_2d(a, ma, k0, t.m0 + rank * kHalf, bar);
+                for (int i = 0; i < nb; ++i) load_3d(b + i * kChunkBytes, maps.m + (second ? 4 : 1), n + 64 * i, k0, t.seg, bar);
+              } else {
+                const int n = kMode == kUp ? t.n0 : t.n0 + (int)rank * kHalf;
+                const bool has_b = n < p.N;
+                arrive_expect_cluster(bar, abytes + (has_b ? kOperandBytes : 0));
+                if (abytes) load_2d(a, ma, k0, t.m0 + rank * kHalf, bar);
+                if (has_b) load_3d(b, maps.m + (kMode == kUp && rank == 1 ? 2 : 1), k0, n, t.seg, bar);
+              }
+            }
+            used = min(used + 1, (uint32_t)kStages);
+            if (++st == kStages) { st = 0; ph ^= 1u; }
+          }
+        }
+      }
+      // the MMAs' arrivals on this CTA's barriers have to come before it may end
+      for (uint32_t i = 0; i < used && ok; ++i) {
+        const uint32_t s = (st + kStages - used + i) % kStages;
+        const uint32_t par = s < st ? ph : ph ^ 1u;
+        ok = wait_bounded(smem_u32(empty + s), par, p.status, s_abort);
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ---------------- products (CTA 0) ----------------
+    if (rank == 0) {
+      constexpr uint32_t idesc = instr_desc(kMode);
+      constexpr uint32_t step_a = a_mn_major(kMode) ? 128u : 2u, step_b = b_mn_major(kMode) ? 128u : 2u;   // K = 16, in 16 bytes
+      const uint64_t da0 = smem_desc(smem0, a_mn_major(kMode) ? kChunkBytes : 16, 1024, kLayoutSwizzle128B);
+      const uint64_t db0 = smem_desc(smem0 + kOperandBytes, b_mn_major(kMode) ? kChunkBytes : 16, 1024, kLayoutSwizzle128B);
+      uint32_t st = 0, ph = 0, unit = 0;
+      bool ok = true;
+      for (int item = first; item < total && ok; item += step) {
+        const Tile t = tile_at<kMode>(p, s_off, s_tile, item);
+        const int nch = chains_of(t);
+        for (int ch = 0; ch < nch && ok; ++ch, ++unit) {
+          const int nkb = blocks_of(t, ch);
+          const uint32_t buf = unit & 1u;
+          ok = __all_sync(0xffffffffu, wait_bounded(smem_u32(acc_empty + buf), ((unit >> 1) & 1u) ^ 1u, p.status, s_abort));
+          if (!ok) break;
+          tc_fence_after();
+          for (int kb = 0; kb < nkb; ++kb) {
+            ok = __all_sync(0xffffffffu, wait_bounded(smem_u32(full + st), ph, p.status, s_abort));
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
+              const uint64_t so = (uint64_t)(st * (kStageBytes >> 4));
+#pragma unroll
+              for (int kk = 0; kk < kBlockK / 16; ++kk)
+                mma_pair(tmem + buf * kTileN, da0 + so + kk * step_a, db0 + so + kk * step_b, idesc, (kb | kk) != 0 ? 1u : 0u);
+              commit_pair(smem_u32(empty + st));
+              if (kb == nkb - 1) commit_pair(smem_u32(acc_full + buf));
+            }
+            __syncwarp();
+            if (++st == kStages) { st = 0; ph ^= 1u; }
+          }
+        }
+      }
+    }
+  } else if (warp == kZeroWarp) {
+    // ---------------- zeros behind the end of a segment ----------------
+    if constexpr (kMode == kWgrad) {
+      uint32_t at = 0, phases = 0;   // blocks passed; phase of each tail barrier
+      bool ok = true;
+      for (int item = first; item < total && ok; item += step) {
+        const Tile t = tile_at<kMode>(p, s_off, s_tile, item);
+        if (t.rows == 0) continue;
+        const int full_chains = t.rows / kChainRows, rest = t.rows - full_chains * kChainRows;
+        at += full_chains * (kChainRows / kBlockK) + (rest + kBlockK - 1) / kBlockK;
+        const int have = t.rows % kBlockK;
+        if (have == 0) continue;
+        const uint32_t st = (at - 1) % kStages;
+        ok = __all_sync(0xffffffffu, wait_bounded(smem_u32(tail + st), (phases >> st) & 1u, p.status, s_abort));
+        if (!ok) break;
+        phases ^= 1u << st;
+        uint8_t* base = smem + st * kStageBytes;
+        const int n16 = (kBlockK - have) * 8;   // 16-byte pieces of the rows to clear (a swizzle stays inside its row)
+        for (int c = 0; c < kStageBytes / kChunkBytes; ++c)
+          for (int i = lane; i < n16; i += 32)
+            *reinterpret_cast<uint4*>(base + c * kChunkBytes + have * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(leader_addr(smem_u32(full + st)));
+      }
+    }
+  } else {
+    // ---------------- epilogue: a row a thread, half of the columns a warp ----------------
+    const int quad = warp & 3, half = warp >> 2;
+    const int local = (int)rank * kHalf + quad * 32 + lane;   // row of the tile
+    uint32_t unit = 0;
+    bool ok = true;
+    for (int item = first; item < total && ok; item += step) {
+      const Tile t = tile_at<kMode>(p, s_off, s_tile, item);
+      const int nch = kMode == kWgrad ? max(chains_of(t), 1) : 1;
+      for (int ch = 0; ch < nch && ok; ++ch) {
+        const bool none = kMode == kWgrad && t.rows == 0;   // a segment without rows: zeros, no products
+        const uint32_t buf = unit & 1u;
+        if (!none) {
+          ok = __all_sync(0xffffffffu, wait_bounded(smem_u32(acc_full + buf), (unit >> 1) & 1u, p.status, s_abort));
+          if (!ok) break;
+          ++unit;
+          tc_fence_after();
+        }
+        const uint32_t acc = tmem + buf * kTileN + ((uint32_t)(quad * 32) << 16);
+        if constexpr (kMode == kWgrad) {
+          const int Mm = t.mat == 2 ? p.M : p.N, Nn = t.mat == 2 ? p.N : p.M;
+          const bool add = ch > 0 || p.accumulate;
+          float* out = (t.mat == 0 ? p.dw0 : t.mat == 1 ? p.dw1 : p.dw2) +
+                       ((size_t)t.seg * Mm + min(t.m0 + local, Mm - 1)) * Nn + t.n0 + half * kHalf;
+          const bool live = t.m0 + local < Mm && !(none && p.accumulate);
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            const bool in = live && t.n0 + half * kHalf + c * 32 < Nn;
+            uint32_t v[32], old[32];
+            if (in && add && !none)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) load_32b(out + c * 32 + 8 * i, old + 8 * i);
+            if (!none) {
+              tmem_ld_32x32b_x32(acc + half * kHalf + c * 32, v);
+              tmem_ld_wait();
+            }
+            if (!in) continue;
+            if (none) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = 0u;
+            } else if (add) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(old[i]) + __uint_as_float(v[i]));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) store_32b(out + c * 32 + 8 * i, v + 8 * i);
+          }
+        } else if ((int)rank * kHalf + quad * 32 < t.rows) {
+          const bool live = local < t.rows;
+          const size_t row = (size_t)(t.m0 + local) * p.N;
+          if constexpr (kMode == kUp) {
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {
+              const int col = half * 64 + c * 32;
+              if (t.n0 + col >= p.N) break;
+              uint32_t vg[32], vu[32];
+              tmem_ld_32x32b_x32(acc + col, vg);
+              tmem_ld_32x32b_x32(acc + kHalf + col, vu);
+              tmem_ld_wait();
+              if (!live) continue;
+              const size_t at = row + t.n0 + col;
+              float g[32], u[32], h[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                g[i] = __uint_as_float(vg[i]);
+                u[i] = __uint_as_float(vu[i]);
+                h[i] = activation(g[i], u[i], p.act, p.limit, p.alpha);
+              }
+              if (p.o0) store_bf16x32(p.o0 + at, g);
+              if (p.o1) store_bf16x32(p.o1 + at, u);
+              store_bf16x32(p.o2 + at, h);
+            }
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              const int col = half * kHalf + c * 32;
+              if (t.n0 + col >= p.N) break;
+              const size_t at = row + t.n0 + col;
+              uint32_t v[32], gu[32];
+              if constexpr (kMode == kDgradAct) {
+                if (live) {
+                  if (p.g) {
+                    load_32b(p.g + at, gu);
+                    load_32b(p.g + at + 16, gu + 8);
+                  }
+                  load_32b(p.u + at, gu + 16);
+                  load_32b(p.u + at + 16, gu + 24);
+                }
+              }
+              tmem_ld_32x32b_x32(acc + col, v);
+              tmem_ld_wait();
+              if (!live) continue;
+              float f[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
+              if constexpr (kMode == kUpSingle) {
+                if (p.o1) store_bf16x32(p.o1 + at, f);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) f[i] = activation(0.0f, f[i], kActRelu2, 0.0f, 0.0f);
+                store_bf16x32(p.o2 + at, f);
+              } else if constexpr (kMode == kDgradAct) {
+                float dg[32], du[32];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  activation_grad(low_bf16(gu[i]), low_bf16(gu[16 + i]), f[2 * i], p.act, p.limit, p.alpha, dg[2 * i], du[2 * i]);
+                  activation_grad(high_bf16(gu[i]), high_bf16(gu[16 + i]), f[2 * i + 1], p.act, p.limit, p.alpha, dg[2 * i + 1],
+                                  du[2 * i + 1]);
+                }
+                if (p.o0) store_bf16x32(p.o0 + at, dg);
+                store_bf16x32(p.o1 + at, du);
+              } else {
+                store_bf16x32(p.o0 + at, f);
+              }
+            }
+          }
+        }
+        if (!none) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_cluster(leader_addr(smem_u32(acc_empty + buf)));
+        }
+      }
+    }
+  }
+
+  // After a wait ran out, copies into shared memory and MMAs may still be under way: they end within
+  // microseconds, the CTA stays ten milliseconds.
+  __syncwarp();
+  if (*s_abort) {
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 10000000ull) __nanosleep(10000);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // no arrival and no MMA of the pair is under way towards either CTA
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      ptr = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  }();
+  return fn;
+}
+
+// BF16 [d2][d1][d0] (d2 = 0: two dimensions), boxes of 64 columns by `rows`.
+bool make_map(CUtensorMap* m, const void* ptr, int64_t d0, int64_t d1, int64_t d2, int rows) {
+  const cuuint64_t dims[3] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2};
+  const cuuint64_t strides[2] = {(cuuint64_t)d0 * 2, (cuuint64_t)d0 * d1 * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)rows, 1}, estr[3] = {1, 1, 1};
+  return encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d2 ? 3 : 2, const_cast<void*>(ptr), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <Mode kMode>
+cudaError_t launch(const Maps& maps, const Args& a, int64_t most_items, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(experts_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+  if (e != cudaSuccess) return e;
+  const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(most_items, num_sms() / 2));
+  return launch_pdl(experts_kernel<kMode>, dim3(2 * pairs), dim3(kThreads), kSmemBytes, s, maps, a);
+}
+
+int div_up(int64_t a, int b) { return (int)((a + b - 1) / b); }
+
+// What the three entry points have in common.
+struct Shape {
+  int64_t R, H, I;
+  int E, act;
+  bool gated;
+};
+
+int check_shape(const int32_t* offsets, int64_t R, int32_t E, int64_t H, int64_t I, uint32_t flags, float limit, float alpha,
+                const void* ws, size_t ws_bytes, size_t need, Shape& sh) {
+  if (R < 0 || E < 1 || H < 1 || I < 1 || H % 32 || I % 32) return MOE_ERR_INVALID_ARG;
+  const uint32_t acts = MOE_FLAG_SWIGLU_CLAMP | MOE_FLAG_ACT_RELU2 | MOE_FLAG_ACT_SWIGLU_OAI;
+  if (flags & ~acts) return MOE_ERR_INVALID_ARG;
+  sh.act = flags == 0 ? kActSwiglu
+           : flags == MOE_FLAG_SWIGLU_CLAMP ? kActSwigluClamp
+           : flags == MOE_FLAG_ACT_RELU2 ? kActRelu2
+           : flags == MOE_FLAG_ACT_SWIGLU_OAI ? kActSwigluOai : -1;
+  if (sh.act < 0) return MOE_ERR_INVALID_ARG;
+  if ((sh.act == kActSwigluClamp || sh.act == kActSwigluOai) && !(std::isfinite(limit) && limit >= 0.0f)) return MOE_ERR_INVALID_ARG;
+  if (sh.act == kActSwigluOai && !std::isfinite(alpha)) return MOE_ERR_INVALID_ARG;
+  if (E > kMaxExperts || R > INT32_MAX || H > (1 << 16) || I > (1 << 16)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  // tiles are counted in 32 bits
+  const int64_t cols = std::max(H, I) / kHalf + 1;
+  if ((R / kTileM + E) * cols > INT32_MAX || 3 * (int64_t)E * cols * cols > INT32_MAX) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!ws || ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (!is_aligned(ws, 256) || !offsets || !is_aligned(offsets, 4)) return MOE_ERR_INVALID_ARG;
+  sh.R = R;
+  sh.H = H;
+  sh.I = I;
+  sh.E = E;
+  sh.gated = sh.act != kActRelu2;
+  return MOE_OK;
+}
+
+Args base_args(const Shape& sh, const int32_t* offsets, void* ws, float limit, float alpha) {
+  Args a = {};
+  a.offsets = offsets;
+  a.status = static_cast<int32_t*>(ws);
+  a.E = sh.E;
+  a.R = (int)sh.R;
+  a.act = sh.act;
+  a.limit = limit;
+  a.alpha = alpha;
+  return a;
+}
+
+int64_t row_items(const Shape& sh, int n_tiles) { return (sh.R / kTileM + std::min<int64_t>(sh.E, sh.R)) * n_tiles; }
+
+constexpr size_t kHeader = 256;   // the status
+
+}  // namespace
+}  // namespace nvfp4moe
+
+using namespace nvfp4moe;
+
+extern "C" {
+
+size_t moe_experts_workspace_size(int64_t R, int64_t I) {
+  if (R < 0 || I < 0 || R > INT32_MAX || I > (1 << 16)) return 0;
+  return kHeader + align_up((size_t)R * (size_t)I * 2);
+}
+
+int moe_experts_forward(const void* rows, const int32_t* offsets, int64_t R, int32_t E, int64_t H, int64_t I,
+                        const void* w_gate, const void* w_up, const void* w_down, uint32_t flags, float swiglu_limit,
+                        float swiglu_alpha, void* g, void* u, void* h, void* out, void* workspace, size_t ws_bytes,
+                        moe_stream_t stream) {
+  Shape sh;
+  const int st = check_shape(offsets, R, E, H, I, flags, swiglu_limit, swiglu_alpha, workspace, ws_bytes,
+                             h || R < 0 || I < 0 ? kHeader : moe_experts_workspace_size(R, I), sh);
+  if (st != MOE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (R == 0) return cudaMemsetAsync(workspace, 0, sizeof(int32_t), s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  if (!rows || !w_up || !w_down || !out || (sh.gated && !w_gate)) return MOE_ERR_INVALID_ARG;
+  if (sh.gated ? (g == nullptr) != (u == nullptr) : g != nullptr) return MOE_ERR_INVALID_ARG;
+  for (const void* p : {rows, sh.gated ? w_gate : nullptr, w_up, w_down})
+    if (!is_aligned(p, 16)) return MOE_ERR_INVALID_ARG;
+  for (const void* p : {g, u, h, out})
+    if (!is_aligned(p, 32)) return MOE_ERR_INVALID_ARG;
+  if (!encoder()) return MOE_ERR_CUDA;
+  void* hb = h ? h : static_cast<uint8_t*>(workspace) + kHeader;
+  Maps m = {};
+  Args a = base_args(sh, offsets, workspace, swiglu_limit, swiglu_alpha);
+  bool ok = make_map(&m.m[0], rows, H, R, 0, kHalf) && make_map(&m.m[3], rows, H, R, 0, kSmallBox) &&
+            make_map(&m.m[1], sh.gated ? w_gate : w_up, H, I, E, kHalf) && make_map(&m.m[2], w_up, H, I, E, kHalf);
+  if (!ok) return MOE_ERR_CUDA;
+  a.N = (int)I;
+  a.nkb = div_up(H, kBlockK);
+  a.n_tiles = div_up(I, sh.gated ? kHalf : kTileN);
+  a.o0 = static_cast<__nv_bfloat16*>(g);
+  a.o1 = static_cast<__nv_bfloat16*>(u);
+  a.o2 = static_cast<__nv_bfloat16*>(hb);
+  a.first = 1;
+  cudaError_t e = sh.gated ? launch<kUp>(m, a, row_items(sh, a.n_tiles), s) : launch<kUpSingle>(m, a, row_items(sh, a.n_tiles), s);
+  if (e != cudaSuccess) return MOE_ERR_CUDA;
+  ok = make_map(&m.m[0], hb, I, R, 0, kHalf) && make_map(&m.m[3], hb, I, R, 0, kSmallBox) &&
+       make_map(&m.m[1], w_down, I, H, E, kHalf);
+  if (!ok) return MOE_ERR_CUDA;
+  a.N = (int)H;
+  a.nkb = div_up(I, kBlockK);
+  a.n_tiles = div_up(H, kTileN);
+  a.o0 = static_cast<__nv_bfloat16*>(out);
+  a.o1 = a.o2 = nullptr;
+  a.first = 0;
+  return launch<kDown>(m, a, row_items(sh, a.n_tiles), s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+int moe_experts_backward(const void* dout, const int32_t* offsets, int64_t R, int32_t E, int64_t H, int64_t I,
+                         const void* w_gate, const void* w_up, const void* w_down, uint32_t flags, float swiglu_limit,
+                         float swiglu_alpha, const void* g, const void* u, void* dg, void* du, void* drows, void* workspace,
+                         size_t ws_bytes, moe_stream_t stream) {
+  Shape sh;
+  const int st = check_shape(offsets, R, E, H, I, flags, swiglu_limit, swiglu_alpha, workspace, ws_bytes, kHeader, sh);
+  if (st != MOE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (R == 0) return cudaMemsetAsync(workspace, 0, sizeof(int32_t), s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  if (!dout || !w_up || !w_down || !u || !du || !drows) return MOE_ERR_INVALID_ARG;
+  if (sh.gated ? !w_gate || !g || !dg : g || dg) return MOE_ERR_INVALID_ARG;
+  for (const void* p : {dout, sh.gated ? w_gate : nullptr, w_up, w_down})
+    if (!is_aligned(p, 16)) return MOE_ERR_INVALID_ARG;
+  for (const void* p : {g, u, (const void*)dg, (const void*)du, (const void*)drows})
+    if (!is_aligned(p, 32)) return MOE_ERR_INVALID_ARG;
+  if (!encoder()) return MOE_ERR_CUDA;
+  Maps m = {};
+  Args a = base_args(sh, offsets, workspace, swiglu_limit, swiglu_alpha);
+  bool ok = make_map(&m.m[0], dout, H, R, 0, kHalf) && make_map(&m.m[3], dout, H, R, 0, kSmallBox) &&
+            make_map(&m.m[1], w_down, I, H, E, kBlockK);
+  if (!ok) return MOE_ERR_CUDA;
+  a.N = (int)I;
+  a.nkb = div_up(H, kBlockK);
+  a.n_tiles = div_up(I, kTileN);
+  a.g = static_cast<const __nv_bfloat16*>(g);
+  a.u = static_cast<const __nv_bfloat16*>(u);
+  a.o0 = static_cast<__nv_bfloat16*>(dg);
+  a.o1 = static_cast<__nv_bfloat16*>(du);
+  a.first = 1;
+  if (launch<kDgradAct>(m, a, row_items(sh, a.n_tiles), s) != cudaSuccess) return MOE_ERR_CUDA;
+  const void* first = sh.gated ? dg : du;
+  ok = make_map(&m.m[0], first, I, R, 0, kHalf) && make_map(&m.m[3], first, I, R, 0, kSmallBox) &&
+       make_map(&m.m[1], sh.gated ? w_gate : w_up, H, I, E, kBlockK) && make_map(&m.m[2], du, I, R, 0, kHalf) &&
+       make_map(&m.m[5], du, I, R, 0, kSmallBox) && make_map(&m.m[4], w_up, H, I, E, kBlockK);
+  if (!ok) return MOE_ERR_CUDA;
+  a.N = (int)H;
+  a.half_kb = div_up(I, kBlockK);
+  a.nkb = a.half_kb * (sh.gated ? 2 : 1);
+  a.n_tiles = div_up(H, kTileN);
+  a.o0 = static_cast<__nv_bfloat16*>(drows);
+  a.o1 = nullptr;
+  a.first = 0;
+  return launch<kDgradRows>(m, a, row_items(sh, a.n_tiles), s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+int moe_experts_weight_grad(const void* rows, const void* dout, const void* h, const void* dg, const void* du,
+                            const int32_t* offsets, int64_t R, int32_t E, int64_t H, int64_t I, uint32_t flags,
+                            float* dw_gate, float* dw_up, float* dw_down, void* workspace, size_t ws_bytes,
+                            moe_stream_t stream) {
+  Shape sh;
+  const bool accumulate = flags & MOE_EXPERTS_ACCUMULATE;
+  const int st = check_shape(offsets, R, E, H, I, flags & ~MOE_EXPERTS_ACCUMULATE, 0.0f, 0.0f, workspace, ws_bytes, kHeader, sh);
+  if (st != MOE_OK) return st;
+  if (!dw_up || !dw_down || (sh.gated ? !dw_gate : dw_gate != nullptr)) return MOE_ERR_INVALID_ARG;
+  for (const void* p : {dw_gate, dw_up, dw_down})
+    if (!is_aligned(p, 32)) return MOE_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (R == 0) {
+    cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(int32_t), s);
+    const size_t n = sizeof(float) * (size_t)E * H * I;
+    for (float* p : {dw_gate, dw_up, dw_down})
+      if (e == cudaSuccess && p && !accumulate) e = cudaMemsetAsync(p, 0, n, s);
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  }
+  if (!rows || !dout || !h || !du || (sh.gated ? !dg : dg != nullptr)) return MOE_ERR_INVALID_ARG;
+  for (const void* p : {rows, dout, h, dg, du})
+    if (!is_aligned(p, 16)) return MOE_ERR_INVALID_ARG;
+  if (!encoder()) return MOE_ERR_CUDA;
+  Maps m = {};
+  const bool ok = make_map(&m.m[0], sh.gated ? dg : du, I, R, 0, kBlockK) && make_map(&m.m[1], rows, H, R, 0, kBlockK) &&
+                  make_map(&m.m[2], du, I, R, 0, kBlockK) && make_map(&m.m[3], dout, H, R, 0, kBlockK) &&
+                  make_map(&m.m[4], h, I, R, 0, kBlockK);
+  if (!ok) return MOE_ERR_CUDA;
+  Args a = base_args(sh, offsets, workspace, 0.0f, 0.0f);
+  a.M = (int)H;
+  a.N = (int)I;
+  a.nmat = sh.gated ? 3 : 2;
+  a.dw0 = dw_gate;
+  a.dw1 = dw_up;
+  a.dw2 = dw_down;
+  a.accumulate = accumulate;
+  a.first = 1;
+  const int64_t items = (int64_t)E * a.nmat * div_up(H, kTileM) * div_up(I, kTileN);
+  return launch<kWgrad>(m, a, items, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -21,6 +21,7 @@
 
 #include "common.cuh"
 #include "ops.h"
+#include "rows.cuh"
 
 namespace nvfp4moe {
 
@@ -28,50 +29,12 @@ namespace {
 
 constexpr int kMaxCols = 16384;
 
-__device__ __forceinline__ void unpack8(uint4 q, float (&f)[8]) {
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = bf16_bits_to_f32(w[i] & 0xFFFFu);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-}
-
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&b);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 // How a row is laid over threads: W warps with J vectors of 8 columns a lane (vector c of lane t:
 // c = j * 32 W + t, so four neighbouring lanes share a 32-element block); a block holds G such row
 // groups, each of which takes every gridDim * G-th row.
 struct RowGrid {
   int J, W, G, blocks;
 };
-
-// Sum of one value per thread over the W warps of a row group, the same on every thread and in a
-// fixed order.  One barrier: `red` holds two rows' partial sums in turn (a warp that writes a row's
-// has passed the barrier of the row before, behind the reads of the one before that).
-__device__ __forceinline__ float row_sum(float v, float* red, int W, int wrow, int group, int G,
-                                         int parity) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (W == 1) return v;
-  const int lane = threadIdx.x & 31;
-  float* mine = red + (parity * G + group) * 32;
-  if (lane == 0) mine[wrow] = v;
-  if (G == 1) __syncthreads();
-  else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(W * 32) : "memory");
-  float s = lane < W ? mine[lane] : 0.0f;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
-}
 
 // h = bf16(x + residual) of one vector, and its squares added to sq.
 __device__ __forceinline__ uint4 add_vec(uint4 x, uint4 r, bool has_res, float& sq) {

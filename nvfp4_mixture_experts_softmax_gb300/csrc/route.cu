@@ -174,6 +174,12 @@ __global__ void __launch_bounds__(1024) plan_scatter_kernel(
 
 }  // namespace
 
+cudaError_t launch_plan_scan(const int32_t* hist, int nchunks, int E, int32_t* base, int32_t* counts,
+                             int32_t* offsets, int32_t* scratch, cudaStream_t s) {
+  return launch_pdl(plan_scan_kernel, dim3((E + 31) / 32), dim3(1024), 0, s, hist, nchunks, E, 0, base,
+                    counts, offsets, (int32_t*)nullptr, scratch);
+}
+
 cudaError_t launch_plan(const PlanArgs& a, cudaStream_t s) {
   const int tpc = plan_tokens_per_chunk(a.k);
   const int nchunks = (a.T + tpc - 1) / tpc;
