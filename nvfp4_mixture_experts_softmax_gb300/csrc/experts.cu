@@ -52,8 +52,8 @@ constexpr int kSmallBox = 32;                   // rows of the small box
 constexpr uint64_t kLimitNs = 2000000000ull;
 
 // The tensor cores truncate where they add, so the FP32 gradients are cut into chains of this many
-// rows (64 additions), added in FP32 by the epilogue in order.
-constexpr int kChainRows = 1024;
+// rows (32 additions), which the epilogue adds up in registers, rounding.
+constexpr int kChainRows = 512;
 
 constexpr int kBarOff = kStages * kStageBytes;
 constexpr int kTableOff = kBarOff + 256;
@@ -102,34 +102,22 @@ __device__ __forceinline__ uint32_t leader_addr(uint32_t bar) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(bar));
   return r;
 }
+// Arrivals on a barrier of either CTA.  Release at CTA scope: what they order are TMA copies, MMAs and reads of
+// tensor memory, which complete on their own terms; at cluster scope each arrival would wait for the thread's
+// memory accesses (0.8 us a stage of the copies: a third of the rate).
 __device__ __forceinline__ void arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 __device__ __forceinline__ void arrive_expect_cluster(uint32_t addr, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(addr), "r"(bytes)
-               : "memory");
+  asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(addr), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n"
-      ".reg .pred p;\n"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
-      "selp.u32 %0, 1, 0, p;\n"
-      "}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(kTryWaitSuspendNs)
-      : "memory");
-  return ok != 0;
-}
-// As mbar_wait_bounded, for barriers that both CTAs of the pair arrive on; gives up as soon as another
-// role of the CTA has.
+// As mbar_wait_bounded; gives up as soon as another role of the CTA has.
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, int32_t* status,
                                              volatile uint32_t* abort) {
-  if (try_wait_cluster(bar, parity)) return true;
+  if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
   for (;;) {
-    if (try_wait_cluster(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     if (*abort) return false;
     if (global_timer_ns() - t0 > kLimitNs) {
       set_status(status, MOE_ERR_DEVICE_TIMEOUT);
@@ -155,21 +143,47 @@ __device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, in
       : "memory");
 }
 
-__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// The MMAs of a block of K = 64 (kStepA, kStepB: 16 of K in units of 16 bytes), and the arrival on `done` in both
+// CTAs once they and all before them are complete; by one elected lane of a converged warp, which keeps the
+// operands in uniform registers (by a lane of a diverged one each MMA costs 105 cycles to issue, nearly
+// the 128 that it runs).
+template <uint32_t kStepA, uint32_t kStepB>
+__device__ __forceinline__ void mma_block(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
+                                          uint32_t done) {
   asm volatile(
       "{\n"
-      ".reg .pred p;\n"
+      ".reg .pred p, q, t;\n"
+      ".reg .b64 a1, a2, a3, b1, b2, b3;\n"
+      ".reg .b16 both;\n"
+      "elect.sync _|q, 0xffffffff;\n"
       "setp.ne.u32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n"
+      "setp.eq.u32 t, %3, %3;\n"
+      "mov.b16 both, 3;\n"
+      "add.u64 a1, %1, %6;\n"
+      "add.u64 a2, a1, %6;\n"
+      "add.u64 a3, a2, %6;\n"
+      "add.u64 b1, %2, %7;\n"
+      "add.u64 b2, b1, %7;\n"
+      "add.u64 b3, b2, %7;\n"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], a1, b1, %3, t;\n"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], a2, b2, %3, t;\n"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], a3, b3, %3, t;\n"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%5], both;\n"
       "}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(done), "n"(kStepA), "n"(kStepB)
       : "memory");
 }
-// Arrives on the barrier at this address in both CTAs once the MMAs issued before are done.
+// The arrival alone, once all MMAs before are complete.
 __device__ __forceinline__ void commit_pair(uint32_t bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-      "h"((uint16_t)3)
+      "{\n"
+      ".reg .pred q;\n"
+      ".reg .b16 both;\n"
+      "mov.b16 both, 3;\n"
+      "elect.sync _|q, 0xffffffff;\n"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], both;\n"
+      "}" ::"r"(bar)
       : "memory");
 }
 
@@ -287,6 +301,14 @@ __device__ __forceinline__ Tile tile_at(const Args& p, const int32_t* s_off, con
   return t;
 }
 
+// Rows of the segment that an item's reduction runs over (kWgrad), all that the MMA and zeroing warps need to know.
+template <Mode kMode>
+__device__ __forceinline__ int reduction_rows(const Args& p, const int32_t* s_off, int item) {
+  if (kMode != kWgrad) return 0;
+  const int seg = item / (p.nmat * ((p.M + kTileM - 1) / kTileM) * ((p.N + kTileN - 1) / kTileN));
+  return s_off[seg + 1] - s_off[seg];
+}
+
 template <Mode kMode>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     experts_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args p) {
@@ -368,9 +390,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;   // pairs
 
   // chains of a tile, and blocks of K of one of them
-  auto chains_of = [&](const Tile& t) { return kMode == kWgrad ? (t.rows + kChainRows - 1) / kChainRows : 1; };
-  auto blocks_of = [&](const Tile& t, int chain) {
-    return kMode == kWgrad ? (min(kChainRows, t.rows - chain * kChainRows) + kBlockK - 1) / kBlockK : p.nkb;
+  auto chains_of = [&](int rows) { return kMode == kWgrad ? (rows + kChainRows - 1) / kChainRows : 1; };
+  auto blocks_of = [&](int rows, int chain) {
+    return kMode == kWgrad ? (min(kChainRows, rows - chain * kChainRows) + kBlockK - 1) / kBlockK : p.nkb;
   };
 
   if (warp == kCopyWarp) {
@@ -380,9 +402,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int item = first; item < total && ok; item += step) {
         const Tile t = tile_at<kMode>(p, s_off, s_tile, item);
-        const int nch = chains_of(t);
+        const int nch = chains_of(t.rows);
         for (int ch = 0; ch < nch && ok; ++ch) {
-          const int nkb = blocks_of(t, ch);
+          const int nkb = blocks_of(t.rows, ch);
           for (int kb = 0; kb < nkb; ++kb) {
             if (!wait_bounded(smem_u32(empty + st), ph ^ 1u, p.status, s_abort)) {
               ok = false;
@@ -439,16 +461,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ---------------- products (CTA 0) ----------------
     if (rank == 0) {
       constexpr uint32_t idesc = instr_desc(kMode);
-      constexpr uint32_t step_a = a_mn_major(kMode) ? 128u : 2u, step_b = b_mn_major(kMode) ? 128u : 2u;   // K = 16, in 16 bytes
       const uint64_t da0 = smem_desc(smem0, a_mn_major(kMode) ? kChunkBytes : 16, 1024, kLayoutSwizzle128B);
       const uint64_t db0 = smem_desc(smem0 + kOperandBytes, b_mn_major(kMode) ? kChunkBytes : 16, 1024, kLayoutSwizzle128B);
       uint32_t st = 0, ph = 0, unit = 0;
       bool ok = true;
       for (int item = first; item < total && ok; item += step) {
-        const Tile t = tile_at<kMode>(p, s_off, s_tile, item);
-        const int nch = chains_of(t);
+        const int rows = reduction_rows<kMode>(p, s_off, item);
+        const int nch = chains_of(rows);
         for (int ch = 0; ch < nch && ok; ++ch, ++unit) {
-          const int nkb = blocks_of(t, ch);
+          const int nkb = blocks_of(rows, ch);
           const uint32_t buf = unit & 1u;
           ok = __all_sync(0xffffffffu, wait_bounded(smem_u32(acc_empty + buf), ((unit >> 1) & 1u) ^ 1u, p.status, s_abort));
           if (!ok) break;
@@ -457,17 +478,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ok = __all_sync(0xffffffffu, wait_bounded(smem_u32(full + st), ph, p.status, s_abort));
             if (!ok) break;
             tc_fence_after();
-            if (lane == 0) {
-              const uint64_t so = (uint64_t)(st * (kStageBytes >> 4));
-#pragma unroll
-              for (int kk = 0; kk < kBlockK / 16; ++kk)
-                mma_pair(tmem + buf * kTileN, da0 + so + kk * step_a, db0 + so + kk * step_b, idesc, (kb | kk) != 0 ? 1u : 0u);
-              commit_pair(smem_u32(empty + st));
-              if (kb == nkb - 1) commit_pair(smem_u32(acc_full + buf));
-            }
-            __syncwarp();
+            const uint64_t so = (uint64_t)(st * (kStageBytes >> 4));
+            mma_block<a_mn_major(kMode) ? 128u : 2u, b_mn_major(kMode) ? 128u : 2u>(tmem + buf * kTileN, da0 + so, db0 + so, idesc,
+                                                                                    kb != 0 ? 1u : 0u, smem_u32(empty + st));
             if (++st == kStages) { st = 0; ph ^= 1u; }
           }
+          if (ok) commit_pair(smem_u32(acc_full + buf));
         }
       }
     }
@@ -477,11 +493,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t at = 0, phases = 0;   // blocks passed; phase of each tail barrier
       bool ok = true;
       for (int item = first; item < total && ok; item += step) {
-        const Tile t = tile_at<kMode>(p, s_off, s_tile, item);
-        if (t.rows == 0) continue;
-        const int full_chains = t.rows / kChainRows, rest = t.rows - full_chains * kChainRows;
-        at += full_chains * (kChainRows / kBlockK) + (rest + kBlockK - 1) / kBlockK;
-        const int have = t.rows % kBlockK;
+        const int rows = reduction_rows<kMode>(p, s_off, item);
+        at += rows / kChainRows * (kChainRows / kBlockK) + (rows % kChainRows + kBlockK - 1) / kBlockK;
+        const int have = rows % kBlockK;
         if (have == 0) continue;
         const uint32_t st = (at - 1) % kStages;
         ok = __all_sync(0xffffffffu, wait_bounded(smem_u32(tail + st), (phases >> st) & 1u, p.status, s_abort));
@@ -492,6 +506,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int c = 0; c < kStageBytes / kChunkBytes; ++c)
           for (int i = lane; i < n16; i += 32)
             *reinterpret_cast<uint4*>(base + c * kChunkBytes + have * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+        // the zeros are read by this CTA's own tensor core; nothing of them goes to the other CTA but the arrival
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) arrive_cluster(leader_addr(smem_u32(full + st)));
@@ -505,46 +520,61 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int item = first; item < total && ok; item += step) {
       const Tile t = tile_at<kMode>(p, s_off, s_tile, item);
-      const int nch = kMode == kWgrad ? max(chains_of(t), 1) : 1;
-      for (int ch = 0; ch < nch && ok; ++ch) {
-        const bool none = kMode == kWgrad && t.rows == 0;   // a segment without rows: zeros, no products
-        const uint32_t buf = unit & 1u;
-        if (!none) {
+      if constexpr (kMode == kWgrad) {
+        // the chains' sums meet in registers: 128 columns a thread
+        float sum[kHalf];
+        const int nch = chains_of(t.rows);
+        for (int ch = 0; ch < nch && ok; ++ch, ++unit) {
+          const uint32_t buf = unit & 1u;
           ok = __all_sync(0xffffffffu, wait_bounded(smem_u32(acc_full + buf), (unit >> 1) & 1u, p.status, s_abort));
           if (!ok) break;
-          ++unit;
           tc_fence_after();
-        }
-        const uint32_t acc = tmem + buf * kTileN + ((uint32_t)(quad * 32) << 16);
-        if constexpr (kMode == kWgrad) {
-          const int Mm = t.mat == 2 ? p.M : p.N, Nn = t.mat == 2 ? p.N : p.M;
-          const bool add = ch > 0 || p.accumulate;
-          float* out = (t.mat == 0 ? p.dw0 : t.mat == 1 ? p.dw1 : p.dw2) +
-                       ((size_t)t.seg * Mm + min(t.m0 + local, Mm - 1)) * Nn + t.n0 + half * kHalf;
-          const bool live = t.m0 + local < Mm && !(none && p.accumulate);
-#pragma unroll 1
+          const uint32_t acc = tmem + buf * kTileN + half * kHalf + ((uint32_t)(quad * 32) << 16);
+#pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const bool in = live && t.n0 + half * kHalf + c * 32 < Nn;
-            uint32_t v[32], old[32];
-            if (in && add && !none)
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(acc + c * 32, v);
+            tmem_ld_wait();
+            if (ch == 0) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) load_32b(out + c * 32 + 8 * i, old + 8 * i);
-            if (!none) {
-              tmem_ld_32x32b_x32(acc + half * kHalf + c * 32, v);
-              tmem_ld_wait();
+              for (int i = 0; i < 32; ++i) sum[c * 32 + i] = __uint_as_float(v[i]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) sum[c * 32 + i] += __uint_as_float(v[i]);
             }
-            if (!in) continue;
-            if (none) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = 0u;
-            } else if (add) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(old[i]) + __uint_as_float(v[i]));
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) store_32b(out + c * 32 + 8 * i, v + 8 * i);
           }
-        } else if ((int)rank * kHalf + quad * 32 < t.rows) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_cluster(leader_addr(smem_u32(acc_empty + buf)));
+        }
+        if (!ok) break;
+        const int Mm = t.mat == 2 ? p.M : p.N, Nn = t.mat == 2 ? p.N : p.M;
+        if (t.m0 + local >= Mm || (nch == 0 && p.accumulate)) continue;
+        float* out = (t.mat == 0 ? p.dw0 : t.mat == 1 ? p.dw1 : p.dw2) + ((size_t)t.seg * Mm + t.m0 + local) * Nn + t.n0 + half * kHalf;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (t.n0 + half * kHalf + c * 32 >= Nn) break;
+          uint32_t v[32];
+          if (p.accumulate) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) load_32b(out + c * 32 + 8 * i, v + 8 * i);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + sum[c * 32 + i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = nch == 0 ? 0u : __float_as_uint(sum[c * 32 + i]);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) store_32b(out + c * 32 + 8 * i, v + 8 * i);
+        }
+      } else {
+        const uint32_t buf = unit & 1u;
+        ok = __all_sync(0xffffffffu, wait_bounded(smem_u32(acc_full + buf), (unit >> 1) & 1u, p.status, s_abort));
+        if (!ok) break;
+        ++unit;
+        tc_fence_after();
+        const uint32_t acc = tmem + buf * kTileN + ((uint32_t)(quad * 32) << 16);
+        if ((int)rank * kHalf + quad * 32 < t.rows) {
           const bool live = local < t.rows;
           const size_t row = (size_t)(t.m0 + local) * p.N;
           if constexpr (kMode == kUp) {
@@ -613,11 +643,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (!none) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) arrive_cluster(leader_addr(smem_u32(acc_empty + buf)));
-        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(leader_addr(smem_u32(acc_empty + buf)));
       }
     }
   }
