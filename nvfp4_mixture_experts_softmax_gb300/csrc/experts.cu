@@ -42,8 +42,9 @@ constexpr int kHalf = 128;                      // rows of A and of B a CTA hold
 constexpr int kBlockK = 64;
 constexpr int kOperandBytes = kHalf * kBlockK * 2;
 constexpr int kChunkBytes = kBlockK * 128;      // MN-major: 64 columns (128 bytes) of 64 rows
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kStageBytes = 2 * kOperandBytes;
+constexpr int kSlabBytes = 32 * 128;            // of an epilogue warp: its 32 rows by 128 bytes on their way out
 constexpr int kEpiWarps = 8, kCopyWarp = 8, kMmaWarp = 9, kZeroWarp = 10;
 constexpr int kThreads = 11 * 32;
 constexpr int kMaxExperts = 1024;
@@ -55,7 +56,8 @@ constexpr uint64_t kLimitNs = 2000000000ull;
 // rows (32 additions), which the epilogue adds up in registers, rounding.
 constexpr int kChainRows = 512;
 
-constexpr int kBarOff = kStages * kStageBytes;
+constexpr int kSlabOff = kStages * kStageBytes;
+constexpr int kBarOff = kSlabOff + kEpiWarps * kSlabBytes;
 constexpr int kTableOff = kBarOff + 256;
 constexpr size_t kSmemBytes = 1024 + kTableOff + 2 * (kMaxExperts + 1) * sizeof(int32_t) + 8;
 static_assert(kSmemBytes <= 232448, "shared memory");
@@ -70,7 +72,8 @@ constexpr uint32_t instr_desc(Mode m) {
 }
 
 struct Maps {
-  CUtensorMap m[6];
+  CUtensorMap m[6];     // operands
+  CUtensorMap out[3];   // what the epilogue writes, in slabs
 };
 
 struct Args {
@@ -86,8 +89,7 @@ struct Args {
   int act;
   float limit, alpha;
   const __nv_bfloat16 *g, *u;            // kDgradAct: the forward pass's
-  __nv_bfloat16 *o0, *o1, *o2;           // kUp: g, u (may be null), h; kDgradAct: dg, du; else out
-  float *dw0, *dw1, *dw2;                // kWgrad: gate, up, down
+  __nv_bfloat16* o[3];                   // kUp: g, u (may be null), h; kDgradAct: dg, du; else out; as maps.out
   int accumulate;
   int first;      // this launch clears the status
 };
@@ -206,13 +208,58 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 __device__ __forceinline__ float low_bf16(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high_bf16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// 32 columns as BF16.
-__device__ __forceinline__ void store_bf16x32(__nv_bfloat16* p, const float (&f)[32]) {
-  uint32_t w[16];
+// Slabs: a lane writes 128 bytes of its row (16-byte pieces in the 128-byte swizzle, so that the lanes' pieces lie in
+// different banks), then one lane stores the whole by TMA: whole lines to L2, where 32 bytes a lane and
+// row went at 11 bytes a cycle and SM.
+__device__ __forceinline__ void slab_put(uint32_t slab, int lane, int piece, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(slab + lane * 128 + ((piece ^ (lane & 7)) << 4)), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
+}
+// The slab may be written again once the copies before have read it.
+__device__ __forceinline__ void slab_begin(int lane) {
+  if (lane == 0) bulk_wait_group_read<0>();
+  __syncwarp();
+}
+__device__ __forceinline__ void slab_store_2d(uint32_t slab, int lane, const CUtensorMap* map, int x, int y) {
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x), "r"(y), "r"(slab)
+                 : "memory");
+    bulk_commit_group();
+  }
+}
+__device__ __forceinline__ void slab_store_3d(uint32_t slab, int lane, const CUtensorMap* map, int x, int y, int z, bool add) {
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    if (add)
+      asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x),
+                   "r"(y), "r"(z), "r"(slab)
+                   : "memory");
+    else
+      asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x), "r"(y),
+                   "r"(z), "r"(slab)
+                   : "memory");
+    bulk_commit_group();
+  }
+}
+
+// 64 columns of 32 rows as BF16, `w` two columns a word: by a slab if all 32 rows belong to the segment, else row by
+// row (32 bytes a store).  `cols`: how many of the 64 there are (32 or more).
+__device__ __forceinline__ void store_bf16x64(const uint32_t (&w)[32], uint32_t slab, int lane, const CUtensorMap* map, int x, int y,
+                                              bool whole, __nv_bfloat16* row, bool live, int cols) {
+  if (whole) {
+    slab_begin(lane);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) w[i] = pack2(f[2 * i], f[2 * i + 1]);
-  store_32b(p, w);
-  store_32b(p + 16, w + 8);
+    for (int i = 0; i < 8; ++i) slab_put(slab, lane, i, w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    slab_store_2d(slab, lane, map, x, y);
+  } else if (live) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (16 * i < cols) store_32b(row + 16 * i, w + 8 * i);
+  }
 }
 
 // The activation and its derivatives by g and u, the clamps passing NaN on.  The fast exponential and
@@ -515,7 +562,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else {
     // ---------------- epilogue: a row a thread, half of the columns a warp ----------------
     const int quad = warp & 3, half = warp >> 2;
-    const int local = (int)rank * kHalf + quad * 32 + lane;   // row of the tile
+    const int slab_row = (int)rank * kHalf + quad * 32;       // first of the warp's rows of the tile
+    const uint32_t slab = smem0 + kSlabOff + warp * kSlabBytes;
     uint32_t unit = 0;
     bool ok = true;
     for (int item = first; item < total && ok; item += step) {
@@ -531,17 +579,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const uint32_t acc = tmem + buf * kTileN + half * kHalf + ((uint32_t)(quad * 32) << 16);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[32];
-            tmem_ld_32x32b_x32(acc + c * 32, v);
+          for (int c = 0; c < kHalf / 16; ++c) {
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(acc + c * 16, v);
             tmem_ld_wait();
-            if (ch == 0) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) sum[c * 32 + i] = __uint_as_float(v[i]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) sum[c * 32 + i] += __uint_as_float(v[i]);
-            }
+            for (int i = 0; i < 16; ++i) sum[c * 16 + i] = ch == 0 ? __uint_as_float(v[i]) : sum[c * 16 + i] + __uint_as_float(v[i]);
           }
           tc_fence_before();
           __syncwarp();
@@ -549,23 +592,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
         const int Mm = t.mat == 2 ? p.M : p.N, Nn = t.mat == 2 ? p.N : p.M;
-        if (t.m0 + local >= Mm || (nch == 0 && p.accumulate)) continue;
-        float* out = (t.mat == 0 ? p.dw0 : t.mat == 1 ? p.dw1 : p.dw2) + ((size_t)t.seg * Mm + t.m0 + local) * Nn + t.n0 + half * kHalf;
+        if (t.m0 + slab_row >= Mm || (nch == 0 && p.accumulate)) continue;   // (32 rows: all of them or none)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          if (t.n0 + half * kHalf + c * 32 >= Nn) break;
-          uint32_t v[32];
-          if (p.accumulate) {
+          const int col = t.n0 + half * kHalf + c * 32;
+          if (col >= Nn) break;
+          slab_begin(lane);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) load_32b(out + c * 32 + 8 * i, v + 8 * i);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + sum[c * 32 + i]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = nch == 0 ? 0u : __float_as_uint(sum[c * 32 + i]);
+          for (int i = 0; i < 8; ++i) {
+            const float* f = sum + c * 32 + 4 * i;
+            if (nch == 0) slab_put(slab, lane, i, 0u, 0u, 0u, 0u);   // a segment without rows
+            else slab_put(slab, lane, i, __float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
           }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) store_32b(out + c * 32 + 8 * i, v + 8 * i);
+          slab_store_3d(slab, lane, maps.out + t.mat, col, t.m0 + slab_row, t.seg, p.accumulate);
         }
       } else {
         const uint32_t buf = unit & 1u;
@@ -574,73 +613,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ++unit;
         tc_fence_after();
         const uint32_t acc = tmem + buf * kTileN + ((uint32_t)(quad * 32) << 16);
-        if ((int)rank * kHalf + quad * 32 < t.rows) {
-          const bool live = local < t.rows;
-          const size_t row = (size_t)(t.m0 + local) * p.N;
-          if constexpr (kMode == kUp) {
+        if (slab_row < t.rows) {
+          const bool live = slab_row + lane < t.rows, whole = slab_row + 32 <= t.rows;
+          const int y = t.m0 + slab_row;
+          const size_t row = (size_t)(y + lane) * p.N;
 #pragma unroll 1
-            for (int c = 0; c < 2; ++c) {
-              const int col = half * 64 + c * 32;
-              if (t.n0 + col >= p.N) break;
-              uint32_t vg[32], vu[32];
-              tmem_ld_32x32b_x32(acc + col, vg);
-              tmem_ld_32x32b_x32(acc + kHalf + col, vu);
-              tmem_ld_wait();
-              if (!live) continue;
-              const size_t at = row + t.n0 + col;
-              float g[32], u[32], h[32];
+          for (int c = 0; c < (kMode == kUp ? 1 : 2); ++c) {
+            const int col = kMode == kUp ? half * 64 : half * kHalf + c * 64, x = t.n0 + col;
+            if (x >= p.N) break;
+            const int cols = min(64, p.N - x);
+            uint32_t w0[32], w1[32], w2[32];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                g[i] = __uint_as_float(vg[i]);
-                u[i] = __uint_as_float(vu[i]);
-                h[i] = activation(g[i], u[i], p.act, p.limit, p.alpha);
-              }
-              if (p.o0) store_bf16x32(p.o0 + at, g);
-              if (p.o1) store_bf16x32(p.o1 + at, u);
-              store_bf16x32(p.o2 + at, h);
-            }
-          } else {
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              const int col = half * kHalf + c * 32;
-              if (t.n0 + col >= p.N) break;
-              const size_t at = row + t.n0 + col;
-              uint32_t v[32], gu[32];
+            for (int q = 0; q < 4; ++q) {      // 16 columns at a time
+              uint32_t v[16], vu[16], gu[16];
               if constexpr (kMode == kDgradAct) {
-                if (live) {
-                  if (p.g) {
-                    load_32b(p.g + at, gu);
-                    load_32b(p.g + at + 16, gu + 8);
-                  }
-                  load_32b(p.u + at, gu + 16);
-                  load_32b(p.u + at + 16, gu + 24);
+                if (live && 16 * q < cols) {
+                  if (p.g) load_32b(p.g + row + x + 16 * q, gu);
+                  load_32b(p.u + row + x + 16 * q, gu + 8);
                 }
               }
-              tmem_ld_32x32b_x32(acc + col, v);
+              tmem_ld_32x32b_x16(acc + col + 16 * q, v);
+              if constexpr (kMode == kUp) tmem_ld_32x32b_x16(acc + kHalf + col + 16 * q, vu);
               tmem_ld_wait();
-              if (!live) continue;
-              float f[32];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
-              if constexpr (kMode == kUpSingle) {
-                if (p.o1) store_bf16x32(p.o1 + at, f);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) f[i] = activation(0.0f, f[i], kActRelu2, 0.0f, 0.0f);
-                store_bf16x32(p.o2 + at, f);
-              } else if constexpr (kMode == kDgradAct) {
-                float dg[32], du[32];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  activation_grad(low_bf16(gu[i]), low_bf16(gu[16 + i]), f[2 * i], p.act, p.limit, p.alpha, dg[2 * i], du[2 * i]);
-                  activation_grad(high_bf16(gu[i]), high_bf16(gu[16 + i]), f[2 * i + 1], p.act, p.limit, p.alpha, dg[2 * i + 1],
-                                  du[2 * i + 1]);
+              for (int i = 0; i < 8; ++i) {
+                const float a = __uint_as_float(v[2 * i]), b = __uint_as_float(v[2 * i + 1]);
+                const int o = 8 * q + i;
+                if constexpr (kMode == kUp) {
+                  const float ua = __uint_as_float(vu[2 * i]), ub = __uint_as_float(vu[2 * i + 1]);
+                  w0[o] = pack2(a, b);
+                  w1[o] = pack2(ua, ub);
+                  w2[o] = pack2(activation(a, ua, p.act, p.limit, p.alpha), activation(b, ub, p.act, p.limit, p.alpha));
+                } else if constexpr (kMode == kUpSingle) {
+                  w1[o] = pack2(a, b);
+                  w2[o] = pack2(activation(0.0f, a, kActRelu2, 0.0f, 0.0f), activation(0.0f, b, kActRelu2, 0.0f, 0.0f));
+                } else if constexpr (kMode == kDgradAct) {
+                  float ga, gb, ua, ub;
+                  activation_grad(low_bf16(gu[i]), low_bf16(gu[8 + i]), a, p.act, p.limit, p.alpha, ga, ua);
+                  activation_grad(high_bf16(gu[i]), high_bf16(gu[8 + i]), b, p.act, p.limit, p.alpha, gb, ub);
+                  w0[o] = pack2(ga, gb);
+                  w1[o] = pack2(ua, ub);
+                } else {
+                  w0[o] = pack2(a, b);
                 }
-                if (p.o0) store_bf16x32(p.o0 + at, dg);
-                store_bf16x32(p.o1 + at, du);
-              } else {
-                store_bf16x32(p.o0 + at, f);
               }
             }
+            if (kMode != kUpSingle && p.o[0]) store_bf16x64(w0, slab, lane, maps.out, x, y, whole, p.o[0] + row + x, live, cols);
+            if (kMode <= kUpSingle || kMode == kDgradAct)
+              if (p.o[1]) store_bf16x64(w1, slab, lane, maps.out + 1, x, y, whole, p.o[1] + row + x, live, cols);
+            if (kMode <= kUpSingle) store_bf16x64(w2, slab, lane, maps.out + 2, x, y, whole, p.o[2] + row + x, live, cols);
           }
         }
         tc_fence_before();
@@ -648,6 +669,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0) arrive_cluster(leader_addr(smem_u32(acc_empty + buf)));
       }
     }
+    if (lane == 0) bulk_wait_group<0>();   // the slabs' copies, before the CTA may end
   }
 
   // After a wait ran out, copies into shared memory and MMAs may still be under way: they end within
@@ -679,11 +701,14 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 }
 
 // BF16 [d2][d1][d0] (d2 = 0: two dimensions), boxes of 64 columns by `rows`.
+// kF32: the same of FP32, 32 columns.
+template <bool kF32 = false>
 bool make_map(CUtensorMap* m, const void* ptr, int64_t d0, int64_t d1, int64_t d2, int rows) {
+  constexpr int kSize = kF32 ? 4 : 2;
   const cuuint64_t dims[3] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2};
-  const cuuint64_t strides[2] = {(cuuint64_t)d0 * 2, (cuuint64_t)d0 * d1 * 2};
-  const cuuint32_t box[3] = {64, (cuuint32_t)rows, 1}, estr[3] = {1, 1, 1};
-  return encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d2 ? 3 : 2, const_cast<void*>(ptr), dims, strides, box, estr,
+  const cuuint64_t strides[2] = {(cuuint64_t)d0 * kSize, (cuuint64_t)d0 * d1 * kSize};
+  const cuuint32_t box[3] = {128 / kSize, (cuuint32_t)rows, 1}, estr[3] = {1, 1, 1};
+  return encoder()(m, kF32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d2 ? 3 : 2, const_cast<void*>(ptr), dims, strides, box, estr,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -745,6 +770,16 @@ Args base_args(const Shape& sh, const int32_t* offsets, void* ws, float limit, f
 
 int64_t row_items(const Shape& sh, int n_tiles) { return (sh.R / kTileM + std::min<int64_t>(sh.E, sh.R)) * n_tiles; }
 
+// The row modes' outputs [R, cols], null: not written.
+bool row_outputs(Maps& m, Args& a, int64_t R, int64_t cols, void* o0, void* o1, void* o2) {
+  void* const o[3] = {o0, o1, o2};
+  for (int i = 0; i < 3; ++i) {
+    a.o[i] = static_cast<__nv_bfloat16*>(o[i]);
+    if (o[i] && !make_map(&m.out[i], o[i], cols, R, 0, 32)) return false;
+  }
+  return true;
+}
+
 constexpr size_t kHeader = 256;   // the status
 
 }  // namespace
@@ -785,9 +820,7 @@ int moe_experts_forward(const void* rows, const int32_t* offsets, int64_t R, int
   a.N = (int)I;
   a.nkb = div_up(H, kBlockK);
   a.n_tiles = div_up(I, sh.gated ? kHalf : kTileN);
-  a.o0 = static_cast<__nv_bfloat16*>(g);
-  a.o1 = static_cast<__nv_bfloat16*>(u);
-  a.o2 = static_cast<__nv_bfloat16*>(hb);
+  if (!row_outputs(m, a, R, I, g, u, hb)) return MOE_ERR_CUDA;
   a.first = 1;
   cudaError_t e = sh.gated ? launch<kUp>(m, a, row_items(sh, a.n_tiles), s) : launch<kUpSingle>(m, a, row_items(sh, a.n_tiles), s);
   if (e != cudaSuccess) return MOE_ERR_CUDA;
@@ -797,8 +830,7 @@ int moe_experts_forward(const void* rows, const int32_t* offsets, int64_t R, int
   a.N = (int)H;
   a.nkb = div_up(I, kBlockK);
   a.n_tiles = div_up(H, kTileN);
-  a.o0 = static_cast<__nv_bfloat16*>(out);
-  a.o1 = a.o2 = nullptr;
+  if (!row_outputs(m, a, R, H, out, nullptr, nullptr)) return MOE_ERR_CUDA;
   a.first = 0;
   return launch<kDown>(m, a, row_items(sh, a.n_tiles), s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
@@ -829,8 +861,7 @@ int moe_experts_backward(const void* dout, const int32_t* offsets, int64_t R, in
   a.n_tiles = div_up(I, kTileN);
   a.g = static_cast<const __nv_bfloat16*>(g);
   a.u = static_cast<const __nv_bfloat16*>(u);
-  a.o0 = static_cast<__nv_bfloat16*>(dg);
-  a.o1 = static_cast<__nv_bfloat16*>(du);
+  if (!row_outputs(m, a, R, I, dg, du, nullptr)) return MOE_ERR_CUDA;
   a.first = 1;
   if (launch<kDgradAct>(m, a, row_items(sh, a.n_tiles), s) != cudaSuccess) return MOE_ERR_CUDA;
   const void* first = sh.gated ? dg : du;
@@ -842,8 +873,7 @@ int moe_experts_backward(const void* dout, const int32_t* offsets, int64_t R, in
   a.half_kb = div_up(I, kBlockK);
   a.nkb = a.half_kb * (sh.gated ? 2 : 1);
   a.n_tiles = div_up(H, kTileN);
-  a.o0 = static_cast<__nv_bfloat16*>(drows);
-  a.o1 = nullptr;
+  if (!row_outputs(m, a, R, H, drows, nullptr, nullptr)) return MOE_ERR_CUDA;
   a.first = 0;
   return launch<kDgradRows>(m, a, row_items(sh, a.n_tiles), s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
@@ -874,15 +904,13 @@ int moe_experts_weight_grad(const void* rows, const void* dout, const void* h, c
   Maps m = {};
   const bool ok = make_map(&m.m[0], sh.gated ? dg : du, I, R, 0, kBlockK) && make_map(&m.m[1], rows, H, R, 0, kBlockK) &&
                   make_map(&m.m[2], du, I, R, 0, kBlockK) && make_map(&m.m[3], dout, H, R, 0, kBlockK) &&
-                  make_map(&m.m[4], h, I, R, 0, kBlockK);
+                  make_map(&m.m[4], h, I, R, 0, kBlockK) && make_map<true>(&m.out[0], sh.gated ? dw_gate : dw_up, H, I, E, 32) &&
+                  make_map<true>(&m.out[1], dw_up, H, I, E, 32) && make_map<true>(&m.out[2], dw_down, I, H, E, 32);
   if (!ok) return MOE_ERR_CUDA;
   Args a = base_args(sh, offsets, workspace, 0.0f, 0.0f);
   a.M = (int)H;
   a.N = (int)I;
   a.nmat = sh.gated ? 3 : 2;
-  a.dw0 = dw_gate;
-  a.dw1 = dw_up;
-  a.dw2 = dw_down;
   a.accumulate = accumulate;
   a.first = 1;
   const int64_t items = (int64_t)E * a.nmat * div_up(H, kTileM) * div_up(I, kTileN);
