@@ -110,9 +110,6 @@ __device__ __forceinline__ uint32_t leader_addr(uint32_t bar) {
 __device__ __forceinline__ void arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
-__device__ __forceinline__ void arrive_expect_cluster(uint32_t addr, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(addr), "r"(bytes) : "memory");
-}
 // As mbar_wait_bounded; gives up as soon as another role of the CTA has.
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, int32_t* status,
                                              volatile uint32_t* abort) {
@@ -129,19 +126,39 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, int3
   }
 }
 
-// TMA loads into this CTA's shared memory that complete on a barrier of either CTA of the pair.
+// TMA loads into this CTA's shared memory that complete on a barrier of either CTA of the pair, and the arrival that
+// announces their bytes; by one elected lane of a converged warp (uniform registers, as for the MMAs: by
+// a lane of a diverged one they took 180 cycles each, and four of them a stage set the weight gradients' pace).
 __device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
-      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "{\n"
+      ".reg .pred q;\n"
+      "elect.sync _|q, 0xffffffff;\n"
+      "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%2, %3}], [%4];\n"
+      "}" ::"r"(dst),
       "l"(map), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
 __device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "{\n"
+      ".reg .pred q;\n"
+      "elect.sync _|q, 0xffffffff;\n"
+      "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%2, %3, %4}], [%5];\n"
+      "}" ::"r"(dst),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void expect_bytes(uint32_t addr, uint32_t bytes) {
+  asm volatile(
+      "{\n"
+      ".reg .pred q;\n"
+      "elect.sync _|q, 0xffffffff;\n"
+      "@q mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;\n"
+      "}" ::"r"(addr),
+      "r"(bytes)
       : "memory");
 }
 
@@ -444,65 +461,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp == kCopyWarp) {
     // ---------------- copies ----------------
-    if (lane == 0) {
-      uint32_t st = 0, ph = 0, used = 0;
-      bool ok = true;
-      for (int item = first; item < total && ok; item += step) {
-        const Tile t = tile_at<kMode>(p, s_off, s_tile, item);
-        const int nch = chains_of(t.rows);
-        for (int ch = 0; ch < nch && ok; ++ch) {
-          const int nkb = blocks_of(t.rows, ch);
-          for (int kb = 0; kb < nkb; ++kb) {
-            if (!wait_bounded(smem_u32(empty + st), ph ^ 1u, p.status, s_abort)) {
-              ok = false;
-              break;
+    uint32_t st = 0, ph = 0, used = 0;
+    bool ok = true;
+    for (int item = first; item < total && ok; item += step) {
+      const Tile t = tile_at<kMode>(p, s_off, s_tile, item);
+      // what of the tile this CTA brings: rows (columns) m of A, n of B, `na`, `nb` chunks of 64 of them
+      const int Mm = kMode != kWgrad ? 0 : t.mat == 2 ? p.M : p.N, Nn = kMode != kWgrad ? p.N : t.mat == 2 ? p.N : p.M;
+      const int m = t.m0 + (int)rank * kHalf, n = kMode == kUp ? t.n0 : t.n0 + (int)rank * kHalf;
+      const int na = m >= Mm ? 0 : m + 64 >= Mm ? 1 : 2, nb = n >= Nn ? 0 : n + 64 >= Nn ? 1 : 2;
+      const int mine = t.rows - (int)rank * kHalf;
+      const uint32_t abytes = kMode == kWgrad ? (uint32_t)na * kChunkBytes
+                              : mine <= 0 ? 0u : mine <= kSmallBox ? kSmallBox * 128u : (uint32_t)kOperandBytes;
+      const uint32_t bytes = abytes + (b_mn_major(kMode) ? (uint32_t)nb * kChunkBytes : nb ? (uint32_t)kOperandBytes : 0u);
+      const bool small = kMode != kWgrad && abytes == kSmallBox * 128u;
+      const CUtensorMap* ma = maps.m + (kMode == kWgrad ? (t.mat == 0 ? 0 : t.mat == 1 ? 2 : 3) : small ? 3 : 0);
+      const CUtensorMap* mb = maps.m + (kMode == kWgrad ? (t.mat == 2 ? 4 : 1) : kMode == kUp && rank == 1 ? 2 : 1);
+      const int nch = chains_of(t.rows);
+      for (int ch = 0; ch < nch && ok; ++ch) {
+        const int nkb = blocks_of(t.rows, ch);
+        for (int kb = 0; kb < nkb; ++kb) {
+          ok = __all_sync(0xffffffffu, wait_bounded(smem_u32(empty + st), ph ^ 1u, p.status, s_abort));
+          if (!ok) break;
+          const uint32_t a = smem0 + st * kStageBytes, b = a + kOperandBytes;
+          uint32_t bar = leader_addr(smem_u32(full + st));
+          if constexpr (kMode == kWgrad) {
+            const int done = ch * kChainRows + kb * kBlockK, row = t.row0 + done;
+            if (done + kBlockK > t.rows) bar = smem_u32(tail + st);   // rows behind the segment are to be zeroed
+            expect_bytes(bar, bytes);
+            if (na > 0) load_2d(a, ma, m, row, bar);
+            if (na > 1) load_2d(a + kChunkBytes, ma, m + 64, row, bar);
+            if (nb > 0) load_2d(b, mb, n, row, bar);
+            if (nb > 1) load_2d(b + kChunkBytes, mb, n + 64, row, bar);
+          } else {
+            int k0 = kb * kBlockK;
+            if (kMode == kDgradRows && kb == p.half_kb) {   // the second source
+              ma = maps.m + (small ? 5 : 2);
+              mb = maps.m + 4;
             }
-            const uint32_t a = smem0 + st * kStageBytes, b = a + kOperandBytes;
-            uint32_t bar = leader_addr(smem_u32(full + st));
-            if constexpr (kMode == kWgrad) {
-              const int Mm = t.mat == 2 ? p.M : p.N, Nn = t.mat == 2 ? p.N : p.M;
-              const CUtensorMap* ma = maps.m + (t.mat == 0 ? 0 : t.mat == 1 ? 2 : 3);
-              const CUtensorMap* mb = maps.m + (t.mat == 2 ? 4 : 1);
-              const int row = t.row0 + ch * kChainRows + kb * kBlockK;
-              const int m = t.m0 + rank * kHalf, n = t.n0 + rank * kHalf;
-              const int na = m >= Mm ? 0 : m + 64 >= Mm ? 1 : 2, nb = n >= Nn ? 0 : n + 64 >= Nn ? 1 : 2;
-              const bool cut = row + kBlockK > t.row0 + t.rows;
-              if (cut) bar = smem_u32(tail + st);
-              if (cut) mbar_arrive_expect_tx(bar, (uint32_t)(na + nb) * kChunkBytes);
-              else arrive_expect_cluster(bar, (uint32_t)(na + nb) * kChunkBytes);
-              for (int i = 0; i < na; ++i) load_2d(a + i * kChunkBytes, ma, m + 64 * i, row, bar);
-              for (int i = 0; i < nb; ++i) load_2d(b + i * kChunkBytes, mb, n + 64 * i, row, bar);
+            if (kMode == kDgradRows && kb >= p.half_kb) k0 -= p.half_kb * kBlockK;
+            expect_bytes(bar, bytes);
+            if (abytes) load_2d(a, ma, k0, m, bar);
+            if constexpr (b_mn_major(kMode)) {
+              if (nb > 0) load_3d(b, mb, n, k0, t.seg, bar);
+              if (nb > 1) load_3d(b + kChunkBytes, mb, n + 64, k0, t.seg, bar);
             } else {
-              const int mine = t.rows - (int)rank * kHalf;   // rows of this CTA's half
-              const uint32_t abytes = mine <= 0 ? 0u : mine <= kSmallBox ? kSmallBox * 128u : (uint32_t)kOperandBytes;
-              const bool second = kMode == kDgradRows && kb >= p.half_kb;
-              const int k0 = (second ? kb - p.half_kb : kb) * kBlockK;
-              const CUtensorMap* ma = maps.m + (abytes == kSmallBox * 128u ? (second ? 5 : 3) : (second ? 2 : 0));
-              if constexpr (b_mn_major(kMode)) {
-                const int n = t.n0 + rank * kHalf;
-                const int nb = n >= p.N ? 0 : n + 64 >= p.N ? 1 : 2;
-                arrive_expect_cluster(bar, abytes + (uint32_t)nb * kChunkBytes);
-                if (abytes) load_2d(a, ma, k0, t.m0 + rank * kHalf, bar);
-                for (int i = 0; i < nb; ++i) load_3d(b + i * kChunkBytes, maps.m + (second ? 4 : 1), n + 64 * i, k0, t.seg, bar);
-              } else {
-                const int n = kMode == kUp ? t.n0 : t.n0 + (int)rank * kHalf;
-                const bool has_b = n < p.N;
-                arrive_expect_cluster(bar, abytes + (has_b ? kOperandBytes : 0));
-                if (abytes) load_2d(a, ma, k0, t.m0 + rank * kHalf, bar);
-                if (has_b) load_3d(b, maps.m + (kMode == kUp && rank == 1 ? 2 : 1), k0, n, t.seg, bar);
-              }
+              if (nb > 0) load_3d(b, mb, k0, n, t.seg, bar);
             }
-            used = min(used + 1, (uint32_t)kStages);
-            if (++st == kStages) { st = 0; ph ^= 1u; }
           }
+          used = min(used + 1, (uint32_t)kStages);
+          if (++st == kStages) { st = 0; ph ^= 1u; }
         }
       }
-      // the MMAs' arrivals on this CTA's barriers have to come before it may end
-      for (uint32_t i = 0; i < used && ok; ++i) {
-        const uint32_t s = (st + kStages - used + i) % kStages;
-        const uint32_t par = s < st ? ph : ph ^ 1u;
-        ok = wait_bounded(smem_u32(empty + s), par, p.status, s_abort);
-      }
+    }
+    // the MMAs' arrivals on this CTA's barriers have to come before it may end
+    for (uint32_t i = 0; i < used && ok; ++i) {
+      const uint32_t s = (st + kStages - used + i) % kStages;
+      const uint32_t par = s < st ? ph : ph ^ 1u;
+      ok = __all_sync(0xffffffffu, wait_bounded(smem_u32(empty + s), par, p.status, s_abort));
     }
   } else if (warp == kMmaWarp) {
     // ---------------- products (CTA 0) ----------------
