@@ -18,8 +18,9 @@
 // stored (rows do not mix).  In the weights' gradients the rows are the reduction: the last block of a
 // segment is zeroed behind the segment's end in shared memory, in both operands, before it is multiplied.
 //
-// Warps of a CTA: 0-7 epilogue (each a quarter of the rows and half of the columns), 8 copies, 9 tensor
-// memory and, in CTA 0, the MMAs of the pair, 10 the zeroing.  Two accumulators (2 x 256 columns) let
+// Warps of a CTA: 0-7 epilogue (each a quarter of the rows and half of the columns), 8 and 11 copies (every other
+// stage each: a load takes 100 cycles to issue, up to four a stage), 9 tensor memory and, in CTA 0, the MMAs of
+// the pair, 10 the zeroing.  Two accumulators (2 x 256 columns) let
 // the epilogue run beside the next tile's products.  Every wait is bounded; one that runs out leaves
 // MOE_ERR_DEVICE_TIMEOUT in the status.
 #include <cuda.h>
@@ -45,8 +46,8 @@ constexpr int kChunkBytes = kBlockK * 128;      // MN-major: 64 columns (128 byt
 constexpr int kStages = 5;
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kSlabBytes = 32 * 128;            // of an epilogue warp: its 32 rows by 128 bytes on their way out
-constexpr int kEpiWarps = 8, kCopyWarp = 8, kMmaWarp = 9, kZeroWarp = 10;
-constexpr int kThreads = 11 * 32;
+constexpr int kEpiWarps = 8, kCopyWarp = 8, kMmaWarp = 9, kZeroWarp = 10, kCopyWarp2 = 11;
+constexpr int kThreads = 12 * 32;
 constexpr int kMaxExperts = 1024;
 constexpr int kGroupM = 8;                      // row tiles that are worked through column by column
 constexpr int kSmallBox = 32;                   // rows of the small box
@@ -459,9 +460,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     return kMode == kWgrad ? (min(kChainRows, rows - chain * kChainRows) + kBlockK - 1) / kBlockK : p.nkb;
   };
 
-  if (warp == kCopyWarp) {
+  if (warp == kCopyWarp || warp == kCopyWarp2) {
     // ---------------- copies ----------------
-    uint32_t st = 0, ph = 0, used = 0;
+    const uint32_t full0 = leader_addr(smem_u32(full));
+    uint32_t st = 0, ph = 0, mine_next = warp == kCopyWarp ? 1u : 0u, filled = 0;   // filled: stages, at most all
     bool ok = true;
     for (int item = first; item < total && ok; item += step) {
       const Tile t = tile_at<kMode>(p, s_off, s_tile, item);
@@ -479,11 +481,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int nch = chains_of(t.rows);
       for (int ch = 0; ch < nch && ok; ++ch) {
         const int nkb = blocks_of(t.rows, ch);
-        for (int kb = 0; kb < nkb; ++kb) {
+        for (int kb = 0; kb < nkb; ++kb, mine_next ^= 1u, st = st + 1 == kStages ? 0 : st + 1, ph ^= st == 0) {
+          filled = min(filled + 1, (uint32_t)kStages);
+          if (kMode == kDgradRows && kb == p.half_kb) {   // the second source
+            ma = maps.m + (small ? 5 : 2);
+            mb = maps.m + 4;
+          }
+          if (!mine_next) continue;
           ok = __all_sync(0xffffffffu, wait_bounded(smem_u32(empty + st), ph ^ 1u, p.status, s_abort));
           if (!ok) break;
           const uint32_t a = smem0 + st * kStageBytes, b = a + kOperandBytes;
-          uint32_t bar = leader_addr(smem_u32(full + st));
+          uint32_t bar = full0 + 8 * st;
           if constexpr (kMode == kWgrad) {
             const int done = ch * kChainRows + kb * kBlockK, row = t.row0 + done;
             if (done + kBlockK > t.rows) bar = smem_u32(tail + st);   // rows behind the segment are to be zeroed
@@ -494,10 +502,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (nb > 1) load_2d(b + kChunkBytes, mb, n + 64, row, bar);
           } else {
             int k0 = kb * kBlockK;
-            if (kMode == kDgradRows && kb == p.half_kb) {   // the second source
-              ma = maps.m + (small ? 5 : 2);
-              mb = maps.m + 4;
-            }
             if (kMode == kDgradRows && kb >= p.half_kb) k0 -= p.half_kb * kBlockK;
             expect_bytes(bar, bytes);
             if (abytes) load_2d(a, ma, k0, m, bar);
@@ -508,16 +512,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               if (nb > 0) load_3d(b, mb, k0, n, t.seg, bar);
             }
           }
-          used = min(used + 1, (uint32_t)kStages);
-          if (++st == kStages) { st = 0; ph ^= 1u; }
         }
       }
     }
-    // the MMAs' arrivals on this CTA's barriers have to come before it may end
-    for (uint32_t i = 0; i < used && ok; ++i) {
-      const uint32_t s = (st + kStages - used + i) % kStages;
-      const uint32_t par = s < st ? ph : ph ^ 1u;
-      ok = __all_sync(0xffffffffu, wait_bounded(smem_u32(empty + s), par, p.status, s_abort));
+    // The MMAs' arrivals on this CTA's barriers have to come before it may end: each warp waits for the stages that it
+    // filled last (d blocks ago), which nobody fills again.
+    for (uint32_t d = 1; d <= filled && ok; ++d) {
+      if (((d & 1u) ? mine_next ^ 1u : mine_next) == 0u) continue;
+      const uint32_t s = st >= d ? st - d : st + kStages - d;
+      ok = __all_sync(0xffffffffu, wait_bounded(smem_u32(empty + s), st >= d ? ph : ph ^ 1u, p.status, s_abort));
     }
   } else if (warp == kMmaWarp) {
     // ---------------- products (CTA 0) ----------------
