@@ -14,240 +14,402 @@
 
 #include "common.cuh"
 #include "ops.h"
-#include "rows.cuh"
 
 namespace nvfp4moe {
 
 namespace {
 
 constexpr int kMaxCols = 16384;
+constexpr int kMostRing = 216 * 1024;   // dynamic shared memory of a launch, at most
+
+// Eight FP32 elements, as uint4 holds eight BF16 ones.
+struct F32x8 {
+  float4 a, b;
+};
 
 // How a row is laid over threads: W warps with J vectors of 8 columns a lane (vector c of lane t:
-// c = j * 32 W + t); a block holds G such row groups, each of which takes every gridDim * G-th row.
+// c = j * 32 W + t); a block holds G such row groups.
 struct NormGrid {
   int J, W, G, blocks;
 };
 
-// The next row is loaded before the current one is reduced.
+// ---- many rows: rows come through a ring in shared memory ----
+//
+// A group of W warps takes every gridDim * G-th row.  Its rows are fetched by bulk copies into a ring of
+// `slots` rows of its own (all of the row's tensors).  Each row has one barrier over the group, behind which
+// all its warps are done with the row before, whose slot is filled again: no other hand-over is needed.  The
+// ring keeps 100 KB and more an SM under way without registers for it, so that a lane can hold two vectors of
+// everything else; arithmetic goes in pairs (f32x2), as instructions, not bytes, are what is short: one
+// vector a lane and scalar arithmetic took 92 and 101 us for 16384 x 4096 and 8191 x 7168 backward, two rows a
+// barrier or not.  slots == 1 (rows so wide that two do not fit): the row ends in a barrier before its slot is filled.
+
+constexpr uint64_t kCopyLimitNs = 1000000000ull;
+
+struct Ring {
+  uint32_t data, bars;     // shared addresses of the group's slots and their barriers
+  uint32_t row_bytes;      // of one tensor
+  int slots, group, G, W;
+  bool issuer;             // the group's thread that starts the copies
+
+  template <int kN>
+  __device__ __forceinline__ uint32_t at(uint32_t s, int tensor) const {
+    return data + (s * kN + tensor) * row_bytes;
+  }
+  template <int kN>
+  __device__ __forceinline__ void fetch(uint32_t s, const void* const (&src)[kN], int count, int64_t row) const {
+    const uint32_t bar = bars + 8 * s;
+    mbar_arrive_expect_tx(bar, (uint32_t)count * row_bytes);
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      if (i < count) bulk_load(at<kN>(s, i), static_cast<const uint8_t*>(src[i]) + row * row_bytes, row_bytes, bar);
+  }
+  // The row of a slot has landed; false if the wait ran out.
+  __device__ __forceinline__ bool landed(uint32_t s, uint32_t phase) const {
+    return mbar_wait_bounded(bars + 8 * s, phase, kCopyLimitNs, nullptr);
+  }
+  __device__ __forceinline__ void barrier() const {
+    if (W == 1) __syncwarp();
+    else if (G == 1) __syncthreads();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(W * 32) : "memory");
+  }
+};
+
+int ring_slots(int G, size_t slot_bytes) {
+  return (int)std::max<size_t>(1, std::min<size_t>(8, 208 * 1024 / G / slot_bytes));
+}
+size_t ring_bytes(int G, int slots, size_t slot_bytes) { return 2048 + (size_t)G * slots * slot_bytes; }
+
+__device__ __forceinline__ Ring make_ring(uint8_t* smem, uint32_t row_bytes, int tensors, int slots, int group, int G, int W, int t) {
+  Ring r;
+  r.bars = smem_u32(smem) + (uint32_t)group * slots * 8;   // (32 groups of 8 slots at most: 2 KB)
+  r.data = smem_u32(smem) + 2048 + (uint32_t)group * slots * tensors * row_bytes;
+  r.row_bytes = row_bytes;
+  r.slots = slots;
+  r.group = group;
+  r.G = G;
+  r.W = W;
+  r.issuer = t == 0;
+  if (r.issuer) {
+    for (int i = 0; i < slots; ++i) mbar_init(r.bars + 8 * i, 1);
+    fence_barrier_init();
+  }
+  return r;
+}
+
+__device__ __forceinline__ void read_vec(uint32_t addr, uint4& q) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void read_vec(uint32_t addr, F32x8& q) {
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(q.a.x), "=f"(q.a.y), "=f"(q.a.z), "=f"(q.a.w) : "r"(addr) : "memory");
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(q.b.x), "=f"(q.b.y), "=f"(q.b.z), "=f"(q.b.w) : "r"(addr + 16) : "memory");
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// The sum over the first 16 lanes (the rows' W <= 16 warps), on each of them and on the others.
+__device__ __forceinline__ float half_warp_sum(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return __shfl_sync(0xffffffffu, v, 0);
+}
+
+// Two FP32 operations an instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{.reg .b64 x, y, z;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nadd.rn.f32x2 z, x, y;\nmov.b64 {%0, %1}, z;}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{.reg .b64 x, y, z;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nmul.rn.f32x2 z, x, y;\nmov.b64 {%0, %1}, z;}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{.reg .b64 x, y, w, z;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nmov.b64 w, {%6, %7};\n"
+      "fma.rn.f32x2 z, x, y, w;\nmov.b64 {%0, %1}, z;}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ void unpack(const uint4& q, float2 (&f)[4]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+}
+__device__ __forceinline__ void unpack(const F32x8& q, float2 (&f)[4]) {
+  f[0] = make_float2(q.a.x, q.a.y);
+  f[1] = make_float2(q.a.z, q.a.w);
+  f[2] = make_float2(q.b.x, q.b.y);
+  f[3] = make_float2(q.b.z, q.b.w);
+}
+__device__ __forceinline__ void pack(const float2 (&f)[4], uint4& q) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f[i].x, f[i].y);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  q = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void pack(const float2 (&f)[4], F32x8& q) {
+  q.a = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+  q.b = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+}
+
+// A warp's share of a row's mean and variance: elements, their mean, the sum of squared distances from it.  The
+// warps' means and the distances between them meet behind the row's one barrier.
+struct Share {
+  float n, mean, dist;
+};
+
 template <typename V, int J>
-__global__ void __launch_bounds__(512, sizeof(V) == 16 && J <= 2 ? 2 : 1) add_layernorm_kernel(
+__global__ void __launch_bounds__(512, 1) add_layernorm_kernel(
     const V* x, const V* residual, const V* __restrict__ gamma, const V* __restrict__ beta, float eps,
-    int64_t rows, int cols, int W, int G, V* h, V* y, float* mean, float* rstd) {
-  __shared__ float red[2 * 16 * 32];
-  const int warp = threadIdx.x >> 5, group = warp / W, wrow = warp - group * W;
-  const int t = wrow * 32 + (threadIdx.x & 31), span = W * 32;   // thread of the row, vectors apart
+    int64_t rows, int cols, int W, int G, int slots, V* h, V* y, float* mean, float* rstd) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ Share red[2][16];
+  constexpr bool kWide = J > 2;   // gamma and beta are read again for each row
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = warp / W, wrow = warp - group * W;
+  const int t = wrow * 32 + lane, span = W * 32;   // thread of the row, vectors apart
   const int nvec = cols / 8;
   const float inv_cols = __fdiv_rn(1.0f, (float)cols);
+  const int tensors = residual ? 2 : 1;
+  const Ring ring = make_ring(smem, (uint32_t)cols * (sizeof(V) / 8), 2, slots, group, G, W, t);
+  __syncthreads();
   griddep_wait();
   griddep_launch();
+  const int64_t row0 = (int64_t)blockIdx.x * G + group, step = (int64_t)gridDim.x * G;
+  const int count = row0 < rows ? (int)((rows - row0 + step - 1) / step) : 0;   // rows of the group
+  const void* const src[2] = {x, residual};
+  if (ring.issuer)
+    for (int n = 0; n < min(slots, count); ++n) ring.fetch<2>(n, src, tensors, row0 + n * step);
   const V zero = {};
-  int64_t row = (int64_t)blockIdx.x * G + group;
-  const int64_t step = (int64_t)gridDim.x * G;
-  V nx[J], nr[J];
-  auto load = [&](int64_t rw) {
+  auto gain = [&](int c, float2 (&f)[4]) { unpack(c < nvec ? gamma[c] : zero, f); };
+  auto bias = [&](int c, float2 (&f)[4]) { unpack(c < nvec && beta ? beta[c] : zero, f); };
+  float2 g[kWide ? 1 : J][4], b[kWide ? 1 : J][4];
+  int mine = 0;   // elements of the warp
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    if constexpr (!kWide) {
+      gain(j * span + t, g[j]);
+      bias(j * span + t, b[j]);
+    }
+    mine += 8 * min(max(nvec - (j * span + wrow * 32), 0), 32);
+  }
+  const float wn = (float)mine, inv_wn = mine ? __fdiv_rn(1.0f, wn) : 0.0f;
+  bool ok = true;
+  uint32_t phase = 0;
+  for (int n = 0, s = 0, par = 0; n < count; ++n, par ^= 1) {   // s: the row's slot
+    ok = ok && ring.landed(s, phase);
+    const int64_t base = (row0 + n * step) * nvec;
+    float2 f[J][4], sum = both(0.0f);
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int c = j * span + t;
-      const bool in = rw < rows && c < nvec;
-      nx[j] = in ? x[rw * nvec + c] : zero;
-      nr[j] = in && residual ? residual[rw * nvec + c] : zero;
-    }
-  };
-  load(row);
-  for (; row < rows; row += step) {
-    const int64_t base = row * nvec;
-    V hv[J];
-    float s = 0.0f;
+      V q = zero;
+      if (c < nvec) {
+        read_vec(ring.at<2>(s, 0) + c * (uint32_t)sizeof(V), q);
+        if (residual) {
+          V e;
+          float2 d[4];
+          unpack(q, f[j]);
+          read_vec(ring.at<2>(s, 1) + c * (uint32_t)sizeof(V), e);
+          unpack(e, d);
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      float f[8];
-      hv[j] = nx[j];
-      unpack8(hv[j], f);
-      if (residual) {
-        float g[8];
-        unpack8(nr[j], g);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] += g[i];
-        pack(f, hv[j]);
-        unpack8(hv[j], f);
+          for (int i = 0; i < 4; ++i) f[j][i] = add2(f[j][i], d[i]);
+          pack(f[j], q);
+          h[base + c] = q;
+        }
       }
+      unpack(q, f[j]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s += f[i];
+      for (int i = 0; i < 4; ++i) sum = add2(sum, f[j][i]);
     }
-    load(row + step);   // (rows are written by their own group only, after this group read them)
-    if (h) {
-#pragma unroll
-      for (int j = 0; j < J; ++j)
-        if (j * span + t < nvec) h[base + j * span + t] = hv[j];
-    }
-    const float m = row_sum(s, red, W, wrow, group, G, 0) * inv_cols;
-    s = 0.0f;
+    const float wm = warp_sum(sum.x + sum.y) * inv_wn;
+    float2 dist = both(0.0f);
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      float f[8];
-      unpack8(hv[j], f);
-      if (j * span + t < nvec)
+      if (j * span + t >= nvec) continue;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s = fmaf(f[i] - m, f[i] - m, s);
+      for (int i = 0; i < 4; ++i) {
+        const float2 d = add2(f[j][i], both(-wm));
+        dist = fma2(d, d, dist);
+      }
     }
-    const float var = row_sum(s, red, W, wrow, group, G, 1) * inv_cols;
+    const float wd = warp_sum(dist.x + dist.y);
+    if (lane == 0) red[par][warp] = Share{wn, ok ? wm : __int_as_float(0x7FC00000), wd};
+    ring.barrier();
+    if (ring.issuer && n > 0 && slots > 1 && n - 1 + slots < count)   // the slot of the row before
+      ring.fetch<2>(s ? s - 1 : slots - 1, src, tensors, row0 + (int64_t)(n - 1 + slots) * step);
+    const Share w = lane < W ? red[par][group * W + lane] : Share{0.0f, 0.0f, 0.0f};
+    const float m = half_warp_sum(w.n * w.mean) * inv_cols;
+    const float var = half_warp_sum(fmaf(w.n * (w.mean - m), w.mean - m, w.dist)) * inv_cols;
     const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(var, eps)));
     if (t == 0) {
-      if (mean) mean[row] = m;
-      if (rstd) rstd[row] = r;
+      if (mean) mean[row0 + n * step] = m;
+      if (rstd) rstd[row0 + n * step] = r;
     }
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int c = j * span + t;
       if (c >= nvec) continue;
-      float v[8], g[8], b[8];
-      unpack8(hv[j], v);
-      unpack8(gamma[c], g);
-      unpack8(beta ? beta[c] : zero, b);
+      if constexpr (kWide) {
+        gain(c, g[0]);
+        bias(c, b[0]);
+      }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = fmaf((v[i] - m) * r, g[i], b[i]);
+      for (int i = 0; i < 4; ++i)
+        f[j][i] = fma2(mul2(add2(f[j][i], both(-m)), both(r)), g[kWide ? 0 : j][i], b[kWide ? 0 : j][i]);
       V o;
-      pack(v, o);
+      pack(f[j], o);
       y[base + c] = o;
     }
+    if (slots == 1) {
+      ring.barrier();
+      if (ring.issuer && n + 1 < count) ring.fetch<2>(0, src, tensors, row0 + (int64_t)(n + 1) * step);
+    }
+    if (++s == slots) {
+      s = 0;
+      phase ^= 1u;
+    }
   }
 }
 
-// The sums of two values over the row's warps; as row_sum, over one barrier.
-__device__ __forceinline__ float2 row_sum2(float2 v, float2* red, int W, int wrow, int group, int G,
-                                           int parity) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-  }
-  if (W == 1) return v;
-  const int lane = threadIdx.x & 31;
-  float2* mine = red + (parity * G + group) * 32;
-  if (lane == 0) mine[wrow] = v;
-  if (G == 1) __syncthreads();
-  else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(W * 32) : "memory");
-  float2 s = lane < W ? mine[lane] : make_float2(0.0f, 0.0f);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
-    s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
-  }
-  return s;
-}
-
-// A thread owns the same J vectors of 8 columns in all rows of its group and keeps their share of
-// dgamma and dbeta in registers; the groups of a block are joined in order at the end, the blocks by
-// column_sums_kernel.
-template <typename V, int J, bool kAhead>
+// A thread owns the same J vectors of 8 columns in all rows of its group and keeps their share of dgamma
+// and dbeta in registers; the groups of a block are joined in order at the end, the blocks by column_sums_kernel.
+template <typename V, int J>
 __global__ void __launch_bounds__(512, 1) add_layernorm_backward_kernel(
     const V* dy, const V* dh, const V* h, const float* __restrict__ mean, const float* __restrict__ rstd,
-    const V* __restrict__ gamma, int64_t rows, int cols, int W, int G, V* dx, bool want_beta,
+    const V* __restrict__ gamma, int64_t rows, int cols, int W, int G, int slots, V* dx, bool want_beta,
     float4* __restrict__ partial) {
-  extern __shared__ float4 s_part[];   // [cols / 4] if G > 1
-  __shared__ float2 red[2 * 16 * 32];
-  const int warp = threadIdx.x >> 5, group = warp / W, wrow = warp - group * W;
-  const int t = wrow * 32 + (threadIdx.x & 31), span = W * 32;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float2 red[2][16];
+  constexpr bool kKeep = J <= 2;   // a and n stay in registers over the barrier, else they are computed again
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = warp / W, wrow = warp - group * W;
+  const int t = wrow * 32 + lane, span = W * 32;
   const int nvec = cols / 8;
   const float inv_cols = __fdiv_rn(1.0f, (float)cols);
+  const int tensors = dh ? 3 : 2;
+  const Ring ring = make_ring(smem, (uint32_t)cols * (sizeof(V) / 8), 3, slots, group, G, W, t);
+  __syncthreads();
   griddep_wait();
   griddep_launch();
+  const int64_t row0 = (int64_t)blockIdx.x * G + group, step = (int64_t)gridDim.x * G;
+  const int count = row0 < rows ? (int)((rows - row0 + step - 1) / step) : 0;
+  const void* const src[3] = {dy, h, dh};
+  if (ring.issuer)
+    for (int n = 0; n < min(slots, count); ++n) ring.fetch<3>(n, src, tensors, row0 + n * step);
   const V zero = {};
-  float dg[J][8], db[J][8];
+  float2 g[kKeep ? J : 1][4];
+  auto gain = [&](int c, float2 (&f)[4]) { unpack(c < nvec ? gamma[c] : zero, f); };
+  float2 dg[J][4], db[J][4];
 #pragma unroll
-  for (int j = 0; j < J; ++j)
+  for (int j = 0; j < J; ++j) {
+    if constexpr (kKeep) gain(j * span + t, g[j]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dg[j][i] = db[j][i] = 0.0f;
-  int64_t row = (int64_t)blockIdx.x * G + group;
-  const int64_t step = (int64_t)gridDim.x * G;
-  V nd[J], nh[J], ne[J];
-  float nm = 0.0f, nr = 0.0f;
-  auto load_dh = [&](int64_t rw) {
+    for (int i = 0; i < 4; ++i) dg[j][i] = db[j][i] = both(0.0f);
+  }
+  // a = gamma dy and n of a vector
+  auto terms = [&](uint32_t s, int j, float m, float r, float2 (&d)[4], float2 (&a)[4], float2 (&nv)[4]) {
+    const int c = j * span + t;
+    V qd, qh;
+    read_vec(ring.at<3>(s, 0) + c * (uint32_t)sizeof(V), qd);
+    read_vec(ring.at<3>(s, 1) + c * (uint32_t)sizeof(V), qh);
+    unpack(qd, d);
+    unpack(qh, nv);
+    if constexpr (!kKeep) gain(c, g[0]);
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const int c = j * span + t;
-      ne[j] = rw < rows && c < nvec && dh ? dh[rw * nvec + c] : zero;
+    for (int i = 0; i < 4; ++i) {
+      nv[i] = mul2(add2(nv[i], both(-m)), both(r));
+      a[i] = mul2(d[i], g[kKeep ? j : 0][i]);
     }
   };
-  auto load = [&](int64_t rw) {
-    nm = rw < rows ? __ldg(mean + rw) : 0.0f;
-    nr = rw < rows ? __ldg(rstd + rw) : 0.0f;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const int c = j * span + t;
-      const bool in = rw < rows && c < nvec;
-      nd[j] = in ? dy[rw * nvec + c] : zero;
-      nh[j] = in ? h[rw * nvec + c] : zero;
+  float nm = count > 0 ? __ldg(mean + row0) : 0.0f, nr = count > 0 ? __ldg(rstd + row0) : 0.0f;
+  bool ok = true;
+  uint32_t phase = 0;
+  for (int n = 0, s = 0, par = 0; n < count; ++n, par ^= 1) {
+    float m = nm;
+    const float r = nr;
+    if (n + 1 < count) {   // the next row's statistics
+      nm = __ldg(mean + row0 + (int64_t)(n + 1) * step);
+      nr = __ldg(rstd + row0 + (int64_t)(n + 1) * step);
     }
-    if (kAhead) load_dh(rw);
-  };
-  if (kAhead) load(row);
-  for (int parity = 0; row < rows; row += step, parity ^= 1) {
-    if (!kAhead) load(row);
-    const float m = nm, r = nr;
-    V qd[J], qh[J], qe[J];
-    float2 s = make_float2(0.0f, 0.0f);
+    ok = ok && ring.landed(s, phase);
+    if (!ok) m = __int_as_float(0x7FC00000);
+    float2 a[kKeep ? J : 1][4], nv[kKeep ? J : 1][4], sa = both(0.0f), sn = both(0.0f);
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      qd[j] = nd[j];
-      qh[j] = nh[j];
-      if (kAhead) qe[j] = ne[j];
       if (j * span + t >= nvec) continue;
-      float d[8], hv[8], g[8];
-      unpack8(qd[j], d);
-      unpack8(qh[j], hv);
-      unpack8(gamma[j * span + t], g);
+      const int k = kKeep ? j : 0;
+      float2 d[4];
+      terms(s, j, m, r, d, a[k], nv[k]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float n = (hv[i] - m) * r, a = d[i] * g[i];
-        s.x += a;
-        s.y = fmaf(a, n, s.y);
-        dg[j][i] = fmaf(d[i], n, dg[j][i]);
-        db[j][i] += d[i];
+      for (int i = 0; i < 4; ++i) {
+        sa = add2(sa, a[k][i]);
+        sn = fma2(a[k][i], nv[k][i], sn);
+        dg[j][i] = fma2(d[i], nv[k][i], dg[j][i]);
+        db[j][i] = add2(db[j][i], d[i]);
       }
     }
-    if constexpr (kAhead) {
-      load(row + step);
-    } else {   // dh is not part of the row's sums
-      load_dh(row);
-#pragma unroll
-      for (int j = 0; j < J; ++j) qe[j] = ne[j];
-    }
-    s = row_sum2(s, red, W, wrow, group, G, parity);
-    const float ma = s.x * inv_cols, mn = s.y * inv_cols;
+    const float2 share = make_float2(warp_sum(sa.x + sa.y), warp_sum(sn.x + sn.y));
+    if (lane == 0) red[par][warp] = share;
+    ring.barrier();
+    if (ring.issuer && n > 0 && slots > 1 && n - 1 + slots < count)   // the slot of the row before
+      ring.fetch<3>(s ? s - 1 : slots - 1, src, tensors, row0 + (int64_t)(n - 1 + slots) * step);
+    const float2 w = lane < W ? red[par][group * W + lane] : make_float2(0.0f, 0.0f);
+    const float ma = half_warp_sum(w.x) * inv_cols, mn = half_warp_sum(w.y) * inv_cols;
+    const int64_t base = (row0 + n * step) * nvec;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const int c = j * span + t;
+      const int c = j * span + t, k = kKeep ? j : 0;
       if (c >= nvec) continue;
-      float d[8], hv[8], e[8], g[8], o[8];
-      unpack8(qd[j], d);
-      unpack8(qh[j], hv);
-      unpack8(qe[j], e);
-      unpack8(gamma[c], g);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float n = (hv[i] - m) * r;
-        o[i] = r * fmaf(-n, mn, fmaf(d[i], g[i], -ma));
-        if (dh) o[i] += e[i];
+      if constexpr (!kKeep) {
+        float2 d[4];
+        terms(s, j, m, r, d, a[0], nv[0]);
       }
+      float2 o[4], e[4];
       V q;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = mul2(both(r), fma2(nv[k][i], both(-mn), add2(a[k][i], both(-ma))));
+      if (dh) {
+        read_vec(ring.at<3>(s, 2) + c * (uint32_t)sizeof(V), q);
+        unpack(q, e);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = add2(o[i], e[i]);
+      }
       pack(o, q);
-      dx[row * nvec + c] = q;
+      dx[base + c] = q;
+    }
+    if (slots == 1) {
+      ring.barrier();
+      if (ring.issuer && n + 1 < count) ring.fetch<3>(0, src, tensors, row0 + (int64_t)(n + 1) * step);
+    }
+    if (++s == slots) {
+      s = 0;
+      phase ^= 1u;
     }
   }
+  // the other groups' sums to the first's, in order, through the ring's memory
+  float4* s_part = reinterpret_cast<float4*>(smem + 2048);   // [cols / 4]
 #pragma unroll
   for (int which = 0; which < 2; ++which) {   // dgamma, then dbeta
     if (which == 1 && !want_beta) break;
-    float(&acc)[J][8] = which ? db : dg;
-    for (int k = 1; k < G; ++k) {   // the other groups' sums to the first's, in order
+    float2(&acc)[J][4] = which ? db : dg;
+    for (int k = 1; k < G; ++k) {
       __syncthreads();
       if (group == k) {
 #pragma unroll
         for (int j = 0; j < J; ++j) {
           const int c = j * span + t;
           if (c >= nvec) continue;
-          s_part[2 * c] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
-          s_part[2 * c + 1] = make_float4(acc[j][4], acc[j][5], acc[j][6], acc[j][7]);
+          s_part[2 * c] = make_float4(acc[j][0].x, acc[j][0].y, acc[j][1].x, acc[j][1].y);
+          s_part[2 * c + 1] = make_float4(acc[j][2].x, acc[j][2].y, acc[j][3].x, acc[j][3].y);
         }
       }
       __syncthreads();
@@ -257,8 +419,10 @@ __global__ void __launch_bounds__(512, 1) add_layernorm_backward_kernel(
           const int c = j * span + t;
           if (c >= nvec) continue;
           const float4 u = s_part[2 * c], v = s_part[2 * c + 1];
-          acc[j][0] += u.x; acc[j][1] += u.y; acc[j][2] += u.z; acc[j][3] += u.w;
-          acc[j][4] += v.x; acc[j][5] += v.y; acc[j][6] += v.z; acc[j][7] += v.w;
+          acc[j][0] = add2(acc[j][0], make_float2(u.x, u.y));
+          acc[j][1] = add2(acc[j][1], make_float2(u.z, u.w));
+          acc[j][2] = add2(acc[j][2], make_float2(v.x, v.y));
+          acc[j][3] = add2(acc[j][3], make_float2(v.z, v.w));
         }
       }
     }
@@ -268,9 +432,83 @@ __global__ void __launch_bounds__(512, 1) add_layernorm_backward_kernel(
       const int c = j * span + t;
       if (c >= nvec) continue;
       float4* p = partial + ((int64_t)which * gridDim.x + blockIdx.x) * (cols / 4) + 2 * c;
-      p[0] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
-      p[1] = make_float4(acc[j][4], acc[j][5], acc[j][6], acc[j][7]);
+      p[0] = make_float4(acc[j][0].x, acc[j][0].y, acc[j][1].x, acc[j][1].y);
+      p[1] = make_float4(acc[j][2].x, acc[j][2].y, acc[j][3].x, acc[j][3].y);
     }
+  }
+}
+
+// ---- few rows: one row a block, loaded straight into registers ----
+template <typename V, int J>
+__global__ void __launch_bounds__(1024, 1) add_layernorm_row_kernel(
+    const V* __restrict__ x, const V* __restrict__ residual, const V* __restrict__ gamma,
+    const V* __restrict__ beta, float eps, int cols, V* h, V* y, float* mean, float* rstd) {
+  __shared__ Share red[32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, span = blockDim.x, W = span / 32, nvec = cols / 8;
+  const float inv_cols = __fdiv_rn(1.0f, (float)cols);
+  griddep_wait();
+  griddep_launch();
+  const int64_t base = (int64_t)blockIdx.x * nvec;
+  const V zero = {};
+  V g[J], b[J];
+  float2 f[J][4], sum = both(0.0f);
+  int mine = 0;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int c = j * span + threadIdx.x;
+    const bool in = c < nvec;
+    V q = in ? x[base + c] : zero;
+    const V e = in && residual ? residual[base + c] : zero;
+    g[j] = in ? gamma[c] : zero;
+    b[j] = in && beta ? beta[c] : zero;
+    if (residual && in) {
+      float2 d[4];
+      unpack(q, f[j]);
+      unpack(e, d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[j][i] = add2(f[j][i], d[i]);
+      pack(f[j], q);
+      h[base + c] = q;
+    }
+    unpack(q, f[j]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum = add2(sum, f[j][i]);
+    mine += 8 * min(max(nvec - (j * span + warp * 32), 0), 32);
+  }
+  const float wm = mine ? __fdiv_rn(warp_sum(sum.x + sum.y), (float)mine) : 0.0f;
+  float2 dist = both(0.0f);
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    if (j * span + (int)threadIdx.x >= nvec) continue;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 d = add2(f[j][i], both(-wm));
+      dist = fma2(d, d, dist);
+    }
+  }
+  const float wd = warp_sum(dist.x + dist.y);
+  if (lane == 0) red[warp] = Share{(float)mine, wm, wd};
+  __syncthreads();
+  const Share w = lane < W ? red[lane] : Share{0.0f, 0.0f, 0.0f};
+  const float m = warp_sum(w.n * w.mean) * inv_cols;
+  const float var = warp_sum(fmaf(w.n * (w.mean - m), w.mean - m, w.dist)) * inv_cols;
+  const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(var, eps)));
+  if (threadIdx.x == 0) {
+    if (mean) mean[blockIdx.x] = m;
+    if (rstd) rstd[blockIdx.x] = r;
+  }
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int c = j * span + threadIdx.x;
+    if (c >= nvec) continue;
+    float2 gf[4], bf[4];
+    unpack(g[j], gf);
+    unpack(b[j], bf);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[j][i] = fma2(mul2(add2(f[j][i], both(-m)), both(r)), gf[i], bf[i]);
+    V o;
+    pack(f[j], o);
+    y[base + c] = o;
   }
 }
 
@@ -287,42 +525,27 @@ __global__ void __launch_bounds__(1024) column_sums_kernel(const float* __restri
   const float* part = partial + (int64_t)blockIdx.y * nb * cols;
   float s = 0.0f;
   if (c < cols)
-#pragma unroll 10
+#pragma unroll 5
     for (int b = warp; b < nb; b += 32) s += __ldcg(part + (int64_t)b * cols + c);
   red[warp][lane] = s;
   __syncthreads();
   // lane w of warp c adds warp w's share of column c
-  s = red[lane][warp];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  s = warp_sum(red[lane][warp]);
   const int col = blockIdx.x * 32 + warp;
   if (lane == 0 && col < cols) (blockIdx.y ? dbeta : dgamma)[col] = s;
 }
 
-// Few rows: as many warps a row as its vectors fill, for the latency.  Many rows: two vectors a
-// lane, at least eight warps a block.
-NormGrid forward_grid(int64_t rows, int nvec, bool f32) {
-  NormGrid g;
-  const bool few = rows <= 2 * (int64_t)num_sms();
-  g.J = nvec > 1024 ? 4 : nvec > 512 || (!few && !f32 && nvec > 32) ? 2 : 1;
-  g.W = (nvec + 32 * g.J - 1) / (32 * g.J);
-  g.G = few ? 1 : std::max(1, 8 / g.W);
-  const int64_t need = (rows + g.G - 1) / g.G;
-  const int64_t most = (int64_t)num_sms() * std::max(1, (!f32 && g.J <= 2 ? 32 : 16) / (g.W * g.G));
-  g.blocks = (int)std::min(need, most);
-  return g;
-}
+// At most kPartBlocks blocks in the backward pass, which the workspace's size goes by: it does not depend on
+// the device.
+constexpr int kPartBlocks = 192;
 
-// At most kPartBlocks blocks, which the workspace's size goes by: it does not depend on the device.
-constexpr int kPartBlocks = 320;
-NormGrid backward_grid(int64_t rows, int nvec) {
+// Two vectors a lane (one for rows of a warp, four above 8192 columns), 16 warps a block.
+NormGrid row_grid(int64_t rows, int nvec) {
   NormGrid g;
-  g.J = nvec > 1024 ? 4 : nvec > 256 ? 2 : 1;
+  g.J = nvec > 1024 ? 4 : nvec > 32 ? 2 : 1;
   g.W = (nvec + 32 * g.J - 1) / (32 * g.J);
-  g.G = std::max(1, 8 / g.W);
-  const int64_t need = (rows + g.G - 1) / g.G;
-  const int64_t most = std::min<int64_t>(kPartBlocks, (int64_t)num_sms() * std::max(1, 16 / (g.W * g.G)));
-  g.blocks = (int)std::max<int64_t>(1, std::min(need, most));
+  g.G = (int)std::min<int64_t>(16 / g.W, std::max<int64_t>(1, rows / num_sms()));   // every SM before every group
+  g.blocks = (int)std::min<int64_t>((rows + g.G - 1) / g.G, std::min(num_sms(), kPartBlocks));
   return g;
 }
 
@@ -330,29 +553,39 @@ template <typename V>
 cudaError_t launch_forward(const void* x, const void* residual, const void* gamma, const void* beta,
                            float eps, int64_t rows, int cols, void* h, void* y, float* mean,
                            float* rstd, cudaStream_t s) {
-  const NormGrid g = forward_grid(rows, cols / 8, sizeof(V) == 32);
-  auto k = g.J == 1 ? add_layernorm_kernel<V, 1> : g.J == 2 ? add_layernorm_kernel<V, 2>
-                                                            : add_layernorm_kernel<V, 4>;
-  return launch_pdl(k, dim3((unsigned)g.blocks), dim3(g.W * g.G * 32), 0, s, static_cast<const V*>(x),
-                    static_cast<const V*>(residual), static_cast<const V*>(gamma),
-                    static_cast<const V*>(beta), eps, rows, cols, g.W, g.G, static_cast<V*>(h),
-                    static_cast<V*>(y), mean, rstd);
+  const V *xv = static_cast<const V*>(x), *rv = static_cast<const V*>(residual);
+  const V *gv = static_cast<const V*>(gamma), *bv = static_cast<const V*>(beta);
+  V *hv = static_cast<V*>(h), *yv = static_cast<V*>(y);
+  const int nvec = cols / 8;
+  if (rows <= 2 * (int64_t)num_sms()) {   // no row of a block would be read ahead
+    const int J = nvec > 1024 ? 2 : 1, threads = (nvec + 32 * J - 1) / (32 * J) * 32;
+    auto k = J == 1 ? add_layernorm_row_kernel<V, 1> : add_layernorm_row_kernel<V, 2>;
+    return launch_pdl(k, dim3((unsigned)rows), dim3(threads), 0, s, xv, rv, gv, bv, eps, cols, hv, yv, mean, rstd);
+  }
+  const NormGrid g = row_grid(rows, nvec);
+  const size_t slot = 2 * (size_t)cols * (sizeof(V) / 8);
+  const int slots = ring_slots(g.G, slot);
+  auto k = g.J == 1 ? add_layernorm_kernel<V, 1> : g.J == 2 ? add_layernorm_kernel<V, 2> : add_layernorm_kernel<V, 4>;
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostRing);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k, dim3((unsigned)g.blocks), dim3(g.W * g.G * 32), ring_bytes(g.G, slots, slot), s, xv, rv, gv, bv, eps, rows,
+                    cols, g.W, g.G, slots, hv, yv, mean, rstd);
 }
 
 template <typename V>
 cudaError_t launch_backward(const void* dy, const void* dh, const void* h, const float* mean,
                             const float* rstd, const void* gamma, int64_t rows, int cols, void* dx,
                             float* dgamma, float* dbeta, void* workspace, cudaStream_t s) {
-  const NormGrid g = backward_grid(rows, cols / 8);
-  constexpr bool kBf16 = sizeof(V) == 16;
-  auto k = g.J == 1   ? add_layernorm_backward_kernel<V, 1, true>
-           : g.J == 2 ? add_layernorm_backward_kernel<V, 2, kBf16>
-                      : add_layernorm_backward_kernel<V, 4, false>;
-  const cudaError_t e = launch_pdl(
-      k, dim3(g.blocks), dim3(g.W * g.G * 32), g.G > 1 ? sizeof(float) * (size_t)cols : 0, s,
-      static_cast<const V*>(dy), static_cast<const V*>(dh), static_cast<const V*>(h), mean, rstd,
-      static_cast<const V*>(gamma), rows, cols, g.W, g.G, static_cast<V*>(dx), dbeta != nullptr,
-      static_cast<float4*>(workspace));
+  const NormGrid g = row_grid(rows, cols / 8);
+  const size_t slot = 3 * (size_t)cols * (sizeof(V) / 8);
+  const int slots = ring_slots(g.G, slot);
+  auto k = g.J == 1 ? add_layernorm_backward_kernel<V, 1> : g.J == 2 ? add_layernorm_backward_kernel<V, 2>
+                                                                     : add_layernorm_backward_kernel<V, 4>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostRing);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(k, dim3(g.blocks), dim3(g.W * g.G * 32), ring_bytes(g.G, slots, slot), s, static_cast<const V*>(dy),
+                 static_cast<const V*>(dh), static_cast<const V*>(h), mean, rstd, static_cast<const V*>(gamma), rows, cols, g.W, g.G,
+                 slots, static_cast<V*>(dx), dbeta != nullptr, static_cast<float4*>(workspace));
   if (e != cudaSuccess) return e;
   return launch_pdl(column_sums_kernel, dim3((unsigned)((cols + 31) / 32), dbeta ? 2 : 1), dim3(1024),
                     0, s, static_cast<const float*>(workspace), g.blocks, cols, dgamma, dbeta);

@@ -1,5 +1,5 @@
-// What the row kernels (norm_mx.cu, layer_norm.cu, tokens.cu) share: vectors of eight elements and sums
-// over the threads of a row.
+// What the row kernels (norm_mx.cu, tokens.cu) share: vectors of eight BF16 elements and sums over the threads
+// of a row.
 #pragma once
 #include "common.cuh"
 
@@ -22,20 +22,6 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
     w[i] = *reinterpret_cast<const uint32_t*>(&b);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// Eight FP32 elements, as uint4 holds eight BF16 ones.
-struct F32x8 {
-  float4 a, b;
-};
-__device__ __forceinline__ void unpack8(const F32x8& q, float (&f)[8]) {
-  f[0] = q.a.x; f[1] = q.a.y; f[2] = q.a.z; f[3] = q.a.w;
-  f[4] = q.b.x; f[5] = q.b.y; f[6] = q.b.z; f[7] = q.b.w;
-}
-__device__ __forceinline__ void pack(const float (&f)[8], uint4& q) { q = pack8(f); }
-__device__ __forceinline__ void pack(const float (&f)[8], F32x8& q) {
-  q.a = make_float4(f[0], f[1], f[2], f[3]);
-  q.b = make_float4(f[4], f[5], f[6], f[7]);
 }
 
 // Sum of one value per thread over the W warps of a row group, the same on every thread and in a
