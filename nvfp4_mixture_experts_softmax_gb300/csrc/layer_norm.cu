@@ -74,8 +74,11 @@ struct Ring {
   }
 };
 
-int ring_slots(int G, size_t slot_bytes) {
-  return (int)std::max<size_t>(1, std::min<size_t>(8, 208 * 1024 / G / slot_bytes));
+// Slots of a group's ring: as many as keep `want` bytes an SM under way, `least` of them where they fit.  More do harm:
+// with 192 KB of reads ahead the forward pass of 16384 x 4096 takes 92 us, with 96 KB 82 us (with 64 KB 105).
+int ring_slots(int G, size_t slot_bytes, size_t want, int least) {
+  const int fit = (int)(208 * 1024 / G / slot_bytes);
+  return std::max(1, std::min({8, fit, std::max(least, (int)(want / G / slot_bytes))}));
 }
 size_t ring_bytes(int G, int slots, size_t slot_bytes) { return 2048 + (size_t)G * slots * slot_bytes; }
 
@@ -109,8 +112,8 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-// The sum over the first 16 lanes (the rows' W <= 16 warps), on each of them and on the others.
-__device__ __forceinline__ float half_warp_sum(float v) {
+// The sum over the first 16 lanes, one for each of the row's warps, on all lanes.
+__device__ __forceinline__ float warps_sum(float v) {
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return __shfl_sync(0xffffffffu, v, 0);
@@ -174,7 +177,7 @@ __global__ void __launch_bounds__(512, 1) add_layernorm_kernel(
     int64_t rows, int cols, int W, int G, int slots, V* h, V* y, float* mean, float* rstd) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Share red[2][16];
-  constexpr bool kWide = J > 2;   // gamma and beta are read again for each row
+  constexpr bool kWide = J > 3;   // gamma and beta are read again for each row
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = warp / W, wrow = warp - group * W;
   const int t = wrow * 32 + lane, span = W * 32;   // thread of the row, vectors apart
   const int nvec = cols / 8;
@@ -248,8 +251,8 @@ __global__ void __launch_bounds__(512, 1) add_layernorm_kernel(
     if (ring.issuer && n > 0 && slots > 1 && n - 1 + slots < count)   // the slot of the row before
       ring.fetch<2>(s ? s - 1 : slots - 1, src, tensors, row0 + (int64_t)(n - 1 + slots) * step);
     const Share w = lane < W ? red[par][group * W + lane] : Share{0.0f, 0.0f, 0.0f};
-    const float m = half_warp_sum(w.n * w.mean) * inv_cols;
-    const float var = half_warp_sum(fmaf(w.n * (w.mean - m), w.mean - m, w.dist)) * inv_cols;
+    const float m = warps_sum(w.n * w.mean) * inv_cols;
+    const float var = warps_sum(fmaf(w.n * (w.mean - m), w.mean - m, w.dist)) * inv_cols;
     const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(var, eps)));
     if (t == 0) {
       if (mean) mean[row0 + n * step] = m;
@@ -363,7 +366,7 @@ __global__ void __launch_bounds__(512, 1) add_layernorm_backward_kernel(
     if (ring.issuer && n > 0 && slots > 1 && n - 1 + slots < count)   // the slot of the row before
       ring.fetch<3>(s ? s - 1 : slots - 1, src, tensors, row0 + (int64_t)(n - 1 + slots) * step);
     const float2 w = lane < W ? red[par][group * W + lane] : make_float2(0.0f, 0.0f);
-    const float ma = half_warp_sum(w.x) * inv_cols, mn = half_warp_sum(w.y) * inv_cols;
+    const float ma = warps_sum(w.x) * inv_cols, mn = warps_sum(w.y) * inv_cols;
     const int64_t base = (row0 + n * step) * nvec;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
@@ -539,10 +542,12 @@ __global__ void __launch_bounds__(1024) column_sums_kernel(const float* __restri
 // the device.
 constexpr int kPartBlocks = 192;
 
-// Two vectors a lane (one for rows of a warp, four above 8192 columns), 16 warps a block.
+// 16 warps a block, two vectors a lane; four above 8192 columns, one up to 256.  A row takes 1.1 us from its arrival to
+// its last store, which a second group hides; of 4104 to 6144 columns two vectors a lane would leave one group of 9 to 12
+// warps, three leave two of 6 to 8 (12000 x 5120: 93 and 82 us, backward 104 and 93).
 NormGrid row_grid(int64_t rows, int nvec) {
   NormGrid g;
-  g.J = nvec > 1024 ? 4 : nvec > 32 ? 2 : 1;
+  g.J = nvec > 1024 ? 4 : nvec <= 32 ? 1 : nvec > 512 && nvec <= 768 ? 3 : 2;
   g.W = (nvec + 32 * g.J - 1) / (32 * g.J);
   g.G = (int)std::min<int64_t>(16 / g.W, std::max<int64_t>(1, rows / num_sms()));   // every SM before every group
   g.blocks = (int)std::min<int64_t>((rows + g.G - 1) / g.G, std::min(num_sms(), kPartBlocks));
@@ -564,8 +569,11 @@ cudaError_t launch_forward(const void* x, const void* residual, const void* gamm
   }
   const NormGrid g = row_grid(rows, nvec);
   const size_t slot = 2 * (size_t)cols * (sizeof(V) / 8);
-  const int slots = ring_slots(g.G, slot);
-  auto k = g.J == 1 ? add_layernorm_kernel<V, 1> : g.J == 2 ? add_layernorm_kernel<V, 2> : add_layernorm_kernel<V, 4>;
+  const int slots = ring_slots(g.G, slot, 120 * 1024, 2);
+  auto k = g.J == 1   ? add_layernorm_kernel<V, 1>
+           : g.J == 2 ? add_layernorm_kernel<V, 2>
+           : g.J == 3 ? add_layernorm_kernel<V, 3>
+                      : add_layernorm_kernel<V, 4>;
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostRing);
   if (e != cudaSuccess) return e;
   return launch_pdl(k, dim3((unsigned)g.blocks), dim3(g.W * g.G * 32), ring_bytes(g.G, slots, slot), s, xv, rv, gv, bv, eps, rows,
@@ -578,9 +586,11 @@ cudaError_t launch_backward(const void* dy, const void* dh, const void* h, const
                             float* dgamma, float* dbeta, void* workspace, cudaStream_t s) {
   const NormGrid g = row_grid(rows, cols / 8);
   const size_t slot = 3 * (size_t)cols * (sizeof(V) / 8);
-  const int slots = ring_slots(g.G, slot);
-  auto k = g.J == 1 ? add_layernorm_backward_kernel<V, 1> : g.J == 2 ? add_layernorm_backward_kernel<V, 2>
-                                                                     : add_layernorm_backward_kernel<V, 4>;
+  const int slots = ring_slots(g.G, slot, 144 * 1024, 3);
+  auto k = g.J == 1   ? add_layernorm_backward_kernel<V, 1>
+           : g.J == 2 ? add_layernorm_backward_kernel<V, 2>
+           : g.J == 3 ? add_layernorm_backward_kernel<V, 3>
+                      : add_layernorm_backward_kernel<V, 4>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostRing);
   if (e != cudaSuccess) return e;
   e = launch_pdl(k, dim3(g.blocks), dim3(g.W * g.G * 32), ring_bytes(g.G, slots, slot), s, static_cast<const V*>(dy),
