@@ -43,9 +43,7 @@ constexpr int kHalf = 128;                      // rows of A and of B a CTA hold
 constexpr int kBlockK = 64;
 constexpr int kOperandBytes = kHalf * kBlockK * 2;
 constexpr int kChunkBytes = kBlockK * 128;      // MN-major: 64 columns (128 bytes) of 64 rows
-constexpr int kStages = 5;
 constexpr int kStageBytes = 2 * kOperandBytes;
-constexpr int kSlabBytes = 32 * 128;            // of an epilogue warp: its 32 rows by 128 bytes on their way out
 constexpr int kEpiWarps = 8, kCopyWarp = 8, kMmaWarp = 9, kZeroWarp = 10, kCopyWarp2 = 11;
 constexpr int kThreads = 12 * 32;
 constexpr int kMaxExperts = 1024;
@@ -57,11 +55,20 @@ constexpr uint64_t kLimitNs = 2000000000ull;
 // rows (32 additions), which the epilogue adds up in registers, rounding.
 constexpr int kChainRows = 512;
 
-constexpr int kSlabOff = kStages * kStageBytes;
-constexpr int kBarOff = kSlabOff + kEpiWarps * kSlabBytes;
-constexpr int kTableOff = kBarOff + 256;
-constexpr size_t kSmemBytes = 1024 + kTableOff + 2 * (kMaxExperts + 1) * sizeof(int32_t) + 8;
-static_assert(kSmemBytes <= 232448, "shared memory");
+// Shared memory: the stages, a slab for each epilogue warp (its 32 rows by 64 or 128 bytes on their way out), barriers,
+// segment tables.  The row modes take six stages and 64-byte slabs (1505 us against 1548 for the forward pass of
+// 65536 rows of 4096 x 1536), the weights' gradients, whose FP32 output is three quarters of their traffic, five and 128-byte
+// slabs (1972 against 2040 us).
+template <Mode kMode>
+struct Layout {
+  static constexpr int kStages = kMode == kWgrad ? 5 : 6;
+  static constexpr int kSlabWidth = kMode == kWgrad ? 128 : 64;   // bytes of a row
+  static constexpr int kSlabOff = kStages * kStageBytes;
+  static constexpr int kBarOff = kSlabOff + kEpiWarps * 32 * kSlabWidth;
+  static constexpr int kTableOff = kBarOff + 256;
+  static constexpr size_t kBytes = 1024 + kTableOff + 2 * (kMaxExperts + 1) * sizeof(int32_t) + 8;
+  static_assert(kBytes <= 232448 && (3 * kStages + 4) * 8 + 12 <= 256, "shared memory");
+};
 
 constexpr bool a_mn_major(Mode m) { return m == kWgrad; }
 constexpr bool b_mn_major(Mode m) { return m == kDgradAct || m == kDgradRows || m == kWgrad; }
@@ -226,12 +233,13 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 __device__ __forceinline__ float low_bf16(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high_bf16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// Slabs: a lane writes 128 bytes of its row (16-byte pieces in the 128-byte swizzle, so that the lanes' pieces lie in
+// Slabs: a lane writes its row's 64 or 128 bytes (16-byte pieces in the swizzle of that width, so that the lanes' pieces lie in
 // different banks), then one lane stores the whole by TMA: whole lines to L2, where 32 bytes a lane and
 // row went at 11 bytes a cycle and SM.
+template <int kWidth>
 __device__ __forceinline__ void slab_put(uint32_t slab, int lane, int piece, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(slab + lane * 128 + ((piece ^ (lane & 7)) << 4)), "r"(a), "r"(b),
-               "r"(c), "r"(d)
+  const int at = kWidth == 128 ? piece ^ (lane & 7) : piece ^ ((lane >> 1) & 3);
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(slab + lane * kWidth + (at << 4)), "r"(a), "r"(b), "r"(c), "r"(d)
                : "memory");
 }
 // The slab may be written again once the copies before have read it.
@@ -269,10 +277,15 @@ __device__ __forceinline__ void slab_store_3d(uint32_t slab, int lane, const CUt
 __device__ __forceinline__ void store_bf16x64(const uint32_t (&w)[32], uint32_t slab, int lane, const CUtensorMap* map, int x, int y,
                                               bool whole, __nv_bfloat16* row, bool live, int cols) {
   if (whole) {
-    slab_begin(lane);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) slab_put(slab, lane, i, w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-    slab_store_2d(slab, lane, map, x, y);
+    for (int c = 0; c < 2; ++c) {
+      if (32 * c >= cols) break;
+      slab_begin(lane);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        slab_put<64>(slab, lane, i, w[16 * c + 4 * i], w[16 * c + 4 * i + 1], w[16 * c + 4 * i + 2], w[16 * c + 4 * i + 3]);
+      slab_store_2d(slab, lane, map, x + 32 * c, y);
+    }
   } else if (live) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -377,9 +390,11 @@ __device__ __forceinline__ int reduction_rows(const Args& p, const int32_t* s_of
 template <Mode kMode>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     experts_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args p) {
+  using L = Layout<kMode>;
+  constexpr int kStages = L::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBarOff);   // [stage], CTA 0's: both CTAs' data has landed
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);   // [stage], CTA 0's: both CTAs' data has landed
   uint64_t* empty = full + kStages;                               // [stage]: the MMAs have read it
   uint64_t* tail = empty + kStages;                               // [stage]: data that is to be zeroed has landed
   uint64_t* acc_full = tail + kStages;                            // [2]
@@ -387,9 +402,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
   volatile uint32_t* s_abort = tmem_slot + 1;
   int32_t* s_bad = reinterpret_cast<int32_t*>(tmem_slot + 2);
-  int32_t* s_off = reinterpret_cast<int32_t*>(smem + kTableOff);
+  int32_t* s_off = reinterpret_cast<int32_t*>(smem + L::kTableOff);
   int32_t* s_tile = s_off + kMaxExperts + 1;
-  static_assert((3 * kStages + 4) * 8 + 12 <= 256, "barrier area");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -581,7 +595,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ---------------- epilogue: a row a thread, half of the columns a warp ----------------
     const int quad = warp & 3, half = warp >> 2;
     const int slab_row = (int)rank * kHalf + quad * 32;       // first of the warp's rows of the tile
-    const uint32_t slab = smem0 + kSlabOff + warp * kSlabBytes;
+    const uint32_t slab = smem0 + L::kSlabOff + warp * 32 * L::kSlabWidth;
     uint32_t unit = 0;
     bool ok = true;
     for (int item = first; item < total && ok; item += step) {
@@ -619,8 +633,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const float* f = sum + c * 32 + 4 * i;
-            if (nch == 0) slab_put(slab, lane, i, 0u, 0u, 0u, 0u);   // a segment without rows
-            else slab_put(slab, lane, i, __float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+            if (nch == 0) slab_put<128>(slab, lane, i, 0u, 0u, 0u, 0u);   // a segment without rows
+            else slab_put<128>(slab, lane, i, __float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
           }
           slab_store_3d(slab, lane, maps.out + t.mat, col, t.m0 + slab_row, t.seg, p.accumulate);
         }
@@ -718,25 +732,23 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return fn;
 }
 
-// BF16 [d2][d1][d0] (d2 = 0: two dimensions), boxes of 64 columns by `rows`.
-// kF32: the same of FP32, 32 columns.
-template <bool kF32 = false>
-bool make_map(CUtensorMap* m, const void* ptr, int64_t d0, int64_t d1, int64_t d2, int rows) {
-  constexpr int kSize = kF32 ? 4 : 2;
+// [d2][d1][d0] (d2 = 0: two dimensions) of BF16, or FP32 if kSize is 4; boxes of `width` bytes by `rows`, swizzled.
+template <int kSize = 2>
+bool make_map(CUtensorMap* m, const void* ptr, int64_t d0, int64_t d1, int64_t d2, int rows, int width = 128) {
   const cuuint64_t dims[3] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2};
   const cuuint64_t strides[2] = {(cuuint64_t)d0 * kSize, (cuuint64_t)d0 * d1 * kSize};
-  const cuuint32_t box[3] = {128 / kSize, (cuuint32_t)rows, 1}, estr[3] = {1, 1, 1};
-  return encoder()(m, kF32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d2 ? 3 : 2, const_cast<void*>(ptr), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const cuuint32_t box[3] = {(cuuint32_t)(width / kSize), (cuuint32_t)rows, 1}, estr[3] = {1, 1, 1};
+  return encoder()(m, kSize == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d2 ? 3 : 2, const_cast<void*>(ptr), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, width == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <Mode kMode>
 cudaError_t launch(const Maps& maps, const Args& a, int64_t most_items, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(experts_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+  cudaError_t e = cudaFuncSetAttribute(experts_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<kMode>::kBytes);
   if (e != cudaSuccess) return e;
   const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(most_items, num_sms() / 2));
-  return launch_pdl(experts_kernel<kMode>, dim3(2 * pairs), dim3(kThreads), kSmemBytes, s, maps, a);
+  return launch_pdl(experts_kernel<kMode>, dim3(2 * pairs), dim3(kThreads), Layout<kMode>::kBytes, s, maps, a);
 }
 
 int div_up(int64_t a, int b) { return (int)((a + b - 1) / b); }
@@ -793,7 +805,7 @@ bool row_outputs(Maps& m, Args& a, int64_t R, int64_t cols, void* o0, void* o1, 
   void* const o[3] = {o0, o1, o2};
   for (int i = 0; i < 3; ++i) {
     a.o[i] = static_cast<__nv_bfloat16*>(o[i]);
-    if (o[i] && !make_map(&m.out[i], o[i], cols, R, 0, 32)) return false;
+    if (o[i] && !make_map(&m.out[i], o[i], cols, R, 0, 32, 64)) return false;
   }
   return true;
 }
@@ -922,8 +934,8 @@ int moe_experts_weight_grad(const void* rows, const void* dout, const void* h, c
   Maps m = {};
   const bool ok = make_map(&m.m[0], sh.gated ? dg : du, I, R, 0, kBlockK) && make_map(&m.m[1], rows, H, R, 0, kBlockK) &&
                   make_map(&m.m[2], du, I, R, 0, kBlockK) && make_map(&m.m[3], dout, H, R, 0, kBlockK) &&
-                  make_map(&m.m[4], h, I, R, 0, kBlockK) && make_map<true>(&m.out[0], sh.gated ? dw_gate : dw_up, H, I, E, 32) &&
-                  make_map<true>(&m.out[1], dw_up, H, I, E, 32) && make_map<true>(&m.out[2], dw_down, I, H, E, 32);
+                  make_map(&m.m[4], h, I, R, 0, kBlockK) && make_map<4>(&m.out[0], sh.gated ? dw_gate : dw_up, H, I, E, 32) &&
+                  make_map<4>(&m.out[1], dw_up, H, I, E, 32) && make_map<4>(&m.out[2], dw_down, I, H, E, 32);
   if (!ok) return MOE_ERR_CUDA;
   Args a = base_args(sh, offsets, workspace, 0.0f, 0.0f);
   a.M = (int)H;
