@@ -22,9 +22,10 @@ namespace nvfp4moe {
 
 namespace {
 
-constexpr int kSortWarps = 32;
-constexpr int kPerWarp = 128;                       // assignments of a warp, in groups of 32
-constexpr int kChunk = kSortWarps * kPerWarp;       // 4096
+constexpr int kPerWarp = 128;                 // assignments of a warp, in groups of 32
+constexpr int kOneWarps = 32;                 // of the only block
+constexpr int kChunkWarps = 8;                // of one of many
+constexpr int kChunk = kChunkWarps * kPerWarp;
 
 // Expert of assignment a, or -1 if it does not count; an id that is neither an expert nor -1 raises
 // the status.  A masked token's ids are not read.
@@ -32,7 +33,7 @@ __device__ __forceinline__ int expert_of(const int32_t* __restrict__ ids,
                                          const uint8_t* __restrict__ mask, int64_t a, int64_t R, int k,
                                          int E, int32_t* status) {
   if (a >= R) return -1;
-  if (mask && mask[a / k] == 0) return -1;
+  if (mask && mask[(uint32_t)a / (uint32_t)k] == 0) return -1;
   const int e = __ldg(ids + a);
   if ((unsigned)e < (unsigned)E) return e;
   if (e != -1) set_status(status, MOE_ERR_INVALID_ARG);
@@ -40,7 +41,7 @@ __device__ __forceinline__ int expert_of(const int32_t* __restrict__ ids,
 }
 
 // Histogram of a chunk; block 0 also clears the scan's block count.
-__global__ void __launch_bounds__(kSortWarps * 32) sort_count_kernel(
+__global__ void __launch_bounds__(kChunkWarps * 32) sort_count_kernel(
     const int32_t* __restrict__ ids, const uint8_t* __restrict__ mask, int64_t R, int k, int E,
     int32_t* __restrict__ hist, int32_t* __restrict__ scan_count, int32_t* status) {
   __shared__ int32_t s_cnt[1024];
@@ -51,17 +52,17 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_count_kernel(
   __syncthreads();
   const int64_t a0 = (int64_t)blockIdx.x * kChunk + threadIdx.x;
 #pragma unroll
-  for (int i = 0; i < kChunk / 1024; ++i) {
-    const int e = expert_of(ids, mask, a0 + i * 1024, R, k, E, status);
+  for (int i = 0; i < kChunk / (kChunkWarps * 32); ++i) {
+    const int e = expert_of(ids, mask, a0 + i * kChunkWarps * 32, R, k, E, status);
     if (e >= 0) atomicAdd(&s_cnt[e], 1);
   }
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += blockDim.x) hist[(int64_t)blockIdx.x * E + e] = s_cnt[e];
 }
 
-// kOne: the only block, which also sums the counts.  Dynamic shared memory: kSortWarps * E uint16.
-template <bool kOne>
-__global__ void __launch_bounds__(kSortWarps * 32) sort_place_kernel(
+// kWarps warps a block; kOne: the only block, which also sums the counts.  Dynamic shared memory: kWarps * E uint16.
+template <int kWarps, bool kOne>
+__global__ void __launch_bounds__(kWarps * 32) sort_place_kernel(
     const int32_t* __restrict__ ids, const uint8_t* __restrict__ mask, int64_t R, int k, int E,
     const int32_t* __restrict__ base, int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
     int32_t* __restrict__ perm_src, int32_t* __restrict__ inv, int32_t* status) {
@@ -70,14 +71,14 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_place_kernel(
   __shared__ int32_t s_scan[32];
   __shared__ int32_t s_total;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < (kSortWarps * E + 1) / 2; i += blockDim.x)
+  for (int i = threadIdx.x; i < (kWarps * E + 1) / 2; i += blockDim.x)
     reinterpret_cast<uint32_t*>(s_rank)[i] = 0u;
   griddep_wait();
   griddep_launch();
   if (kOne && threadIdx.x == 0) *status = 0;
   __syncthreads();
   uint16_t* mine = s_rank + warp * E;
-  const int64_t a0 = (int64_t)blockIdx.x * kChunk + warp * kPerWarp + lane;
+  const int64_t a0 = (int64_t)blockIdx.x * (kWarps * kPerWarp) + warp * kPerWarp + lane;
   int ex[kPerWarp / 32], rank[kPerWarp / 32];
 #pragma unroll
   for (int i = 0; i < kPerWarp / 32; ++i) ex[i] = expert_of(ids, mask, a0 + i * 32, R, k, E, status);
@@ -91,26 +92,27 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_place_kernel(
     __syncwarp();
   }
   __syncthreads();
-  const int e = threadIdx.x;   // (E <= 1024 threads)
-  int32_t sum = 0;
-  if (e < E)
-    for (int w = 0; w < kSortWarps; ++w) {
-      const int c = s_rank[w * E + e];
-      s_rank[w * E + e] = (uint16_t)sum;
-      sum += c;
+  if (!kOne && threadIdx.x == 0) s_total = __ldg(offsets + E);
+  for (int e = threadIdx.x; e < (kOne ? 1024 : E); e += kWarps * 32) {   // (kOne: one round of 1024 threads)
+    int32_t sum = 0;
+    if (e < E)
+      for (int w = 0; w < kWarps; ++w) {
+        const int c = s_rank[w * E + e];
+        s_rank[w * E + e] = (uint16_t)sum;
+        sum += c;
+      }
+    if constexpr (kOne) {
+      int32_t total;
+      const int32_t off = block_exclusive_scan(sum, s_scan, total);
+      if (e < E) {
+        s_base[e] = off;
+        counts[e] = sum;
+        offsets[e] = off;
+      }
+      if (e == 0) offsets[E] = s_total = total;
+    } else {
+      s_base[e] = __ldg(offsets + e) + __ldg(base + (int64_t)blockIdx.x * E + e);
     }
-  if constexpr (kOne) {
-    int32_t total;
-    const int32_t off = block_exclusive_scan(sum, s_scan, total);
-    if (e < E) {
-      s_base[e] = off;
-      counts[e] = sum;
-      offsets[e] = off;
-    }
-    if (e == 0) offsets[E] = s_total = total;
-  } else {
-    if (e < E) s_base[e] = __ldg(offsets + e) + __ldg(base + (int64_t)blockIdx.x * E + e);
-    if (e == 0) s_total = __ldg(offsets + E);
   }
   __syncthreads();
   const int64_t total = s_total;
@@ -121,7 +123,7 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_place_kernel(
     int32_t p = -1;
     if (ex[i] >= 0) {
       p = s_base[ex[i]] + mine[ex[i]] + rank[i];
-      perm_src[p] = (int32_t)(a / k);
+      perm_src[p] = (int32_t)((uint32_t)a / (uint32_t)k);
     }
     inv[a] = p;
     if (a >= total) perm_src[a] = -1;   // (rows behind the last expert's)
@@ -231,7 +233,7 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(
     return;
   }
   const uint4* src = rows + p * nvec;
-  const uint4* d = dy + a / k * nvec;
+  const uint4* d = dy + (int64_t)((uint32_t)a / (uint32_t)k) * nvec;
   uint4* dst = drows + p * nvec;
   const float wa = __ldg(w + a);
   float s = 0.0f;
@@ -277,7 +279,8 @@ int routing_check(int64_t T, int32_t k, int64_t cols, int64_t row_bytes) {
   return MOE_OK;
 }
 
-int chunks_of(int64_t R) { return (int)((R + kChunk - 1) / kChunk); }
+// Chunks, 1 if one block does it all.
+int chunks_of(int64_t R) { return R <= kOneWarps * kPerWarp ? 1 : (int)((R + kChunk - 1) / kChunk); }
 
 }  // namespace
 }  // namespace nvfp4moe
@@ -307,15 +310,16 @@ int moe_sort_tokens(const int32_t* topk_ids, const uint8_t* mask, int32_t T, int
   const int64_t R = (int64_t)T * k;
   const int n = chunks_of(R);
   int32_t* status = static_cast<int32_t*>(workspace);
-  const size_t smem = sizeof(uint16_t) * kSortWarps * E + 4;
-  // the most that any E needs, so that no call depends on an earlier one's setting
-  constexpr int kMost = sizeof(uint16_t) * kSortWarps * 1024 + 4;
-  auto place = n <= 1 ? sort_place_kernel<true> : sort_place_kernel<false>;
-  cudaError_t e = cudaFuncSetAttribute(place, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
-  if (e != cudaSuccess) return MOE_ERR_CUDA;
-  if (n <= 1) {
-    e = launch_pdl(place, dim3(1), dim3(kSortWarps * 32), smem, s, topk_ids, mask, R, (int)k, (int)E,
-                   (const int32_t*)nullptr, counts, offsets, perm_src, inv, status);
+  cudaError_t e = cudaSuccess;
+  if (n == 1) {
+    auto place = sort_place_kernel<kOneWarps, true>;
+    const size_t smem = sizeof(uint16_t) * kOneWarps * E + 4;
+    // above the default limit (static memory counts too): the most that any E needs, so that no call depends on another's
+    if (smem > 40 * 1024)
+      e = cudaFuncSetAttribute(place, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(uint16_t) * kOneWarps * 1024 + 4);
+    if (e == cudaSuccess)
+      e = launch_pdl(place, dim3(1), dim3(kOneWarps * 32), smem, s, topk_ids, mask, R, (int)k, (int)E, (const int32_t*)nullptr, counts,
+                     offsets, perm_src, inv, status);
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
   }
   int32_t* hist = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + 256);
@@ -324,12 +328,11 @@ int moe_sort_tokens(const int32_t* topk_ids, const uint8_t* mask, int32_t T, int
   int32_t* scratch = base + part;
   e = cudaMemsetAsync(status, 0, sizeof(int32_t), s);
   if (e == cudaSuccess)
-    e = launch_pdl(sort_count_kernel, dim3(n), dim3(kSortWarps * 32), 0, s, topk_ids, mask, R, (int)k, (int)E,
-                   hist, scratch, status);
+    e = launch_pdl(sort_count_kernel, dim3(n), dim3(kChunkWarps * 32), 0, s, topk_ids, mask, R, (int)k, (int)E, hist, scratch, status);
   if (e == cudaSuccess) e = launch_plan_scan(hist, n, E, base, counts, offsets, scratch, s);
   if (e == cudaSuccess)
-    e = launch_pdl(place, dim3(n), dim3(kSortWarps * 32), smem, s, topk_ids, mask, R, (int)k, (int)E,
-                   (const int32_t*)base, counts, offsets, perm_src, inv, status);
+    e = launch_pdl(sort_place_kernel<kChunkWarps, false>, dim3(n), dim3(kChunkWarps * 32), sizeof(uint16_t) * kChunkWarps * E + 4, s,
+                   topk_ids, mask, R, (int)k, (int)E, (const int32_t*)base, counts, offsets, perm_src, inv, status);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
