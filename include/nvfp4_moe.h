@@ -264,7 +264,8 @@ int moe_add_rmsnorm_backward(const void* dy, const void* dh, const void* h, cons
  *   16-byte aligned, cols a multiple of 8, at most 16384; mean, rstd: NULL or device FP32 [rows] (m and s).
  *   residual and h are both given or both NULL (then h is x itself); beta NULL: none.  h may be the buffer
  *   of residual or of x (in place); no other two buffers may overlap.
- * A NaN or infinity makes its own row NaN.  No workspace, one launch.  rows == 0 is MOE_OK. */
+ * A NaN or infinity makes its own row NaN; squared distances are summed in FP32, so rows that spread over more than
+ * 2^63 overflow (s = 0).  No workspace, one launch.  rows == 0 is MOE_OK. */
 #define MOE_ROWS_F32 1u
 int moe_add_layernorm(const void* x, const void* residual, const void* gamma, const void* beta,
                       float eps, int64_t rows, int64_t cols, uint32_t flags, void* h, void* y,
@@ -314,7 +315,8 @@ int moe_plan(const float* logits, int32_t T, int32_t E, int32_t k, int32_t* topk
  * of dy[t] and rows[inv[t*k+j]], 0 without a row.  drows may be the buffer of rows; rows of drows that no
  * assignment names stay as they were.
  * In all three an inv outside [0, R) stands for no row (its weight is not read), and two assignments may
- * not name the same row.  x, y, rows 16-byte aligned, the rest 4.  One launch each, no workspace.
+ * not name the same row.  x, y, rows 16-byte aligned, the rest 4; but for drows no output may overlap an
+ * input.  One launch each, no workspace.
  * ------------------------------------------------------------------------------------------- */
 size_t moe_sort_tokens_workspace_size(int32_t T, int32_t E, int32_t k);
 int moe_sort_tokens(const int32_t* topk_ids, const uint8_t* mask, int32_t T, int32_t E, int32_t k,
@@ -347,7 +349,7 @@ int moe_combine_rows_backward(const void* dy, const void* rows, const int32_t* i
  * add; the weights' gradients are cut into chains of 64 such additions.  All sums run in a fixed order.
  * Rows from offsets[E] on are neither used (they may hold anything) nor written; NaN and infinities
  * stay in their row, in the weights' gradients in their segment.
- * H, I multiples of 32, at most 65536; E <= 1024; R < 2^31.  Inputs 16-byte aligned, outputs, g and u 32-byte;
+ * H, I multiples of 32, at most 65536; E <= 1024; R < 2^31 - 256.  Inputs 16-byte aligned, outputs, g and u 32-byte;
  * no output may overlap an input.  workspace: 256-byte aligned, its first word the device status; 256 bytes,
  * for a forward call without h moe_experts_workspace_size(R, I).  Two launches, the weights' gradients one.
  * ------------------------------------------------------------------------------------------- */

@@ -772,7 +772,7 @@ int check_shape(const int32_t* offsets, int64_t R, int32_t E, int64_t H, int64_t
   if (sh.act < 0) return MOE_ERR_INVALID_ARG;
   if ((sh.act == kActSwigluClamp || sh.act == kActSwigluOai) && !(std::isfinite(limit) && limit >= 0.0f)) return MOE_ERR_INVALID_ARG;
   if (sh.act == kActSwigluOai && !std::isfinite(alpha)) return MOE_ERR_INVALID_ARG;
-  if (E > kMaxExperts || R > INT32_MAX || H > (1 << 16) || I > (1 << 16)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (E > kMaxExperts || R > INT32_MAX - kTileM || H > (1 << 16) || I > (1 << 16)) return MOE_ERR_UNSUPPORTED_SHAPE;
   // tiles are counted in 32 bits
   const int64_t cols = std::max(H, I) / kHalf + 1;
   if ((R / kTileM + E) * cols > INT32_MAX || 3 * (int64_t)E * cols * cols > INT32_MAX) return MOE_ERR_UNSUPPORTED_SHAPE;

@@ -343,7 +343,7 @@ int moe_permute_rows(const void* x, const int32_t* inv, int32_t T, int32_t k, in
   if (R < 0) return MOE_ERR_INVALID_ARG;
   if (R > INT32_MAX) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (T == 0 || R == 0) return MOE_OK;
-  if (!x || !inv || !rows || !is_aligned(x, 16) || !is_aligned(rows, 16) || !is_aligned(inv, 4)) return MOE_ERR_INVALID_ARG;
+  if (!x || !inv || !rows || x == rows || !is_aligned(x, 16) || !is_aligned(rows, 16) || !is_aligned(inv, 4)) return MOE_ERR_INVALID_ARG;
   const int nvec = (int)(row_bytes / 16), span = row_span(nvec), per = 256 / span;
   const cudaError_t e = launch_pdl(permute_kernel, dim3((unsigned)((T + per - 1) / per), (unsigned)((nvec + span - 1) / span)),
                                    dim3(256), 0, reinterpret_cast<cudaStream_t>(stream), static_cast<const uint4*>(x), inv,
@@ -360,7 +360,7 @@ int moe_combine_rows(const void* rows, const int32_t* inv, const float* topk_w, 
   if (R < 0) return MOE_ERR_INVALID_ARG;
   if (R > INT32_MAX) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (T == 0) return MOE_OK;
-  if ((!rows && R > 0) || !inv || !y || !is_aligned(rows, 16) || !is_aligned(y, 16) || !is_aligned(inv, 4) || !is_aligned(topk_w, 4))
+  if ((!rows && R > 0) || !inv || !y || rows == y || !is_aligned(rows, 16) || !is_aligned(y, 16) || !is_aligned(inv, 4) || !is_aligned(topk_w, 4))
     return MOE_ERR_INVALID_ARG;
   const int nvec = (int)(cols / (f32 ? 4 : 8)), span = row_span(nvec), per = 256 / span;
   const cudaError_t e = launch_pdl(f32 ? combine_kernel<true> : combine_kernel<false>,

@@ -66,7 +66,7 @@ def test_sort(moe, kw, want):
     (dict(rb=0), -1), (dict(rb=(1 << 20) + 16), -2), (dict(R=-1), -1), (dict(R=1 << 31), -2), (dict(x=None), -1), (dict(inv=None), -1),
     (dict(rows=None), -1), (dict(x=P + 8), -1), (dict(rows=P + 8), -1), (dict(inv=P + 2), -1)])
 def test_permute(moe, kw, want):
-    a = dict(x=P, inv=P, T=4, k=2, rb=64, R=8, rows=P)
+    a = dict(x=P, inv=P, T=4, k=2, rb=64, R=8, rows=2 * P)
     a.update(kw)
     assert moe.lib().moe_permute_rows(a["x"], a["inv"], a["T"], a["k"], a["rb"], a["R"], a["rows"], None) == want
 
@@ -76,7 +76,7 @@ def test_permute(moe, kw, want):
     (dict(cols=1 << 40), -2), (dict(flags=2), -1), (dict(flags=1, cols=6), -1), (dict(R=-1), -1), (dict(rows=None), -1), (dict(inv=None), -1),
     (dict(y=None), -1), (dict(rows=P + 8), -1), (dict(y=P + 8), -1), (dict(w=P + 2), -1)])
 def test_combine(moe, kw, want):
-    a = dict(rows=P, inv=P, w=P, T=4, k=2, cols=64, R=8, flags=0, y=P)
+    a = dict(rows=P, inv=P, w=P, T=4, k=2, cols=64, R=8, flags=0, y=2 * P)
     a.update(kw)
     assert moe.lib().moe_combine_rows(a["rows"], a["inv"], a["w"], a["T"], a["k"], a["cols"], a["R"], a["flags"], a["y"], None) == want
 
@@ -151,3 +151,10 @@ def test_by_name_without_a_device(moe, name):
         getattr(moe, name)(**{n: x for n in OPS[name]})
     with pytest.raises(ValueError, match="required"):
         getattr(moe, name)(**{n: x for n in OPS[name][1:]})
+
+
+def test_in_place_moves_are_refused(moe):
+    """Rows cannot be laid out, or summed, into the buffer that they are read from."""
+    L = moe.lib()
+    assert L.moe_permute_rows(P, P, 4, 2, 64, 8, P, None) == -1
+    assert L.moe_combine_rows(P, P, P, 4, 2, 64, 8, 0, P, None) == -1
