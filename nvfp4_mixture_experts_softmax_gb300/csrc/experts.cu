@@ -272,24 +272,18 @@ __device__ __forceinline__ void slab_store_3d(uint32_t slab, int lane, const CUt
   }
 }
 
-// 64 columns of 32 rows as BF16, `w` two columns a word: by a slab if all 32 rows belong to the segment, else row by
-// row (32 bytes a store).  `cols`: how many of the 64 there are (32 or more).
-__device__ __forceinline__ void store_bf16x64(const uint32_t (&w)[32], uint32_t slab, int lane, const CUtensorMap* map, int x, int y,
-                                              bool whole, __nv_bfloat16* row, bool live, int cols) {
+// 32 columns of 32 rows as BF16, `w` two columns a word: by a slab if all 32 rows belong to the segment, else row by
+// row (32 bytes a store).
+__device__ __forceinline__ void store_bf16x32(const uint32_t (&w)[16], uint32_t slab, int lane, const CUtensorMap* map, int x, int y,
+                                              bool whole, __nv_bfloat16* row, bool live) {
   if (whole) {
+    slab_begin(lane);
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      if (32 * c >= cols) break;
-      slab_begin(lane);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        slab_put<64>(slab, lane, i, w[16 * c + 4 * i], w[16 * c + 4 * i + 1], w[16 * c + 4 * i + 2], w[16 * c + 4 * i + 3]);
-      slab_store_2d(slab, lane, map, x + 32 * c, y);
-    }
+    for (int i = 0; i < 4; ++i) slab_put<64>(slab, lane, i, w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    slab_store_2d(slab, lane, map, x, y);
   } else if (live) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (16 * i < cols) store_32b(row + 16 * i, w + 8 * i);
+    store_32b(row, w);
+    store_32b(row + 16, w + 8);
   }
 }
 
@@ -639,62 +633,74 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           slab_store_3d(slab, lane, maps.out + t.mat, col, t.m0 + slab_row, t.seg, p.accumulate);
         }
       } else {
+        constexpr int kGroups = kMode == kUp ? 2 : 4;    // of 32 columns a warp
+        const bool any = slab_row < t.rows, live = slab_row + lane < t.rows, whole = slab_row + 32 <= t.rows;
+        const int y = t.m0 + slab_row, col0 = half * kGroups * 32;
+        const size_t row = (size_t)(y + lane) * p.N;
+        // kDgradAct: g and u, read two groups ahead, the first two before the products are there (read when they are
+        // needed, eight waits of a load each made the epilogue as long as the products)
+        uint32_t gu[kMode == kDgradAct ? 2 : 1][32];
+        auto read_gu = [&](int k, uint32_t (&to)[32]) {
+          const int x = t.n0 + col0 + 32 * k;
+          if (!live || x >= p.N) return;
+          if (p.g) {
+            load_32b(p.g + row + x, to);
+            load_32b(p.g + row + x + 16, to + 8);
+          }
+          load_32b(p.u + row + x, to + 16);
+          load_32b(p.u + row + x + 16, to + 24);
+        };
+        if constexpr (kMode == kDgradAct) {
+          read_gu(0, gu[0]);
+          read_gu(1, gu[1]);
+        }
         const uint32_t buf = unit & 1u;
         ok = __all_sync(0xffffffffu, wait_bounded(smem_u32(acc_full + buf), (unit >> 1) & 1u, p.status, s_abort));
         if (!ok) break;
         ++unit;
         tc_fence_after();
-        const uint32_t acc = tmem + buf * kTileN + ((uint32_t)(quad * 32) << 16);
-        if (slab_row < t.rows) {
-          const bool live = slab_row + lane < t.rows, whole = slab_row + 32 <= t.rows;
-          const int y = t.m0 + slab_row;
-          const size_t row = (size_t)(y + lane) * p.N;
-#pragma unroll 1
-          for (int c = 0; c < (kMode == kUp ? 1 : 2); ++c) {
-            const int col = kMode == kUp ? half * 64 : half * kHalf + c * 64, x = t.n0 + col;
-            if (x >= p.N) break;
-            const int cols = min(64, p.N - x);
-            uint32_t w0[32], w1[32], w2[32];
+        const uint32_t acc = tmem + buf * kTileN + col0 + ((uint32_t)(quad * 32) << 16);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {      // 16 columns at a time
-              uint32_t v[16], vu[16], gu[16];
-              if constexpr (kMode == kDgradAct) {
-                if (live && 16 * q < cols) {
-                  if (p.g) load_32b(p.g + row + x + 16 * q, gu);
-                  load_32b(p.u + row + x + 16 * q, gu + 8);
-                }
-              }
-              tmem_ld_32x32b_x16(acc + col + 16 * q, v);
-              if constexpr (kMode == kUp) tmem_ld_32x32b_x16(acc + kHalf + col + 16 * q, vu);
-              tmem_ld_wait();
+        for (int k = 0; k < kGroups; ++k) {
+          const int x = t.n0 + col0 + 32 * k;
+          if (!any || x >= p.N) break;
+          uint32_t w0[16], w1[16], w2[16];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float a = __uint_as_float(v[2 * i]), b = __uint_as_float(v[2 * i + 1]);
-                const int o = 8 * q + i;
-                if constexpr (kMode == kUp) {
-                  const float ua = __uint_as_float(vu[2 * i]), ub = __uint_as_float(vu[2 * i + 1]);
-                  w0[o] = pack2(a, b);
-                  w1[o] = pack2(ua, ub);
-                  w2[o] = pack2(activation(a, ua, p.act, p.limit, p.alpha), activation(b, ub, p.act, p.limit, p.alpha));
-                } else if constexpr (kMode == kUpSingle) {
-                  w1[o] = pack2(a, b);
-                  w2[o] = pack2(activation(0.0f, a, kActRelu2, 0.0f, 0.0f), activation(0.0f, b, kActRelu2, 0.0f, 0.0f));
-                } else if constexpr (kMode == kDgradAct) {
-                  float ga, gb, ua, ub;
-                  activation_grad(low_bf16(gu[i]), low_bf16(gu[8 + i]), a, p.act, p.limit, p.alpha, ga, ua);
-                  activation_grad(high_bf16(gu[i]), high_bf16(gu[8 + i]), b, p.act, p.limit, p.alpha, gb, ub);
-                  w0[o] = pack2(ga, gb);
-                  w1[o] = pack2(ua, ub);
-                } else {
-                  w0[o] = pack2(a, b);
-                }
+          for (int q = 0; q < 2; ++q) {      // 16 columns at a time
+            uint32_t v[16], vu[16];
+            tmem_ld_32x32b_x16(acc + 32 * k + 16 * q, v);
+            if constexpr (kMode == kUp) tmem_ld_32x32b_x16(acc + kHalf + 32 * k + 16 * q, vu);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float a = __uint_as_float(v[2 * i]), b = __uint_as_float(v[2 * i + 1]);
+              const int o = 8 * q + i;
+              if constexpr (kMode == kUp) {
+                const float ua = __uint_as_float(vu[2 * i]), ub = __uint_as_float(vu[2 * i + 1]);
+                w0[o] = pack2(a, b);
+                w1[o] = pack2(ua, ub);
+                w2[o] = pack2(activation(a, ua, p.act, p.limit, p.alpha), activation(b, ub, p.act, p.limit, p.alpha));
+              } else if constexpr (kMode == kUpSingle) {
+                w1[o] = pack2(a, b);
+                w2[o] = pack2(activation(0.0f, a, kActRelu2, 0.0f, 0.0f), activation(0.0f, b, kActRelu2, 0.0f, 0.0f));
+              } else if constexpr (kMode == kDgradAct) {
+                const uint32_t gw = gu[k & 1][o], uw = gu[k & 1][16 + o];
+                float ga, gb, ua, ub;
+                activation_grad(low_bf16(gw), low_bf16(uw), a, p.act, p.limit, p.alpha, ga, ua);
+                activation_grad(high_bf16(gw), high_bf16(uw), b, p.act, p.limit, p.alpha, gb, ub);
+                w0[o] = pack2(ga, gb);
+                w1[o] = pack2(ua, ub);
+              } else {
+                w0[o] = pack2(a, b);
               }
             }
-            if (kMode != kUpSingle && p.o[0]) store_bf16x64(w0, slab, lane, maps.out, x, y, whole, p.o[0] + row + x, live, cols);
-            if (kMode <= kUpSingle || kMode == kDgradAct)
-              if (p.o[1]) store_bf16x64(w1, slab, lane, maps.out + 1, x, y, whole, p.o[1] + row + x, live, cols);
-            if (kMode <= kUpSingle) store_bf16x64(w2, slab, lane, maps.out + 2, x, y, whole, p.o[2] + row + x, live, cols);
           }
+          if constexpr (kMode == kDgradAct)
+            if (k + 2 < kGroups) read_gu(k + 2, gu[k & 1]);
+          if (kMode != kUpSingle && p.o[0]) store_bf16x32(w0, slab, lane, maps.out, x, y, whole, p.o[0] + row + x, live);
+          if (kMode <= kUpSingle || kMode == kDgradAct)
+            if (p.o[1]) store_bf16x32(w1, slab, lane, maps.out + 1, x, y, whole, p.o[1] + row + x, live);
+          if (kMode <= kUpSingle) store_bf16x32(w2, slab, lane, maps.out + 2, x, y, whole, p.o[2] + row + x, live);
         }
         tc_fence_before();
         __syncwarp();
