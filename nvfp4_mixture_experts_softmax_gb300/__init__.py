@@ -618,8 +618,8 @@ def router_loss_backward(handle, logits, topk_ids, stats, grad_losses=None, grad
                          router: str = "softmax", dlogits=None):
     """Gradient [T, E] FP32 of the logits from grad_losses [2] FP32 (on the device; the gradients
     of the balance and z losses) and grad_topk_w [T, k] FP32 (of the top-k weights); either may be
-    None.  The latter comes from the caller's own backward pass through the experts, which this library
-    does not have.  stats: what router_loss returned for the same logits, ids, mask and router.
+    None.  The latter is the dtopk_w of combine_tokens_backward, or comes from the caller's own backward pass
+    through the experts.  stats: what router_loss returned for the same logits, ids, mask and router.
     stream: a torch.cuda.Stream to launch on."""
     T, E, k = _routing_shape(logits, topk_ids)
     dev = logits.get_device()
