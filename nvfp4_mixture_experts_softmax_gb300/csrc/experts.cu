@@ -58,9 +58,11 @@ constexpr int kGroupM = 8;                      // row tiles that are worked thr
 constexpr int kSmallBox = 32;                   // rows of the small box
 constexpr uint64_t kLimitNs = 2000000000ull;
 
-// The tensor cores truncate where they add, so the FP32 gradients are cut into chains of this many
-// rows (32 additions), which the epilogue adds up in registers, rounding.
-constexpr int kChainRows = 512;
+// The tensor cores truncate where they add, so the FP32 gradients are cut into chains of about eight blocks (at most
+// eleven: 44 additions), of equal length but for one block, which the epilogue adds up in registers, rounding.  A short
+// last chain would cost the epilogue as much as a long one.
+__device__ __forceinline__ int chain_count(int blocks) { return blocks == 0 ? 0 : max(1, (blocks + 4) / 8); }
+__device__ __forceinline__ int chain_blocks(int blocks, int chains, int chain) { return blocks / chains + (chain < blocks % chains); }
 
 // Shared memory: the stages, a slab for each epilogue warp (its 32 rows by 64 or 128 bytes on their way out), barriers,
 // segment tables.  The row modes take six stages and 64-byte slabs (1505 us against 1548 for the forward pass of
@@ -469,11 +471,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             : s_tile[p.E] * p.n_tiles;
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;   // pairs
 
-  // chains of a tile, and blocks of K of one of them
-  auto chains_of = [&](int rows) { return kMode == kWgrad ? (rows + kChainRows - 1) / kChainRows : 1; };
-  auto blocks_of = [&](int rows, int chain) {
-    return kMode == kWgrad ? (min(kChainRows, rows - chain * kChainRows) + kBlockK - 1) / kBlockK : p.nkb;
-  };
+  // blocks of K = 64 of an item, its chains, and the blocks of one of them
+  auto blocks_of = [&](int rows) { return kMode == kWgrad ? (rows + kBlockK - 1) / kBlockK : p.nkb; };
+  auto chains_of = [&](int blocks) { return kMode == kWgrad ? chain_count(blocks) : 1; };
+  auto part_of = [&](int blocks, int chains, int ch) { return kMode == kWgrad ? chain_blocks(blocks, chains, ch) : blocks; };
 
   if (warp == kCopyWarp || warp == kCopyWarp2) {
     // ---------------- copies ----------------
@@ -493,39 +494,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool small = kMode != kWgrad && abytes == kSmallBox * 128u;
       const CUtensorMap* ma = maps.m + (kMode == kWgrad ? (t.mat == 0 ? 0 : t.mat == 1 ? 2 : 3) : small ? 3 : 0);
       const CUtensorMap* mb = maps.m + (kMode == kWgrad ? (t.mat == 2 ? 4 : 1) : kMode == kUp && rank == 1 ? 2 : 1);
-      const int nch = chains_of(t.rows);
-      for (int ch = 0; ch < nch && ok; ++ch) {
-        const int nkb = blocks_of(t.rows, ch);
-        for (int kb = 0; kb < nkb; ++kb, mine_next ^= 1u, st = st + 1 == kStages ? 0 : st + 1, ph ^= st == 0) {
-          filled = min(filled + 1, (uint32_t)kStages);
-          if (kMode == kDgradRows && kb == p.half_kb) {   // the second source
-            ma = maps.m + (small ? 5 : 2);
-            mb = maps.m + 4;
-          }
-          if (!mine_next) continue;
-          ok = __all_sync(0xffffffffu, wait_bounded(smem_u32(empty + st), ph ^ 1u, p.status, s_abort));
-          if (!ok) break;
-          const uint32_t a = smem0 + st * kStageBytes, b = a + kOperandBytes;
-          uint32_t bar = full0 + 8 * st;
-          if constexpr (kMode == kWgrad) {
-            const int done = ch * kChainRows + kb * kBlockK, row = t.row0 + done;
-            if (done + kBlockK > t.rows) bar = smem_u32(tail + st);   // rows behind the segment are to be zeroed
-            expect_bytes(bar, bytes);
-            if (na > 0) load_2d(a, ma, m, row, bar);
-            if (na > 1) load_2d(a + kChunkBytes, ma, m + 64, row, bar);
-            if (nb > 0) load_2d(b, mb, n, row, bar);
-            if (nb > 1) load_2d(b + kChunkBytes, mb, n + 64, row, bar);
+      const int nkb = blocks_of(t.rows);
+      for (int kb = 0; kb < nkb; ++kb, mine_next ^= 1u, st = st + 1 == kStages ? 0 : st + 1, ph ^= st == 0) {
+        filled = min(filled + 1, (uint32_t)kStages);
+        if (kMode == kDgradRows && kb == p.half_kb) {   // the second source
+          ma = maps.m + (small ? 5 : 2);
+          mb = maps.m + 4;
+        }
+        if (!mine_next) continue;
+        ok = __all_sync(0xffffffffu, wait_bounded(smem_u32(empty + st), ph ^ 1u, p.status, s_abort));
+        if (!ok) break;
+        const uint32_t a = smem0 + st * kStageBytes, b = a + kOperandBytes;
+        uint32_t bar = full0 + 8 * st;
+        if constexpr (kMode == kWgrad) {
+          const int done = kb * kBlockK, row = t.row0 + done;
+          if (done + kBlockK > t.rows) bar = smem_u32(tail + st);   // rows behind the segment are to be zeroed
+          expect_bytes(bar, bytes);
+          if (na > 0) load_2d(a, ma, m, row, bar);
+          if (na > 1) load_2d(a + kChunkBytes, ma, m + 64, row, bar);
+          if (nb > 0) load_2d(b, mb, n, row, bar);
+          if (nb > 1) load_2d(b + kChunkBytes, mb, n + 64, row, bar);
+        } else {
+          int k0 = kb * kBlockK;
+          if (kMode == kDgradRows && kb >= p.half_kb) k0 -= p.half_kb * kBlockK;
+          expect_bytes(bar, bytes);
+          if (abytes) load_2d(a, ma, k0, m, bar);
+          if constexpr (b_mn_major(kMode)) {
+            if (nb > 0) load_3d(b, mb, n, k0, t.seg, bar);
+            if (nb > 1) load_3d(b + kChunkBytes, mb, n + 64, k0, t.seg, bar);
           } else {
-            int k0 = kb * kBlockK;
-            if (kMode == kDgradRows && kb >= p.half_kb) k0 -= p.half_kb * kBlockK;
-            expect_bytes(bar, bytes);
-            if (abytes) load_2d(a, ma, k0, m, bar);
-            if constexpr (b_mn_major(kMode)) {
-              if (nb > 0) load_3d(b, mb, n, k0, t.seg, bar);
-              if (nb > 1) load_3d(b + kChunkBytes, mb, n + 64, k0, t.seg, bar);
-            } else {
-              if (nb > 0) load_3d(b, mb, k0, n, t.seg, bar);
-            }
+            if (nb > 0) load_3d(b, mb, k0, n, t.seg, bar);
           }
         }
       }
@@ -546,10 +544,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t st = 0, ph = 0, unit = 0;
       bool ok = true;
       for (int item = first; item < total && ok; item += step) {
-        const int rows = reduction_rows<kMode>(p, s_off, item);
-        const int nch = chains_of(rows);
+        const int blocks = blocks_of(reduction_rows<kMode>(p, s_off, item)), nch = chains_of(blocks);
         for (int ch = 0; ch < nch && ok; ++ch, ++unit) {
-          const int nkb = blocks_of(rows, ch);
+          const int nkb = part_of(blocks, nch, ch);
           const uint32_t buf = unit & 1u;
           ok = __all_sync(0xffffffffu, wait_bounded(smem_u32(acc_empty + buf), ((unit >> 1) & 1u) ^ 1u, p.status, s_abort));
           if (!ok) break;
@@ -574,7 +571,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int item = first; item < total && ok; item += step) {
         const int rows = reduction_rows<kMode>(p, s_off, item);
-        at += rows / kChainRows * (kChainRows / kBlockK) + (rows % kChainRows + kBlockK - 1) / kBlockK;
+        at += blocks_of(rows);
         const int have = rows % kBlockK;
         if (have == 0) continue;
         const uint32_t st = (at - 1) % kStages;
@@ -604,7 +601,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if constexpr (kMode == kWgrad) {
         // the chains' sums meet in registers: 128 columns a thread
         float sum[kHalf];
-        const int nch = chains_of(t.rows);
+        const int nch = chains_of(blocks_of(t.rows));
         for (int ch = 0; ch < nch && ok; ++ch, ++unit) {
           const uint32_t buf = unit & 1u;
           ok = __all_sync(0xffffffffu, wait_bounded(smem_u32(acc_full + buf), (unit >> 1) & 1u, p.status, s_abort));
