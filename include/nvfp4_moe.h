@@ -337,16 +337,16 @@ int moe_combine_rows_backward(const void* dy, const void* rows, const int32_t* i
  * computed).  w_gate, w_up [E,I,H], w_down [E,H,I] BF16, as moe_quantize_weights takes them.  Per row
  *   g = x Wg^T, u = x Wu^T, h = bf16(act(g, u)) from the FP32 g and u, out = h Wd^T
  * with the activation of flags (none: silu(g) * u; MOE_FLAG_SWIGLU_CLAMP, MOE_FLAG_ACT_SWIGLU_OAI with
- * swiglu_limit and swiglu_alpha; MOE_FLAG_ACT_RELU2: no gate, w_gate and g are NULL or not read).
+ * swiglu_limit and swiglu_alpha; MOE_FLAG_ACT_RELU2: no gate, w_gate is not read, g, dg and dw_gate are NULL).
  *   forward:  out [R,H]; g, u [R,I], what the backward pass reads (both NULL: not kept; relu2: u alone); h [R,I]
  *             (NULL: kept in the workspace for the call), what the weights' gradient reads.
  *   backward: from dout [R,H], g and u: dg, du [R,I] = bf16 of the gradients of g and u (a clamp's gradient
  *             is 0 beyond its limit), and drows [R,H] = dg Wg + du Wu.
  *   weights:  dw_gate = dg^T rows, dw_up = du^T rows [E,I,H], dw_down = dout^T h [E,H,I], FP32, per
  *             segment; overwritten (zeros for an expert without rows) or, with MOE_EXPERTS_ACCUMULATE in
- *             flags, added to.  relu2: dg and dw_gate NULL.
+ *             flags, added to (by the memory system, which may take subnormal values for zero).
  * All BF16 tensors: products accumulate in FP32, one rounding at the end.  The tensor cores truncate where they
- * add; the weights' gradients are cut into chains of 64 such additions.  All sums run in a fixed order.
+ * add; the weights' gradients are cut into chains of at most 44 such additions.  All sums run in a fixed order.
  * Rows from offsets[E] on are neither used (they may hold anything) nor written; NaN and infinities
  * stay in their row, in the weights' gradients in their segment.
  * H, I multiples of 32, at most 65536; E <= 1024; R < 2^31 - 256.  Inputs 16-byte aligned, outputs, g and u 32-byte;

@@ -19,11 +19,11 @@
 // segment is zeroed behind the segment's end in shared memory, in both operands, before it is multiplied.
 //
 // What bounds it, device times: with rows enough the tensor cores (one expert, 8192 rows of 4096 x 4096: forward 1.92
-// PFLOP/s, gradients of the rows 1.75, of the weights 1.63); 64 experts of uneven size, 65536 rows of 4096 x 1536:
-// forward 1.52 ms (1.63 PFLOP/s: an eighth of the row tiles' rows lie behind their segment), weights' gradients 2.0 ms
-// (1.23: 4.8 GB of FP32 results, which small segments write as fast as HBM takes them); few rows an expert: reading the
-// weights (64 tokens to 8 of 128 experts of 2048 x 768 198 us, 6.0 TB/s; one token 26 us; gradients of the rows of 8192 tokens to 8 of
-// 256 experts of 2048 x 512 440 us, 5.4 TB/s).
+// PFLOP/s, gradients of the rows 1.74, of the weights 1.75); 64 experts of uneven size, 65536 rows of 4096 x 1536:
+// forward 1.49 ms (1.65 PFLOP/s: an eighth of the row tiles' rows lie behind their segment), weights' gradients 1.99 ms
+// (1.25: 4.8 GB of FP32 results beside the operands' way from L2); few rows an expert: reading the weights (64 tokens to 8
+// of 128 experts of 2048 x 768 195 us, 6.1 TB/s; one token 26 us; gradients of the rows of 8192 tokens to 8 of 256
+// experts of 2048 x 512 435 us, 5.4 TB/s).
 //
 // Warps of a CTA: 0-7 epilogue (each a quarter of the rows and half of the columns), 8 and 11 copies (every other
 // stage each: a load takes 100 cycles to issue, up to four a stage), 9 tensor memory and, in CTA 0, the MMAs of
@@ -783,9 +783,9 @@ int check_shape(const int32_t* offsets, int64_t R, int32_t E, int64_t H, int64_t
   if ((sh.act == kActSwigluClamp || sh.act == kActSwigluOai) && !(std::isfinite(limit) && limit >= 0.0f)) return MOE_ERR_INVALID_ARG;
   if (sh.act == kActSwigluOai && !std::isfinite(alpha)) return MOE_ERR_INVALID_ARG;
   if (E > kMaxExperts || R > INT32_MAX - kTileM || H > (1 << 16) || I > (1 << 16)) return MOE_ERR_UNSUPPORTED_SHAPE;
-  // tiles are counted in 32 bits
+  // tiles are counted in 32 bits, with room for a pair's next one
   const int64_t cols = std::max(H, I) / kHalf + 1;
-  if ((R / kTileM + E) * cols > INT32_MAX || 3 * (int64_t)E * cols * cols > INT32_MAX) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if ((R / kTileM + E) * cols > 1 << 30 || 3 * (int64_t)E * cols * cols > 1 << 30) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (!ws || ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
   if (!is_aligned(ws, 256) || !offsets || !is_aligned(offsets, 4)) return MOE_ERR_INVALID_ARG;
   sh.R = R;
