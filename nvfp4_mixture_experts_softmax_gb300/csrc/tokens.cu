@@ -139,7 +139,7 @@ __device__ __forceinline__ int64_t row_of(const int32_t* __restrict__ inv, int64
   return p >= 0 && p < R ? p : -1;
 }
 
-// A row over `span` threads, 256 / span rows a block; blockIdx.y takes pieces of kVecs * span vectors of a row.
+// A row over `span` threads, 256 / span rows a block; blockIdx.y takes pieces of span vectors of a row.
 __global__ void __launch_bounds__(256) permute_kernel(const uint4* __restrict__ x,
                                                       const int32_t* __restrict__ inv, int T, int k,
                                                       int64_t R, int nvec, int span,
