@@ -265,7 +265,8 @@ int moe_add_rmsnorm_backward(const void* dy, const void* dh, const void* h, cons
  *   residual and h are both given or both NULL (then h is x itself); beta NULL: none.  h may be the buffer
  *   of residual or of x (in place); no other two buffers may overlap.
  * A NaN or infinity makes its own row NaN; squared distances are summed in FP32, so rows that spread over more than
- * 2^63 overflow (s = 0).  No workspace, one launch.  rows == 0 is MOE_OK. */
+ * 2^63 overflow (s = 0).  A block whose wait for its own copies runs out (about a second) leaves NaN, here and in
+ * the backward pass.  No workspace, one launch.  rows == 0 is MOE_OK. */
 #define MOE_ROWS_F32 1u
 int moe_add_layernorm(const void* x, const void* residual, const void* gamma, const void* beta,
                       float eps, int64_t rows, int64_t cols, uint32_t flags, void* h, void* y,

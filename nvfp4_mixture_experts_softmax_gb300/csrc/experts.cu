@@ -54,8 +54,10 @@ constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kEpiWarps = 8, kCopyWarp = 8, kMmaWarp = 9, kZeroWarp = 10, kCopyWarp2 = 11;
 constexpr int kThreads = 12 * 32;
 constexpr int kMaxExperts = 1024;
-constexpr int kGroupM = 8;                      // row tiles that are worked through column by column
-constexpr int kSmallBox = 32;                   // rows of the small box
+constexpr int kGroupM = 8;                      // row tiles that are worked through column by column (4, 8, 16: the weights'
+                                                // gradients of 64 experts 1974, 1961, 1986 us)
+constexpr int kSmallBox = 32;                   // of up to so many rows a CTA fetches no more (8 tokens to 8 of 128 experts:
+                                                // 92 us instead of 96)
 constexpr uint64_t kLimitNs = 2000000000ull;
 
 // The tensor cores truncate where they add, so the FP32 gradients are cut into chains of about eight blocks (at most
