@@ -429,6 +429,9 @@ def run(cfg: MoeConfig, wbuf, x, logits, k=None, y=None, workspace=None, debug=F
 # object costs 1.1 us of a call's 9)
 _stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream",
                          lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+# the current device's index, CUDA being initialised (there are tensors on it): half the time of
+# torch.cuda.current_device
+_device_index = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _scoped(fn):
@@ -447,7 +450,7 @@ def _scoped(fn):
         if not first.is_cuda:
             raise ValueError(f"{fn.__name__} needs CUDA tensors, got one on {first.device}")
         dev = first.get_device()
-        if stream is None and dev == torch.cuda.current_device():
+        if stream is None and dev == _device_index():
             return fn(_stream_handle(dev), *args, **kw)
         if stream is not None and stream.device != first.device:
             raise ValueError(f"{fn.__name__}: the stream is on {stream.device}, the tensors on "
@@ -711,12 +714,12 @@ def add_layernorm(handle, x, residual, gamma, beta=None, eps: float = 1e-5, want
         if want_stats:
             out["mean"] = torch.empty(rows, dtype=_F32, device=dev)
             out["rstd"] = torch.empty(rows, dtype=_F32, device=dev)
-    get = out.get
+    get, line, each = out.get, (cols,), (rows,)
     st = lib().moe_add_layernorm(
         _given(x, "x", dt, shape, dev), _given(residual, "residual", dt, shape, dev),
-        _given(_need(gamma, "gamma"), "gamma", dt, (cols,), dev), _given(beta, "beta", dt, (cols,), dev), eps, rows,
+        _given(_need(gamma, "gamma"), "gamma", dt, line, dev), _given(beta, "beta", dt, line, dev), eps, rows,
         cols, flags, _given(get("h"), "h", dt, shape, dev), _given(_need(get("y"), "y"), "y", dt, shape, dev),
-        _given(get("mean"), "mean", _F32, (rows,), dev), _given(get("rstd"), "rstd", _F32, (rows,), dev), handle)
+        _given(get("mean"), "mean", _F32, each, dev), _given(get("rstd"), "rstd", _F32, each, dev), handle)
     if st:
         _check(st, "moe_add_layernorm")
     return out
