@@ -56,8 +56,13 @@ constexpr int kThreads = 12 * 32;
 constexpr int kMaxExperts = 1024;
 constexpr int kGroupM = 8;                      // row tiles that are worked through column by column (4, 8, 16: the weights'
                                                 // gradients of 64 experts 1974, 1961, 1986 us)
-constexpr int kSmallBox = 32;                   // of up to so many rows a CTA fetches no more (8 tokens to 8 of 128 experts:
-                                                // 92 us instead of 96)
+// Rows of the small box.  Of a tile's half that is not full a CTA fetches boxes of so many rows, and zeros (boxes outside
+// the tensor) in the place of the rows behind the segment: they need less power when they are multiplied, and power is
+// what sets the clock under load (64 tokens to 8 of 128 experts 208 and 200 us, 4096 tokens to 8 of 64 experts of 7168 x 2048
+// 1980 and 1955 us).  Up to kFewRows rows in all no zeros, and one box where one holds the rows: the time of a few tokens is that of
+// their copies' issue (1 token 26.6 us against 34.9, 4 tokens 59.5 against 66.8; from 16 on no difference).
+constexpr int kSmallBox = 32;
+constexpr int kFewRows = 128;
 constexpr uint64_t kLimitNs = 2000000000ull;
 
 // The tensor cores truncate where they add, so the FP32 gradients are cut into chains of about eight blocks (at most
@@ -110,6 +115,7 @@ struct Args {
   const __nv_bfloat16 *g, *u;            // kDgradAct: the forward pass's
   __nv_bfloat16* o[3];                   // kUp: g, u (may be null), h; kDgradAct: dg, du; else out; as maps.out
   int accumulate;
+  int zeros;      // more than kFewRows rows
   int first;      // this launch clears the status
 };
 
@@ -490,10 +496,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int m = t.m0 + (int)rank * kHalf, n = kMode == kUp ? t.n0 : t.n0 + (int)rank * kHalf;
       const int na = m >= Mm ? 0 : m + 64 >= Mm ? 1 : 2, nb = n >= Nn ? 0 : n + 64 >= Nn ? 1 : 2;
       const int mine = t.rows - (int)rank * kHalf;
+      const bool part = kMode != kWgrad && mine < kHalf, zeros = part && p.zeros;
       const uint32_t abytes = kMode == kWgrad ? (uint32_t)na * kChunkBytes
+                              : !part || zeros ? (uint32_t)kOperandBytes
                               : mine <= 0 ? 0u : mine <= kSmallBox ? kSmallBox * 128u : (uint32_t)kOperandBytes;
       const uint32_t bytes = abytes + (b_mn_major(kMode) ? (uint32_t)nb * kChunkBytes : nb ? (uint32_t)kOperandBytes : 0u);
-      const bool small = kMode != kWgrad && abytes == kSmallBox * 128u;
+      const bool small = part && mine > 0 && (zeros || mine <= kSmallBox);
       const CUtensorMap* ma = maps.m + (kMode == kWgrad ? (t.mat == 0 ? 0 : t.mat == 1 ? 2 : 3) : small ? 3 : 0);
       const CUtensorMap* mb = maps.m + (kMode == kWgrad ? (t.mat == 2 ? 4 : 1) : kMode == kUp && rank == 1 ? 2 : 1);
       const int nkb = blocks_of(t.rows);
@@ -520,7 +528,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           int k0 = kb * kBlockK;
           if (kMode == kDgradRows && kb >= p.half_kb) k0 -= p.half_kb * kBlockK;
           expect_bytes(bar, bytes);
-          if (abytes) load_2d(a, ma, k0, m, bar);
+          if (zeros && mine > 0) {
+#pragma unroll
+            for (int i = 0; i < kHalf / kSmallBox; ++i)
+              load_2d(a + i * kSmallBox * 128, ma, k0, i * kSmallBox < mine ? m + i * kSmallBox : p.R, bar);
+          } else if (abytes) {
+            load_2d(a, ma, k0, mine > 0 ? m : p.R, bar);
+          }
           if constexpr (b_mn_major(kMode)) {
             if (nb > 0) load_3d(b, mb, n, k0, t.seg, bar);
             if (nb > 1) load_3d(b + kChunkBytes, mb, n + 64, k0, t.seg, bar);
@@ -805,6 +819,7 @@ Args base_args(const Shape& sh, const int32_t* offsets, void* ws, float limit, f
   a.E = sh.E;
   a.R = (int)sh.R;
   a.act = sh.act;
+  a.zeros = sh.R > kFewRows;
   a.limit = limit;
   a.alpha = alpha;
   return a;
