@@ -20,10 +20,10 @@
 //
 // What bounds it, device times: with rows enough the tensor cores (one expert, 8192 rows of 4096 x 4096: forward 1.92
 // PFLOP/s, gradients of the rows 1.74, of the weights 1.75); 64 experts of uneven size, 65536 rows of 4096 x 1536:
-// forward 1.49 ms (1.65 PFLOP/s: an eighth of the row tiles' rows lie behind their segment), weights' gradients 1.99 ms
-// (1.25: 4.8 GB of FP32 results beside the operands' way from L2); few rows an expert: reading the weights (64 tokens to 8
-// of 128 experts of 2048 x 768 195 us, 6.1 TB/s; one token 26 us; gradients of the rows of 8192 tokens to 8 of 256
-// experts of 2048 x 512 435 us, 5.4 TB/s).
+// forward 1.49 ms (1.65 PFLOP/s: an eighth of the row tiles' rows lie behind their segment; 1.70 ms once the power cap
+// lowers the clock), weights' gradients 1.98 ms (1.25: 4.8 GB of FP32 results beside the operands' way from L2); few
+// rows an expert: reading the weights (64 tokens to 8 of 128 experts of 2048 x 768 194 us, 6.1 TB/s; one token 27 us;
+// gradients of the rows of 8192 tokens to 8 of 256 experts of 2048 x 512 435 us, 5.4 TB/s).
 //
 // Warps of a CTA: 0-7 epilogue (each a quarter of the rows and half of the columns), 8 and 11 copies (every other
 // stage each: a load takes 100 cycles to issue, up to four a stage), 9 tensor memory and, in CTA 0, the MMAs of
