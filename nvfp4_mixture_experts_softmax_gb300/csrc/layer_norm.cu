@@ -169,10 +169,10 @@ __device__ __forceinline__ void pack(const float2 (&f)[4], F32x8& q) {
   q.b = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
 }
 
-// A warp's share of a row's mean and variance: elements, their mean, the sum of squared distances from it.  The
-// warps' means and the distances between them meet behind the row's one barrier.
-struct Share {
-  float n, mean, dist;
+// A warp's share of a row's mean and variance: elements, their sum, their mean and the sum of squared distances from it.
+// The warps' sums and the distances between their means meet behind the row's one barrier.
+struct __align__(16) Share {
+  float n, sum, mean, dist;
 };
 
 template <typename V, int J>
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(512, 1) add_layernorm_kernel(
 #pragma unroll
       for (int i = 0; i < 4; ++i) sum = add2(sum, f[j][i]);
     }
-    const float wm = warp_sum(sum.x + sum.y) * inv_wn;
+    const float ws = warp_sum(sum.x + sum.y), wm = ws * inv_wn;
     float2 dist = both(0.0f);
 #pragma unroll
     for (int j = 0; j < J; ++j) {
@@ -250,12 +250,12 @@ __global__ void __launch_bounds__(512, 1) add_layernorm_kernel(
       }
     }
     const float wd = warp_sum(dist.x + dist.y);
-    if (lane == 0) red[par][warp] = Share{wn, ok ? wm : __int_as_float(0x7FC00000), wd};
+    if (lane == 0) red[par][warp] = Share{wn, ok ? ws : __int_as_float(0x7FC00000), wm, wd};
     ring.barrier();
     if (ring.issuer && n > 0 && slots > 1 && n - 1 + slots < count)   // the slot of the row before
       ring.fetch<2>(s ? s - 1 : slots - 1, src, tensors, row0 + (int64_t)(n - 1 + slots) * step);
-    const Share w = lane < W ? red[par][group * W + lane] : Share{0.0f, 0.0f, 0.0f};
-    const float m = warps_sum(w.n * w.mean) * inv_cols;
+    const Share w = lane < W ? red[par][group * W + lane] : Share{0.0f, 0.0f, 0.0f, 0.0f};
+    const float m = warps_sum(w.sum) * inv_cols;
     const float var = warps_sum(fmaf(w.n * (w.mean - m), w.mean - m, w.dist)) * inv_cols;
     const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(var, eps)));
     if (t == 0) {
@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(1024, 1) add_layernorm_row_kernel(
     for (int i = 0; i < 4; ++i) sum = add2(sum, f[j][i]);
     mine += 8 * min(max(nvec - (j * span + warp * 32), 0), 32);
   }
-  const float wm = mine ? __fdiv_rn(warp_sum(sum.x + sum.y), (float)mine) : 0.0f;
+  const float ws = warp_sum(sum.x + sum.y), wm = mine ? __fdiv_rn(ws, (float)mine) : 0.0f;
   float2 dist = both(0.0f);
 #pragma unroll
   for (int j = 0; j < J; ++j) {
@@ -494,10 +494,10 @@ __global__ void __launch_bounds__(1024, 1) add_layernorm_row_kernel(
     }
   }
   const float wd = warp_sum(dist.x + dist.y);
-  if (lane == 0) red[warp] = Share{(float)mine, wm, wd};
+  if (lane == 0) red[warp] = Share{(float)mine, ws, wm, wd};
   __syncthreads();
-  const Share w = lane < W ? red[lane] : Share{0.0f, 0.0f, 0.0f};
-  const float m = warp_sum(w.n * w.mean) * inv_cols;
+  const Share w = lane < W ? red[lane] : Share{0.0f, 0.0f, 0.0f, 0.0f};
+  const float m = warp_sum(w.sum) * inv_cols;
   const float var = warp_sum(fmaf(w.n * (w.mean - m), w.mean - m, w.dist)) * inv_cols;
   const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(var, eps)));
   if (threadIdx.x == 0) {
