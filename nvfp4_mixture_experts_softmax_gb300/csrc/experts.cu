@@ -131,9 +131,27 @@ __device__ __forceinline__ uint32_t leader_addr(uint32_t bar) {
 }
 // Arrivals on a barrier of either CTA.  Release at CTA scope: what they order are TMA copies, MMAs and reads of
 // tensor memory, which complete on their own terms; at cluster scope each arrival would wait for the thread's
-// memory accesses (0.8 us a stage of the copies: a third of the rate).
+// memory accesses (0.8 us a stage of the copies: a third of the rate).  Ordinary stores do not complete on their own
+// terms: an arrival that announces them to the other CTA releases at cluster scope, and the wait for it acquires there.
 __device__ __forceinline__ void arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ void arrive_release_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+// One more poll of a phase that is known to be complete, for what it acquires.
+__device__ __forceinline__ bool acquire_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      "selp.u32 %0, 1, 0, p;\n"
+      "}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 // As mbar_wait_bounded; gives up as soon as another role of the CTA has.
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, int32_t* status,
@@ -560,7 +578,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t st = 0, ph = 0, unit = 0;
       bool ok = true;
       for (int item = first; item < total && ok; item += step) {
-        const int blocks = blocks_of(reduction_rows<kMode>(p, s_off, item)), nch = chains_of(blocks);
+        const int rows = reduction_rows<kMode>(p, s_off, item), blocks = blocks_of(rows), nch = chains_of(blocks);
+        const bool tail_end = kMode == kWgrad && rows % kBlockK != 0;   // the item's last block has been zeroed in part
         for (int ch = 0; ch < nch && ok; ++ch, ++unit) {
           const int nkb = part_of(blocks, nch, ch);
           const uint32_t buf = unit & 1u;
@@ -570,6 +589,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int kb = 0; kb < nkb; ++kb) {
             ok = __all_sync(0xffffffffu, wait_bounded(smem_u32(full + st), ph, p.status, s_abort));
             if (!ok) break;
+            if (tail_end && ch == nch - 1 && kb == nkb - 1) acquire_cluster(smem_u32(full + st), ph);
             tc_fence_after();
             const uint64_t so = (uint64_t)(st * (kStageBytes >> 4));
             mma_block<a_mn_major(kMode) ? 128u : 2u, b_mn_major(kMode) ? 128u : 2u>(tmem + buf * kTileN, da0 + so, db0 + so, idesc,
@@ -599,10 +619,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int c = 0; c < kStageBytes / kChunkBytes; ++c)
           for (int i = lane; i < n16; i += 32)
             *reinterpret_cast<uint4*>(base + c * kChunkBytes + have * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-        // the zeros are read by this CTA's own tensor core; nothing of them goes to the other CTA but the arrival
+        // The MMAs that read the zeros are CTA 0's, and CTA 1's half of B is an operand of both halves of the tile: CTA 1's
+        // stores are released to the cluster, CTA 0's have only its own MMA warp to reach.
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) arrive_cluster(leader_addr(smem_u32(full + st)));
+        if (lane == 0) {
+          if (rank == 0) mbar_arrive(smem_u32(full + st));
+          else arrive_release_cluster(leader_addr(smem_u32(full + st)));
+        }
       }
     }
   } else {
