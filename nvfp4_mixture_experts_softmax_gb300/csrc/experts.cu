@@ -15,8 +15,8 @@
 // Wg, CTA 1 the same rows of Wu, so that each thread of the epilogue holds g and u of its row.
 //
 // Tiles of 256 rows of one segment: a tile's rows behind the segment are read and multiplied, but not
-// stored (rows do not mix).  In the weights' gradients the rows are the reduction: the last block of a
-// segment is zeroed behind the segment's end in shared memory, in both operands, before it is multiplied.
+// stored (rows do not mix).  In the weights' gradients the rows are the reduction, and a segment's last block has zeros in the
+// place of the rows that are not its own, in both operands (window_map below).
 //
 // What bounds it, device times: with rows enough the tensor cores (one expert, 8192 rows of 4096 x 4096: forward 1.92
 // PFLOP/s, gradients of the rows 1.74, of the weights 1.75); 64 experts of uneven size, 65536 rows of 4096 x 1536:
@@ -25,10 +25,9 @@
 // rows an expert: reading the weights (64 tokens to 8 of 128 experts of 2048 x 768 194 us, 6.1 TB/s; one token 27 us;
 // gradients of the rows of 8192 tokens to 8 of 256 experts of 2048 x 512 435 us, 5.4 TB/s).
 //
-// Warps of a CTA: 0-7 epilogue (each a quarter of the rows and half of the columns), 8 and 11 copies (every other
+// Warps of a CTA: 0-7 epilogue (each a quarter of the rows and half of the columns), 8 and 10 copies (every other
 // stage each: a load takes 100 cycles to issue, up to four a stage), 9 tensor memory and, in CTA 0, the MMAs of
-// the pair, 10 the zeroing.  Two accumulators (2 x 256 columns) let
-// the epilogue run beside the next tile's products.  Every wait is bounded; one that runs out leaves
+// the pair.  Two accumulators (2 x 256 columns) let the epilogue run beside the next tile's products.  Every wait is bounded; one that runs out leaves
 // MOE_ERR_DEVICE_TIMEOUT in the status.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -51,8 +50,8 @@ constexpr int kBlockK = 64;
 constexpr int kOperandBytes = kHalf * kBlockK * 2;
 constexpr int kChunkBytes = kBlockK * 128;      // MN-major: 64 columns (128 bytes) of 64 rows
 constexpr int kStageBytes = 2 * kOperandBytes;
-constexpr int kEpiWarps = 8, kCopyWarp = 8, kMmaWarp = 9, kZeroWarp = 10, kCopyWarp2 = 11;
-constexpr int kThreads = 12 * 32;
+constexpr int kEpiWarps = 8, kCopyWarp = 8, kMmaWarp = 9, kCopyWarp2 = 10;
+constexpr int kThreads = 11 * 32;
 constexpr int kMaxExperts = 1024;
 constexpr int kGroupM = 8;                      // row tiles that are worked through column by column (4, 8, 16: the weights'
                                                 // gradients of 64 experts 1974, 1961, 1986 us)
@@ -83,7 +82,7 @@ struct Layout {
   static constexpr int kBarOff = kSlabOff + kEpiWarps * 32 * kSlabWidth;
   static constexpr int kTableOff = kBarOff + 256;
   static constexpr size_t kBytes = 1024 + kTableOff + 2 * (kMaxExperts + 1) * sizeof(int32_t) + 8;
-  static_assert(kBytes <= 232448 && (3 * kStages + 4) * 8 + 12 <= 256, "shared memory");
+  static_assert(kBytes <= 232448 && (2 * kStages + 4) * 8 + 12 <= 256, "shared memory");
 };
 
 constexpr bool a_mn_major(Mode m) { return m == kWgrad; }
@@ -131,27 +130,10 @@ __device__ __forceinline__ uint32_t leader_addr(uint32_t bar) {
 }
 // Arrivals on a barrier of either CTA.  Release at CTA scope: what they order are TMA copies, MMAs and reads of
 // tensor memory, which complete on their own terms; at cluster scope each arrival would wait for the thread's
-// memory accesses (0.8 us a stage of the copies: a third of the rate).  Ordinary stores do not complete on their own
-// terms: an arrival that announces them to the other CTA releases at cluster scope, and the wait for it acquires there.
+// memory accesses (0.8 us a stage of the copies: a third of the rate).  No ordinary store to
+// shared memory is read by the other CTA or its MMAs.
 __device__ __forceinline__ void arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-__device__ __forceinline__ void arrive_release_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-// One more poll of a phase that is known to be complete, for what it acquires.
-__device__ __forceinline__ bool acquire_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n"
-      ".reg .pred p;\n"
-      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-      "selp.u32 %0, 1, 0, p;\n"
-      "}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
 }
 // As mbar_wait_bounded; gives up as soon as another role of the CTA has.
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, int32_t* status,
@@ -408,7 +390,7 @@ __device__ __forceinline__ Tile tile_at(const Args& p, const int32_t* s_off, con
   return t;
 }
 
-// Rows of the segment that an item's reduction runs over (kWgrad), all that the MMA and zeroing warps need to know.
+// Rows of the segment that an item's reduction runs over (kWgrad), all that the MMA warp needs to know.
 template <Mode kMode>
 __device__ __forceinline__ int reduction_rows(const Args& p, const int32_t* s_off, int item) {
   if (kMode != kWgrad) return 0;
@@ -425,8 +407,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);   // [stage], CTA 0's: both CTAs' data has landed
   uint64_t* empty = full + kStages;                               // [stage]: the MMAs have read it
-  uint64_t* tail = empty + kStages;                               // [stage]: data that is to be zeroed has landed
-  uint64_t* acc_full = tail + kStages;                            // [2]
+  uint64_t* acc_full = empty + kStages;                           // [2]
   uint64_t* acc_empty = acc_full + 2;                             // [2], CTA 0's
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
   volatile uint32_t* s_abort = tmem_slot + 1;
@@ -440,7 +421,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_u32(full + s), 2);    // one arrival of each CTA, and the bytes
       mbar_init(smem_u32(empty + s), 1);
-      mbar_init(smem_u32(tail + s), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(acc_full + b), 1);
@@ -533,15 +513,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, wait_bounded(smem_u32(empty + st), ph ^ 1u, p.status, s_abort));
         if (!ok) break;
         const uint32_t a = smem0 + st * kStageBytes, b = a + kOperandBytes;
-        uint32_t bar = full0 + 8 * st;
+        const uint32_t bar = full0 + 8 * st;
         if constexpr (kMode == kWgrad) {
-          const int done = kb * kBlockK, row = t.row0 + done;
-          if (done + kBlockK > t.rows) bar = smem_u32(tail + st);   // rows behind the segment are to be zeroed
+          const int done = kb * kBlockK, row = t.row0 + done, from = min(t.rows - done, kBlockK) - kBlockK;
           expect_bytes(bar, bytes);
-          if (na > 0) load_2d(a, ma, m, row, bar);
-          if (na > 1) load_2d(a + kChunkBytes, ma, m + 64, row, bar);
-          if (nb > 0) load_2d(b, mb, n, row, bar);
-          if (nb > 1) load_2d(b + kChunkBytes, mb, n + 64, row, bar);
+          if (na > 0) load_3d(a, ma, m, from, row, bar);
+          if (na > 1) load_3d(a + kChunkBytes, ma, m + 64, from, row, bar);
+          if (nb > 0) load_3d(b, mb, n, from, row, bar);
+          if (nb > 1) load_3d(b + kChunkBytes, mb, n + 64, from, row, bar);
         } else {
           int k0 = kb * kBlockK;
           if (kMode == kDgradRows && kb >= p.half_kb) k0 -= p.half_kb * kBlockK;
@@ -578,8 +557,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t st = 0, ph = 0, unit = 0;
       bool ok = true;
       for (int item = first; item < total && ok; item += step) {
-        const int rows = reduction_rows<kMode>(p, s_off, item), blocks = blocks_of(rows), nch = chains_of(blocks);
-        const bool tail_end = kMode == kWgrad && rows % kBlockK != 0;   // the item's last block has been zeroed in part
+        const int blocks = blocks_of(reduction_rows<kMode>(p, s_off, item)), nch = chains_of(blocks);
         for (int ch = 0; ch < nch && ok; ++ch, ++unit) {
           const int nkb = part_of(blocks, nch, ch);
           const uint32_t buf = unit & 1u;
@@ -589,7 +567,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int kb = 0; kb < nkb; ++kb) {
             ok = __all_sync(0xffffffffu, wait_bounded(smem_u32(full + st), ph, p.status, s_abort));
             if (!ok) break;
-            if (tail_end && ch == nch - 1 && kb == nkb - 1) acquire_cluster(smem_u32(full + st), ph);
             tc_fence_after();
             const uint64_t so = (uint64_t)(st * (kStageBytes >> 4));
             mma_block<a_mn_major(kMode) ? 128u : 2u, b_mn_major(kMode) ? 128u : 2u>(tmem + buf * kTileN, da0 + so, db0 + so, idesc,
@@ -597,35 +574,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (++st == kStages) { st = 0; ph ^= 1u; }
           }
           if (ok) commit_pair(smem_u32(acc_full + buf));
-        }
-      }
-    }
-  } else if (warp == kZeroWarp) {
-    // ---------------- zeros behind the end of a segment ----------------
-    if constexpr (kMode == kWgrad) {
-      uint32_t at = 0, phases = 0;   // blocks passed; phase of each tail barrier
-      bool ok = true;
-      for (int item = first; item < total && ok; item += step) {
-        const int rows = reduction_rows<kMode>(p, s_off, item);
-        at += blocks_of(rows);
-        const int have = rows % kBlockK;
-        if (have == 0) continue;
-        const uint32_t st = (at - 1) % kStages;
-        ok = __all_sync(0xffffffffu, wait_bounded(smem_u32(tail + st), (phases >> st) & 1u, p.status, s_abort));
-        if (!ok) break;
-        phases ^= 1u << st;
-        uint8_t* base = smem + st * kStageBytes;
-        const int n16 = (kBlockK - have) * 8;   // 16-byte pieces of the rows to clear (a swizzle stays inside its row)
-        for (int c = 0; c < kStageBytes / kChunkBytes; ++c)
-          for (int i = lane; i < n16; i += 32)
-            *reinterpret_cast<uint4*>(base + c * kChunkBytes + have * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-        // The MMAs that read the zeros are CTA 0's, and CTA 1's half of B is an operand of both halves of the tile: CTA 1's
-        // stores are released to the cluster, CTA 0's have only its own MMA warp to reach.
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (rank == 0) mbar_arrive(smem_u32(full + st));
-          else arrive_release_cluster(leader_addr(smem_u32(full + st)));
         }
       }
     }
@@ -791,6 +739,17 @@ bool make_map(CUtensorMap* m, const void* ptr, int64_t d0, int64_t d1, int64_t d
   return encoder()(m, kSize == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d2 ? 3 : 2, const_cast<void*>(ptr), dims, strides, box, estr,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, width == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The weights' gradients' operand [R, cols]: the 64 rows from any row on as a dimension of their own (its stride is a row,
+// as the next dimension's), so that a box from coordinate -z of it holds z rows of zeros and then the 64 - z rows from the
+// last coordinate on: a segment's last block, nothing of its neighbour read.  The rows' order in a block is
+// free, as both operands have the same.
+bool window_map(CUtensorMap* m, const void* ptr, int64_t cols, int64_t R) {
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, kBlockK, (cuuint64_t)R}, strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)cols * 2};
+  const cuuint32_t box[3] = {64, kBlockK, 1}, estr[3] = {1, 1, 1};
+  return encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <Mode kMode>
@@ -983,9 +942,8 @@ int moe_experts_weight_grad(const void* rows, const void* dout, const void* h, c
     if (!is_aligned(p, 16)) return MOE_ERR_INVALID_ARG;
   if (!encoder()) return MOE_ERR_CUDA;
   Maps m = {};
-  const bool ok = make_map(&m.m[0], sh.gated ? dg : du, I, R, 0, kBlockK) && make_map(&m.m[1], rows, H, R, 0, kBlockK) &&
-                  make_map(&m.m[2], du, I, R, 0, kBlockK) && make_map(&m.m[3], dout, H, R, 0, kBlockK) &&
-                  make_map(&m.m[4], h, I, R, 0, kBlockK) && make_map<4>(&m.out[0], sh.gated ? dw_gate : dw_up, H, I, E, 32) &&
+  const bool ok = window_map(&m.m[0], sh.gated ? dg : du, I, R) && window_map(&m.m[1], rows, H, R) && window_map(&m.m[2], du, I, R) &&
+                  window_map(&m.m[3], dout, H, R) && window_map(&m.m[4], h, I, R) && make_map<4>(&m.out[0], sh.gated ? dw_gate : dw_up, H, I, E, 32) &&
                   make_map<4>(&m.out[1], dw_up, H, I, E, 32) && make_map<4>(&m.out[2], dw_down, I, H, E, 32);
   if (!ok) return MOE_ERR_CUDA;
   Args a = base_args(sh, offsets, workspace, 0.0f, 0.0f);

@@ -47,3 +47,38 @@ def test_neighbours_stay_out(moe, H, I):
     for _ in range(20):
         again = moe.experts_weight_grad(x, dout, {"h": h}, {"dg": dg, "du": du}, plan, workspace=ws)
         assert all(torch.equal(again[k].view(torch.int32), first[k].view(torch.int32)) for k in first)
+
+
+def test_one_long_ragged_segment(moe):
+    """One expert of 6e8 + 37 narrow rows, 2.5 s of products: no wait of the kernel lasts that long, as none spans more than
+    a block or a chain.  Whole numbers in a few rows: the sums are exact."""
+    if torch.cuda.mem_get_info()[0] < 60 * 2 ** 30:
+        pytest.skip("needs 60 GB of device memory")
+    R = 600_000_037
+    x = torch.zeros(R, 32, dtype=BF16, device="cuda")
+    at = torch.tensor([0, 63, 64, 2 ** 28 + 5, R // 2, R - 38, R - 37, R - 36, R - 1], device="cuda")
+    x[at] = torch.randint(-8, 9, (len(at), 32), device="cuda", generator=torch.Generator(device="cuda").manual_seed(5)).to(BF16)
+    some = x[at].double()
+    plan = {"offsets": torch.tensor([0, R], dtype=torch.int32, device="cuda")}
+    ws = moe.experts_workspace(0, 32)
+    w = moe.experts_weight_grad(x, x, {"h": x}, {"du": x}, plan, workspace=ws)
+    assert moe.last_device_status(ws) == 0
+    for name in ("w_up", "w_down"):
+        assert torch.equal(w[name][0].double(), some.t() @ some)
+    del x
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("lens", [[1], [63, 65], [5, 1, 2], [0, 0, 17, 0, 700]])
+def test_first_and_last_rows_of_the_tensors(moe, lens):
+    """Segments whose last block is also the first rows, or the last ones, of the tensors."""
+    g = torch.Generator(device="cuda").manual_seed(sum(lens))
+    off = torch.tensor([0] + lens).cumsum(0)
+    R = int(off[-1])
+    x, d, h, du = (torch.randn(R, w, device="cuda", generator=g).to(BF16) for w in (160, 160, 96, 96))
+    w = moe.experts_weight_grad(x, d, {"h": h}, {"du": du}, {"offsets": off.to(torch.int32).cuda()})
+    for name, left, right in (("w_up", du, x), ("w_down", d, h)):
+        for e in range(len(lens)):
+            a, b = (t[off[e]:off[e + 1]].double() for t in (left, right))
+            bound = (44 * STEP + 2 * U) * (a.abs().t() @ b.abs())
+            assert bool(((w[name][e].double() - a.t() @ b).abs() <= bound).all()), (name, e)
