@@ -316,8 +316,8 @@ int moe_plan(const float* logits, int32_t T, int32_t E, int32_t k, int32_t* topk
  * of dy[t] and rows[inv[t*k+j]], 0 without a row.  drows may be the buffer of rows; rows of drows that no
  * assignment names stay as they were.
  * In all three an inv outside [0, R) stands for no row (its weight is not read), and two assignments may
- * not name the same row.  x, y, rows 16-byte aligned, the rest 4; but for drows no output may overlap an
- * input.  One launch each, no workspace.
+ * not name the same row.  x, y, rows 16-byte aligned, the rest 4; but for drows in the place of rows no output may
+ * overlap an input (rows == x, y == rows and drows == dy are MOE_ERR_INVALID_ARG).  One launch each, no workspace.
  * ------------------------------------------------------------------------------------------- */
 size_t moe_sort_tokens_workspace_size(int32_t T, int32_t E, int32_t k);
 int moe_sort_tokens(const int32_t* topk_ids, const uint8_t* mask, int32_t T, int32_t E, int32_t k,

@@ -384,7 +384,7 @@ int moe_combine_rows_backward(const void* dy, const void* rows, const int32_t* i
   if (R < 0) return MOE_ERR_INVALID_ARG;
   if (R > INT32_MAX) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (T == 0) return MOE_OK;
-  if (!dy || !inv || !topk_w || !dtopk_w || ((!rows || !drows) && R > 0)) return MOE_ERR_INVALID_ARG;
+  if (!dy || dy == drows || !inv || !topk_w || !dtopk_w || ((!rows || !drows) && R > 0)) return MOE_ERR_INVALID_ARG;
   for (const void* p : {dy, rows, (const void*)drows})
     if (!is_aligned(p, 16)) return MOE_ERR_INVALID_ARG;
   if (!is_aligned(inv, 4) || !is_aligned(topk_w, 4) || !is_aligned(dtopk_w, 4)) return MOE_ERR_INVALID_ARG;
