@@ -349,7 +349,7 @@ int moe_permute_rows(const void* x, const int32_t* inv, int32_t T, int32_t k, in
   if (T == 0 || R == 0) return MOE_OK;
   if (!x || !inv || !rows || x == rows || !is_aligned(x, 16) || !is_aligned(rows, 16) || !is_aligned(inv, 4)) return MOE_ERR_INVALID_ARG;
   const int nvec = (int)(row_bytes / 16), span = row_span(nvec), per = 256 / span;
-  const cudaError_t e = launch_pdl(permute_kernel, dim3((unsigned)((T + per - 1) / per), (unsigned)((nvec + span - 1) / span)),
+  const cudaError_t e = launch_pdl(permute_kernel, dim3((unsigned)(((int64_t)T + per - 1) / per), (unsigned)((nvec + span - 1) / span)),
                                    dim3(256), 0, reinterpret_cast<cudaStream_t>(stream), static_cast<const uint4*>(x), inv,
                                    (int)T, (int)k, R, nvec, span, static_cast<uint4*>(rows));
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
@@ -368,7 +368,7 @@ int moe_combine_rows(const void* rows, const int32_t* inv, const float* topk_w, 
     return MOE_ERR_INVALID_ARG;
   const int nvec = (int)(cols / (f32 ? 4 : 8)), span = row_span(nvec), per = 256 / span;
   const cudaError_t e = launch_pdl(f32 ? combine_kernel<true> : combine_kernel<false>,
-                                   dim3((unsigned)((T + per - 1) / per), (unsigned)((nvec + span - 1) / span)), dim3(256), 0,
+                                   dim3((unsigned)(((int64_t)T + per - 1) / per), (unsigned)((nvec + span - 1) / span)), dim3(256), 0,
                                    reinterpret_cast<cudaStream_t>(stream), static_cast<const uint4*>(rows), inv, topk_w, (int)T,
                                    (int)k, R, nvec, span, static_cast<uint4*>(y));
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
