@@ -220,11 +220,12 @@ __global__ void __launch_bounds__(256) combine_kernel(const uint4* __restrict__ 
   y[t * nvec + c] = o;
 }
 
-// A warp an assignment.  The k warps of a token read its dy after one another, from L2 or L1.
+// A warp an assignment.  The k warps of a token read its dy after one another, from L2 or L1.  drows may be the buffer of
+// rows: a thread reads a vector of it before it alone writes it, four vectors ahead.
 template <bool kF32>
 __global__ void __launch_bounds__(256) combine_backward_kernel(
-    const uint4* __restrict__ dy, const uint4* __restrict__ rows, const int32_t* __restrict__ inv,
-    const float* __restrict__ w, int64_t A, int k, int64_t R, int nvec, uint4* __restrict__ drows,
+    const uint4* __restrict__ dy, const uint4* rows, const int32_t* __restrict__ inv,
+    const float* __restrict__ w, int64_t A, int k, int64_t R, int nvec, uint4* drows,
     float* __restrict__ dw) {
   griddep_wait();
   griddep_launch();
@@ -241,29 +242,40 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(
   uint4* dst = drows + p * nvec;
   const float wa = __ldg(w + a);
   float s = 0.0f;
-#pragma unroll 4
-  for (int c = lane; c < nvec; c += 32) {
-    const uint4 qd = __ldg(d + c), qr = __ldg(src + c);
-    uint4 o;
-    if constexpr (kF32) {
-      const float fd[4] = {__uint_as_float(qd.x), __uint_as_float(qd.y), __uint_as_float(qd.z), __uint_as_float(qd.w)};
-      const float fr[4] = {__uint_as_float(qr.x), __uint_as_float(qr.y), __uint_as_float(qr.z), __uint_as_float(qr.w)};
+  for (int c0 = lane; c0 < nvec; c0 += 4 * 32) {
+    uint4 qd[4], qr[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s = fmaf(fd[i], fr[i], s);
-      o = make_uint4(__float_as_uint(wa * fd[0]), __float_as_uint(wa * fd[1]), __float_as_uint(wa * fd[2]),
-                     __float_as_uint(wa * fd[3]));
-    } else {
-      float fd[8], fr[8];
-      unpack8(qd, fd);
-      unpack8(qr, fr);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        s = fmaf(fd[i], fr[i], s);
-        fd[i] *= wa;
-      }
-      o = pack8(fd);
+    for (int i = 0; i < 4; ++i) {
+      const int c = c0 + i * 32;
+      if (c >= nvec) continue;
+      qd[i] = __ldg(d + c);
+      qr[i] = src[c];
     }
-    dst[c] = o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = c0 + i * 32;
+      if (c >= nvec) continue;
+      uint4 o;
+      if constexpr (kF32) {
+        const float fd[4] = {__uint_as_float(qd[i].x), __uint_as_float(qd[i].y), __uint_as_float(qd[i].z), __uint_as_float(qd[i].w)};
+        const float fr[4] = {__uint_as_float(qr[i].x), __uint_as_float(qr[i].y), __uint_as_float(qr[i].z), __uint_as_float(qr[i].w)};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s = fmaf(fd[e], fr[e], s);
+        o = make_uint4(__float_as_uint(wa * fd[0]), __float_as_uint(wa * fd[1]), __float_as_uint(wa * fd[2]),
+                       __float_as_uint(wa * fd[3]));
+      } else {
+        float fd[8], fr[8];
+        unpack8(qd[i], fd);
+        unpack8(qr[i], fr);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          s = fmaf(fd[e], fr[e], s);
+          fd[e] *= wa;
+        }
+        o = pack8(fd);
+      }
+      dst[c] = o;
+    }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);

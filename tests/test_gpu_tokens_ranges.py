@@ -59,3 +59,26 @@ def test_sort_of_most_tokens(moe):
     assert torch.equal(p, plan["offsets"].long()[a % 3] + a // 3) and torch.equal(plan["perm_src"][p].long(), a)
     del ids, plan
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,cols,k", [(1, 8, 1), (3000, 1032, 1), (2500, 4096, 4), (700, 16392, 2)])
+def test_gradients_over_the_rows(moe, dtype, T, cols, k):
+    """drows in the buffer of rows: the bits of a call with a buffer of its own, at sizes with many rows an SM."""
+    g = torch.Generator(device="cuda").manual_seed(T + cols)
+    ids = torch.rand(T, 16, device="cuda", generator=g).topk(k, -1).indices.to(torch.int32)
+    plan = moe.sort_tokens(ids, 16, mask=torch.arange(T, device="cuda") % 7 != 3)
+    n = int(plan["offsets"][-1])
+    dy, rows = (torch.randn(r, cols, device="cuda", generator=g).to(dtype) for r in (T, T * k))
+    rows[n:] = float("nan")
+    w = torch.rand(T, k, device="cuda", generator=g)
+    want = moe.combine_tokens_backward(dy, rows, plan, w)
+    for _ in range(3):
+        own = rows.clone()
+        got = moe.combine_tokens_backward(dy, own, plan, w, out={"drows": own, "dtopk_w": torch.empty_like(w)})
+        assert torch.equal(got["drows"][:n], want["drows"][:n]) and torch.equal(got["dtopk_w"], want["dtopk_w"])
+        assert bool(own[n:].isnan().all())
+    inv = plan["inv"].long().reshape(T, k)
+    keep = inv >= 0
+    exact = (w.double()[..., None] * dy.double()[:, None])[keep]
+    assert bool(((got["drows"][inv[keep]].double() - exact).abs() <= (HALF[dtype] + 2.0 ** -23) * exact.abs()).all())
