@@ -446,9 +446,11 @@ __global__ void __launch_bounds__(512, 1) add_layernorm_backward_kernel(
 }
 
 // ---- few rows (forward): one row a block, loaded straight into registers ----
+//
+// h may be the buffer of x or residual: a thread has read its vectors of both before it writes any.
 template <typename V, int J>
 __global__ void __launch_bounds__(1024, 1) add_layernorm_row_kernel(
-    const V* __restrict__ x, const V* __restrict__ residual, const V* __restrict__ gamma,
+    const V* x, const V* residual, const V* __restrict__ gamma,
     const V* __restrict__ beta, float eps, int cols, V* h, V* y, float* mean, float* rstd) {
   __shared__ Share red[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, span = blockDim.x, W = span / 32, nvec = cols / 8;
@@ -457,27 +459,31 @@ __global__ void __launch_bounds__(1024, 1) add_layernorm_row_kernel(
   griddep_launch();
   const int64_t base = (int64_t)blockIdx.x * nvec;
   const V zero = {};
-  V g[J], b[J];
+  V q[J], e[J], g[J], b[J];
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int c = j * span + threadIdx.x;
+    const bool in = c < nvec;
+    q[j] = in ? x[base + c] : zero;
+    e[j] = in && residual ? residual[base + c] : zero;
+  }
   float2 f[J][4], sum = both(0.0f);
   int mine = 0;
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     const int c = j * span + threadIdx.x;
-    const bool in = c < nvec;
-    V q = in ? x[base + c] : zero;
-    const V e = in && residual ? residual[base + c] : zero;
-    g[j] = in ? gamma[c] : zero;
-    b[j] = in && beta ? beta[c] : zero;
-    if (residual && in) {
+    g[j] = c < nvec ? gamma[c] : zero;
+    b[j] = c < nvec && beta ? beta[c] : zero;
+    if (residual && c < nvec) {
       float2 d[4];
-      unpack(q, f[j]);
-      unpack(e, d);
+      unpack(q[j], f[j]);
+      unpack(e[j], d);
 #pragma unroll
       for (int i = 0; i < 4; ++i) f[j][i] = add2(f[j][i], d[i]);
-      pack(f[j], q);
-      h[base + c] = q;
+      pack(f[j], q[j]);
+      h[base + c] = q[j];
     }
-    unpack(q, f[j]);
+    unpack(q[j], f[j]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) sum = add2(sum, f[j][i]);
     mine += 8 * min(max(nvec - (j * span + warp * 32), 0), 32);
