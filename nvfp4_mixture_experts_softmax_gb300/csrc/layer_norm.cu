@@ -46,14 +46,35 @@ struct NormGrid {
 // everything else; arithmetic goes in pairs (f32x2), as instructions, not bytes, are what is short: one
 // vector a lane and scalar arithmetic took 92 and 101 us for 16384 x 4096 and 8191 x 7168 backward, two rows a
 // barrier or not.  slots == 1 (rows so wide that two do not fit): the row ends in a barrier before its slot is filled.
+//
+// A thread whose wait for a row runs out sets the block's `stop`: the block's rows from there on become NaN (h, which is stored
+// before the row's barrier, at the end), issuers start no more copies (a row's slot is filled again behind the next row's
+// barrier, so a read of `stop` between the row's own barrier and that is in time), the threads that then wait in vain
+// give up too, and at the end each issuer waits, again with a limit, for the copies that it did start, before their
+// memory is used for anything else or left.
 
 constexpr uint64_t kCopyLimitNs = 1000000000ull;
+
+// The wait for a row that has not landed yet; false if it ran out, here or elsewhere in the block.  Out of line: inside the loop
+// over rows its code costs the forward pass of 8191 x 7168 73.5 us instead of 71.1.
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t phase, volatile uint32_t* stop) {
+  const uint64_t t0 = global_timer_ns();
+  for (;;) {
+    if (mbar_try_wait(bar, phase)) return true;
+    if (*stop) return false;
+    if (global_timer_ns() - t0 > kCopyLimitNs) {
+      *stop = 1u;
+      return false;
+    }
+  }
+}
 
 struct Ring {
   uint32_t data, bars;     // shared addresses of the group's slots and their barriers
   uint32_t row_bytes;      // of one tensor
   int slots, group, G, W;
   bool issuer;             // the group's thread that starts the copies
+  volatile uint32_t* stop; // the block's: a wait has run out
 
   template <int kN>
   __device__ __forceinline__ uint32_t at(uint32_t s, int tensor) const {
@@ -69,7 +90,13 @@ struct Ring {
   }
   // The row of a slot has landed; false if the wait ran out.
   __device__ __forceinline__ bool landed(uint32_t s, uint32_t phase) const {
-    return mbar_wait_bounded(bars + 8 * s, phase, kCopyLimitNs, nullptr);
+    return mbar_try_wait(bars + 8 * s, phase) || wait_on(bars + 8 * s, phase, stop);
+  }
+  // The first `issued` rows' copies have ended (the issuer, after a stop): slot s was filled last by row
+  // s + k * slots, in phase k.
+  __device__ void drain(int issued) const {
+    for (int s = 0; s < min(slots, issued); ++s)
+      mbar_wait_bounded(bars + 8 * s, (uint32_t)((issued - 1 - s) / slots) & 1u, kCopyLimitNs, nullptr);
   }
   __device__ __forceinline__ void barrier() const {
     if (W == 1) __syncwarp();
@@ -86,8 +113,11 @@ int ring_slots(int G, size_t slot_bytes, size_t want, int least) {
 }
 size_t ring_bytes(int G, int slots, size_t slot_bytes) { return 2048 + (size_t)G * slots * slot_bytes; }
 
-__device__ __forceinline__ Ring make_ring(uint8_t* smem, uint32_t row_bytes, int tensors, int slots, int group, int G, int W, int t) {
+__device__ __forceinline__ Ring make_ring(uint8_t* smem, uint32_t* stop, uint32_t row_bytes, int tensors, int slots, int group, int G, int W,
+                                          int t) {
   Ring r;
+  r.stop = stop;
+  if (threadIdx.x == 0) *stop = 0u;
   r.bars = smem_u32(smem) + (uint32_t)group * slots * 8;   // (32 groups of 8 slots at most: 2 KB)
   r.data = smem_u32(smem) + 2048 + (uint32_t)group * slots * tensors * row_bytes;
   r.row_bytes = row_bytes;
@@ -103,6 +133,11 @@ __device__ __forceinline__ Ring make_ring(uint8_t* smem, uint32_t row_bytes, int
   return r;
 }
 
+__device__ __forceinline__ void set_nan(uint4& q) { q = make_uint4(~0u, ~0u, ~0u, ~0u); }
+__device__ __forceinline__ void set_nan(F32x8& q) {
+  const float v = __int_as_float(0x7FC00000);
+  q.a = q.b = make_float4(v, v, v, v);
+}
 __device__ __forceinline__ void read_vec(uint32_t addr, uint4& q) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(addr) : "memory");
 }
@@ -181,21 +216,23 @@ __global__ void __launch_bounds__(512, 1) add_layernorm_kernel(
     int64_t rows, int cols, int W, int G, int slots, V* h, V* y, float* mean, float* rstd) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Share red[2][16];
+  __shared__ uint32_t s_stop;
   constexpr bool kWide = J > 3;   // gamma and beta are read again for each row
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = warp / W, wrow = warp - group * W;
   const int t = wrow * 32 + lane, span = W * 32;   // thread of the row, vectors apart
   const int nvec = cols / 8;
   const float inv_cols = __fdiv_rn(1.0f, (float)cols);
   const int tensors = residual ? 2 : 1;
-  const Ring ring = make_ring(smem, (uint32_t)cols * (sizeof(V) / 8), 2, slots, group, G, W, t);
+  const Ring ring = make_ring(smem, &s_stop, (uint32_t)cols * (sizeof(V) / 8), 2, slots, group, G, W, t);
   __syncthreads();
   griddep_wait();
   griddep_launch();
   const int64_t row0 = (int64_t)blockIdx.x * G + group, step = (int64_t)gridDim.x * G;
   const int count = row0 < rows ? (int)((rows - row0 + step - 1) / step) : 0;   // rows of the group
   const void* const src[2] = {x, residual};
+  int issued = min(slots, count);   // rows whose copies have been started
   if (ring.issuer)
-    for (int n = 0; n < min(slots, count); ++n) ring.fetch<2>(n, src, tensors, row0 + n * step);
+    for (int n = 0; n < issued; ++n) ring.fetch<2>(n, src, tensors, row0 + n * step);
   const V zero = {};
   auto gain = [&](int c, float2 (&f)[4]) { unpack(c < nvec ? gamma[c] : zero, f); };
   auto bias = [&](int c, float2 (&f)[4]) { unpack(c < nvec && beta ? beta[c] : zero, f); };
@@ -209,6 +246,7 @@ __global__ void __launch_bounds__(512, 1) add_layernorm_kernel(
     }
     mine += 8 * min(max(nvec - (j * span + wrow * 32), 0), 32);
   }
+  int lost = count;   // first of the group's rows that was lost
   const float wn = (float)mine, inv_wn = mine ? __fdiv_rn(1.0f, wn) : 0.0f;
   bool ok = true;
   uint32_t phase = 0;
@@ -250,12 +288,19 @@ __global__ void __launch_bounds__(512, 1) add_layernorm_kernel(
       }
     }
     const float wd = warp_sum(dist.x + dist.y);
-    if (lane == 0) red[par][warp] = Share{wn, ok ? ws : __int_as_float(0x7FC00000), wm, wd};
+    if (lane == 0) red[par][warp] = Share{wn, ws, wm, wd};
     ring.barrier();
-    if (ring.issuer && n > 0 && slots > 1 && n - 1 + slots < count)   // the slot of the row before
+    const bool stopped = *ring.stop;
+    if (ring.issuer && n > 0 && slots > 1 && n - 1 + slots < count && !stopped) {   // the slot of the row before
       ring.fetch<2>(s ? s - 1 : slots - 1, src, tensors, row0 + (int64_t)(n - 1 + slots) * step);
+      ++issued;
+    }
     const Share w = lane < W ? red[par][group * W + lane] : Share{0.0f, 0.0f, 0.0f, 0.0f};
-    const float m = warps_sum(w.sum) * inv_cols;
+    float m = warps_sum(w.sum) * inv_cols;
+    if (stopped) {
+      m = __int_as_float(0x7FC00000);
+      lost = min(lost, n);
+    }
     const float var = warps_sum(fmaf(w.n * (w.mean - m), w.mean - m, w.dist)) * inv_cols;
     const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(var, eps)));
     if (t == 0) {
@@ -279,13 +324,23 @@ __global__ void __launch_bounds__(512, 1) add_layernorm_kernel(
     }
     if (slots == 1) {
       ring.barrier();
-      if (ring.issuer && n + 1 < count) ring.fetch<2>(0, src, tensors, row0 + (int64_t)(n + 1) * step);
+      if (ring.issuer && n + 1 < count && !*ring.stop) {
+        ring.fetch<2>(0, src, tensors, row0 + (int64_t)(n + 1) * step);
+        ++issued;
+      }
     }
     if (++s == slots) {
       s = 0;
       phase ^= 1u;
     }
   }
+  if (*ring.stop && residual) {
+    V q;
+    set_nan(q);
+    for (int n = lost; n < count; ++n)
+      for (int c = t; c < nvec; c += span) h[(row0 + n * step) * nvec + c] = q;
+  }
+  if (ring.issuer && *ring.stop) ring.drain(issued);
 }
 
 // A thread owns the same J vectors of 8 columns in all rows of its group and keeps their share of dgamma
@@ -297,21 +352,23 @@ __global__ void __launch_bounds__(512, 1) add_layernorm_backward_kernel(
     float4* __restrict__ partial) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float2 red[2][16];
+  __shared__ uint32_t s_stop;
   constexpr bool kKeep = J <= 2;   // a and n stay in registers over the barrier, else they are computed again
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = warp / W, wrow = warp - group * W;
   const int t = wrow * 32 + lane, span = W * 32;
   const int nvec = cols / 8;
   const float inv_cols = __fdiv_rn(1.0f, (float)cols);
   const int tensors = dh ? 3 : 2;
-  const Ring ring = make_ring(smem, (uint32_t)cols * (sizeof(V) / 8), 3, slots, group, G, W, t);
+  const Ring ring = make_ring(smem, &s_stop, (uint32_t)cols * (sizeof(V) / 8), 3, slots, group, G, W, t);
   __syncthreads();
   griddep_wait();
   griddep_launch();
   const int64_t row0 = (int64_t)blockIdx.x * G + group, step = (int64_t)gridDim.x * G;
   const int count = row0 < rows ? (int)((rows - row0 + step - 1) / step) : 0;
   const void* const src[3] = {dy, h, dh};
+  int issued = min(slots, count);   // rows whose copies have been started
   if (ring.issuer)
-    for (int n = 0; n < min(slots, count); ++n) ring.fetch<3>(n, src, tensors, row0 + n * step);
+    for (int n = 0; n < issued; ++n) ring.fetch<3>(n, src, tensors, row0 + n * step);
   const V zero = {};
   float2 g[kKeep ? J : 1][4];
   auto gain = [&](int c, float2 (&f)[4]) { unpack(c < nvec ? gamma[c] : zero, f); };
@@ -349,6 +406,7 @@ __global__ void __launch_bounds__(512, 1) add_layernorm_backward_kernel(
     }
     ok = ok && ring.landed(s, phase);
     if (!ok) m = __int_as_float(0x7FC00000);
+    const bool more = !*ring.stop;
     float2 a[kKeep ? J : 1][4], nv[kKeep ? J : 1][4], sa = both(0.0f), sn = both(0.0f);
 #pragma unroll
     for (int j = 0; j < J; ++j) {
@@ -367,8 +425,10 @@ __global__ void __launch_bounds__(512, 1) add_layernorm_backward_kernel(
     const float2 share = make_float2(warp_sum(sa.x + sa.y), warp_sum(sn.x + sn.y));
     if (lane == 0) red[par][warp] = share;
     ring.barrier();
-    if (ring.issuer && n > 0 && slots > 1 && n - 1 + slots < count)   // the slot of the row before
+    if (ring.issuer && n > 0 && slots > 1 && n - 1 + slots < count && more) {   // the slot of the row before
       ring.fetch<3>(s ? s - 1 : slots - 1, src, tensors, row0 + (int64_t)(n - 1 + slots) * step);
+      ++issued;
+    }
     const float2 w = lane < W ? red[par][group * W + lane] : make_float2(0.0f, 0.0f);
     const float ma = warps_sum(w.x) * inv_cols, mn = warps_sum(w.y) * inv_cols;
     const int64_t base = (row0 + n * step) * nvec;
@@ -395,12 +455,23 @@ __global__ void __launch_bounds__(512, 1) add_layernorm_backward_kernel(
     }
     if (slots == 1) {
       ring.barrier();
-      if (ring.issuer && n + 1 < count) ring.fetch<3>(0, src, tensors, row0 + (int64_t)(n + 1) * step);
+      if (ring.issuer && n + 1 < count && !*ring.stop) {
+        ring.fetch<3>(0, src, tensors, row0 + (int64_t)(n + 1) * step);
+        ++issued;
+      }
     }
     if (++s == slots) {
       s = 0;
       phase ^= 1u;
     }
+  }
+  if (ring.issuer && *ring.stop) ring.drain(issued);
+  __syncthreads();
+  if (*ring.stop) {
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) dg[j][i] = db[j][i] = both(__int_as_float(0x7FC00000));
   }
   // the other groups' sums to the first's, in order, through the ring's memory
   float4* s_part = reinterpret_cast<float4*>(smem + 2048);   // [cols / 4]
