@@ -158,6 +158,14 @@ __device__ __forceinline__ float warps_sum(float v) {
   return __shfl_sync(0xffffffffu, v, 0);
 }
 
+// sum / cols, correctly rounded as a quotient by a corrected reciprocal is (div_rn_by_recip): the mean of a constant row is its
+// value, where sum * (1 / cols) is a step off for most cols, and a step of a large value is far from 0 against eps.  A sum that
+// is not finite stays.
+__device__ __forceinline__ float row_mean(float sum, float cols, float inv_cols) {
+  const float q = div_rn_by_recip(sum, cols, inv_cols);
+  return isfinite(sum) ? q : sum;
+}
+
 // Two FP32 operations an instruction.
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   float2 r;
@@ -296,7 +304,7 @@ __global__ void __launch_bounds__(512, 1) add_layernorm_kernel(
       ++issued;
     }
     const Share w = lane < W ? red[par][group * W + lane] : Share{0.0f, 0.0f, 0.0f, 0.0f};
-    float m = warps_sum(w.sum) * inv_cols;
+    float m = row_mean(warps_sum(w.sum), (float)cols, inv_cols);
     if (stopped) {
       m = __int_as_float(0x7FC00000);
       lost = min(lost, n);
@@ -574,7 +582,7 @@ __global__ void __launch_bounds__(1024, 1) add_layernorm_row_kernel(
   if (lane == 0) red[warp] = Share{(float)mine, ws, wm, wd};
   __syncthreads();
   const Share w = lane < W ? red[lane] : Share{0.0f, 0.0f, 0.0f, 0.0f};
-  const float m = warp_sum(w.sum) * inv_cols;
+  const float m = row_mean(warp_sum(w.sum), (float)cols, inv_cols);
   const float var = warp_sum(fmaf(w.n * (w.mean - m), w.mean - m, w.dist)) * inv_cols;
   const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(var, eps)));
   if (threadIdx.x == 0) {

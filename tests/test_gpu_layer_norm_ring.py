@@ -31,3 +31,17 @@ def test_in_place(moe, rows, cols, dtype):
         out = {"h": (a, b)[place], "y": torch.full_like(x, float("nan"))}
         moe.add_layernorm(a, b, gamma, out=out)
         assert torch.equal(out["h"], want["h"]) and torch.equal(out["y"], want["y"])
+
+
+@pytest.mark.parametrize("rows,cols", [(40, 24), (300, 1000), (300, 7168), (40, 12296), (20000, 264), (9000, 1000), (2003, 5120), (1300, 12296)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_constant_rows(moe, rows, cols, dtype):
+    """Rows of one value of 8 significant bits: at most 16384 of them add up within FP32's 24 bits, in any order, so their mean is
+    the value itself and y is beta, however large the value is against eps."""
+    beta = normal(cols)(cols).to(dtype)
+    c = (torch.randint(129, 256, (rows, 1), device="cuda", generator=torch.Generator(device="cuda").manual_seed(cols)).float()
+         * torch.tensor([1.0, -0.25, 512.0], device="cuda").repeat(rows)[:rows, None])
+    x = c.to(dtype).expand(rows, cols).contiguous()
+    o = moe.add_layernorm(x, None, torch.ones(cols, device="cuda").to(dtype), beta, 1e-12, want_stats=True)
+    assert torch.equal(o["mean"], c[:, 0])
+    assert torch.equal(o["y"], beta.expand(rows, cols))
