@@ -82,3 +82,25 @@ def test_first_and_last_rows_of_the_tensors(moe, lens):
             a, b = (t[off[e]:off[e + 1]].double() for t in (left, right))
             bound = (44 * STEP + 2 * U) * (a.abs().t() @ b.abs())
             assert bool(((w[name][e].double() - a.t() @ b).abs() <= bound).all()), (name, e)
+
+
+@pytest.mark.parametrize("H,I", [(96, 160), (256, 512)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_chains(moe, H, I, accumulate):
+    """Segments at the edges of one, two and more chains: eleven blocks of 64 rows are one chain, twelve are two."""
+    lens = [704, 705, 703, 64, 1216, 1217, 0, 2049, 5000]
+    g = torch.Generator(device="cuda").manual_seed(H)
+    off = torch.tensor([0] + lens).cumsum(0)
+    R = int(off[-1])
+    x, d, h, dg, du = (torch.randn(R, w, device="cuda", generator=g).to(BF16) for w in (H, H, I, I, I))
+    before = {k: torch.randn(len(lens), *s, device="cuda", generator=g) for k, s in (("w_gate", (I, H)), ("w_up", (I, H)), ("w_down", (H, I)))}
+    out = {k: v.clone() for k, v in before.items()}
+    w = moe.experts_weight_grad(x, d, {"h": h}, {"dg": dg, "du": du}, {"offsets": off.to(torch.int32).cuda()}, accumulate=accumulate, out=out)
+    for name, left, right in (("w_gate", dg, x), ("w_up", du, x), ("w_down", d, h)):
+        for e, rows in enumerate(lens):
+            a, b = (t[off[e]:off[e + 1]].double() for t in (left, right))
+            old = before[name][e].double() if accumulate else torch.zeros((), dtype=torch.float64, device="cuda")
+            chains = (((rows + 63) // 64) + 4) // 8
+            size = a.abs().t() @ b.abs()
+            bound = (44 * STEP + (chains + 1) * U) * size + U * old.abs()
+            assert bool(((w[name][e].double() - a.t() @ b - old).abs() <= bound).all()), (name, e)
