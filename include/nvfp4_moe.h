@@ -264,9 +264,9 @@ int moe_add_rmsnorm_backward(const void* dy, const void* dh, const void* h, cons
  *   16-byte aligned, cols a multiple of 8, at most 16384; mean, rstd: NULL or device FP32 [rows] (m and s).
  *   residual and h are both given or both NULL (then h is x itself); beta NULL: none.  h may be the buffer
  *   of residual or of x (in place); no other two buffers may overlap.
- * A NaN or infinity makes its own row NaN; squared distances are summed in FP32, so rows that spread over more than
- * 2^63 overflow (s = 0).  A block whose wait for its own copies runs out (about a second) leaves NaN, here and in
- * the backward pass.  No workspace, one launch.  rows == 0 is MOE_OK. */
+ * A NaN or infinity makes its own row NaN; elements and squared distances are summed in FP32, so a row whose sum
+ * overflows becomes NaN and one that spreads over more than 2^63 has s = 0.  A block whose wait for its own copies runs
+ * out (about a second) leaves NaN from that row on, here and in the backward pass, whose sums over rows are NaN then.  No workspace, one launch.  rows == 0 is MOE_OK. */
 #define MOE_ROWS_F32 1u
 int moe_add_layernorm(const void* x, const void* residual, const void* gamma, const void* beta,
                       float eps, int64_t rows, int64_t cols, uint32_t flags, void* h, void* y,
@@ -347,7 +347,8 @@ int moe_combine_rows_backward(const void* dy, const void* rows, const int32_t* i
  *             segment; overwritten (zeros for an expert without rows) or, with MOE_EXPERTS_ACCUMULATE in
  *             flags, added to (by the memory system, which may take subnormal values for zero).
  * All BF16 tensors: products accumulate in FP32, one rounding at the end.  The tensor cores truncate where they
- * add; the weights' gradients are cut into chains of at most 44 such additions.  All sums run in a fixed order.
+ * add: K / 16 additions an element (at most 2^-22 of the terms' magnitudes each) before the rounding to BF16, in the
+ * weights' gradients, which stay FP32, chains of at most 44.  All sums run in a fixed order.
  * Rows from offsets[E] on are neither used (they may hold anything) nor written; NaN and infinities
  * stay in their row, in the weights' gradients in their segment.
  * H, I multiples of 32, at most 65536; E <= 1024; R < 2^31 - 256.  Inputs 16-byte aligned, outputs, g and u 32-byte;

@@ -3,7 +3,10 @@
 //   forward      g = x Wg^T, u = x Wu^T, h = bf16(act(g, u)), out = h Wd^T
 //   backward     dh = dout Wd, (dg, du) = bf16(dh * act'(g, u)), dx = dg Wg + du Wu
 //   weights      dWg = dg^T x, dWu = du^T x, dWd = dout^T h   (FP32)
-// One kernel, a mode for each product.  The products accumulate in FP32 in tensor memory; h, dg and du
+// One kernel, a mode for each product.  The products accumulate in FP32 in tensor memory, where the tensor cores truncate; the
+// row modes leave that as one chain of K / 16 additions, since their results are rounded to BF16 (of K = 4096 0.2% of
+// the elements of g and u then round to the other neighbour than the exact sum, 0.035% after FP32 products that round; the
+// outputs' error against 64 bits is 1.67e-3 and 1.66e-3).  h, dg and du
 // are rounded to BF16 because the tensor cores read them again (and the backward pass as tensors of
 // its own), everything else is rounded once, where it is stored.
 //
@@ -21,7 +24,8 @@
 // What bounds it, device times: with rows enough the tensor cores (one expert, 8192 rows of 4096 x 4096: forward 1.92
 // PFLOP/s, gradients of the rows 1.74, of the weights 1.75); 64 experts of uneven size, 65536 rows of 4096 x 1536:
 // forward 1.49 ms (1.65 PFLOP/s: an eighth of the row tiles' rows lie behind their segment; 1.70 ms once the power cap
-// lowers the clock), weights' gradients 1.98 ms (1.25: 4.8 GB of FP32 results beside the operands' way from L2); few
+// lowers the clock), weights' gradients 1.95 to 2.0 ms (1.25: 4.8 GB of FP32 results beside the operands' way from L2), added to
+// earlier ones 2.65 ms (the results are read, too); few
 // rows an expert: reading the weights (64 tokens to 8 of 128 experts of 2048 x 768 194 us, 6.1 TB/s; one token 27 us;
 // gradients of the rows of 8192 tokens to 8 of 256 experts of 2048 x 512 435 us, 5.4 TB/s).
 //

@@ -9,10 +9,12 @@
 // dgamma_c = sum over rows of dy * n,  dbeta_c = sum over rows of dy.  Both row sums go over one barrier.
 //
 // Both are bound by HBM: every element is read and written once.  Device time of a call, share of the copy rate:
-// forward with a residual 16384 x 4096 81.8 us (97%), 8191 x 7168 72 us (96%), 12000 x 5120 82 us (88%), 20000 x 256
-// 12.6 us (47%), one row of 2048 1.8 us; backward with dh 16384 x 4096 84 us (94%), 8191 x 7168 83.5 us (83%: one group of 14
-// warps, whose row takes 1.5 us from its arrival to its last store), 12000 x 5120 93 us (78%), 20000 x 1024 33 us (72%).
-// 2.5 to 5 us of the backward pass are the join of the blocks' sums.
+// forward with a residual 16384 x 4096 81.8 us (97%), FP32 166 us (95%), 8191 x 7168 71.3 us (97%), 12000 x 5120 83 us (87%),
+// 20000 x 256 12.7 us (47%), one row of 2048 1.7 us; backward with dh 16384 x 4096 84 us (94%), FP32 without dh 133 us (89%),
+// 8191 x 7168 82.5 us (84%: one group of 14 warps, whose row takes 1.5 us from its arrival to its last store), 12000 x 5120 94 us
+// (77%), 20000 x 1024 33 us (73%).  Narrow rows wait: a row is a chain of a read, two reductions, a barrier and a store of about
+// 1.5 us (backward 1.8), and an SM works on 16 rows of 256 columns, 8 of 1024 at a time, so that 20000 rows are 8 to 16 such
+// chains, one after another.  2.5 to 5 us of the backward pass are the join of the blocks' sums.
 #include <algorithm>
 #include <cmath>
 

@@ -15,7 +15,8 @@
 // All three are traffic alone: a row is read once for its k copies, k rows for one sum, and the backward
 // pass makes one pass over the rows for both gradients.  Device times: sort and permute of 32768 x 2048 to 8 experts each
 // 189 us (89% of the copy rate; the sort 15 us of it: three launches that each wait for the one before), combine
-// 8192 x 7168 from 8 165 us (94%), combine backward 16384 x 4096 from 4 170 us (99%); one token of 2048: sort and permute
+// 8192 x 7168 from 8 165 us (94%), FP32 307 us (the copy rate), combine backward 16384 x 4096 from 4 165 us, FP32 327 us (the copy
+// rate); one token of 2048: sort and permute
 // 4.1 us; 64 x 7168 combined 2.8 us.
 #include "common.cuh"
 #include "ops.h"
