@@ -18,8 +18,8 @@
 // Wg, CTA 1 the same rows of Wu, so that each thread of the epilogue holds g and u of its row.
 //
 // Tiles of 256 rows of one segment: a tile's rows behind the segment are read and multiplied, but not
-// stored (rows do not mix).  In the weights' gradients the rows are the reduction, and a segment's last block has zeros in the
-// place of the rows that are not its own, in both operands (window_map below).
+// stored (rows do not mix).  In the weights' gradients the rows are the reduction: the last block of a
+// segment is zeroed behind the segment's end in shared memory, in both operands, before it is multiplied.
 //
 // What bounds it, device times: with rows enough the tensor cores (one expert, 8192 rows of 4096 x 4096: forward 1.92
 // PFLOP/s, gradients of the rows 1.74, of the weights 1.75); 64 experts of uneven size, 65536 rows of 4096 x 1536:
@@ -29,9 +29,10 @@
 // rows an expert: reading the weights (64 tokens to 8 of 128 experts of 2048 x 768 194 us, 6.1 TB/s; one token 27 us;
 // gradients of the rows of 8192 tokens to 8 of 256 experts of 2048 x 512 435 us, 5.4 TB/s).
 //
-// Warps of a CTA: 0-7 epilogue (each a quarter of the rows and half of the columns), 8 and 10 copies (every other
+// Warps of a CTA: 0-7 epilogue (each a quarter of the rows and half of the columns), 8 and 11 copies (every other
 // stage each: a load takes 100 cycles to issue, up to four a stage), 9 tensor memory and, in CTA 0, the MMAs of
-// the pair.  Two accumulators (2 x 256 columns) let the epilogue run beside the next tile's products.  Every wait is bounded; one that runs out leaves
+// the pair, 10 the zeroing.  Two accumulators (2 x 256 columns) let
+// the epilogue run beside the next tile's products.  Every wait is bounded; one that runs out leaves
 // MOE_ERR_DEVICE_TIMEOUT in the status.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -54,13 +55,14 @@ constexpr int kBlockK = 64;
 constexpr int kOperandBytes = kHalf * kBlockK * 2;
 constexpr int kChunkBytes = kBlockK * 128;      // MN-major: 64 columns (128 bytes) of 64 rows
 constexpr int kStageBytes = 2 * kOperandBytes;
-constexpr int kEpiWarps = 8, kCopyWarp = 8, kMmaWarp = 9, kCopyWarp2 = 10;
-constexpr int kThreads = 11 * 32;
+constexpr int kEpiWarps = 8, kCopyWarp = 8, kMmaWarp = 9, kZeroWarp = 10, kCopyWarp2 = 11;
+constexpr int kThreads = 12 * 32;
 constexpr int kMaxExperts = 1024;
 constexpr int kGroupM = 8;                      // row tiles that are worked through column by column (4, 8, 16: the weights'
                                                 // gradients of 64 experts 1974, 1961, 1986 us)
-// Rows of the small box.  Of a tile's half that is not full a CTA fetches boxes of so many rows, and zeros (boxes outside
-// the tensor) in the place of the rows behind the segment: they need less power when they are multiplied, and power is
+// Rows of the small box.  Of a tile's half that is not full a CTA fetches boxes of so many rows, and zeros in the place of the rows
+// behind the segment (boxes of the columns behind the last, from row 0 on: outside the tensor, but not at an address
+// outside its memory, as rows behind the last would be): they need less power when they are multiplied, and power is
 // what sets the clock under load (64 tokens to 8 of 128 experts 208 and 200 us, 4096 tokens to 8 of 64 experts of 7168 x 2048
 // 1980 and 1955 us).  Up to kFewRows rows in all no zeros, and one box where one holds the rows: the time of a few tokens is that of
 // their copies' issue (1 token 26.6 us against 34.9, 4 tokens 59.5 against 66.8; from 16 on no difference).
@@ -86,7 +88,7 @@ struct Layout {
   static constexpr int kBarOff = kSlabOff + kEpiWarps * 32 * kSlabWidth;
   static constexpr int kTableOff = kBarOff + 256;
   static constexpr size_t kBytes = 1024 + kTableOff + 2 * (kMaxExperts + 1) * sizeof(int32_t) + 8;
-  static_assert(kBytes <= 232448 && (2 * kStages + 4) * 8 + 12 <= 256, "shared memory");
+  static_assert(kBytes <= 232448 && (3 * kStages + 4) * 8 + 12 <= 256, "shared memory");
 };
 
 constexpr bool a_mn_major(Mode m) { return m == kWgrad; }
@@ -110,6 +112,7 @@ struct Args {
   int N;          // columns of the output (gate/up: of each)
   int M;          // kWgrad: H and N: I of the down matrix, the other way round for gate and up
   int n_tiles;    // column tiles
+  int K;          // columns of A (not kWgrad)
   int nkb;        // blocks of K = 64 of a tile (not kWgrad)
   int half_kb;    // kDgradRows: blocks of the first source
   int nmat;       // kWgrad: 3, or 2 without a gate
@@ -134,10 +137,27 @@ __device__ __forceinline__ uint32_t leader_addr(uint32_t bar) {
 }
 // Arrivals on a barrier of either CTA.  Release at CTA scope: what they order are TMA copies, MMAs and reads of
 // tensor memory, which complete on their own terms; at cluster scope each arrival would wait for the thread's
-// memory accesses (0.8 us a stage of the copies: a third of the rate).  No ordinary store to
-// shared memory is read by the other CTA or its MMAs.
+// memory accesses (0.8 us a stage of the copies: a third of the rate).  Ordinary stores do not complete on their own
+// terms: an arrival that announces them to the other CTA releases at cluster scope, and the wait for it acquires there.
 __device__ __forceinline__ void arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ void arrive_release_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+// One more poll of a phase that is known to be complete, for what it acquires.
+__device__ __forceinline__ bool acquire_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      "selp.u32 %0, 1, 0, p;\n"
+      "}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 // As mbar_wait_bounded; gives up as soon as another role of the CTA has.
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, int32_t* status,
@@ -148,6 +168,27 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, int3
     if (mbar_try_wait(bar, parity)) return true;
     if (*abort) return false;
     if (global_timer_ns() - t0 > kLimitNs) {
+      set_status(status, MOE_ERR_DEVICE_TIMEOUT);
+      *abort = 1u;
+      return false;
+    }
+  }
+}
+
+// The same where many blocks pass before the phase completes (the zeroing warp's wait for the end of a segment, which may be
+// seconds long): the limit starts again whenever the ring is seen to have turned, by the phase of one of its barriers.
+__device__ __forceinline__ bool wait_while_turning(uint32_t bar, uint32_t parity, uint32_t beat, int32_t* status, volatile uint32_t* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  uint64_t t0 = global_timer_ns();
+  bool seen = mbar_test_wait(beat, 0);
+  for (;;) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    const bool now = mbar_test_wait(beat, 0);
+    if (now != seen) {
+      seen = now;
+      t0 = global_timer_ns();
+    } else if (global_timer_ns() - t0 > kLimitNs) {
       set_status(status, MOE_ERR_DEVICE_TIMEOUT);
       *abort = 1u;
       return false;
@@ -394,7 +435,7 @@ __device__ __forceinline__ Tile tile_at(const Args& p, const int32_t* s_off, con
   return t;
 }
 
-// Rows of the segment that an item's reduction runs over (kWgrad), all that the MMA warp needs to know.
+// Rows of the segment that an item's reduction runs over (kWgrad), all that the MMA and zeroing warps need to know.
 template <Mode kMode>
 __device__ __forceinline__ int reduction_rows(const Args& p, const int32_t* s_off, int item) {
   if (kMode != kWgrad) return 0;
@@ -411,7 +452,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);   // [stage], CTA 0's: both CTAs' data has landed
   uint64_t* empty = full + kStages;                               // [stage]: the MMAs have read it
-  uint64_t* acc_full = empty + kStages;                           // [2]
+  uint64_t* tail = empty + kStages;                               // [stage]: data that is to be zeroed has landed
+  uint64_t* acc_full = tail + kStages;                            // [2]
   uint64_t* acc_empty = acc_full + 2;                             // [2], CTA 0's
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
   volatile uint32_t* s_abort = tmem_slot + 1;
@@ -425,6 +467,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_u32(full + s), 2);    // one arrival of each CTA, and the bytes
       mbar_init(smem_u32(empty + s), 1);
+      mbar_init(smem_u32(tail + s), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(acc_full + b), 1);
@@ -517,14 +560,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, wait_bounded(smem_u32(empty + st), ph ^ 1u, p.status, s_abort));
         if (!ok) break;
         const uint32_t a = smem0 + st * kStageBytes, b = a + kOperandBytes;
-        const uint32_t bar = full0 + 8 * st;
+        uint32_t bar = full0 + 8 * st;
         if constexpr (kMode == kWgrad) {
-          const int done = kb * kBlockK, row = t.row0 + done, from = min(t.rows - done, kBlockK) - kBlockK;
+          const int done = kb * kBlockK, row = t.row0 + done;
+          if (done + kBlockK > t.rows) bar = smem_u32(tail + st);   // rows behind the segment are to be zeroed
           expect_bytes(bar, bytes);
-          if (na > 0) load_3d(a, ma, m, from, row, bar);
-          if (na > 1) load_3d(a + kChunkBytes, ma, m + 64, from, row, bar);
-          if (nb > 0) load_3d(b, mb, n, from, row, bar);
-          if (nb > 1) load_3d(b + kChunkBytes, mb, n + 64, from, row, bar);
+          if (na > 0) load_2d(a, ma, m, row, bar);
+          if (na > 1) load_2d(a + kChunkBytes, ma, m + 64, row, bar);
+          if (nb > 0) load_2d(b, mb, n, row, bar);
+          if (nb > 1) load_2d(b + kChunkBytes, mb, n + 64, row, bar);
         } else {
           int k0 = kb * kBlockK;
           if (kMode == kDgradRows && kb >= p.half_kb) k0 -= p.half_kb * kBlockK;
@@ -532,9 +576,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (zeros && mine > 0) {
 #pragma unroll
             for (int i = 0; i < kHalf / kSmallBox; ++i)
-              load_2d(a + i * kSmallBox * 128, ma, k0, i * kSmallBox < mine ? m + i * kSmallBox : p.R, bar);
+              load_2d(a + i * kSmallBox * 128, ma, i * kSmallBox < mine ? k0 : p.K, i * kSmallBox < mine ? m + i * kSmallBox : 0, bar);
           } else if (abytes) {
-            load_2d(a, ma, k0, mine > 0 ? m : p.R, bar);
+            load_2d(a, ma, mine > 0 ? k0 : p.K, mine > 0 ? m : 0, bar);
           }
           if constexpr (b_mn_major(kMode)) {
             if (nb > 0) load_3d(b, mb, n, k0, t.seg, bar);
@@ -561,7 +605,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t st = 0, ph = 0, unit = 0;
       bool ok = true;
       for (int item = first; item < total && ok; item += step) {
-        const int blocks = blocks_of(reduction_rows<kMode>(p, s_off, item)), nch = chains_of(blocks);
+        const int rows = reduction_rows<kMode>(p, s_off, item), blocks = blocks_of(rows), nch = chains_of(blocks);
+        const bool tail_end = kMode == kWgrad && rows % kBlockK != 0;   // the item's last block has been zeroed in part
         for (int ch = 0; ch < nch && ok; ++ch, ++unit) {
           const int nkb = part_of(blocks, nch, ch);
           const uint32_t buf = unit & 1u;
@@ -571,6 +616,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int kb = 0; kb < nkb; ++kb) {
             ok = __all_sync(0xffffffffu, wait_bounded(smem_u32(full + st), ph, p.status, s_abort));
             if (!ok) break;
+            if (tail_end && ch == nch - 1 && kb == nkb - 1) acquire_cluster(smem_u32(full + st), ph);
             tc_fence_after();
             const uint64_t so = (uint64_t)(st * (kStageBytes >> 4));
             mma_block<a_mn_major(kMode) ? 128u : 2u, b_mn_major(kMode) ? 128u : 2u>(tmem + buf * kTileN, da0 + so, db0 + so, idesc,
@@ -578,6 +624,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (++st == kStages) { st = 0; ph ^= 1u; }
           }
           if (ok) commit_pair(smem_u32(acc_full + buf));
+        }
+      }
+    }
+  } else if (warp == kZeroWarp) {
+    // ---------------- zeros behind the end of a segment ----------------
+    if constexpr (kMode == kWgrad) {
+      uint32_t at = 0, phases = 0;   // blocks passed; phase of each tail barrier
+      bool ok = true;
+      for (int item = first; item < total && ok; item += step) {
+        const int rows = reduction_rows<kMode>(p, s_off, item);
+        at += blocks_of(rows);
+        const int have = rows % kBlockK;
+        if (have == 0) continue;
+        const uint32_t st = (at - 1) % kStages;
+        ok = __all_sync(0xffffffffu, wait_while_turning(smem_u32(tail + st), (phases >> st) & 1u, smem_u32(empty), p.status, s_abort));
+        if (!ok) break;
+        phases ^= 1u << st;
+        uint8_t* base = smem + st * kStageBytes;
+        const int n16 = (kBlockK - have) * 8;   // 16-byte pieces of the rows to clear (a swizzle stays inside its row)
+        for (int c = 0; c < kStageBytes / kChunkBytes; ++c)
+          for (int i = lane; i < n16; i += 32)
+            *reinterpret_cast<uint4*>(base + c * kChunkBytes + have * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+        // The MMAs that read the zeros are CTA 0's, and CTA 1's half of B is an operand of both halves of the tile: CTA 1's
+        // stores are released to the cluster, CTA 0's have only its own MMA warp to reach.
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (rank == 0) mbar_arrive(smem_u32(full + st));
+          else arrive_release_cluster(leader_addr(smem_u32(full + st)));
         }
       }
     }
@@ -745,17 +820,6 @@ bool make_map(CUtensorMap* m, const void* ptr, int64_t d0, int64_t d1, int64_t d
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The weights' gradients' operand [R, cols]: the 64 rows from any row on as a dimension of their own (its stride is a row,
-// as the next dimension's), so that a box from coordinate -z of it holds z rows of zeros and then the 64 - z rows from the
-// last coordinate on: a segment's last block, nothing of its neighbour read.  The rows' order in a block is
-// free, as both operands have the same.
-bool window_map(CUtensorMap* m, const void* ptr, int64_t cols, int64_t R) {
-  const cuuint64_t dims[3] = {(cuuint64_t)cols, kBlockK, (cuuint64_t)R}, strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)cols * 2};
-  const cuuint32_t box[3] = {64, kBlockK, 1}, estr[3] = {1, 1, 1};
-  return encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <Mode kMode>
 cudaError_t launch(const Maps& maps, const Args& a, int64_t most_items, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(experts_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<kMode>::kBytes);
@@ -862,6 +926,7 @@ int moe_experts_forward(const void* rows, const int32_t* offsets, int64_t R, int
             make_map(&m.m[1], sh.gated ? w_gate : w_up, H, I, E, kHalf) && make_map(&m.m[2], w_up, H, I, E, kHalf);
   if (!ok) return MOE_ERR_CUDA;
   a.N = (int)I;
+  a.K = (int)H;
   a.nkb = div_up(H, kBlockK);
   a.n_tiles = div_up(I, sh.gated ? kHalf : kTileN);
   if (!row_outputs(m, a, R, I, g, u, hb)) return MOE_ERR_CUDA;
@@ -872,6 +937,7 @@ int moe_experts_forward(const void* rows, const int32_t* offsets, int64_t R, int
        make_map(&m.m[1], w_down, I, H, E, kHalf);
   if (!ok) return MOE_ERR_CUDA;
   a.N = (int)H;
+  a.K = (int)I;
   a.nkb = div_up(I, kBlockK);
   a.n_tiles = div_up(H, kTileN);
   if (!row_outputs(m, a, R, H, out, nullptr, nullptr)) return MOE_ERR_CUDA;
@@ -901,6 +967,7 @@ int moe_experts_backward(const void* dout, const int32_t* offsets, int64_t R, in
             make_map(&m.m[1], w_down, I, H, E, kBlockK);
   if (!ok) return MOE_ERR_CUDA;
   a.N = (int)I;
+  a.K = (int)H;
   a.nkb = div_up(H, kBlockK);
   a.n_tiles = div_up(I, kTileN);
   a.g = static_cast<const __nv_bfloat16*>(g);
@@ -914,6 +981,7 @@ int moe_experts_backward(const void* dout, const int32_t* offsets, int64_t R, in
        make_map(&m.m[5], du, I, R, 0, kSmallBox) && make_map(&m.m[4], w_up, H, I, E, kBlockK);
   if (!ok) return MOE_ERR_CUDA;
   a.N = (int)H;
+  a.K = (int)I;
   a.half_kb = div_up(I, kBlockK);
   a.nkb = a.half_kb * (sh.gated ? 2 : 1);
   a.n_tiles = div_up(H, kTileN);
@@ -946,8 +1014,9 @@ int moe_experts_weight_grad(const void* rows, const void* dout, const void* h, c
     if (!is_aligned(p, 16)) return MOE_ERR_INVALID_ARG;
   if (!encoder()) return MOE_ERR_CUDA;
   Maps m = {};
-  const bool ok = window_map(&m.m[0], sh.gated ? dg : du, I, R) && window_map(&m.m[1], rows, H, R) && window_map(&m.m[2], du, I, R) &&
-                  window_map(&m.m[3], dout, H, R) && window_map(&m.m[4], h, I, R) && make_map<4>(&m.out[0], sh.gated ? dw_gate : dw_up, H, I, E, 32) &&
+  const bool ok = make_map(&m.m[0], sh.gated ? dg : du, I, R, 0, kBlockK) && make_map(&m.m[1], rows, H, R, 0, kBlockK) &&
+                  make_map(&m.m[2], du, I, R, 0, kBlockK) && make_map(&m.m[3], dout, H, R, 0, kBlockK) &&
+                  make_map(&m.m[4], h, I, R, 0, kBlockK) && make_map<4>(&m.out[0], sh.gated ? dw_gate : dw_up, H, I, E, 32) &&
                   make_map<4>(&m.out[1], dw_up, H, I, E, 32) && make_map<4>(&m.out[2], dw_down, I, H, E, 32);
   if (!ok) return MOE_ERR_CUDA;
   Args a = base_args(sh, offsets, workspace, 0.0f, 0.0f);
