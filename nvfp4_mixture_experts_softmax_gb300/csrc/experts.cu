@@ -18,8 +18,8 @@
 // Wg, CTA 1 the same rows of Wu, so that each thread of the epilogue holds g and u of its row.
 //
 // Tiles of 256 rows of one segment: a tile's rows behind the segment are read and multiplied, but not
-// stored (rows do not mix).  In the weights' gradients the rows are the reduction: the last block of a
-// segment is zeroed behind the segment's end in shared memory, in both operands, before it is multiplied.
+// stored (rows do not mix).  In the weights' gradients the rows are the reduction, and a segment's last block has zeros in the
+// place of the rows that are not its own, in both operands, brought by the copies as the rows are (WgradMaps below).
 //
 // What bounds it, device times: with rows enough the tensor cores (one expert, 8192 rows of 4096 x 4096: forward 1.92
 // PFLOP/s, gradients of the rows 1.74, of the weights 1.75); 64 experts of uneven size, 65536 rows of 4096 x 1536:
@@ -29,10 +29,9 @@
 // rows an expert: reading the weights (64 tokens to 8 of 128 experts of 2048 x 768 194 us, 6.1 TB/s; one token 27 us;
 // gradients of the rows of 8192 tokens to 8 of 256 experts of 2048 x 512 435 us, 5.4 TB/s).
 //
-// Warps of a CTA: 0-7 epilogue (each a quarter of the rows and half of the columns), 8 and 11 copies (every other
+// Warps of a CTA: 0-7 epilogue (each a quarter of the rows and half of the columns), 8 and 10 copies (every other
 // stage each: a load takes 100 cycles to issue, up to four a stage), 9 tensor memory and, in CTA 0, the MMAs of
-// the pair, 10 the zeroing.  Two accumulators (2 x 256 columns) let
-// the epilogue run beside the next tile's products.  Every wait is bounded; one that runs out leaves
+// the pair.  Two accumulators (2 x 256 columns) let the epilogue run beside the next tile's products.  Every wait is bounded; one that runs out leaves
 // MOE_ERR_DEVICE_TIMEOUT in the status.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -55,8 +54,8 @@ constexpr int kBlockK = 64;
 constexpr int kOperandBytes = kHalf * kBlockK * 2;
 constexpr int kChunkBytes = kBlockK * 128;      // MN-major: 64 columns (128 bytes) of 64 rows
 constexpr int kStageBytes = 2 * kOperandBytes;
-constexpr int kEpiWarps = 8, kCopyWarp = 8, kMmaWarp = 9, kZeroWarp = 10, kCopyWarp2 = 11;
-constexpr int kThreads = 12 * 32;
+constexpr int kEpiWarps = 8, kCopyWarp = 8, kMmaWarp = 9, kCopyWarp2 = 10;
+constexpr int kThreads = 11 * 32;
 constexpr int kMaxExperts = 1024;
 constexpr int kGroupM = 8;                      // row tiles that are worked through column by column (4, 8, 16: the weights'
                                                 // gradients of 64 experts 1974, 1961, 1986 us)
@@ -88,7 +87,7 @@ struct Layout {
   static constexpr int kBarOff = kSlabOff + kEpiWarps * 32 * kSlabWidth;
   static constexpr int kTableOff = kBarOff + 256;
   static constexpr size_t kBytes = 1024 + kTableOff + 2 * (kMaxExperts + 1) * sizeof(int32_t) + 8;
-  static_assert(kBytes <= 232448 && (3 * kStages + 4) * 8 + 12 <= 256, "shared memory");
+  static_assert(kBytes <= 232448 && (2 * kStages + 4) * 8 + 12 <= 256, "shared memory");
 };
 
 constexpr bool a_mn_major(Mode m) { return m == kWgrad; }
@@ -104,6 +103,21 @@ struct Maps {
   CUtensorMap m[6];     // operands
   CUtensorMap out[3];   // what the epilogue writes, in slabs
 };
+
+// The weights' gradients: operands dg, rows, du, dout, h in blocks of 64 rows, and in boxes of 2^i rows for a segment's last
+// block.  `have` rows of it are two boxes of the largest 2^i <= have, from the first row and up to the last (one, if
+// that is all of them; where they overlap they bring the same), and the zeros behind them are two boxes of zeros alike.
+// So a copy reads nothing of the next segment and starts inside its tensor, and only the copy engine writes what the
+// pair's products read: at most 16 copies where a full block takes 4.  (Cleared by a warp's stores, whose release
+// to the other CTA and acquire cost 1 us an item: 64 experts of 511 rows, 7168 x 2048, 2922 us against 2580.)
+constexpr int kHeights = 6;
+struct WgradMaps {
+  CUtensorMap m[5], part[5][kHeights], zero[kHeights];
+  CUtensorMap out[3];
+};
+template <Mode kMode> struct MapsOf { using T = Maps; };
+template <> struct MapsOf<kWgrad> { using T = WgradMaps; };
+__device__ const uint4 g_zeros[(1 << (kHeights - 1)) * 8] = {};   // 128 bytes a row
 
 struct Args {
   const int32_t* offsets;
@@ -137,27 +151,10 @@ __device__ __forceinline__ uint32_t leader_addr(uint32_t bar) {
 }
 // Arrivals on a barrier of either CTA.  Release at CTA scope: what they order are TMA copies, MMAs and reads of
 // tensor memory, which complete on their own terms; at cluster scope each arrival would wait for the thread's
-// memory accesses (0.8 us a stage of the copies: a third of the rate).  Ordinary stores do not complete on their own
-// terms: an arrival that announces them to the other CTA releases at cluster scope, and the wait for it acquires there.
+// memory accesses (0.8 us a stage of the copies: a third of the rate).  No ordinary store to
+// shared memory is read by the other CTA or its MMAs.
 __device__ __forceinline__ void arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-__device__ __forceinline__ void arrive_release_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-// One more poll of a phase that is known to be complete, for what it acquires.
-__device__ __forceinline__ bool acquire_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n"
-      ".reg .pred p;\n"
-      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-      "selp.u32 %0, 1, 0, p;\n"
-      "}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
 }
 // As mbar_wait_bounded; gives up as soon as another role of the CTA has.
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, int32_t* status,
@@ -168,27 +165,6 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, int3
     if (mbar_try_wait(bar, parity)) return true;
     if (*abort) return false;
     if (global_timer_ns() - t0 > kLimitNs) {
-      set_status(status, MOE_ERR_DEVICE_TIMEOUT);
-      *abort = 1u;
-      return false;
-    }
-  }
-}
-
-// The same where many blocks pass before the phase completes (the zeroing warp's wait for the end of a segment, which may be
-// seconds long): the limit starts again whenever the ring is seen to have turned, by the phase of one of its barriers.
-__device__ __forceinline__ bool wait_while_turning(uint32_t bar, uint32_t parity, uint32_t beat, int32_t* status, volatile uint32_t* abort) {
-  if (mbar_try_wait(bar, parity)) return true;
-  uint64_t t0 = global_timer_ns();
-  bool seen = mbar_test_wait(beat, 0);
-  for (;;) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*abort) return false;
-    const bool now = mbar_test_wait(beat, 0);
-    if (now != seen) {
-      seen = now;
-      t0 = global_timer_ns();
-    } else if (global_timer_ns() - t0 > kLimitNs) {
       set_status(status, MOE_ERR_DEVICE_TIMEOUT);
       *abort = 1u;
       return false;
@@ -435,7 +411,7 @@ __device__ __forceinline__ Tile tile_at(const Args& p, const int32_t* s_off, con
   return t;
 }
 
-// Rows of the segment that an item's reduction runs over (kWgrad), all that the MMA and zeroing warps need to know.
+// Rows of the segment that an item's reduction runs over (kWgrad), all that the MMA warp needs to know.
 template <Mode kMode>
 __device__ __forceinline__ int reduction_rows(const Args& p, const int32_t* s_off, int item) {
   if (kMode != kWgrad) return 0;
@@ -445,15 +421,14 @@ __device__ __forceinline__ int reduction_rows(const Args& p, const int32_t* s_of
 
 template <Mode kMode>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    experts_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args p) {
+    experts_kernel(const __grid_constant__ typename MapsOf<kMode>::T maps, const __grid_constant__ Args p) {
   using L = Layout<kMode>;
   constexpr int kStages = L::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);   // [stage], CTA 0's: both CTAs' data has landed
   uint64_t* empty = full + kStages;                               // [stage]: the MMAs have read it
-  uint64_t* tail = empty + kStages;                               // [stage]: data that is to be zeroed has landed
-  uint64_t* acc_full = tail + kStages;                            // [2]
+  uint64_t* acc_full = empty + kStages;                           // [2]
   uint64_t* acc_empty = acc_full + 2;                             // [2], CTA 0's
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
   volatile uint32_t* s_abort = tmem_slot + 1;
@@ -467,7 +442,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_u32(full + s), 2);    // one arrival of each CTA, and the bytes
       mbar_init(smem_u32(empty + s), 1);
-      mbar_init(smem_u32(tail + s), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(acc_full + b), 1);
@@ -547,8 +521,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                               : mine <= 0 ? 0u : mine <= kSmallBox ? kSmallBox * 128u : (uint32_t)kOperandBytes;
       const uint32_t bytes = abytes + (b_mn_major(kMode) ? (uint32_t)nb * kChunkBytes : nb ? (uint32_t)kOperandBytes : 0u);
       const bool small = part && mine > 0 && (zeros || mine <= kSmallBox);
-      const CUtensorMap* ma = maps.m + (kMode == kWgrad ? (t.mat == 0 ? 0 : t.mat == 1 ? 2 : 3) : small ? 3 : 0);
-      const CUtensorMap* mb = maps.m + (kMode == kWgrad ? (t.mat == 2 ? 4 : 1) : kMode == kUp && rank == 1 ? 2 : 1);
+      const int ia = kMode == kWgrad ? (t.mat == 0 ? 0 : t.mat == 1 ? 2 : 3) : small ? 3 : 0;
+      const int ib = kMode == kWgrad ? (t.mat == 2 ? 4 : 1) : kMode == kUp && rank == 1 ? 2 : 1;
+      const CUtensorMap *ma = maps.m + ia, *mb = maps.m + ib;
       const int nkb = blocks_of(t.rows);
       for (int kb = 0; kb < nkb; ++kb, mine_next ^= 1u, st = st + 1 == kStages ? 0 : st + 1, ph ^= st == 0) {
         filled = min(filled + 1, (uint32_t)kStages);
@@ -560,15 +535,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, wait_bounded(smem_u32(empty + st), ph ^ 1u, p.status, s_abort));
         if (!ok) break;
         const uint32_t a = smem0 + st * kStageBytes, b = a + kOperandBytes;
-        uint32_t bar = full0 + 8 * st;
+        const uint32_t bar = full0 + 8 * st;
         if constexpr (kMode == kWgrad) {
-          const int done = kb * kBlockK, row = t.row0 + done;
-          if (done + kBlockK > t.rows) bar = smem_u32(tail + st);   // rows behind the segment are to be zeroed
-          expect_bytes(bar, bytes);
-          if (na > 0) load_2d(a, ma, m, row, bar);
-          if (na > 1) load_2d(a + kChunkBytes, ma, m + 64, row, bar);
-          if (nb > 0) load_2d(b, mb, n, row, bar);
-          if (nb > 1) load_2d(b + kChunkBytes, mb, n + 64, row, bar);
+          const int done = kb * kBlockK, row = t.row0 + done, have = t.rows - done;
+          if (have >= kBlockK) {
+            expect_bytes(bar, bytes);
+            if (na > 0) load_2d(a, ma, m, row, bar);
+            if (na > 1) load_2d(a + kChunkBytes, ma, m + 64, row, bar);
+            if (nb > 0) load_2d(b, mb, n, row, bar);
+            if (nb > 1) load_2d(b + kChunkBytes, mb, n + 64, row, bar);
+          } else {
+            const int lv = 31 - __clz(have), lz = 31 - __clz(kBlockK - have), hv = 1 << lv, hz = 1 << lz;
+            const bool v2 = have > hv, z2 = kBlockK - have > hz;
+            expect_bytes(bar, (uint32_t)((na + nb) * ((v2 ? 2 * hv : hv) + (z2 ? 2 * hz : hz)) * 128));
+            auto last_block = [&](uint32_t to, const CUtensorMap* map, int x) {
+              load_2d(to, map, x, row, bar);
+              if (v2) load_2d(to + (have - hv) * 128, map, x, row + have - hv, bar);
+              load_2d(to + have * 128, maps.zero + lz, 0, 0, bar);
+              if (z2) load_2d(to + (kBlockK - hz) * 128, maps.zero + lz, 0, 0, bar);
+            };
+            if (na > 0) last_block(a, maps.part[ia] + lv, m);
+            if (na > 1) last_block(a + kChunkBytes, maps.part[ia] + lv, m + 64);
+            if (nb > 0) last_block(b, maps.part[ib] + lv, n);
+            if (nb > 1) last_block(b + kChunkBytes, maps.part[ib] + lv, n + 64);
+          }
         } else {
           int k0 = kb * kBlockK;
           if (kMode == kDgradRows && kb >= p.half_kb) k0 -= p.half_kb * kBlockK;
@@ -605,8 +595,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t st = 0, ph = 0, unit = 0;
       bool ok = true;
       for (int item = first; item < total && ok; item += step) {
-        const int rows = reduction_rows<kMode>(p, s_off, item), blocks = blocks_of(rows), nch = chains_of(blocks);
-        const bool tail_end = kMode == kWgrad && rows % kBlockK != 0;   // the item's last block has been zeroed in part
+        const int blocks = blocks_of(reduction_rows<kMode>(p, s_off, item)), nch = chains_of(blocks);
         for (int ch = 0; ch < nch && ok; ++ch, ++unit) {
           const int nkb = part_of(blocks, nch, ch);
           const uint32_t buf = unit & 1u;
@@ -616,7 +605,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int kb = 0; kb < nkb; ++kb) {
             ok = __all_sync(0xffffffffu, wait_bounded(smem_u32(full + st), ph, p.status, s_abort));
             if (!ok) break;
-            if (tail_end && ch == nch - 1 && kb == nkb - 1) acquire_cluster(smem_u32(full + st), ph);
             tc_fence_after();
             const uint64_t so = (uint64_t)(st * (kStageBytes >> 4));
             mma_block<a_mn_major(kMode) ? 128u : 2u, b_mn_major(kMode) ? 128u : 2u>(tmem + buf * kTileN, da0 + so, db0 + so, idesc,
@@ -624,35 +612,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (++st == kStages) { st = 0; ph ^= 1u; }
           }
           if (ok) commit_pair(smem_u32(acc_full + buf));
-        }
-      }
-    }
-  } else if (warp == kZeroWarp) {
-    // ---------------- zeros behind the end of a segment ----------------
-    if constexpr (kMode == kWgrad) {
-      uint32_t at = 0, phases = 0;   // blocks passed; phase of each tail barrier
-      bool ok = true;
-      for (int item = first; item < total && ok; item += step) {
-        const int rows = reduction_rows<kMode>(p, s_off, item);
-        at += blocks_of(rows);
-        const int have = rows % kBlockK;
-        if (have == 0) continue;
-        const uint32_t st = (at - 1) % kStages;
-        ok = __all_sync(0xffffffffu, wait_while_turning(smem_u32(tail + st), (phases >> st) & 1u, smem_u32(empty), p.status, s_abort));
-        if (!ok) break;
-        phases ^= 1u << st;
-        uint8_t* base = smem + st * kStageBytes;
-        const int n16 = (kBlockK - have) * 8;   // 16-byte pieces of the rows to clear (a swizzle stays inside its row)
-        for (int c = 0; c < kStageBytes / kChunkBytes; ++c)
-          for (int i = lane; i < n16; i += 32)
-            *reinterpret_cast<uint4*>(base + c * kChunkBytes + have * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-        // The MMAs that read the zeros are CTA 0's, and CTA 1's half of B is an operand of both halves of the tile: CTA 1's
-        // stores are released to the cluster, CTA 0's have only its own MMA warp to reach.
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (rank == 0) mbar_arrive(smem_u32(full + st));
-          else arrive_release_cluster(leader_addr(smem_u32(full + st)));
         }
       }
     }
@@ -821,7 +780,7 @@ bool make_map(CUtensorMap* m, const void* ptr, int64_t d0, int64_t d1, int64_t d
 }
 
 template <Mode kMode>
-cudaError_t launch(const Maps& maps, const Args& a, int64_t most_items, cudaStream_t s) {
+cudaError_t launch(const typename MapsOf<kMode>::T& maps, const Args& a, int64_t most_items, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(experts_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<kMode>::kBytes);
   if (e != cudaSuccess) return e;
   const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(most_items, num_sms() / 2));
@@ -1013,11 +972,18 @@ int moe_experts_weight_grad(const void* rows, const void* dout, const void* h, c
   for (const void* p : {rows, dout, h, dg, du})
     if (!is_aligned(p, 16)) return MOE_ERR_INVALID_ARG;
   if (!encoder()) return MOE_ERR_CUDA;
-  Maps m = {};
-  const bool ok = make_map(&m.m[0], sh.gated ? dg : du, I, R, 0, kBlockK) && make_map(&m.m[1], rows, H, R, 0, kBlockK) &&
-                  make_map(&m.m[2], du, I, R, 0, kBlockK) && make_map(&m.m[3], dout, H, R, 0, kBlockK) &&
-                  make_map(&m.m[4], h, I, R, 0, kBlockK) && make_map<4>(&m.out[0], sh.gated ? dw_gate : dw_up, H, I, E, 32) &&
-                  make_map<4>(&m.out[1], dw_up, H, I, E, 32) && make_map<4>(&m.out[2], dw_down, I, H, E, 32);
+  WgradMaps m = {};
+  void* zeros = nullptr;
+  if (cudaGetSymbolAddress(&zeros, g_zeros) != cudaSuccess) return MOE_ERR_CUDA;
+  const void* const operands[5] = {sh.gated ? dg : du, rows, du, dout, h};
+  bool ok = make_map<4>(&m.out[0], sh.gated ? dw_gate : dw_up, H, I, E, 32) && make_map<4>(&m.out[1], dw_up, H, I, E, 32) &&
+            make_map<4>(&m.out[2], dw_down, I, H, E, 32);
+  for (int i = 0; i < 5; ++i) {
+    const int64_t cols = i == 1 || i == 3 ? H : I;
+    ok = ok && make_map(&m.m[i], operands[i], cols, R, 0, kBlockK);
+    for (int l = 0; l < kHeights; ++l) ok = ok && make_map(&m.part[i][l], operands[i], cols, R, 0, 1 << l);
+  }
+  for (int l = 0; l < kHeights; ++l) ok = ok && make_map(&m.zero[l], zeros, 64, 1 << (kHeights - 1), 0, 1 << l);
   if (!ok) return MOE_ERR_CUDA;
   Args a = base_args(sh, offsets, workspace, 0.0f, 0.0f);
   a.M = (int)H;
