@@ -24,8 +24,8 @@
 // What bounds it, device times: with rows enough the tensor cores (one expert, 8192 rows of 4096 x 4096: forward 1.92
 // PFLOP/s, gradients of the rows 1.74, of the weights 1.75); 64 experts of uneven size, 65536 rows of 4096 x 1536:
 // forward 1.49 ms (1.65 PFLOP/s: an eighth of the row tiles' rows lie behind their segment; 1.70 ms once the power cap
-// lowers the clock), weights' gradients 1.95 to 2.0 ms (1.25: 4.8 GB of FP32 results beside the operands' way from L2), added to
-// earlier ones 2.65 ms (the results are read, too); few
+// lowers the clock), weights' gradients 1.95 to 2.0 ms (1.25: 4.8 GB of FP32 results beside the operands' way from L2; 2.09 ms under the power cap),
+// added to earlier ones 2.68 ms (the results are read, too); few
 // rows an expert: reading the weights (64 tokens to 8 of 128 experts of 2048 x 768 194 us, 6.1 TB/s; one token 27 us;
 // gradients of the rows of 8192 tokens to 8 of 256 experts of 2048 x 512 435 us, 5.4 TB/s).
 //

@@ -104,3 +104,37 @@ def test_chains(moe, H, I, accumulate):
             size = a.abs().t() @ b.abs()
             bound = (44 * STEP + (chains + 1) * U) * size + U * old.abs()
             assert bool(((w[name][e].double() - a.t() @ b - old).abs() <= bound).all()), (name, e)
+
+
+def test_tensors_that_fill_their_memory(moe):
+    """Every tensor is a whole number of the allocator's 2 MB blocks, so that it begins and ends with them: segments of a few
+    rows at its beginning and its end, tiles that are mostly zeros, all three passes."""
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    R, H, I, lens = 8192, 1024, 1024, [3, 130, 0, 1, 700, 5000, 2351, 5, 2]
+    assert sum(lens) == R
+    E = len(lens)
+    g = torch.Generator(device="cuda").manual_seed(31)
+    n = lambda *s, scale=1.0: (torch.randn(*s, device="cuda", generator=g, dtype=BF16) * scale)  # noqa: E731
+    x, dout = n(R, H), n(R, H, scale=0.1)
+    wg, wu, wd = n(E, I, H, scale=0.03), n(E, I, H, scale=0.03), n(E, H, I, scale=0.03)
+    off = torch.tensor([0] + lens).cumsum(0)
+    plan = {"offsets": off.to(torch.int32).cuda()}
+    ws = moe.experts_workspace(R, I)
+    torch.cuda.empty_cache()
+    o = moe.experts_forward(x, plan, wg, wu, wd, keep=True, workspace=ws)
+    b = moe.experts_backward(dout, o, plan, wg, wu, wd, workspace=ws)
+    w = moe.experts_weight_grad(x, dout, o, b, plan, workspace=ws)
+    assert moe.last_device_status(ws) == 0
+    half = 2.0 ** -8
+    for e, rows in enumerate(lens):
+        r = slice(int(off[e]), int(off[e + 1]))
+        for got, left, right in ((o["u"], x, wu[e].t()), (o["g"], x, wg[e].t()), (o["out"], o["h"], wd[e].t())):
+            want, size = left[r].double() @ right.double(), left[r].double().abs() @ right.double().abs()
+            assert bool(((got[r].double() - want).abs() <= half * want.abs() + (1024 / 16 + 4) * STEP * size * (1 + half)).all()), e
+        dx = b["dg"][r].double() @ wg[e].double() + b["du"][r].double() @ wu[e].double()
+        size = b["dg"][r].double().abs() @ wg[e].double().abs() + b["du"][r].double().abs() @ wu[e].double().abs()
+        assert bool(((b["drows"][r].double() - dx).abs() <= half * dx.abs() + (2048 / 16 + 4) * STEP * size * (1 + half)).all()), e
+        for name, left, right in (("w_gate", b["dg"], x), ("w_up", b["du"], x), ("w_down", dout, o["h"])):
+            want, size = left[r].double().t() @ right[r].double(), left[r].double().abs().t() @ right[r].double().abs()
+            assert bool(((w[name][e].double() - want).abs() <= (44 * STEP + (rows / 512 + 2) * U) * size).all()), (name, e)
